@@ -61,7 +61,8 @@ typedef enum {
     MOE_ERR_DEVICE_BAD_EXPERT_ID = 7, /* an id outside [0, E) was seen */
     MOE_ERR_DEVICE_TIMEOUT = 8,       /* a bounded device wait gave up */
     MOE_ERR_DEVICE_FP16_RANGE = 9,    /* a value is not representable in fp16 */
-    MOE_ERR_DEVICE_BAD_LOGIT = 10     /* a router logit is NaN or +inf */
+    MOE_ERR_DEVICE_BAD_LOGIT = 10,    /* a router logit is NaN or +inf */
+    MOE_ERR_DEVICE_BAD_INDEX = 11     /* a position, slot, page or length out of range (moe_attn.h) */
 } moe_status_t;
 
 /* Which matrix a prepacked buffer holds. */

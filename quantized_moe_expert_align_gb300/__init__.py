@@ -29,6 +29,7 @@ MOE_ERR_DEVICE_BAD_EXPERT_ID = 7
 MOE_ERR_DEVICE_TIMEOUT = 8
 MOE_ERR_DEVICE_FP16_RANGE = 9
 MOE_ERR_DEVICE_BAD_LOGIT = 10
+MOE_ERR_DEVICE_BAD_INDEX = 11
 MOE_PACK_W13 = 1
 MOE_PACK_W2 = 2
 
@@ -53,8 +54,32 @@ class moe_diag_t(ctypes.Structure):
                 ("token_tile2", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class moe_kv_cache_t(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("type", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32)]
+
+
 _lock = threading.Lock()
 _lib = None
+
+
+def _attn_signatures():
+    """The entry points of ``include/moe_attn.h``."""
+    i, p, sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
+    n, f = ctypes.c_int64, ctypes.c_float
+    cache, psz = ctypes.POINTER(moe_kv_cache_t), ctypes.POINTER(ctypes.c_size_t)
+    return {
+        "moe_kv_cache_size": (i, [i, i, i, i, i, psz, psz]),
+        "moe_qk_rope_append": (i, [p, n, p, n, p, n, p, p, f, p, i, i, i, p, p, p, n, p, n, cache,
+                                   i, i, i, i, p, sz, p]),
+        "moe_kv_gather": (i, [cache, p, i, p, i, i, p, n, p, n, p, sz, p]),
+        "moe_attn_decode_workspace_size": (sz, [i, i, i, i]),
+        "moe_attn_decode": (i, [p, n, cache, p, i, p, f, p, n, p, i, i, p, sz, p]),
+        "moe_attn_prefill_workspace_size": (sz, [i, i, i, i, i]),
+        "moe_attn_prefill": (i, [p, n, p, n, p, n, p, p, i, i, i, i, i, i, i, f, p, n, p, p, sz,
+                                 p]),
+    }
 
 
 def load(path: str = LIB_PATH):
@@ -84,6 +109,7 @@ def load(path: str = LIB_PATH):
             "moe_w4a16_get_diag": (i, [ctypes.POINTER(moe_diag_t)]),
             "moe_w4a16_workspace_views": (i, [i, i, i, i, i, ctypes.POINTER(moe_ws_views_t)]),
         }
+        sig.update(_attn_signatures())
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
             fn.restype = res
@@ -308,3 +334,10 @@ def forward_routed(hidden, logits, k, w13, w2, E, I, out=None, workspace=None, s
     _check(moe_w4a16_forward_routed(hidden, logits.contiguous(), w13, w2, out, ids, w, M, k, E,
                                     H, I, ws, stream), "moe_w4a16_forward_routed")
     return out, ids, w
+
+
+# The attention half of a decoder layer (moe_attn.h).
+from .attention import (AttnWorkspace, KVCache, MOE_ATTN_STATUS_BYTES,  # noqa: E402
+                        MOE_KV_BF16, MOE_KV_FP8, attn_decode, attn_prefill, kv_gather,
+                        moe_attn_decode_workspace_size, moe_attn_prefill_workspace_size,
+                        moe_kv_cache_size, qk_rope_append, rope_table)

@@ -1,0 +1,298 @@
+"""Attention half of a decoder layer: torch conveniences over ``include/moe_attn.h``.
+
+Each function checks shapes and types, allocates what the caller did not
+pass, calls the C entry point of the same name and raises ``MoeError`` on a
+host-side error.  Errors found on the device are in the workspace's status
+word (``moe_w4a16_get_device_status(workspace.buf)``).
+
+Rows may be strided between tokens (the three parts of one fused projection);
+the heads of a token and the values of a head are contiguous.  Tensors have
+to live on the current device and be ready on the stream of the call (the
+current stream unless ``stream`` is given).
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import quantized_moe_expert_align_gb300 as _moe
+
+MOE_KV_BF16 = 0
+MOE_KV_FP8 = 1
+MOE_ATTN_STATUS_BYTES = 256
+
+
+def moe_kv_cache_size(type, num_pages, page_size, Hkv, D):
+    """(status, data bytes, scale bytes) of a cache."""
+    d, s = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    st = _moe.load().moe_kv_cache_size(type, num_pages, page_size, Hkv, D, ctypes.byref(d),
+                                       ctypes.byref(s))
+    return st, d.value, s.value
+
+
+def moe_attn_decode_workspace_size(B, Hq, Hkv, D):
+    return _moe.load().moe_attn_decode_workspace_size(B, Hq, Hkv, D)
+
+
+def moe_attn_prefill_workspace_size(B, Tq, Hq, Hkv, D):
+    return _moe.load().moe_attn_prefill_workspace_size(B, Tq, Hq, Hkv, D)
+
+
+def rope_table(max_pos, rot, base=10000.0, factor=1.0, original_max=None, beta_fast=32.0,
+               beta_slow=1.0, magnitude=None, device="cuda"):
+    """cos_sin [max_pos][rot] fp32 (rot/2 cosines, then rot/2 sines), from
+    angles computed in 64 bits.
+
+    Pair i turns by pos * f_i with f_i = base^(-2i/rot).  For contexts longer
+    than the model was trained on, ``factor`` > 1:
+    * ``original_max`` None: every f_i is divided by ``factor`` (positions
+      interpolated linearly);
+    * ``original_max`` given: by parts.  A pair that makes at least
+      ``beta_fast`` turns within ``original_max`` positions keeps f_i, one
+      that makes at most ``beta_slow`` turns has it divided by ``factor``, and
+      in between the two are blended linearly in the pair's index.
+    ``magnitude`` multiplies cosines and sines (by parts, default
+    0.1 ln(factor) + 1; else 1), which scales q and k and so the attention's
+    scores by its square.
+    """
+    import torch
+    if rot % 2 or rot < 0 or max_pos < 1 or factor < 1.0:
+        raise ValueError("rope_table: rot even, max_pos >= 1, factor >= 1")
+    i = torch.arange(rot // 2, dtype=torch.float64, device=device)
+    f = base ** (-2.0 * i / max(rot, 1))
+    if factor > 1.0 and original_max is None:
+        f = f / factor
+    elif factor > 1.0:
+        def index_of(turns):   # the (real) pair index that makes `turns` turns
+            return rot / 2 * math.log(original_max / (2 * math.pi * turns)) / math.log(base)
+        lo = max(math.floor(index_of(beta_fast)), 0)
+        hi = min(math.ceil(index_of(beta_slow)), rot // 2 - 1)
+        blend = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        f = f * (1 - blend) + f / factor * blend
+        if magnitude is None:
+            magnitude = 0.1 * math.log(factor) + 1.0
+    a = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * f
+    return (torch.cat([a.cos(), a.sin()], 1) * (1.0 if magnitude is None else magnitude)).float()
+
+
+class KVCache:
+    """A paged key/value cache over caller-owned tensors: ``data``
+    [num_pages][Hkv][2][page_size][D] bfloat16 or float8_e4m3fn and, for the
+    latter, ``scales`` [num_pages][Hkv][2][page_size] float32."""
+
+    def __init__(self, data, scales=None):
+        import torch
+        if (data.dim() != 5 or data.shape[2] != 2 or not data.is_contiguous() or
+                not data.is_cuda):
+            raise ValueError("KVCache: data is a contiguous [num_pages][Hkv][2][page_size][D] "
+                             "on a GPU")
+        if data.dtype == torch.bfloat16 and scales is None:
+            kind = MOE_KV_BF16
+        elif data.dtype == torch.float8_e4m3fn and scales is not None:
+            kind = MOE_KV_FP8
+            if (scales.dtype != torch.float32 or scales.shape != data.shape[:4] or
+                    not scales.is_contiguous() or scales.device != data.device):
+                raise ValueError("KVCache: scales is a contiguous float32 "
+                                 "[num_pages][Hkv][2][page_size] on data's device")
+        else:
+            raise ValueError("KVCache: bfloat16 data, or float8_e4m3fn data with scales")
+        self.data, self.scales = data, scales
+        self.num_pages, self.Hkv, _, self.page_size, self.D = data.shape
+        self._c = _moe.moe_kv_cache_t(data.data_ptr(), None if scales is None else scales.data_ptr(),
+                                      kind, self.num_pages, self.page_size, self.Hkv, self.D)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, num_pages, Hkv, D, page_size=64, fp8=True, device="cuda"):
+        """A new cache (contents undefined until tokens are appended)."""
+        import torch
+        shape = (num_pages, Hkv, 2, page_size, D)
+        if fp8:
+            return cls(torch.empty(shape, dtype=torch.float8_e4m3fn, device=device),
+                       torch.empty(shape[:4], dtype=torch.float32, device=device))
+        return cls(torch.empty(shape, dtype=torch.bfloat16, device=device))
+
+
+class AttnWorkspace:
+    """A reusable workspace: ``op`` "decode" or "prefill" sized for up to B
+    sequences and ``rows`` query rows in all; without ``op``, for
+    qk_rope_append and kv_gather.  ``buf`` is what the status call takes."""
+
+    def __init__(self, device, op=None, B=0, rows=0, Hq=1, Hkv=1, D=128):
+        if op is None:
+            n = MOE_ATTN_STATUS_BYTES
+        elif op == "decode":
+            n = moe_attn_decode_workspace_size(B, Hq, Hkv, D)
+        elif op == "prefill":
+            n = moe_attn_prefill_workspace_size(B, rows, Hq, Hkv, D)
+        else:
+            raise ValueError(f"AttnWorkspace: unknown op {op!r}")
+        if n == 0:
+            raise _moe.MoeError(_moe.MOE_ERR_INVALID_ARG, "AttnWorkspace")
+        self.nbytes = n
+        self.buf = _moe._empty_bytes(n, device)
+        self._ptr = self.buf.data_ptr()
+
+
+def _bf16(t, name, *shape):
+    import torch
+    if t.dtype != torch.bfloat16 or t.shape != shape or not t.is_cuda:
+        raise ValueError(f"{name}: bfloat16 {shape} on a GPU expected, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+
+
+def _rows(t, name, T, H, D):
+    """Checks rows [T][H][D] with contiguous heads; the stride between tokens."""
+    _bf16(t, name, T, H, D)
+    st = t.stride()
+    if T and (st[2] != 1 or (H > 1 and st[1] != D)):
+        raise ValueError(f"{name}: the heads of a token have to be contiguous")
+    return st[0] if T > 1 else H * D
+
+
+def _i32(t, name, *shape):
+    import torch
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: contiguous int32 {shape} on a GPU expected, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _made(t, stream):
+    """A buffer allocated here for a call on ``stream``: when that is not the
+    current stream, torch must not reuse the memory before the call is done."""
+    if stream is not None:
+        import torch
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream)
+        t.record_stream(stream)
+    return t
+
+
+def _rows_out(T, H, D, device, stream):
+    import torch
+    return _made(torch.empty((T, H, D), dtype=torch.bfloat16, device=device), stream)
+
+
+def _workspace(ws, stream, device, *size):
+    if ws is None:
+        ws = AttnWorkspace(device, *size)
+        _made(ws.buf, stream)
+    return ws
+
+
+def qk_rope_append(q, k, v, cos_sin, positions, cache, slots, q_norm=None, k_norm=None, eps=1e-6,
+                   interleaved=False, q_out=None, k_out=None, workspace=None, stream=None):
+    """Norm, rotation and cache write of T new tokens: q [T][Hq][D], k and v
+    [T][Hkv][D], cos_sin [max_pos][rot] (None: no rotation), positions and
+    slots [T] int32, cache a KVCache or None.  Returns q_out; ``k_out`` True
+    or a tensor also returns the rotated keys, as (q_out, k_out)."""
+    import torch
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    sq, sk, sv = _rows(q, "q", T, Hq, D), _rows(k, "k", T, Hkv, D), _rows(v, "v", T, Hkv, D)
+    max_pos, rot = cos_sin.shape if cos_sin is not None else (0, 0)
+    if rot:
+        if cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous() or not cos_sin.is_cuda:
+            raise ValueError("cos_sin: contiguous float32 [max_pos][rot] on a GPU expected")
+        _i32(positions, "positions", T)
+    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if w is not None:
+            _bf16(w, name, D)
+            if not w.is_contiguous():
+                raise ValueError(f"{name}: contiguous expected")
+    if cache is not None:
+        _i32(slots, "slots", T)
+    if q_out is None:
+        q_out = _rows_out(T, Hq, D, q.device, stream)
+    if k_out is True:
+        k_out = _rows_out(T, Hkv, D, q.device, stream)
+    sqo = _rows(q_out, "q_out", T, Hq, D)
+    sko = _rows(k_out, "k_out", T, Hkv, D) if k_out is not None else 0
+    ws = _workspace(workspace, stream, q.device)
+    _moe._check(_moe.load().moe_qk_rope_append(
+        _p(q), sq, _p(k), sk, _p(v), sv, _p(q_norm), _p(k_norm), eps, _p(cos_sin), max_pos, rot,
+        int(interleaved), _p(positions) if rot else None, _p(slots) if cache is not None else None,
+        _p(q_out), sqo, _p(k_out), sko, cache._ref if cache is not None else None, T, Hq, Hkv, D,
+        ws._ptr, ws.nbytes, _moe._stream(stream)), "moe_qk_rope_append")
+    return q_out if k_out is None else (q_out, k_out)
+
+
+def kv_gather(cache, page_table, cu_k, total, k_out=None, v_out=None, workspace=None, stream=None):
+    """The cached tokens of B sequences as packed bf16 (k, v)
+    [total][Hkv][D]; page_table [B][n] and cu_k [B+1] int32."""
+    B, n = page_table.shape
+    _i32(page_table, "page_table", B, n)
+    _i32(cu_k, "cu_k", B + 1)
+    shape = (total, cache.Hkv, cache.D)
+    if k_out is None:
+        k_out = _rows_out(*shape, page_table.device, stream)
+    if v_out is None:
+        v_out = _rows_out(*shape, page_table.device, stream)
+    ws = _workspace(workspace, stream, page_table.device)
+    _moe._check(_moe.load().moe_kv_gather(
+        cache._ref, _p(page_table), n, _p(cu_k), B, total, _p(k_out),
+        _rows(k_out, "k_out", *shape), _p(v_out), _rows(v_out, "v_out", *shape), ws._ptr,
+        ws.nbytes, _moe._stream(stream)), "moe_kv_gather")
+    return k_out, v_out
+
+
+def attn_decode(q, cache, page_table, seq_lens, scale=None, out=None, lse=None, workspace=None,
+                stream=None):
+    """Attention of one token of each of B sequences over its cached tokens:
+    q [B][Hq][D], page_table [B][n] and seq_lens [B] int32; scale defaults to
+    D^-1/2.  Returns out [B][Hq][D]; ``lse`` True or a float32 [B][Hq] tensor
+    also returns the logsumexp, as (out, lse)."""
+    B, Hq, D = q.shape
+    if D != cache.D:
+        raise ValueError(f"q has heads of {D}, the cache of {cache.D}")
+    n = page_table.shape[1]
+    _i32(page_table, "page_table", B, n)
+    _i32(seq_lens, "seq_lens", B)
+    sq = _rows(q, "q", B, Hq, D)
+    if out is None:
+        out = _rows_out(B, Hq, D, q.device, stream)
+    so = _rows(out, "out", B, Hq, D)
+    lse = _lse(lse, B, Hq, q.device, stream)
+    ws = _workspace(workspace, stream, q.device, "decode", B, B, Hq, cache.Hkv, D)
+    _moe._check(_moe.load().moe_attn_decode(
+        _p(q), sq, cache._ref, _p(page_table), n, _p(seq_lens), D ** -0.5 if scale is None else scale,
+        _p(out), so, _p(lse), B, Hq, ws._ptr, ws.nbytes, _moe._stream(stream)), "moe_attn_decode")
+    return out if lse is None else (out, lse)
+
+
+def attn_prefill(q, k, v, cu_q, cu_k, causal=True, scale=None, out=None, lse=None, workspace=None,
+                 stream=None):
+    """Attention over packed sequences: q [Tq][Hq][D], k and v [Tk][Hkv][D],
+    cu_q and cu_k [B+1] int32; the last query of a sequence stands at its last
+    key.  Returns out [Tq][Hq][D]; ``lse`` True or a float32 [Tq][Hq] tensor
+    also returns the logsumexp, as (out, lse)."""
+    Tq, Hq, D = q.shape
+    Tk, Hkv, _ = k.shape
+    B = cu_q.shape[0] - 1
+    _i32(cu_q, "cu_q", B + 1)
+    _i32(cu_k, "cu_k", B + 1)
+    sq, sk, sv = _rows(q, "q", Tq, Hq, D), _rows(k, "k", Tk, Hkv, D), _rows(v, "v", Tk, Hkv, D)
+    if out is None:
+        out = _rows_out(Tq, Hq, D, q.device, stream)
+    so = _rows(out, "out", Tq, Hq, D)
+    lse = _lse(lse, Tq, Hq, q.device, stream)
+    ws = _workspace(workspace, stream, q.device, "prefill", B, Tq, Hq, Hkv, D)
+    _moe._check(_moe.load().moe_attn_prefill(
+        _p(q), sq, _p(k), sk, _p(v), sv, _p(cu_q), _p(cu_k), B, Tq, Tk, Hq, Hkv, D, int(causal),
+        D ** -0.5 if scale is None else scale, _p(out), so, _p(lse), ws._ptr, ws.nbytes,
+        _moe._stream(stream)), "moe_attn_prefill")
+    return out if lse is None else (out, lse)
+
+
+def _lse(lse, T, Hq, device, stream):
+    import torch
+    if lse is True:
+        return _made(torch.empty((T, Hq), dtype=torch.float32, device=device), stream)
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, Hq) or
+                            not lse.is_contiguous() or not lse.is_cuda):
+        raise ValueError(f"lse: contiguous float32 {(T, Hq)} on a GPU expected")
+    return lse

@@ -170,14 +170,6 @@ FwdLayout fwd_layout(int M, int k, int E, int H, int I) {
     return l;
 }
 
-namespace {
-
-// Per host thread: calls from several threads (or for several devices from
-// several threads) never write the same record.
-thread_local moe_diag_t g_diag = {2, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 moe_status_t check_device() {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -196,6 +188,14 @@ moe_status_t check_device() {
     if (dev >= 0 && dev < 64) support[dev] = ok ? 1 : 2;
     return ok ? MOE_OK : MOE_ERR_UNSUPPORTED_DEVICE;
 }
+
+namespace {
+
+// Per host thread: calls from several threads (or for several devices from
+// several threads) never write the same record.
+thread_local moe_diag_t g_diag = {2, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+
+bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 bool routing_sizes_ok(int M, int k, int E) {
     return M >= 0 && k >= 1 && k <= 64 && E >= 1 && E <= 1024 && (int64_t)M * k < INT_MAX;
@@ -263,6 +263,8 @@ const char *moe_status_string(moe_status_t s) {
         case MOE_ERR_DEVICE_TIMEOUT: return "MOE_ERR_DEVICE_TIMEOUT: a bounded device wait gave up";
         case MOE_ERR_DEVICE_FP16_RANGE: return "MOE_ERR_DEVICE_FP16_RANGE: value not representable in fp16";
         case MOE_ERR_DEVICE_BAD_LOGIT: return "MOE_ERR_DEVICE_BAD_LOGIT: a router logit is NaN or +inf";
+        case MOE_ERR_DEVICE_BAD_INDEX:
+            return "MOE_ERR_DEVICE_BAD_INDEX: a position, cache slot, page or length is out of range";
     }
     return "MOE_ERR_UNKNOWN";
 }

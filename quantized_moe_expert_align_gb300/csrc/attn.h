@@ -1,0 +1,80 @@
+// attn.h -- arguments and launchers of the attention half of a decoder layer
+// (rope_append.cu, attn_decode.cu, attn_prefill.cu).
+#pragma once
+
+#include "moe_attn.h"
+#include "moe_internal.h"
+
+namespace moe {
+
+// A paged cache as the kernels see it.
+struct KvView {
+    const uint8_t *data;
+    const float *scales;
+    int num_pages, page_shift, Hkv;  // page_size = 1 << page_shift
+};
+
+struct AppendArgs {
+    const uint16_t *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const uint16_t *q_norm, *k_norm;
+    float eps;
+    const float *cos_sin;
+    int max_pos, rot, interleaved;
+    const int32_t *positions, *slots;
+    uint16_t *q_out, *k_out;
+    int64_t q_out_stride, k_out_stride;
+    uint8_t *data;   // cache; null: nothing is cached
+    float *scales;
+    int cache_type, num_pages, page_shift;
+    int T, Hq, Hkv, D;
+    Ctrl *ctrl;
+};
+cudaError_t launch_append(const AppendArgs &a, cudaStream_t s);
+
+struct GatherKvArgs {
+    KvView kv;
+    int cache_type, D;
+    const int32_t *page_table;
+    int table_stride;
+    const int32_t *cu_k;
+    int B, Tk;
+    uint16_t *k_out, *v_out;
+    int64_t k_out_stride, v_out_stride;
+    Ctrl *ctrl;
+};
+cudaError_t launch_kv_gather(const GatherKvArgs &a, cudaStream_t s);
+
+struct DecodeAttnArgs {
+    const uint16_t *q;
+    int64_t q_stride;
+    KvView kv;
+    int cache_type, D;
+    const int32_t *page_table;
+    int table_stride;
+    const int32_t *seq_lens;
+    float scale;
+    uint16_t *out;
+    int64_t out_stride;
+    float *lse;
+    int B, Hq;
+    uint8_t *workspace;
+};
+size_t decode_attn_workspace(int B, int Hq, int Hkv, int D);
+cudaError_t launch_attn_decode(const DecodeAttnArgs &a, cudaStream_t s);
+
+struct PrefillArgs {
+    const uint16_t *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t *cu_q, *cu_k;
+    int B, Tq, Tk, Hq, Hkv, D, causal;
+    float scale;
+    uint16_t *out;
+    int64_t out_stride;
+    float *lse;
+    uint8_t *workspace;
+};
+size_t prefill_workspace(int B, int Tq, int Hq, int Hkv, int D);
+cudaError_t launch_attn_prefill(const PrefillArgs &a, cudaStream_t s);
+
+}  // namespace moe
