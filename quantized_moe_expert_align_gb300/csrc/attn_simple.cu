@@ -10,12 +10,6 @@ namespace {
 
 constexpr int kWarps = 4;
 
-__device__ __forceinline__ float e4m3_to_float(uint8_t b) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)b));
-    return __half2float(__ushort_as_half((uint16_t)h));
-}
-
 // E = D / 32 values a lane; load(j, kv, x) brings this lane's values of key /
 // value row j.
 template <int E, class Load>
@@ -45,50 +39,6 @@ __device__ __forceinline__ void attend(const float (&q)[E], int n, const Load &l
 #pragma unroll
     for (int i = 0; i < E; ++i) o[i] *= inv;
     lse = l == 0.f ? -INFINITY : m + logf(l);
-}
-
-template <int D, bool FP8>
-__global__ void decode_simple(DecodeAttnArgs a) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    Ctrl *ctrl = reinterpret_cast<Ctrl *>(a.workspace);
-    const int page = 1 << a.kv.page_shift;
-    if (blockIdx.x == 0) {
-        if (threadIdx.x >= 32) return;
-        int bad = 0x7fffffff;
-        for (int b = lane; b < a.B; b += 32) {
-            const int n = a.seq_lens[b];
-            bool ok = n >= 0 && n <= (int64_t)a.table_stride * page;
-            for (int i = 0; ok && i < (n + page - 1) / page; ++i)
-                ok = (unsigned)a.page_table[(size_t)b * a.table_stride + i] < (unsigned)a.kv.num_pages;
-            if (!ok && b < bad) bad = b;
-        }
-        bad = __reduce_min_sync(0xffffffffu, bad);
-        if (lane == 0) {
-            ctrl->status = bad == 0x7fffffff ? MOE_OK : MOE_ERR_DEVICE_BAD_INDEX;
-            ctrl->detail = bad == 0x7fffffff ? 0 : bad;
-        }
-        return;
-    }
-    const int64_t row = (int64_t)(blockIdx.x - 1) * kWarps + (threadIdx.x >> 5);
-    if (row >= (int64_t)a.B * a.Hq) return;
-    const int b = (int)(row / a.Hq), h = (int)(row % a.Hq), hk = h / (a.Hq / a.kv.Hkv);
-    int n = a.seq_lens[b];
-    n = n < 0 ? 0 : (int)min((int64_t)n, (int64_t)a.table_stride * page);
-    float q[E], o[E], lse;
-    for (int i = 0; i < E; ++i)
-        q[i] = bf16_bits_to_float(a.q[b * a.q_stride + h * D + lane * E + i]) * a.scale;
-    const int32_t *table = a.page_table + (size_t)b * a.table_stride;
-    attend<E>(q, n, [&](int j, int kv, float (&x)[E]) {
-        const int pg = min(max(table[j >> a.kv.page_shift], 0), a.kv.num_pages - 1);
-        const size_t r = ((((size_t)pg * a.kv.Hkv + hk) * 2 + kv) << a.kv.page_shift) + (j & (page - 1));
-        for (int i = 0; i < E; ++i)
-            x[i] = FP8 ? e4m3_to_float(a.kv.data[r * D + lane * E + i]) * a.kv.scales[r]
-                       : bf16_bits_to_float(reinterpret_cast<const uint16_t *>(a.kv.data)[r * D + lane * E + i]);
-    }, o, lse);
-    for (int i = 0; i < E; ++i)
-        a.out[b * a.out_stride + h * D + lane * E + i] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i]));
-    if (a.lse && lane == 0) a.lse[row] = lse;
 }
 
 template <int D>
@@ -135,20 +85,7 @@ __global__ void prefill_simple(PrefillArgs a) {
 
 }  // namespace
 
-size_t decode_attn_workspace(int, int, int, int) { return sizeof(Ctrl); }
 size_t prefill_workspace(int, int, int, int, int) { return sizeof(Ctrl); }
-
-cudaError_t launch_attn_decode(const DecodeAttnArgs &a, cudaStream_t s) {
-    const int grid = (int)(((int64_t)a.B * a.Hq + kWarps - 1) / kWarps) + 1;
-    const bool fp8 = a.cache_type == MOE_KV_FP8;
-    if (a.D == 128)
-        fp8 ? decode_simple<128, true><<<grid, kWarps * 32, 0, s>>>(a)
-            : decode_simple<128, false><<<grid, kWarps * 32, 0, s>>>(a);
-    else
-        fp8 ? decode_simple<64, true><<<grid, kWarps * 32, 0, s>>>(a)
-            : decode_simple<64, false><<<grid, kWarps * 32, 0, s>>>(a);
-    return cudaGetLastError();
-}
 
 cudaError_t launch_attn_prefill(const PrefillArgs &a, cudaStream_t s) {
     const int grid = (int)(((int64_t)a.Tq * a.Hq + kWarps - 1) / kWarps) + 1;
