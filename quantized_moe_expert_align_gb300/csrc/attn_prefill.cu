@@ -1,0 +1,664 @@
+// attn_prefill.cu -- attention over packed prompts on the tensor cores.
+//
+// For a query row with keys 0 .. limit - 1:  o = sum_j p_j v_j / sum_j p_j,
+// p_j = 2^(s_j - r), s_j = scale log2(e) q . k_j and r a reference close to
+// the running maximum.  4 D multiply-adds' worth of work per visible pair
+// and head against 4 D bytes per key and 256 rows: the tensor pipe bounds it.
+//
+// One persistent block per SM takes work items of 256 rows: two tiles of 128
+// rows of one key/value head, a row being one (token, query head of the
+// group) pair, so grouped heads share every key tile and short prompts fill
+// the rows.  Key/value tiles have 128 keys.  Per tile t and key tile j:
+//   S_t = Q_t K_j^T      tcgen05.mma, operands in shared memory (TMA, 128 B swizzle)
+//   P_t = 2^(S_t - r)    one thread per row: registers, rounded to bf16 into
+//                        the tensor memory of S_t
+//   O_t += P_t V_j       tcgen05.mma, P_t from tensor memory
+// One warp issues the products of both tiles alternately, so that one tile's
+// softmax runs under the other tile's products; one warp copies; one clears
+// the rows of a last value tile that belong to the next sequence (a weight
+// of 0 would not stop their NaN).  The reference r is raised, and O_t
+// rescaled, only when a row's maximum exceeds it by 2^8: the sums are in
+// fp32, where p <= 2^8 costs nothing.
+//
+// A planning kernel lists the items by falling number of key tiles; the
+// blocks take them from a counter, longest first.
+#include "attn_common.cuh"
+#include "gemm_tc.h"
+
+namespace moe {
+namespace {
+
+using namespace attn;
+
+constexpr int kTile = 128;       // rows of a tile, keys of a key tile
+constexpr int kThreads = 384;    // two softmax warpgroups, one of single-warp roles
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kFixWarp = 10;
+constexpr int kPlanThreads = 1024;
+constexpr int kBuckets = 1024;
+constexpr float kSlack = 8.f;    // a row's maximum may exceed its reference by this
+
+struct PlanHead {
+    int32_t items, next;   // (sequence, block) pairs; the next item to take
+};
+struct PrefillLayout {
+    size_t ctrl, head, list, total;
+};
+// Items: every sequence has at most one partly filled block.
+__host__ __device__ inline PrefillLayout prefill_layout(int B, int Tq, int tokens) {
+    PrefillLayout l;
+    l.ctrl = 0;
+    l.head = 256;
+    l.list = 512;
+    l.total = l.list + ((size_t)Tq / tokens + B) * sizeof(int2);
+    return l;
+}
+// Query heads of a row tile and tokens of a row tile, for groups of G heads.
+__host__ __device__ inline int tile_heads(int G) { return G < kTile ? G : kTile; }
+__host__ __device__ inline int tile_tokens(int G) { return kTile / tile_heads(G); }
+
+template <int D>
+struct Cfg {
+    static constexpr int kTileB = kTile * D * 2;           // a Q, K or V tile
+    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr size_t kSmem = (size_t)(2 + kStages) * kTileB + 1024 + 1024;
+    static_assert(kSmem > 114 * 1024, "one block per SM: all of tensor memory is its own");
+};
+
+// A work item as the roles see it.
+struct Item {
+    int q0, nq, k0, nk;    // rows of the sequence
+    int tok0;              // the item's first token within the sequence
+    int hk, h0, heads;     // key/value head; first query head and their number
+    int tiles[2];          // key tiles of each row tile
+    int done;
+};
+
+struct Shared {
+    uint64_t q_full[2], q_empty[2], kv_full[8], kv_empty[8], s_full[2], p_ready[2], o_done[2];
+    uint64_t item_full[2], item_empty[2], tail[8], finished;
+    uint32_t tmem;
+    int abort;
+    Item item[2];
+};
+static_assert(sizeof(Shared) <= 1024, "shared block");
+
+__device__ __forceinline__ bool seq_ok(const PrefillArgs &a, int b) {
+    const int q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1);
+    const int k0 = __ldg(a.cu_k + b), k1 = __ldg(a.cu_k + b + 1);
+    return q0 >= 0 && q1 >= q0 && q1 <= a.Tq && k0 >= 0 && k1 >= k0 && k1 <= a.Tk;
+}
+// Keys that token `tok` of a sequence sees.
+__device__ __forceinline__ int keys_seen(int causal, int tok, int nq, int nk) {
+    return causal ? max(0, min(nk, tok + nk - nq + 1)) : nk;
+}
+
+// ------------------------------------------------------------------- planning
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PrefillArgs a, const int tokens) {
+    __shared__ int count[kBuckets], warp_sum[kPlanThreads / 32], first_bad;
+    const PrefillLayout L = prefill_layout(a.B, a.Tq, tokens);
+    const int tid = threadIdx.x, lane = tid & 31;
+    pdl_trigger();
+    count[tid] = 0;
+    if (tid == 0) first_bad = 0x7fffffff;
+    __syncthreads();
+    const int64_t room = (int64_t)a.Tq / tokens + a.B;
+    // a block's bucket: fewest key tiles last
+    auto bucket = [&](int blk, int nq, int nk) {
+        const int last = min(nq, (blk + 1) * tokens) - 1;
+        const int tiles = (keys_seen(a.causal, last, nq, nk) + kTile - 1) / kTile;
+        return kBuckets - 1 - min(kBuckets - 1, tiles);
+    };
+    // one warp per sequence, one lane per block
+    for (int pass = 0; pass < 2; ++pass) {
+        for (int b = tid >> 5; b < a.B; b += kPlanThreads / 32) {
+            if (!seq_ok(a, b)) {
+                if (lane == 0) atomicMin(&first_bad, b);
+                continue;
+            }
+            const int nq = __ldg(a.cu_q + b + 1) - __ldg(a.cu_q + b);
+            const int nk = __ldg(a.cu_k + b + 1) - __ldg(a.cu_k + b);
+            for (int blk = lane; blk < (nq + tokens - 1) / tokens; blk += 32) {
+                const int at = atomicAdd(&count[bucket(blk, nq, nk)], 1);
+                // (overlapping sequences may ask for more items than rows)
+                if (pass && at < room) reinterpret_cast<int2 *>(a.workspace + L.list)[at] = make_int2(b, blk);
+            }
+        }
+        __syncthreads();
+        if (pass) break;
+        // counts -> first places
+        const int mine = count[tid];
+        int scan = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, scan, o);
+            if (lane >= o) scan += v;
+        }
+        if (lane == 31) warp_sum[tid >> 5] = scan;
+        __syncthreads();
+        int before = 0;
+        for (int w = 0; w < tid >> 5; ++w) before += warp_sum[w];
+        count[tid] = before + scan - mine;
+        if (tid == kPlanThreads - 1) {
+            PlanHead *h = reinterpret_cast<PlanHead *>(a.workspace + L.head);
+            h->items = (int)min((int64_t)(before + scan), room);
+            h->next = 0;
+            Ctrl *ctrl = reinterpret_cast<Ctrl *>(a.workspace);
+            ctrl->status = first_bad == 0x7fffffff ? MOE_OK : MOE_ERR_DEVICE_BAD_INDEX;
+            ctrl->detail = first_bad == 0x7fffffff ? 0 : first_bad;
+        }
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------------ the products
+// kind::f16 with bf16 operands and fp32 sums; trans_b: B is stored along N.
+__host__ __device__ constexpr uint32_t idesc_bf16(uint32_t n, bool trans_b) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((trans_b ? 1u : 0u) << 16) | ((n >> 3) << 17) |
+           ((128u >> 4) << 24);
+}
+// Values [key][d] as the operand whose contraction runs over the keys:
+// 128-byte rows of 64 columns, 8-row groups 1024 bytes apart (stride
+// offset), the second 64 columns `half` bytes on (leading offset).
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t addr, uint32_t half) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(half >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+__device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+        "%30, %31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+          "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+          "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
+          "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
+          "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+        "%29, %30, %31, %32};" ::"r"(taddr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+        "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]),
+        "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]),
+        "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]),
+        "f"(v[29]), "f"(v[30]), "f"(v[31])
+        : "memory");
+}
+// x * a + b and x + y on pairs of fp32
+__device__ __forceinline__ float2 fma2(float2 x, float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, a, b, r;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 a, {%4, %5};\n\t"
+        "mov.b64 b, {%6, %7};\n\tfma.rn.f32x2 r, x, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, r;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 r, x, y;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtensorMap map_q,
+               const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+    using C = Cfg<D>;
+    constexpr int S = C::kStages;
+    constexpr int kHalves = D / 64;
+    constexpr uint32_t kHalfB = kTile * 128;
+    extern __shared__ uint8_t raw[];
+    const uint32_t raw_u = smem_u32(raw);
+    uint8_t *base = raw + ((1024 - (raw_u & 1023)) & 1023);
+    const uint32_t q_smem = smem_u32(base), kv_smem = q_smem + 2 * C::kTileB;
+    Shared *sm = reinterpret_cast<Shared *>(base + (size_t)(2 + S) * C::kTileB);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = a.Hq / a.Hkv, Gt = tile_heads(G), tpt = tile_tokens(G);
+    const PrefillLayout L = prefill_layout(a.B, a.Tq, 2 * tpt);
+    Ctrl *ctrl = reinterpret_cast<Ctrl *>(a.workspace);
+
+    if (warp == kMmaWarp) tmem_alloc(&sm->tmem, 512);
+    if (threadIdx.x == 0) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&sm->q_full[t], 1);
+            mbar_init(&sm->q_empty[t], 1);
+            mbar_init(&sm->s_full[t], 1);
+            mbar_init(&sm->p_ready[t], 4);
+            mbar_init(&sm->o_done[t], 1);
+            mbar_init(&sm->item_full[t], 1);
+            mbar_init(&sm->item_empty[t], 8 + 2);  // softmax warps, product and clearing warps
+        }
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&sm->kv_full[i], 1);
+            mbar_init(&sm->kv_empty[i], 1);
+            mbar_init(&sm->tail[i], 1);
+        }
+        mbar_init(&sm->finished, 1);
+        fence_barrier_init();
+        sm->abort = 0;
+        prefetch_tensormap(&map_q);
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_v);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm->tmem;
+    const uint32_t s_col = tmem, o_col = tmem + 2 * kTile;  // S_t at 128 t, O_t at 256 + 128 t
+
+    // The next item; false when there is none or a wait gave up.  Every role
+    // but the copying one walks the items with this.
+    auto take = [&](uint32_t n, Item &it) {
+        if (!warp_wait_flag(&sm->item_full[n & 1], (n >> 1) & 1, &sm->abort, 1)) return false;
+        it = sm->item[n & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->item_empty[n & 1]);
+        return it.done == 0;
+    };
+    // A value tile whose rows past the sequence's end belong to others.
+    auto ragged = [&](const Item &it, int j) {
+        return (j + 1) * kTile > it.nk && it.k0 + it.nk < a.Tk;
+    };
+
+    if (warp >= kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == kLoadWarp) {
+            // ---------------- copies, and the items for everyone
+            pdl_wait();
+            const PlanHead *head = reinterpret_cast<const PlanHead *>(a.workspace + L.head);
+            const int HV = a.Hkv * HT;
+            const int64_t total = (int64_t)*(volatile const int32_t *)&head->items * HV;
+            int64_t idx = blockIdx.x;
+            uint32_t n = 0, kv = 0;
+            for (;; ++n) {
+                Item it = {};
+                it.done = idx >= total;
+                if (!it.done) {
+                    const int2 e = reinterpret_cast<const int2 *>(a.workspace + L.list)[idx / HV];
+                    const int hv = (int)(idx % HV);
+                    it.q0 = __ldg(a.cu_q + e.x);
+                    it.nq = __ldg(a.cu_q + e.x + 1) - it.q0;
+                    it.k0 = __ldg(a.cu_k + e.x);
+                    it.nk = __ldg(a.cu_k + e.x + 1) - it.k0;
+                    it.tok0 = e.y * 2 * tpt;
+                    it.hk = hv / HT;
+                    const int g0 = (hv % HT) * Gt;
+                    it.h0 = it.hk * G + g0;
+                    it.heads = min(Gt, G - g0);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const int t0 = it.tok0 + t * tpt, last = min(it.nq, t0 + tpt) - 1;
+                        it.tiles[t] = last < t0 ? 0 : (keys_seen(a.causal, last, it.nq, it.nk) + kTile - 1) / kTile;
+                    }
+                }
+                if (!warp_wait_flag(&sm->item_empty[n & 1], ((n >> 1) & 1) ^ 1, &sm->abort, 2)) break;
+                if (lane == 0) {
+                    sm->item[n & 1] = it;
+                    mbar_arrive(&sm->item_full[n & 1]);
+                }
+                __syncwarp();
+                if (it.done) break;
+                // (the next item's number is on its way during the copies)
+                int64_t nxt = 0;
+                if (lane == 0)
+                    nxt = (int64_t)gridDim.x +
+                          atomicAdd(&reinterpret_cast<PlanHead *>(a.workspace + L.head)->next, 1);
+                const int tiles = max(it.tiles[0], it.tiles[1]);
+                bool ok = true;
+                auto copy_kv = [&](const CUtensorMap *map, int j, bool tail) {
+                    const uint32_t s = kv % S, ph = (kv / S) & 1;
+                    ok = ok && warp_wait_flag(&sm->kv_empty[s], ph ^ 1, &sm->abort, 3);
+                    if (!ok) return;
+                    if (lane == 0) {
+                        uint64_t *bar = tail ? &sm->tail[s] : &sm->kv_full[s];
+                        mbar_arrive_expect_tx(bar, C::kTileB);
+                        tma_load_4d(base + (2 + s) * C::kTileB, map, 0, it.k0 + j * kTile, it.hk, 0, bar);
+                    }
+                    __syncwarp();
+                    ++kv;
+                };
+                for (int j = 0; j < tiles && ok; ++j) {
+                    copy_kv(&map_k, j, false);
+                    if (j == 0) {
+                        for (int t = 0; t < 2 && ok; ++t) {
+                            ok = warp_wait_flag(&sm->q_empty[t], (n & 1) ^ 1, &sm->abort, 4);
+                            if (ok && lane == 0) {
+                                // (a tile without rows is loaded all the same: its phases go on)
+                                mbar_arrive_expect_tx(&sm->q_full[t], (uint32_t)(Gt * tpt) * D * 2);
+                                for (int h = 0; h < kHalves; ++h)
+                                    tma_load_4d(base + t * C::kTileB + h * kHalfB, &map_q, 0, it.h0,
+                                                it.q0 + it.tok0 + t * tpt, h, &sm->q_full[t]);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    if (ok) copy_kv(&map_v, j, ragged(it, j));
+                }
+                if (!ok) break;
+                if (tiles == 0) {
+                    // no copies: the other roles' phases of q go on without them
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        ok = warp_wait_flag(&sm->q_empty[t], (n & 1) ^ 1, &sm->abort, 4);
+                        if (ok && lane == 0) mbar_arrive(&sm->q_full[t]);
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                }
+                idx = __shfl_sync(0xffffffffu, nxt, 0);
+            }
+            // (after a give-up) nothing of this warp's may still be in flight
+            if (*(volatile int *)&sm->abort) {
+                const long long t0 = clock64();
+                while (clock64() - t0 < (1ll << 24)) __nanosleep(1000);
+            }
+        } else if (warp == kMmaWarp) {
+            // ---------------- products
+            const uint64_t q_desc = sdesc_k_sw128(q_smem), k_desc = sdesc_k_sw128(kv_smem);
+            const uint64_t v_desc = sdesc_mn_sw128(kv_smem, kHalfB);
+            constexpr uint32_t kIdS = idesc_bf16(kTile, false), kIdO = idesc_bf16(D, true);
+            uint32_t kv = 0;             // key and value tiles waited for
+            uint32_t p_ph[2] = {0, 0};
+            Item it;
+            bool ok = true;
+            auto qk = [&](int t, uint32_t s) {  // S_t = Q_t K^T
+                if (elect_one()) {
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        const uint32_t off = ((j >> 2) * kHalfB + (j & 3) * 32) >> 4;
+                        mma_bf16_ss(s_col + t * kTile, q_desc + ((t * C::kTileB) >> 4) + off,
+                                    k_desc + ((s * C::kTileB) >> 4) + off, kIdS, j > 0);
+                    }
+                    tc_commit(&sm->s_full[t]);
+                }
+                __syncwarp();
+            };
+            auto commit = [&](uint64_t *bar) {
+                if (elect_one()) tc_commit(bar);
+                __syncwarp();
+            };
+            auto wait_kv = [&]() {
+                ok = ok && warp_wait_flag(&sm->kv_full[kv % S], (kv / S) & 1, &sm->abort, 5);
+                tc_fence_after();
+                return kv++ % S;
+            };
+            for (uint32_t n = 0; ok && take(n, it); ++n) {
+                const int tiles = max(it.tiles[0], it.tiles[1]);
+                uint32_t k_stage = 0;
+                if (tiles > 0) k_stage = wait_kv();
+                for (int t = 0; t < 2 && ok; ++t) {
+                    ok = warp_wait_flag(&sm->q_full[t], n & 1, &sm->abort, 6);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (it.tiles[t] > 0) qk(t, k_stage);
+                    if (it.tiles[t] <= 1) commit(&sm->q_empty[t]);
+                }
+                if (!ok) break;
+                if (tiles > 0) commit(&sm->kv_empty[k_stage]);
+                for (int j = 0; j < tiles && ok; ++j) {
+                    const uint32_t v_stage = wait_kv();
+                    const bool more = j + 1 < tiles;
+                    uint32_t next_k = 0;
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        if (j < it.tiles[t]) {
+                            ok = warp_wait_flag(&sm->p_ready[t], p_ph[t], &sm->abort, 7);
+                            if (!ok) break;
+                            p_ph[t] ^= 1;
+                            tc_fence_after();
+                            if (elect_one()) {
+#pragma unroll
+                                for (int i = 0; i < kTile / 16; ++i)
+                                    mma_f16_ts(o_col + t * kTile, s_col + t * kTile + i * 8,
+                                               v_desc + ((v_stage * C::kTileB + i * 2048) >> 4), kIdO,
+                                               j > 0 || i > 0);
+                                tc_commit(&sm->o_done[t]);
+                            }
+                            __syncwarp();
+                        }
+                        if (t == 1) commit(&sm->kv_empty[v_stage]);
+                        if (more && t == 0) next_k = wait_kv();
+                        if (!ok) break;
+                        if (j + 1 < it.tiles[t]) {
+                            qk(t, next_k);
+                            if (j + 2 == it.tiles[t]) commit(&sm->q_empty[t]);
+                        }
+                    }
+                    if (ok && more) commit(&sm->kv_empty[next_k]);
+                }
+            }
+            // everything issued has finished before the block ends
+            commit(&sm->finished);
+            wait_own(&sm->finished, 0);
+        } else if (warp == kFixWarp) {
+            // ---------------- last value tiles: zeros past the sequence's end
+            Item it;
+            uint32_t kv = 0, ph = 0;  // ph: one phase bit per stage
+            for (uint32_t n = 0; take(n, it); ++n) {
+                const int tiles = max(it.tiles[0], it.tiles[1]);
+                kv += 2 * tiles;
+                if (tiles == 0 || !ragged(it, tiles - 1)) continue;
+                const uint32_t s = (kv - 1) % S;
+                if (!warp_wait_flag(&sm->tail[s], (ph >> s) & 1, &sm->abort, 8)) break;
+                ph ^= 1u << s;
+                uint8_t *v = base + (2 + s) * C::kTileB;
+                const int from = it.nk - (tiles - 1) * kTile;
+                for (int h = 0; h < kHalves; ++h)
+                    for (int i = from * 8 + lane; i < kTile * 8; i += 32)
+                        *reinterpret_cast<uint4 *>(v + h * kHalfB + i * 16) = make_uint4(0, 0, 0, 0);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm->kv_full[s]);
+            }
+        }
+    } else {
+        // ---------------- softmax: warpgroup t has row tile t, a thread a row
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const int t = warp >> 2;
+        const int r = threadIdx.x & 127;
+        const uint32_t lane_base = (uint32_t)(warp & 3) * 32 << 16;
+        const uint32_t s_t = s_col + t * kTile + lane_base, o_t = o_col + t * kTile + lane_base;
+        const int tok_r = r / Gt, g = r % Gt;
+        const float sl = a.scale * kLog2e;
+        uint32_t s_ph = 0, o_ph = 0;  // o_ph: parity of the next product to finish
+        Item it;
+        bool ok = true;
+        for (uint32_t n = 0; ok && take(n, it); ++n) {
+            const int tok = it.tok0 + t * tpt + tok_r;
+            const bool live = tok_r < tpt && tok < it.nq && g < it.heads;
+            // (rows that do not exist ask for no masking)
+            const int limit = live ? keys_seen(a.causal, tok, it.nq, it.nk) : 0x3fffffff;
+            const int least = __reduce_min_sync(0xffffffffu, limit);
+            float ref = -INFINITY;  // the row's reference, in log2 units
+            float l = 0.f;
+            const int tiles = it.tiles[t];
+            for (int j = 0; j < tiles; ++j) {
+                ok = warp_wait_flag(&sm->s_full[t], s_ph, &sm->abort, 9);
+                if (!ok) break;
+                s_ph ^= 1;
+                tc_fence_after();
+                float x[kTile];
+#pragma unroll
+                for (int c = 0; c < kTile; c += 32) tmem_ld32(s_t + c, x + c);
+                tc_wait_ld();
+                if ((j + 1) * kTile > least) {
+                    const int lim = limit - j * kTile;
+#pragma unroll
+                    for (int c = 0; c < kTile; ++c) x[c] = c < lim ? x[c] : -INFINITY;
+                }
+                float m4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                for (int c = 4; c < kTile; c += 4)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], x[c + e]);
+                const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl;
+                const bool raise = top > ref + kSlack;
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float to = raise ? top : ref;
+                    const float f = raise ? ex2(ref - to) : 1.f;
+                    l *= f;
+                    ref = to;
+                    if (j > 0) {
+                        // the last product into O_t has to be over
+                        ok = warp_wait_flag(&sm->o_done[t], o_ph ^ 1, &sm->abort, 10);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            tmem_ld32(o_t + c, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] *= f;
+                            tmem_st32(o_t + c, o);
+                        }
+                    }
+                }
+                o_ph ^= 1;
+                const float z = ref == -INFINITY ? 0.f : ref;
+                const float2 sl2 = make_float2(sl, sl), nz2 = make_float2(-z, -z);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int c = 0; c < kTile; c += 32) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float2 y = fma2(make_float2(x[c + 2 * e], x[c + 2 * e + 1]), sl2, nz2);
+                        y.x = ex2(y.x);
+                        y.y = ex2(y.y);
+                        sum[e & 1] = add2(sum[e & 1], y);
+                        p[e] = pack_bf16(y.x, y.y);
+                    }
+                    tmem_st16(s_t + c / 2, p);
+                }
+                const float2 both = add2(sum[0], sum[1]);
+                l += both.x + both.y;
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm->p_ready[t]);
+            }
+            if (!ok) break;
+            // ---- the rows' outputs
+            const float inv = 1.f / l;
+            const bool none = l == 0.f;  // no key: zeros
+            uint16_t *out = a.out + (it.q0 + tok) * a.out_stride + (it.h0 + g) * D;
+            if (tiles > 0) {
+                ok = warp_wait_flag(&sm->o_done[t], o_ph ^ 1, &sm->abort, 11);
+                if (!ok) break;
+                tc_fence_after();
+            }
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                if (tiles > 0) {
+                    tmem_ld32(o_t + c, o);
+                    tc_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
+                if (live) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4 *>(out + c + e) =
+                            make_uint4(pack_bf16(o[e], o[e + 1]), pack_bf16(o[e + 2], o[e + 3]),
+                                       pack_bf16(o[e + 4], o[e + 5]), pack_bf16(o[e + 6], o[e + 7]));
+                }
+            }
+            if (a.lse && live)
+                a.lse[(size_t)(it.q0 + tok) * a.Hq + it.h0 + g] =
+                    none ? -INFINITY : (ref + __log2f(l)) * kLn2;
+            // (O_t is read: the next item's first p_ready comes after this)
+            tc_fence_before();
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && sm->abort) set_status(ctrl, MOE_ERR_DEVICE_TIMEOUT, sm->abort);
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_relinquish();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D>
+cudaError_t run(const PrefillArgs &a, int sms, cudaStream_t s) {
+    using C = Cfg<D>;
+    const int G = a.Hq / a.Hkv, Gt = tile_heads(G), tpt = tile_tokens(G), HT = (G + Gt - 1) / Gt;
+    CUtensorMap mq, mk, mv;
+    {
+        const uint64_t dims[4] = {64, (uint64_t)a.Hq, (uint64_t)a.Tq, D / 64};
+        const uint64_t strides[3] = {D * 2, (uint64_t)a.q_stride * 2, 128};
+        const uint32_t box[4] = {64, (uint32_t)Gt, (uint32_t)tpt, 1};
+        if (!encode_tensor_map(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, a.q, dims, strides, box,
+                               CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+    }
+    for (int i = 0; i < 2; ++i) {
+        // (no keys at all: nothing is copied, any valid map will do)
+        const uint16_t *p = a.Tk > 0 ? (i ? a.v : a.k) : a.q;
+        const uint64_t dims[4] = {64, (uint64_t)(a.Tk > 0 ? a.Tk : 1), (uint64_t)a.Hkv, D / 64};
+        const uint64_t strides[3] = {(uint64_t)(i ? a.v_stride : a.k_stride) * 2, D * 2, 128};
+        const uint32_t box[4] = {64, kTile, 1, D / 64};
+        if (!encode_tensor_map(i ? &mv : &mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p, dims, strides,
+                               box, CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+    }
+    plan_kernel<<<1, kPlanThreads, 0, s>>>(a, 2 * tpt);
+    cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    auto fn = prefill_kernel<D>;
+    err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    if (err != cudaSuccess) return err;
+    const int64_t most = ((int64_t)a.Tq / (2 * tpt) + a.B) * a.Hkv * HT;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, a, HT, mq, mk, mv);
+}
+
+}  // namespace
+
+size_t prefill_workspace(int B, int Tq, int Hq, int Hkv, int) {
+    return align_up(prefill_layout(B, Tq, 2 * tile_tokens(Hq / Hkv)).total, 256);
+}
+
+cudaError_t launch_attn_prefill(const PrefillArgs &a, cudaStream_t s) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const int sms = tc_grid(dev);
+    if (sms < 1) return cudaErrorInvalidDevice;
+    return a.D == 128 ? run<128>(a, sms, s) : run<64>(a, sms, s);
+}
+
+}  // namespace moe
