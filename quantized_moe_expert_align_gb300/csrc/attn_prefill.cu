@@ -22,6 +22,8 @@
 //
 // A planning kernel lists the items by falling number of key tiles; the
 // blocks take them from a counter, longest first.
+#include <type_traits>
+
 #include "attn_common.cuh"
 #include "gemm_tc.h"
 
@@ -31,14 +33,24 @@ namespace {
 using namespace attn;
 
 constexpr int kTile = 128;       // rows of a tile, keys of a key tile
+constexpr int kHalf = kTile / 2;
 constexpr int kThreads = 384;    // two softmax warpgroups, one of single-warp roles
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kFixWarp = 10;
+constexpr int kMmaWarp = 8, kLoadWarp = 10, kFixWarp = 11;  // (product warps: 8 and 9)
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 1024;
+constexpr int kApart = 4;        // items of at least this many key tiles run their row tiles offset
 constexpr float kSlack = 8.f;    // a row's maximum may exceed its reference by this
 
 struct PlanHead {
     int32_t items, next;   // (sequence, block) pairs; the next item to take
+};
+// One sequence's block of 256 rows for every head: what does not depend on
+// the head.
+struct __align__(16) Block {
+    int32_t q0, nq, k0, nk;   // rows of the sequence
+    int32_t tok0;             // the block's first token within the sequence
+    int32_t tiles0, tiles1;   // key tiles of each row tile
+    int32_t pad;
 };
 struct PrefillLayout {
     size_t ctrl, head, list, total;
@@ -49,7 +61,7 @@ __host__ __device__ inline PrefillLayout prefill_layout(int B, int Tq, int token
     l.ctrl = 0;
     l.head = 256;
     l.list = 512;
-    l.total = l.list + ((size_t)Tq / tokens + B) * sizeof(int2);
+    l.total = l.list + ((size_t)Tq / tokens + B) * sizeof(Block);
     return l;
 }
 // Query heads of a row tile and tokens of a row tile, for groups of G heads.
@@ -60,22 +72,25 @@ template <int D>
 struct Cfg {
     static constexpr int kTileB = kTile * D * 2;           // a Q, K or V tile
     static constexpr int kStages = D == 128 ? 5 : 8;
+    // Tensor memory (512 columns): S_t 2 x 128, O_t 2 x D.  Heads of 64 leave
+    // 128 columns for the weights P_t, so that the next scores can be computed
+    // as soon as S_t is in registers; heads of 128 put P_t over S_t.
+    static constexpr bool kOwnP = D == 64;
     static constexpr size_t kSmem = (size_t)(2 + kStages) * kTileB + 1024 + 1024;
     static_assert(kSmem > 114 * 1024, "one block per SM: all of tensor memory is its own");
 };
 
 // A work item as the roles see it.
 struct Item {
-    int q0, nq, k0, nk;    // rows of the sequence
-    int tok0;              // the item's first token within the sequence
+    Block b;
     int hk, h0, heads;     // key/value head; first query head and their number
-    int tiles[2];          // key tiles of each row tile
     int done;
 };
 
 struct Shared {
-    uint64_t q_full[2], q_empty[2], kv_full[8], kv_empty[8], s_full[2], p_ready[2], o_done[2];
-    uint64_t item_full[2], item_empty[2], tail[8], finished;
+    uint64_t q_full[2], q_empty[2], kv_full[8], kv_empty[8], s_full[2], s_free[2];
+    uint64_t p_ready[2][2], o_done[2];  // p_ready: [row tile][half of the key tile]
+    uint64_t item_full[2], item_empty[2], tail[8], offset, finished;
     uint32_t tmem;
     int abort;
     Item item[2];
@@ -93,7 +108,8 @@ __device__ __forceinline__ int keys_seen(int causal, int tok, int nq, int nk) {
 }
 
 // ------------------------------------------------------------------- planning
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PrefillArgs a, const int tokens) {
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PrefillArgs a, const int tpt) {
+    const int tokens = 2 * tpt;  // of a block
     __shared__ int count[kBuckets], warp_sum[kPlanThreads / 32], first_bad;
     const PrefillLayout L = prefill_layout(a.B, a.Tq, tokens);
     const int tid = threadIdx.x, lane = tid & 31;
@@ -115,12 +131,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PrefillArgs a,
                 if (lane == 0) atomicMin(&first_bad, b);
                 continue;
             }
-            const int nq = __ldg(a.cu_q + b + 1) - __ldg(a.cu_q + b);
-            const int nk = __ldg(a.cu_k + b + 1) - __ldg(a.cu_k + b);
+            const int q0 = __ldg(a.cu_q + b), nq = __ldg(a.cu_q + b + 1) - q0;
+            const int k0 = __ldg(a.cu_k + b), nk = __ldg(a.cu_k + b + 1) - k0;
             for (int blk = lane; blk < (nq + tokens - 1) / tokens; blk += 32) {
                 const int at = atomicAdd(&count[bucket(blk, nq, nk)], 1);
                 // (overlapping sequences may ask for more items than rows)
-                if (pass && at < room) reinterpret_cast<int2 *>(a.workspace + L.list)[at] = make_int2(b, blk);
+                if (!pass || at >= room) continue;
+                auto tiles_of = [&](int t0) {  // of the row tile from token t0 on
+                    const int last = min(nq, t0 + tpt) - 1;
+                    return last < t0 ? 0 : (keys_seen(a.causal, last, nq, nk) + kTile - 1) / kTile;
+                };
+                const int t0 = blk * tokens;
+                const Block e = {q0, nq, k0, nk, t0, tiles_of(t0), tiles_of(t0 + tpt), 0};
+                reinterpret_cast<Block *>(a.workspace + L.list)[at] = e;
             }
         }
         __syncthreads();
@@ -190,17 +213,10 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
         : "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float *v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
-        "%29, %30, %31, %32};" ::"r"(taddr),
-        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
-        "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]),
-        "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]),
-        "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]),
-        "f"(v[29]), "f"(v[30]), "f"(v[31])
-        : "memory");
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 // x * a + b and x + y on pairs of fp32
 __device__ __forceinline__ float2 fma2(float2 x, float2 a, float2 b) {
@@ -233,7 +249,9 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
     uint8_t *base = raw + ((1024 - (raw_u & 1023)) & 1023);
     const uint32_t q_smem = smem_u32(base), kv_smem = q_smem + 2 * C::kTileB;
     Shared *sm = reinterpret_cast<Shared *>(base + (size_t)(2 + S) * C::kTileB);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (a broadcast tells the compiler that these are the same in all lanes:
+    // the copy and product instructions want their operands in uniform registers)
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int G = a.Hq / a.Hkv, Gt = tile_heads(G), tpt = tile_tokens(G);
     const PrefillLayout L = prefill_layout(a.B, a.Tq, 2 * tpt);
     Ctrl *ctrl = reinterpret_cast<Ctrl *>(a.workspace);
@@ -244,17 +262,19 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
             mbar_init(&sm->q_full[t], 1);
             mbar_init(&sm->q_empty[t], 1);
             mbar_init(&sm->s_full[t], 1);
-            mbar_init(&sm->p_ready[t], 4);
+            mbar_init(&sm->s_free[t], 4);
+            for (int h = 0; h < 2; ++h) mbar_init(&sm->p_ready[t][h], 4);
             mbar_init(&sm->o_done[t], 1);
             mbar_init(&sm->item_full[t], 1);
-            mbar_init(&sm->item_empty[t], 8 + 2);  // softmax warps, product and clearing warps
+            mbar_init(&sm->item_empty[t], 8 + 3);  // softmax, product and clearing warps
         }
         for (int i = 0; i < S; ++i) {
             mbar_init(&sm->kv_full[i], 1);
-            mbar_init(&sm->kv_empty[i], 1);
+            mbar_init(&sm->kv_empty[i], 2);
             mbar_init(&sm->tail[i], 1);
         }
-        mbar_init(&sm->finished, 1);
+        mbar_init(&sm->offset, 1);
+        mbar_init(&sm->finished, 2);
         fence_barrier_init();
         sm->abort = 0;
         prefetch_tensormap(&map_q);
@@ -264,8 +284,12 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sm->tmem;
-    const uint32_t s_col = tmem, o_col = tmem + 2 * kTile;  // S_t at 128 t, O_t at 256 + 128 t
+    // S_t, O_t and P_t in tensor memory, all of which is this block's: its
+    // address is 0 (anything else is reported like a wait that gave up)
+    if (sm->tmem != 0) sm->abort = 20;
+    constexpr uint32_t s_col = 0, o_col = 2 * kTile;
+    constexpr uint32_t p_col = C::kOwnP ? o_col + 2 * D : s_col;
+    constexpr uint32_t kPStep = C::kOwnP ? kTile / 2 : kTile;
 
     // The next item; false when there is none or a wait gave up.  Every role
     // but the copying one walks the items with this.
@@ -278,40 +302,34 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
     };
     // A value tile whose rows past the sequence's end belong to others.
     auto ragged = [&](const Item &it, int j) {
-        return (j + 1) * kTile > it.nk && it.k0 + it.nk < a.Tk;
+        return (j + 1) * kTile > it.b.nk && it.b.k0 + it.b.nk < a.Tk;
     };
 
     if (warp >= kMmaWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == kLoadWarp) {
             // ---------------- copies, and the items for everyone
             pdl_wait();
             const PlanHead *head = reinterpret_cast<const PlanHead *>(a.workspace + L.head);
             const int HV = a.Hkv * HT;
             const int64_t total = (int64_t)*(volatile const int32_t *)&head->items * HV;
+            const Block *list = reinterpret_cast<const Block *>(a.workspace + L.list);
+            int *counter = &reinterpret_cast<PlanHead *>(a.workspace + L.head)->next;
+            // Item n + 1's entry and item n + 2's number are fetched while
+            // item n's copies are issued.
             int64_t idx = blockIdx.x;
+            int64_t ahead = 0;  // (lane 0)
+            if (lane == 0) ahead = (int64_t)gridDim.x + atomicAdd(counter, 1);
+            Block blk = idx < total ? list[idx / HV] : Block{};
             uint32_t n = 0, kv = 0;
             for (;; ++n) {
-                Item it = {};
+                Item it;
+                it.b = blk;
                 it.done = idx >= total;
-                if (!it.done) {
-                    const int2 e = reinterpret_cast<const int2 *>(a.workspace + L.list)[idx / HV];
-                    const int hv = (int)(idx % HV);
-                    it.q0 = __ldg(a.cu_q + e.x);
-                    it.nq = __ldg(a.cu_q + e.x + 1) - it.q0;
-                    it.k0 = __ldg(a.cu_k + e.x);
-                    it.nk = __ldg(a.cu_k + e.x + 1) - it.k0;
-                    it.tok0 = e.y * 2 * tpt;
-                    it.hk = hv / HT;
-                    const int g0 = (hv % HT) * Gt;
-                    it.h0 = it.hk * G + g0;
-                    it.heads = min(Gt, G - g0);
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const int t0 = it.tok0 + t * tpt, last = min(it.nq, t0 + tpt) - 1;
-                        it.tiles[t] = last < t0 ? 0 : (keys_seen(a.causal, last, it.nq, it.nk) + kTile - 1) / kTile;
-                    }
-                }
+                const int hv = (int)(idx % HV), g0 = (hv % HT) * Gt;
+                it.hk = hv / HT;
+                it.h0 = it.hk * G + g0;
+                it.heads = min(Gt, G - g0);
                 if (!warp_wait_flag(&sm->item_empty[n & 1], ((n >> 1) & 1) ^ 1, &sm->abort, 2)) break;
                 if (lane == 0) {
                     sm->item[n & 1] = it;
@@ -319,12 +337,10 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
                 }
                 __syncwarp();
                 if (it.done) break;
-                // (the next item's number is on its way during the copies)
-                int64_t nxt = 0;
-                if (lane == 0)
-                    nxt = (int64_t)gridDim.x +
-                          atomicAdd(&reinterpret_cast<PlanHead *>(a.workspace + L.head)->next, 1);
-                const int tiles = max(it.tiles[0], it.tiles[1]);
+                idx = __shfl_sync(0xffffffffu, ahead, 0);
+                if (idx < total) blk = list[idx / HV];
+                if (lane == 0) ahead = (int64_t)gridDim.x + atomicAdd(counter, 1);
+                const int tiles = max(it.b.tiles0, it.b.tiles1);
                 bool ok = true;
                 auto copy_kv = [&](const CUtensorMap *map, int j, bool tail) {
                     const uint32_t s = kv % S, ph = (kv / S) & 1;
@@ -333,13 +349,13 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
                     if (lane == 0) {
                         uint64_t *bar = tail ? &sm->tail[s] : &sm->kv_full[s];
                         mbar_arrive_expect_tx(bar, C::kTileB);
-                        tma_load_4d(base + (2 + s) * C::kTileB, map, 0, it.k0 + j * kTile, it.hk, 0, bar);
+                        tma_load_4d(base + (2 + s) * C::kTileB, map, 0, it.b.k0 + j * kTile, it.hk, 0, bar);
                     }
                     __syncwarp();
                     ++kv;
                 };
                 for (int j = 0; j < tiles && ok; ++j) {
-                    copy_kv(&map_k, j, false);
+                    if (!C::kOwnP || j == 0) copy_kv(&map_k, j, false);
                     if (j == 0) {
                         for (int t = 0; t < 2 && ok; ++t) {
                             ok = warp_wait_flag(&sm->q_empty[t], (n & 1) ^ 1, &sm->abort, 4);
@@ -348,11 +364,13 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
                                 mbar_arrive_expect_tx(&sm->q_full[t], (uint32_t)(Gt * tpt) * D * 2);
                                 for (int h = 0; h < kHalves; ++h)
                                     tma_load_4d(base + t * C::kTileB + h * kHalfB, &map_q, 0, it.h0,
-                                                it.q0 + it.tok0 + t * tpt, h, &sm->q_full[t]);
+                                                it.b.q0 + it.b.tok0 + t * tpt, h, &sm->q_full[t]);
                             }
                             __syncwarp();
                         }
                     }
+                    // (in the order in which the products want them)
+                    if (C::kOwnP && ok && j + 1 < tiles) copy_kv(&map_k, j + 1, false);
                     if (ok) copy_kv(&map_v, j, ragged(it, j));
                 }
                 if (!ok) break;
@@ -365,103 +383,149 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
                     }
                     if (!ok) break;
                 }
-                idx = __shfl_sync(0xffffffffu, nxt, 0);
             }
             // (after a give-up) nothing of this warp's may still be in flight
             if (*(volatile int *)&sm->abort) {
                 const long long t0 = clock64();
                 while (clock64() - t0 < (1ll << 24)) __nanosleep(1000);
             }
-        } else if (warp == kMmaWarp) {
-            // ---------------- products
+        } else if (warp < kLoadWarp) {
+            // ---------------- products of row tile t
+            auto products = [&](auto tile) {
+            constexpr int t = decltype(tile)::value;
             const uint64_t q_desc = sdesc_k_sw128(q_smem), k_desc = sdesc_k_sw128(kv_smem);
             const uint64_t v_desc = sdesc_mn_sw128(kv_smem, kHalfB);
             constexpr uint32_t kIdS = idesc_bf16(kTile, false), kIdO = idesc_bf16(D, true);
-            uint32_t kv = 0;             // key and value tiles waited for
-            uint32_t p_ph[2] = {0, 0};
+            uint32_t stage = 0, stage_ph = 0;         // the next key or value tile
+            uint32_t p_ph = 0, f_ph = 1, off_ph = 0;
             Item it;
             bool ok = true;
-            auto qk = [&](int t, uint32_t s) {  // S_t = Q_t K^T
-                if (elect_one()) {
-#pragma unroll
-                    for (int j = 0; j < D / 16; ++j) {
-                        const uint32_t off = ((j >> 2) * kHalfB + (j & 3) * 32) >> 4;
-                        mma_bf16_ss(s_col + t * kTile, q_desc + ((t * C::kTileB) >> 4) + off,
-                                    k_desc + ((s * C::kTileB) >> 4) + off, kIdS, j > 0);
-                    }
-                    tc_commit(&sm->s_full[t]);
-                }
-                __syncwarp();
-            };
+            const uint64_t qd = q_desc + ((t * C::kTileB) >> 4);
+            const uint32_t s_t = s_col + t * kTile, o_t = o_col + t * D, p_t = p_col + t * kPStep;
             auto commit = [&](uint64_t *bar) {
                 if (elect_one()) tc_commit(bar);
                 __syncwarp();
             };
-            auto wait_kv = [&]() {
-                ok = ok && warp_wait_flag(&sm->kv_full[kv % S], (kv / S) & 1, &sm->abort, 5);
+            auto next_stage = [&]() {  // waits for the next key or value tile
+                ok = ok && warp_wait_flag(&sm->kv_full[stage], stage_ph, &sm->abort, 5);
                 tc_fence_after();
-                return kv++ % S;
-            };
-            for (uint32_t n = 0; ok && take(n, it); ++n) {
-                const int tiles = max(it.tiles[0], it.tiles[1]);
-                uint32_t k_stage = 0;
-                if (tiles > 0) k_stage = wait_kv();
-                for (int t = 0; t < 2 && ok; ++t) {
-                    ok = warp_wait_flag(&sm->q_full[t], n & 1, &sm->abort, 6);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (it.tiles[t] > 0) qk(t, k_stage);
-                    if (it.tiles[t] <= 1) commit(&sm->q_empty[t]);
+                const uint32_t s = stage;
+                if (++stage == S) {
+                    stage = 0;
+                    stage_ph ^= 1;
                 }
-                if (!ok) break;
-                if (tiles > 0) commit(&sm->kv_empty[k_stage]);
-                for (int j = 0; j < tiles && ok; ++j) {
-                    const uint32_t v_stage = wait_kv();
-                    const bool more = j + 1 < tiles;
-                    uint32_t next_k = 0;
-                    for (int t = 0; t < 2 && ok; ++t) {
-                        if (j < it.tiles[t]) {
-                            ok = warp_wait_flag(&sm->p_ready[t], p_ph[t], &sm->abort, 7);
-                            if (!ok) break;
-                            p_ph[t] ^= 1;
-                            tc_fence_after();
-                            if (elect_one()) {
+                return s;
+            };
+            // S_t = Q_t K^T; `last`: of this item, so that Q_t is free after it
+            auto qk = [&](uint32_t s, bool last) {
+                if (C::kOwnP) {  // (else the last product with P_t came before)
+                    ok = ok && warp_wait_flag(&sm->s_free[t], f_ph, &sm->abort, 12);
+                    if (!ok) return;
+                    f_ph ^= 1;
+                    tc_fence_after();
+                }
+                if (elect_one()) {
+                    const uint64_t kd = k_desc + ((s * C::kTileB) >> 4);
 #pragma unroll
-                                for (int i = 0; i < kTile / 16; ++i)
-                                    mma_f16_ts(o_col + t * kTile, s_col + t * kTile + i * 8,
-                                               v_desc + ((v_stage * C::kTileB + i * 2048) >> 4), kIdO,
-                                               j > 0 || i > 0);
-                                tc_commit(&sm->o_done[t]);
-                            }
-                            __syncwarp();
-                        }
-                        if (t == 1) commit(&sm->kv_empty[v_stage]);
-                        if (more && t == 0) next_k = wait_kv();
-                        if (!ok) break;
-                        if (j + 1 < it.tiles[t]) {
-                            qk(t, next_k);
-                            if (j + 2 == it.tiles[t]) commit(&sm->q_empty[t]);
+                    for (int j = 0; j < D / 16; ++j) {
+                        const uint32_t off = ((j >> 2) * kHalfB + (j & 3) * 32) >> 4;
+                        mma_bf16_ss(s_t, qd + off, kd + off, kIdS, j > 0);
+                    }
+                    tc_commit(&sm->s_full[t]);
+                    tc_commit(&sm->kv_empty[s]);
+                    if (last) tc_commit(&sm->q_empty[t]);
+                }
+                __syncwarp();
+            };
+            // O_t += P_t V, by halves of the keys
+            auto pv = [&](uint32_t s, bool first, bool tell) {
+                const uint64_t vd = v_desc + ((s * C::kTileB) >> 4);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    ok = ok && warp_wait_flag(&sm->p_ready[t][h], p_ph, &sm->abort, 7);
+                    if (!ok) return;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int i = h * kTile / 32; i < (h + 1) * kTile / 32; ++i)
+                            mma_f16_ts(o_t, p_t + i * 8, vd + ((i * 2048) >> 4), kIdO,
+                                       i > 0 ? 1u : (first ? 0u : 1u));
+                        if (h == 1) {
+                            tc_commit(&sm->o_done[t]);
+                            tc_commit(&sm->kv_empty[s]);
                         }
                     }
-                    if (ok && more) commit(&sm->kv_empty[next_k]);
+                    __syncwarp();
+                    if (tell && h == 0 && lane == 0) mbar_arrive(&sm->offset);
+                }
+                p_ph ^= 1;
+            };
+            for (uint32_t n = 0; ok && take(n, it); ++n) {
+                const int n0 = __shfl_sync(0xffffffffu, it.b.tiles0, 0);
+                const int n1 = __shfl_sync(0xffffffffu, it.b.tiles1, 0);
+                const int nt = t ? n1 : n0, tiles = max(n0, n1);
+                uint32_t s = 0;
+                if (tiles > 0) s = next_stage();
+                ok = ok && warp_wait_flag(&sm->q_full[t], n & 1, &sm->abort, 6);
+                if (!ok) break;
+                tc_fence_after();
+                // The second tile starts half a softmax behind the first: two
+                // tiles in step would want the tensor pipe, and then the
+                // exponentials, at the same time.
+                const bool apart = min(n0, n1) >= kApart;
+                if (apart && t == 1) {
+                    ok = warp_wait_flag(&sm->offset, off_ph, &sm->abort, 13);
+                    if (!ok) break;
+                    off_ph ^= 1;
+                }
+                if (nt > 0)
+                    qk(s, nt == 1);
+                else {  // (the other tile's stages, and a Q_t that is not used)
+                    commit(&sm->q_empty[t]);
+                    if (tiles > 0) commit(&sm->kv_empty[s]);
+                }
+                // the scores of key tile j + 1
+                auto next_scores = [&](int j) {
+                    if (j + 1 >= tiles) return;
+                    const uint32_t k = next_stage();
+                    if (!ok) return;
+                    if (j + 1 < nt)
+                        qk(k, j + 2 == nt);
+                    else
+                        commit(&sm->kv_empty[k]);
+                };
+                for (int j = 0; j < tiles && ok; ++j) {
+                    if (C::kOwnP) next_scores(j);
+                    const uint32_t v = next_stage();
+                    if (!ok) break;
+                    if (j < nt)
+                        pv(v, j == 0, j == 0 && apart && t == 0);
+                    else
+                        commit(&sm->kv_empty[v]);
+                    if (!C::kOwnP && ok) next_scores(j);
                 }
             }
             // everything issued has finished before the block ends
             commit(&sm->finished);
             wait_own(&sm->finished, 0);
+            };
+            if (warp == kMmaWarp)
+                products(std::integral_constant<int, 0>{});
+            else
+                products(std::integral_constant<int, 1>{});
         } else if (warp == kFixWarp) {
             // ---------------- last value tiles: zeros past the sequence's end
             Item it;
             uint32_t kv = 0, ph = 0;  // ph: one phase bit per stage
             for (uint32_t n = 0; take(n, it); ++n) {
-                const int tiles = max(it.tiles[0], it.tiles[1]);
+                const int tiles = max(it.b.tiles0, it.b.tiles1);
                 kv += 2 * tiles;
                 if (tiles == 0 || !ragged(it, tiles - 1)) continue;
                 const uint32_t s = (kv - 1) % S;
                 if (!warp_wait_flag(&sm->tail[s], (ph >> s) & 1, &sm->abort, 8)) break;
                 ph ^= 1u << s;
                 uint8_t *v = base + (2 + s) * C::kTileB;
-                const int from = it.nk - (tiles - 1) * kTile;
+                const int from = it.b.nk - (tiles - 1) * kTile;
                 for (int h = 0; h < kHalves; ++h)
                     for (int i = from * 8 + lane; i < kTile * 8; i += 32)
                         *reinterpret_cast<uint4 *>(v + h * kHalfB + i * 16) = make_uint4(0, 0, 0, 0);
@@ -472,46 +536,58 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
         }
     } else {
         // ---------------- softmax: warpgroup t has row tile t, a thread a row
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int t = warp >> 2;
         const int r = threadIdx.x & 127;
         const uint32_t lane_base = (uint32_t)(warp & 3) * 32 << 16;
-        const uint32_t s_t = s_col + t * kTile + lane_base, o_t = o_col + t * kTile + lane_base;
+        const uint32_t s_t = s_col + t * kTile + lane_base, o_t = o_col + t * D + lane_base;
+        const uint32_t p_t = p_col + t * kPStep + lane_base;
         const int tok_r = r / Gt, g = r % Gt;
         const float sl = a.scale * kLog2e;
-        uint32_t s_ph = 0, o_ph = 0;  // o_ph: parity of the next product to finish
+        uint32_t ph = 0;  // parity of this warpgroup's count of key tiles
         Item it;
         bool ok = true;
         for (uint32_t n = 0; ok && take(n, it); ++n) {
-            const int tok = it.tok0 + t * tpt + tok_r;
-            const bool live = tok_r < tpt && tok < it.nq && g < it.heads;
+            const int tok = it.b.tok0 + t * tpt + tok_r;
+            const bool live = tok_r < tpt && tok < it.b.nq && g < it.heads;
             // (rows that do not exist ask for no masking)
-            const int limit = live ? keys_seen(a.causal, tok, it.nq, it.nk) : 0x3fffffff;
+            const int limit = live ? keys_seen(a.causal, tok, it.b.nq, it.b.nk) : 0x3fffffff;
             const int least = __reduce_min_sync(0xffffffffu, limit);
             float ref = -INFINITY;  // the row's reference, in log2 units
             float l = 0.f;
-            const int tiles = it.tiles[t];
+            const int tiles = t ? it.b.tiles1 : it.b.tiles0;
             for (int j = 0; j < tiles; ++j) {
-                ok = warp_wait_flag(&sm->s_full[t], s_ph, &sm->abort, 9);
+                ok = warp_wait_flag(&sm->s_full[t], ph, &sm->abort, 9);
                 if (!ok) break;
-                s_ph ^= 1;
                 tc_fence_after();
                 float x[kTile];
 #pragma unroll
                 for (int c = 0; c < kTile; c += 32) tmem_ld32(s_t + c, x + c);
                 tc_wait_ld();
+                if (C::kOwnP) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm->s_free[t]);
+                }
                 if ((j + 1) * kTile > least) {
                     const int lim = limit - j * kTile;
 #pragma unroll
-                    for (int c = 0; c < kTile; ++c) x[c] = c < lim ? x[c] : -INFINITY;
+                    for (int c = 0; c < kTile; c += 32)
+                        if (j * kTile + c + 32 > least) {
+#pragma unroll
+                            for (int e = c; e < c + 32; ++e) x[e] = e < lim ? x[e] : -INFINITY;
+                        }
                 }
                 float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                for (int c = 4; c < kTile; c += 4)
+                for (int c = 4; c + 8 <= kTile; c += 8)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], x[c + e]);
+                    for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], x[c + 2 * e], x[c + 2 * e + 1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], x[kTile - 4 + e]);
                 const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl;
                 const bool raise = top > ref + kSlack;
+                bool over = !C::kOwnP || j == 0;  // P_t may be written
                 if (__any_sync(0xffffffffu, raise)) {
                     const float to = raise ? top : ref;
                     const float f = raise ? ex2(ref - to) : 1.f;
@@ -519,21 +595,27 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
                     ref = to;
                     if (j > 0) {
                         // the last product into O_t has to be over
-                        ok = warp_wait_flag(&sm->o_done[t], o_ph ^ 1, &sm->abort, 10);
+                        ok = warp_wait_flag(&sm->o_done[t], ph ^ 1, &sm->abort, 10);
                         if (!ok) break;
+                        over = true;
                         tc_fence_after();
 #pragma unroll
-                        for (int c = 0; c < D; c += 32) {
-                            float o[32];
-                            tmem_ld32(o_t + c, o);
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(o_t + c, o);
                             tc_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] *= f;
-                            tmem_st32(o_t + c, o);
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st16(o_t + c, o);
                         }
                     }
                 }
-                o_ph ^= 1;
+                if (!over) {  // the last product with P_t has to be over
+                    ok = warp_wait_flag(&sm->o_done[t], ph ^ 1, &sm->abort, 10);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
                 const float z = ref == -INFINITY ? 0.f : ref;
                 const float2 sl2 = make_float2(sl, sl), nz2 = make_float2(-z, -z);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -548,22 +630,34 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
                         sum[e & 1] = add2(sum[e & 1], y);
                         p[e] = pack_bf16(y.x, y.y);
                     }
-                    tmem_st16(s_t + c / 2, p);
+                    tmem_st16(p_t + c / 2, p);
+                    if (c % kHalf) {  // half of the weights: their product may start
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm->p_ready[t][c / kHalf]);
+                    }
                 }
                 const float2 both = add2(sum[0], sum[1]);
                 l += both.x + both.y;
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm->p_ready[t]);
+                ph ^= 1;
             }
             if (!ok) break;
             // ---- the rows' outputs
             const float inv = 1.f / l;
             const bool none = l == 0.f;  // no key: zeros
-            uint16_t *out = a.out + (it.q0 + tok) * a.out_stride + (it.h0 + g) * D;
+            // Four neighbouring lanes hand each other 16-byte pieces, so that
+            // a store covers 64 bytes of each of 8 rows: this lane's rows are
+            // then those of its four, its piece lane % 4.
+            uint16_t *rows[4];
+            const int64_t at = live ? (int64_t)(it.b.q0 + tok) * a.out_stride + (it.h0 + g) * D : -1;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t v = __shfl_sync(0xffffffffu, at, (lane & ~3) + k);
+                rows[k] = v < 0 ? nullptr : a.out + v + (lane & 3) * 8;
+            }
             if (tiles > 0) {
-                ok = warp_wait_flag(&sm->o_done[t], o_ph ^ 1, &sm->abort, 11);
+                ok = warp_wait_flag(&sm->o_done[t], ph ^ 1, &sm->abort, 11);
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -577,18 +671,32 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = 0.f;
                 }
+                uint32_t u[4][4];  // [piece of 8 columns][word]
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
-                if (live) {
+                for (int e = 0; e < 16; ++e)
+                    u[e / 4][e % 4] = none ? 0u : pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
+                // a 4 x 4 transposition of pieces in two exchanges
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        *reinterpret_cast<uint4 *>(out + c + e) =
-                            make_uint4(pack_bf16(o[e], o[e + 1]), pack_bf16(o[e + 2], o[e + 3]),
-                                       pack_bf16(o[e + 4], o[e + 5]), pack_bf16(o[e + 6], o[e + 7]));
+                for (int b = 1; b < 4; b <<= 1) {
+                    const bool up = (lane & b) != 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k & b) continue;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t give = up ? u[k][e] : u[k | b][e];
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, give, b);
+                            if (up) u[k][e] = got; else u[k | b][e] = got;
+                        }
+                    }
                 }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (rows[k])
+                        *reinterpret_cast<uint4 *>(rows[k] + c) = make_uint4(u[k][0], u[k][1], u[k][2], u[k][3]);
             }
             if (a.lse && live)
-                a.lse[(size_t)(it.q0 + tok) * a.Hq + it.h0 + g] =
+                a.lse[(size_t)(it.b.q0 + tok) * a.Hq + it.h0 + g] =
                     none ? -INFINITY : (ref + __log2f(l)) * kLn2;
             // (O_t is read: the next item's first p_ready comes after this)
             tc_fence_before();
@@ -599,7 +707,7 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
     if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_relinquish();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(sm->tmem, 512);
     }
 }
 
@@ -626,7 +734,7 @@ cudaError_t run(const PrefillArgs &a, int sms, cudaStream_t s) {
                                box, CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
     }
-    plan_kernel<<<1, kPlanThreads, 0, s>>>(a, 2 * tpt);
+    plan_kernel<<<1, kPlanThreads, 0, s>>>(a, tpt);
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     auto fn = prefill_kernel<D>;
