@@ -17,6 +17,15 @@ import math
 
 import quantized_moe_expert_align_gb300 as _moe
 
+torch = None  # bound by the first call: importing this package does not import it
+
+
+def _need_torch():
+    global torch
+    if torch is None:
+        import torch as t
+        torch = t
+
 MOE_KV_BF16 = 0
 MOE_KV_FP8 = 1
 MOE_ATTN_STATUS_BYTES = 256
@@ -55,7 +64,7 @@ def rope_table(max_pos, rot, base=10000.0, factor=1.0, original_max=None, beta_f
     0.1 ln(factor) + 1; else 1), which scales q and k and so the attention's
     scores by its square.
     """
-    import torch
+    _need_torch()
     if rot % 2 or rot < 0 or max_pos < 1 or factor < 1.0:
         raise ValueError("rope_table: rot even, max_pos >= 1, factor >= 1")
     i = torch.arange(rot // 2, dtype=torch.float64, device=device)
@@ -81,7 +90,7 @@ class KVCache:
     latter, ``scales`` [num_pages][Hkv][2][page_size] float32."""
 
     def __init__(self, data, scales=None):
-        import torch
+        _need_torch()
         if (data.dim() != 5 or data.shape[2] != 2 or not data.is_contiguous() or
                 not data.is_cuda):
             raise ValueError("KVCache: data is a contiguous [num_pages][Hkv][2][page_size][D] "
@@ -105,7 +114,7 @@ class KVCache:
     @classmethod
     def empty(cls, num_pages, Hkv, D, page_size=64, fp8=True, device="cuda"):
         """A new cache (contents undefined until tokens are appended)."""
-        import torch
+        _need_torch()
         shape = (num_pages, Hkv, 2, page_size, D)
         if fp8:
             return cls(torch.empty(shape, dtype=torch.float8_e4m3fn, device=device),
@@ -134,24 +143,24 @@ class AttnWorkspace:
         self._ptr = self.buf.data_ptr()
 
 
-def _bf16(t, name, *shape):
-    import torch
-    if t.dtype != torch.bfloat16 or t.shape != shape or not t.is_cuda:
-        raise ValueError(f"{name}: bfloat16 {shape} on a GPU expected, got {t.dtype} "
+def _bf16(t, name, n):
+    if t.dtype != torch.bfloat16 or t.shape != (n,) or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: contiguous bfloat16 {(n,)} on a GPU expected, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
 
 
 def _rows(t, name, T, H, D):
     """Checks rows [T][H][D] with contiguous heads; the stride between tokens."""
-    _bf16(t, name, T, H, D)
+    if t.dtype != torch.bfloat16 or t.shape != (T, H, D) or not t.is_cuda:
+        raise ValueError(f"{name}: bfloat16 {(T, H, D)} on a GPU expected, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
     st = t.stride()
     if T and (st[2] != 1 or (H > 1 and st[1] != D)):
         raise ValueError(f"{name}: the heads of a token have to be contiguous")
     return st[0] if T > 1 else H * D
 
 
-def _i32(t, name, *shape):
-    import torch
+def _i32(t, name, shape):
     if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name}: contiguous int32 {shape} on a GPU expected, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
@@ -161,11 +170,18 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+def _on(stream, t):
+    """The stream handle of a call: the current stream of t's device unless
+    ``stream`` (a torch stream or a handle) is given."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return getattr(stream, "cuda_stream", stream)
+
+
 def _made(t, stream):
     """A buffer allocated here for a call on ``stream``: when that is not the
     current stream, torch must not reuse the memory before the call is done."""
     if stream is not None:
-        import torch
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(stream)
         t.record_stream(stream)
@@ -173,7 +189,6 @@ def _made(t, stream):
 
 
 def _rows_out(T, H, D, device, stream):
-    import torch
     return _made(torch.empty((T, H, D), dtype=torch.bfloat16, device=device), stream)
 
 
@@ -190,7 +205,7 @@ def qk_rope_append(q, k, v, cos_sin, positions, cache, slots, q_norm=None, k_nor
     [T][Hkv][D], cos_sin [max_pos][rot] (None: no rotation), positions and
     slots [T] int32, cache a KVCache or None.  Returns q_out; ``k_out`` True
     or a tensor also returns the rotated keys, as (q_out, k_out)."""
-    import torch
+    _need_torch()
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     sq, sk, sv = _rows(q, "q", T, Hq, D), _rows(k, "k", T, Hkv, D), _rows(v, "v", T, Hkv, D)
@@ -198,14 +213,12 @@ def qk_rope_append(q, k, v, cos_sin, positions, cache, slots, q_norm=None, k_nor
     if rot:
         if cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous() or not cos_sin.is_cuda:
             raise ValueError("cos_sin: contiguous float32 [max_pos][rot] on a GPU expected")
-        _i32(positions, "positions", T)
+        _i32(positions, "positions", (T,))
     for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
         if w is not None:
             _bf16(w, name, D)
-            if not w.is_contiguous():
-                raise ValueError(f"{name}: contiguous expected")
     if cache is not None:
-        _i32(slots, "slots", T)
+        _i32(slots, "slots", (T,))
     if q_out is None:
         q_out = _rows_out(T, Hq, D, q.device, stream)
     if k_out is True:
@@ -217,16 +230,17 @@ def qk_rope_append(q, k, v, cos_sin, positions, cache, slots, q_norm=None, k_nor
         _p(q), sq, _p(k), sk, _p(v), sv, _p(q_norm), _p(k_norm), eps, _p(cos_sin), max_pos, rot,
         int(interleaved), _p(positions) if rot else None, _p(slots) if cache is not None else None,
         _p(q_out), sqo, _p(k_out), sko, cache._ref if cache is not None else None, T, Hq, Hkv, D,
-        ws._ptr, ws.nbytes, _moe._stream(stream)), "moe_qk_rope_append")
+        ws._ptr, ws.nbytes, _on(stream, q)), "moe_qk_rope_append")
     return q_out if k_out is None else (q_out, k_out)
 
 
 def kv_gather(cache, page_table, cu_k, total, k_out=None, v_out=None, workspace=None, stream=None):
     """The cached tokens of B sequences as packed bf16 (k, v)
     [total][Hkv][D]; page_table [B][n] and cu_k [B+1] int32."""
+    _need_torch()
     B, n = page_table.shape
-    _i32(page_table, "page_table", B, n)
-    _i32(cu_k, "cu_k", B + 1)
+    _i32(page_table, "page_table", (B, n))
+    _i32(cu_k, "cu_k", (B + 1,))
     shape = (total, cache.Hkv, cache.D)
     if k_out is None:
         k_out = _rows_out(*shape, page_table.device, stream)
@@ -236,7 +250,7 @@ def kv_gather(cache, page_table, cu_k, total, k_out=None, v_out=None, workspace=
     _moe._check(_moe.load().moe_kv_gather(
         cache._ref, _p(page_table), n, _p(cu_k), B, total, _p(k_out),
         _rows(k_out, "k_out", *shape), _p(v_out), _rows(v_out, "v_out", *shape), ws._ptr,
-        ws.nbytes, _moe._stream(stream)), "moe_kv_gather")
+        ws.nbytes, _on(stream, page_table)), "moe_kv_gather")
     return k_out, v_out
 
 
@@ -246,12 +260,13 @@ def attn_decode(q, cache, page_table, seq_lens, scale=None, out=None, lse=None, 
     q [B][Hq][D], page_table [B][n] and seq_lens [B] int32; scale defaults to
     D^-1/2.  Returns out [B][Hq][D]; ``lse`` True or a float32 [B][Hq] tensor
     also returns the logsumexp, as (out, lse)."""
+    _need_torch()
     B, Hq, D = q.shape
     if D != cache.D:
         raise ValueError(f"q has heads of {D}, the cache of {cache.D}")
     n = page_table.shape[1]
-    _i32(page_table, "page_table", B, n)
-    _i32(seq_lens, "seq_lens", B)
+    _i32(page_table, "page_table", (B, n))
+    _i32(seq_lens, "seq_lens", (B,))
     sq = _rows(q, "q", B, Hq, D)
     if out is None:
         out = _rows_out(B, Hq, D, q.device, stream)
@@ -260,7 +275,7 @@ def attn_decode(q, cache, page_table, seq_lens, scale=None, out=None, lse=None, 
     ws = _workspace(workspace, stream, q.device, "decode", B, B, Hq, cache.Hkv, D)
     _moe._check(_moe.load().moe_attn_decode(
         _p(q), sq, cache._ref, _p(page_table), n, _p(seq_lens), D ** -0.5 if scale is None else scale,
-        _p(out), so, _p(lse), B, Hq, ws._ptr, ws.nbytes, _moe._stream(stream)), "moe_attn_decode")
+        _p(out), so, _p(lse), B, Hq, ws._ptr, ws.nbytes, _on(stream, q)), "moe_attn_decode")
     return out if lse is None else (out, lse)
 
 
@@ -270,11 +285,12 @@ def attn_prefill(q, k, v, cu_q, cu_k, causal=True, scale=None, out=None, lse=Non
     cu_q and cu_k [B+1] int32; the last query of a sequence stands at its last
     key.  Returns out [Tq][Hq][D]; ``lse`` True or a float32 [Tq][Hq] tensor
     also returns the logsumexp, as (out, lse)."""
+    _need_torch()
     Tq, Hq, D = q.shape
     Tk, Hkv, _ = k.shape
     B = cu_q.shape[0] - 1
-    _i32(cu_q, "cu_q", B + 1)
-    _i32(cu_k, "cu_k", B + 1)
+    _i32(cu_q, "cu_q", (B + 1,))
+    _i32(cu_k, "cu_k", (B + 1,))
     sq, sk, sv = _rows(q, "q", Tq, Hq, D), _rows(k, "k", Tk, Hkv, D), _rows(v, "v", Tk, Hkv, D)
     if out is None:
         out = _rows_out(Tq, Hq, D, q.device, stream)
@@ -284,12 +300,11 @@ def attn_prefill(q, k, v, cu_q, cu_k, causal=True, scale=None, out=None, lse=Non
     _moe._check(_moe.load().moe_attn_prefill(
         _p(q), sq, _p(k), sk, _p(v), sv, _p(cu_q), _p(cu_k), B, Tq, Tk, Hq, Hkv, D, int(causal),
         D ** -0.5 if scale is None else scale, _p(out), so, _p(lse), ws._ptr, ws.nbytes,
-        _moe._stream(stream)), "moe_attn_prefill")
+        _on(stream, q)), "moe_attn_prefill")
     return out if lse is None else (out, lse)
 
 
 def _lse(lse, T, Hq, device, stream):
-    import torch
     if lse is True:
         return _made(torch.empty((T, Hq), dtype=torch.float32, device=device), stream)
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, Hq) or

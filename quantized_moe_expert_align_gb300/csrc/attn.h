@@ -2,10 +2,28 @@
 // (rope_append.cu, attn_decode.cu, attn_prefill.cu).
 #pragma once
 
+#include <atomic>
+
 #include "moe_attn.h"
 #include "moe_internal.h"
 
 namespace moe {
+
+// Raises a kernel's dynamic shared memory limit, once per device (ordinals
+// of 64 and more: at every call).
+struct SmemOnce {
+    std::atomic<uint64_t> done{0};
+    cudaError_t set(const void *fn, size_t bytes) {
+        int dev = 0;
+        cudaError_t err = cudaGetDevice(&dev);
+        if (err != cudaSuccess) return err;
+        const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+        if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+        err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+        return err;
+    }
+};
 
 // A paged cache as the kernels see it.
 struct KvView {

@@ -727,7 +727,8 @@ cudaError_t run(const DecodeAttnArgs &a, int sms, cudaStream_t s) {
     int grid = C::kBlocks * sms < kMaxGrid ? C::kBlocks * sms : kMaxGrid;
     if (units < grid) grid = (int)units;
     auto fn = decode_kernel<D, FP8, NT>;
-    cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    static SmemOnce once;
+    cudaError_t err = once.set(reinterpret_cast<const void *>(fn), C::kSmem);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);

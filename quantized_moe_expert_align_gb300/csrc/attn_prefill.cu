@@ -738,7 +738,8 @@ cudaError_t run(const PrefillArgs &a, int sms, cudaStream_t s) {
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     auto fn = prefill_kernel<D>;
-    err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    static SmemOnce once;
+    err = once.set(reinterpret_cast<const void *>(fn), C::kSmem);
     if (err != cudaSuccess) return err;
     const int64_t most = ((int64_t)a.Tq / (2 * tpt) + a.B) * a.Hkv * HT;
     cudaLaunchConfig_t cfg = {};

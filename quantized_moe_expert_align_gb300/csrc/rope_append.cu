@@ -8,22 +8,47 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;        // gather
+constexpr int kAppendThreads = 64;
 
-__device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void unpack4(const uint2 &u, float (&x)[4]) {
+    x[0] = __uint_as_float(u.x << 16);
+    x[1] = __uint_as_float(u.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(u.y << 16);
+    x[3] = __uint_as_float(u.y & 0xFFFF0000u);
+}
+// Two interleaved pieces of 4 -> the first and the second sides of their
+// pairs, and back.
+__device__ __forceinline__ void sides(float (&x)[4], float (&y)[4]) {
+    const float a[4] = {x[0], x[2], y[0], y[2]}, b[4] = {x[1], x[3], y[1], y[3]};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = a[i], y[i] = b[i];
+}
+__device__ __forceinline__ void pieces(float (&x)[4], float (&y)[4]) {
+    const float a[4] = {x[0], y[0], x[1], y[1]}, b[4] = {x[2], y[2], x[3], y[3]};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = a[i], y[i] = b[i];
+}
+// x y and x y + z on pairs of fp32
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, r;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 r, x, y;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, r;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 r, x, y, z;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+    return r;
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&b);
-}
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
 }
 // 4 floats -> 4 e4m3 codes (nearest-even, beyond 448: 448; NaN: NaN)
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -47,12 +72,12 @@ __device__ __forceinline__ void from_e4m3x4(uint32_t w, float (&f)[4]) {
 
 // Smallest index over a block (INT_MAX: none), in thread 0.
 __device__ __forceinline__ int block_min(int v) {
-    __shared__ int part[kThreads / 32];
+    __shared__ int part[32];
     v = __reduce_min_sync(0xffffffffu, v);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
     if (threadIdx.x == 0)
-        for (int i = 1; i < kThreads / 32; ++i) v = min(v, part[i]);
+        for (int i = 1; i < blockDim.x / 32; ++i) v = min(v, part[i]);
     return v;
 }
 constexpr int kNone = 0x7fffffff;
@@ -67,135 +92,200 @@ __device__ __forceinline__ bool token_ok(const AppendArgs &a, int t, int &slot) 
     return pos_ok && slot >= -1 && slot < (a.num_pages << a.page_shift);
 }
 
-// Block 0 looks every token over and writes the status word; block
-// 1 + t * gridDim.y... handles one part of token t's heads: groups of D/8
-// lanes take one head each (8 values a lane), so the norm and the cache
-// scale are shuffles within a group, and a half-layout pair's partner is
-// another lane of the group.
+// Block (0, 0) looks every token over and writes the status word; blocks
+// (1 + t, y) share the heads of token t.  A group of D/8 lanes takes one head
+// (a row), 8 values a lane in two pieces of 4 that hold both sides of its
+// pairs: pieces rot/2 apart in the half layout, neighbours otherwise.  The
+// rotation then needs no other lane; the norm and the cache scale are
+// shuffles within the group.
+//
+// HBM bounds the work, but with 4 values in and 2 to 4 bytes out per value
+// the instructions come close: norm weights, cosines and sines of a lane's
+// four pairs are folded into 16 factors once per token, each kind of row has
+// its own loop, and the arithmetic is on pairs of fp32.
+enum Kind { kQuery, kKey, kValue };
+
+// A lane's place in a row.
+struct Place {
+    int lane, dA, dB;
+    uint32_t group;   // the lanes of its group
+};
+
+// a' = rms (a ac - b bs), b' = rms (b bc + a as) of a lane's pairs, two at a time
+struct Turn {
+    float2 ac[2], as[2], bc[2], bs[2];
+};
+
+// The weights of a lane's pairs, one from each side, by pairs of pairs.
+__device__ __forceinline__ Turn fold(const uint16_t *w, const Place &p, bool interleaved, float4 c, float4 s) {
+    float x[4] = {1.f, 1.f, 1.f, 1.f}, y[4] = {1.f, 1.f, 1.f, 1.f};
+    if (w) {
+        unpack4(__ldg(reinterpret_cast<const uint2 *>(w + p.dA)), x);
+        unpack4(__ldg(reinterpret_cast<const uint2 *>(w + p.dB)), y);
+    }
+    if (interleaved) sides(x, y);
+    Turn t;
+    t.ac[0] = make_float2(x[0] * c.x, x[1] * c.y);
+    t.ac[1] = make_float2(x[2] * c.z, x[3] * c.w);
+    t.as[0] = make_float2(x[0] * s.x, x[1] * s.y);
+    t.as[1] = make_float2(x[2] * s.z, x[3] * s.w);
+    t.bc[0] = make_float2(y[0] * c.x, y[1] * c.y);
+    t.bc[1] = make_float2(y[2] * c.z, y[3] * c.w);
+    t.bs[0] = make_float2(-y[0] * s.x, -y[1] * s.y);
+    t.bs[1] = make_float2(-y[2] * s.z, -y[3] * s.w);
+    return t;
+}
+
+// Rows r, r + step, ... < n of one kind, the next two on the way at any time.
+template <int D, bool FP8, int KIND>
+__device__ __forceinline__ void walk(const AppendArgs &a, const Place &p, const Turn &f, bool norm,
+                                     const uint16_t *src, uint16_t *dst, int &r, int n, int step, int slot,
+                                     const uint2 (&ahead)[2][2]) {
+    constexpr int L = D / 8;
+    uint2 in[2][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        if (KIND == kQuery) {
+            in[u][0] = ahead[u][0];
+            in[u][1] = ahead[u][1];
+        } else if (r + u * step < n) {
+            in[u][0] = *reinterpret_cast<const uint2 *>(src + (r + u * step) * D + p.dA);
+            in[u][1] = *reinterpret_cast<const uint2 *>(src + (r + u * step) * D + p.dB);
+        }
+    }
+    const size_t page = (size_t)(max(slot, 0) >> a.page_shift);
+    const size_t row0 = ((page * a.Hkv * 2 + (KIND == kValue)) << a.page_shift) +
+                        (slot & ((1 << a.page_shift) - 1));
+    const bool cached = KIND != kQuery && slot >= 0;
+    while (r < n) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if (r >= n) return;
+            float x[4], y[4];
+            unpack4(in[u][0], x);
+            unpack4(in[u][1], y);
+            if (r + 2 * step < n) {
+                in[u][0] = *reinterpret_cast<const uint2 *>(src + (r + 2 * step) * D + p.dA);
+                in[u][1] = *reinterpret_cast<const uint2 *>(src + (r + 2 * step) * D + p.dB);
+            }
+            if (KIND != kValue) {
+                float2 rms = make_float2(1.f, 1.f);
+                if (norm) {
+                    float2 q = mul2(make_float2(x[0], x[1]), make_float2(x[0], x[1]));
+                    q = fma2(make_float2(x[2], x[3]), make_float2(x[2], x[3]), q);
+                    q = fma2(make_float2(y[0], y[1]), make_float2(y[0], y[1]), q);
+                    q = fma2(make_float2(y[2], y[3]), make_float2(y[2], y[3]), q);
+                    float ss = q.x + q.y;
+#pragma unroll
+                    for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(p.group, ss, o);
+                    rms.x = rms.y = rsqrtf(ss * (1.0f / D) + a.eps);
+                }
+                if (a.interleaved) sides(x, y);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float2 A = mul2(make_float2(x[2 * k], x[2 * k + 1]), rms);
+                    const float2 B = mul2(make_float2(y[2 * k], y[2 * k + 1]), rms);
+                    const float2 A2 = fma2(A, f.ac[k], mul2(B, f.bs[k]));
+                    const float2 B2 = fma2(B, f.bc[k], mul2(A, f.as[k]));
+                    x[2 * k] = A2.x;
+                    x[2 * k + 1] = A2.y;
+                    y[2 * k] = B2.x;
+                    y[2 * k + 1] = B2.y;
+                }
+                if (a.interleaved) pieces(x, y);
+            }
+            const uint2 oA = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
+            const uint2 oB = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
+            if (KIND != kValue && dst) {
+                *reinterpret_cast<uint2 *>(dst + r * D + p.dA) = oA;
+                *reinterpret_cast<uint2 *>(dst + r * D + p.dB) = oB;
+            }
+            if (cached) {
+                const size_t row = row0 + ((size_t)(r * 2) << a.page_shift);
+                if (FP8) {
+                    // the largest magnitude by its bits: above every number
+                    // stand infinity and then NaN
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+                        top = max(top, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+                    }
+#pragma unroll
+                    for (int o = L / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(p.group, top, o));
+                    const float amax = __uint_as_float(top >= 0x7F800000u ? 0x7FFFFFFFu : top);
+                    const float inv = top == 0 ? 0.f : 448.0f / amax;
+                    *reinterpret_cast<uint32_t *>(a.data + row * D + p.dA) =
+                        e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+                    *reinterpret_cast<uint32_t *>(a.data + row * D + p.dB) =
+                        e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+                    if (p.lane == 0) a.scales[row] = amax / 448.0f;
+                } else {
+                    uint16_t *to = reinterpret_cast<uint16_t *>(a.data) + row * D;
+                    *reinterpret_cast<uint2 *>(to + p.dA) = oA;
+                    *reinterpret_cast<uint2 *>(to + p.dB) = oB;
+                }
+            }
+            r += step;
+        }
+    }
+}
+
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     constexpr int L = D / 8;               // lanes per head
-    constexpr int NG = kThreads / L;       // groups per block
+    constexpr int NG = kAppendThreads / L; // groups per block
     if (blockIdx.x == 0) {
         if (blockIdx.y) return;
         int bad = kNone, slot;
-        for (int t = threadIdx.x; t < a.T; t += kThreads)
-            if (bad == kNone && !token_ok(a, t, slot)) bad = t;
+#pragma unroll 4
+        for (int t = threadIdx.x; t < a.T; t += kAppendThreads)
+            if (!token_ok(a, t, slot)) bad = min(bad, t);
         bad = block_min(bad);
         if (threadIdx.x == 0) write_status(a.ctrl, bad);
         return;
     }
     const int t = blockIdx.x - 1;
-    const int lane = threadIdx.x % L;
-    const int d0 = lane * 8;
+    Place p;
+    p.lane = threadIdx.x % L;
+    p.group = (L == 32 ? 0xffffffffu : (1u << (L & 31)) - 1) << ((threadIdx.x & 31) / L * L);
+    const int half = a.rot / 2;
+    const bool turned = p.lane * 8 < a.rot;
+    const bool apart = turned && !a.interleaved;
+    p.dA = apart ? p.lane * 4 : p.lane * 8;
+    p.dB = apart ? half + p.lane * 4 : p.lane * 8 + 4;
+    // The token's rows in order, q, k and v: this group takes r, r + step, ...
+    // The first loads go out before anything that depends on the position.
+    const int step = gridDim.y * NG;
+    int r = blockIdx.y * NG + threadIdx.x / L;
+    const uint16_t *q = a.q + t * a.q_stride;
+    uint2 ahead[2][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+        if (r + u * step < a.Hq) {
+            ahead[u][0] = *reinterpret_cast<const uint2 *>(q + (r + u * step) * D + p.dA);
+            ahead[u][1] = *reinterpret_cast<const uint2 *>(q + (r + u * step) * D + p.dB);
+        }
     int slot;
     if (!token_ok(a, t, slot)) return;
-    // this lane's cosines and signed sines: out = x c + partner s
-    float c[8], s[8];
-    const bool turned = d0 < a.rot;
-    const int half = a.rot / 2;
-    int partner = threadIdx.x & 31;
+    // this lane's four pairs are the pairs 4 lane .. 4 lane + 3
+    float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (turned) {
-        const float *row = a.cos_sin + (size_t)__ldg(a.positions + t) * a.rot;
-        if (a.interleaved) {
-            const float4 cc = __ldg(reinterpret_cast<const float4 *>(row + d0 / 2));
-            const float4 ss = __ldg(reinterpret_cast<const float4 *>(row + half + d0 / 2));
-            const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                c[i] = cv[i / 2];
-                s[i] = (i & 1) ? sv[i / 2] : -sv[i / 2];
-            }
-        } else {
-            const bool first = d0 < half;
-            const int i0 = first ? d0 : d0 - half;
-            partner += first ? half / 8 : -(half / 8);
-            const float sign = first ? -1.f : 1.f;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float4 cc = __ldg(reinterpret_cast<const float4 *>(row + i0) + j);
-                const float4 ss = __ldg(reinterpret_cast<const float4 *>(row + half + i0) + j);
-                c[4 * j] = cc.x, c[4 * j + 1] = cc.y, c[4 * j + 2] = cc.z, c[4 * j + 3] = cc.w;
-                s[4 * j] = sign * ss.x, s[4 * j + 1] = sign * ss.y;
-                s[4 * j + 2] = sign * ss.z, s[4 * j + 3] = sign * ss.w;
-            }
-        }
+        const float *row = a.cos_sin + (size_t)__ldg(a.positions + t) * a.rot + p.lane * 4;
+        c = __ldg(reinterpret_cast<const float4 *>(row));
+        s = __ldg(reinterpret_cast<const float4 *>(row + half));
     }
-    const int rows = a.Hq + 2 * a.Hkv;
-    // (every lane of a warp runs every pass: the shuffles need them all)
-    for (int r0 = blockIdx.y * NG; r0 < rows; r0 += gridDim.y * NG) {
-        const int r = r0 + threadIdx.x / L;
-        const bool live = r < rows;
-        const int kind = r < a.Hq ? 0 : (r < a.Hq + a.Hkv ? 1 : 2);
-        const int h = kind == 0 ? r : (kind == 1 ? r - a.Hq : r - a.Hq - a.Hkv);
-        const uint16_t *src = kind == 0 ? a.q + t * a.q_stride
-                                        : (kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride);
-        uint4 in = make_uint4(0, 0, 0, 0);
-        if (live) in = *reinterpret_cast<const uint4 *>(src + h * D + d0);
-        float x[8];
-        unpack8(in, x);
-        const uint16_t *w = kind == 0 ? a.q_norm : (kind == 1 ? a.k_norm : nullptr);
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-        for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (w) {
-            const float r_ = rsqrtf(ss * (1.0f / D) + a.eps);
-            float wf[8];
-            unpack8(__ldg(reinterpret_cast<const uint4 *>(w + d0)), wf);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = x[i] * r_ * wf[i];
-        }
-        float p[8];
-        if (a.interleaved) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = x[i ^ 1];
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = __shfl_sync(0xffffffffu, x[i], partner);
-        }
-        if (turned && kind < 2) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], c[i], p[i] * s[i]);
-        }
-        float amax = 0.f, scale = 0.f;
-        if (FP8) {
-            float nan = 0.f;  // NaN if any value is infinite or NaN
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                amax = fmaxf(amax, fabsf(x[i]));
-                nan = fmaf(x[i], 0.f, nan);
-            }
-#pragma unroll
-            for (int o = L / 2; o; o >>= 1) {
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                nan += __shfl_xor_sync(0xffffffffu, nan, o);
-            }
-            amax += nan;
-        }
-        if (!live) continue;
-        if (kind == 0) {
-            *reinterpret_cast<uint4 *>(a.q_out + t * a.q_out_stride + h * D + d0) = pack8(x);
-            continue;
-        }
-        if (kind == 1 && a.k_out)
-            *reinterpret_cast<uint4 *>(a.k_out + t * a.k_out_stride + h * D + d0) = pack8(x);
-        if (slot < 0) continue;
-        const size_t page = (size_t)(slot >> a.page_shift);
-        const size_t row = (((page * a.Hkv + h) * 2 + (kind - 1)) << a.page_shift) +
-                           (slot & ((1 << a.page_shift) - 1));
-        if (FP8) {
-            scale = amax / 448.0f;
-            const float inv = amax > 0.f ? 448.0f / amax : (amax == 0.f ? 0.f : amax);
-            const uint2 o = make_uint2(e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
-                                       e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
-            *reinterpret_cast<uint2 *>(a.data + row * D + d0) = o;
-            if (lane == 0) a.scales[row] = scale;
-        } else {
-            *reinterpret_cast<uint4 *>(a.data + (row * D + d0) * 2) = pack8(x);
-        }
-    }
+    if (r < a.Hq)
+        walk<D, FP8, kQuery>(a, p, fold(a.q_norm, p, a.interleaved, c, s), a.q_norm != nullptr, q,
+                             a.q_out + t * a.q_out_stride, r, a.Hq, step, slot, ahead);
+    r -= a.Hq;
+    if (r < a.Hkv)
+        walk<D, FP8, kKey>(a, p, fold(a.k_norm, p, a.interleaved, c, s), a.k_norm != nullptr,
+                           a.k + t * a.k_stride, a.k_out ? a.k_out + t * a.k_out_stride : nullptr, r,
+                           a.Hkv, step, slot, ahead);
+    r -= a.Hkv;
+    if (r < a.Hkv && slot >= 0)
+        walk<D, FP8, kValue>(a, p, Turn{}, false, a.v + t * a.v_stride, nullptr, r, a.Hkv, step, slot, ahead);
 }
 
 // Sequence of packed row t: the last b with cu[b] <= t (cu[0] <= t assumed;
@@ -257,47 +347,69 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(GatherKvArgs a) {
     }
     __syncthreads();
     const int lane = threadIdx.x % L;
-    const int n = nt * a.kv.Hkv * 2;
-#pragma unroll 4
-    for (int w = threadIdx.x / L; w < n; w += NG) {
-        const int i = w % nt, hk = w / nt;  // hk = h * 2 + (0 K, 1 V)
-        const int64_t b = base[i];
-        uint4 o = make_uint4(0, 0, 0, 0);
-        if (b >= 0) {
-            const size_t row = (size_t)b + ((size_t)hk << a.kv.page_shift);
-            if (FP8) {
-                const uint2 u = __ldg(reinterpret_cast<const uint2 *>(a.kv.data + row * D) + lane);
-                const float sc = __ldg(a.kv.scales + row);
-                float x[4], y[4];
-                from_e4m3x4(u.x, x);
-                from_e4m3x4(u.y, y);
-                o = make_uint4(pack2(x[0] * sc, x[1] * sc), pack2(x[2] * sc, x[3] * sc),
-                               pack2(y[0] * sc, y[1] * sc), pack2(y[2] * sc, y[3] * sc));
-            } else {
-                o = __ldg(reinterpret_cast<const uint4 *>(a.kv.data + row * D * 2) + lane);
+    const int n = kGatherTokens * a.kv.Hkv * 2;
+    // kWay rows' loads are in flight before the first is written
+    constexpr int kWay = 4;
+    for (int w0 = threadIdx.x / L; w0 < n; w0 += NG * kWay) {
+        uint4 u[kWay];
+        float sc[kWay];
+#pragma unroll
+        for (int k = 0; k < kWay; ++k) {
+            const int w = w0 + k * NG;
+            const int i = w % kGatherTokens, hk = w / kGatherTokens;  // hk = h * 2 + (0 K, 1 V)
+            const int64_t b = w < n && i < nt ? base[i] : -1;
+            u[k] = make_uint4(0, 0, 0, 0);
+            sc[k] = 0.f;
+            if (b >= 0) {
+                const size_t row = (size_t)b + ((size_t)hk << a.kv.page_shift);
+                if (FP8) {
+                    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(a.kv.data + row * D) + lane);
+                    u[k].x = v.x;
+                    u[k].y = v.y;
+                    sc[k] = __ldg(a.kv.scales + row);
+                } else {
+                    u[k] = __ldg(reinterpret_cast<const uint4 *>(a.kv.data + row * D * 2) + lane);
+                }
             }
         }
-        const int t = t0 + i, h = hk >> 1;
-        uint16_t *dst = (hk & 1) ? a.v_out + t * a.v_out_stride : a.k_out + t * a.k_out_stride;
-        *(reinterpret_cast<uint4 *>(dst + h * D) + lane) = o;
+#pragma unroll
+        for (int k = 0; k < kWay; ++k) {
+            const int w = w0 + k * NG;
+            const int i = w % kGatherTokens, hk = w / kGatherTokens;
+            if (w >= n || i >= nt) continue;
+            uint4 o = u[k];
+            if (FP8) {
+                float x[4], y[4];
+                from_e4m3x4(u[k].x, x);
+                from_e4m3x4(u[k].y, y);
+                o = make_uint4(pack2(x[0] * sc[k], x[1] * sc[k]), pack2(x[2] * sc[k], x[3] * sc[k]),
+                               pack2(y[0] * sc[k], y[1] * sc[k]), pack2(y[2] * sc[k], y[3] * sc[k]));
+            }
+            const int t = t0 + i, h = hk >> 1;
+            uint16_t *dst = (hk & 1) ? a.v_out + t * a.v_out_stride : a.k_out + t * a.k_out_stride;
+            *(reinterpret_cast<uint4 *>(dst + h * D) + lane) = o;
+        }
     }
 }
 
 }  // namespace
 
+template <int D, bool FP8>
+static void append(const AppendArgs &a, cudaStream_t s) {
+    // Few tokens: one row per group, so that the heads of a token spread over
+    // blocks (latency counts).  Many: a block takes a whole token, so that its
+    // position's cosines and the weights are fetched once.
+    constexpr int kGroups = kAppendThreads / (D / 8);
+    const int passes = (a.Hq + 2 * a.Hkv + kGroups - 1) / kGroups;
+    append_kernel<D, FP8><<<dim3(a.T + 1, a.T < 1024 ? passes : 1), kAppendThreads, 0, s>>>(a);
+}
+
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
-    const int L = a.D / 8, groups = kThreads / L;
-    const int passes = (a.Hq + 2 * a.Hkv + groups - 1) / groups;
-    // few tokens: one pass of heads per block; many: one block per token
-    const int parts = a.T >= 1024 ? 1 : passes;
-    const dim3 grid(a.T + 1, parts);
     const bool fp8 = a.cache_type == MOE_KV_FP8 && a.data;
     if (a.D == 128)
-        fp8 ? append_kernel<128, true><<<grid, kThreads, 0, s>>>(a)
-            : append_kernel<128, false><<<grid, kThreads, 0, s>>>(a);
+        fp8 ? append<128, true>(a, s) : append<128, false>(a, s);
     else
-        fp8 ? append_kernel<64, true><<<grid, kThreads, 0, s>>>(a)
-            : append_kernel<64, false><<<grid, kThreads, 0, s>>>(a);
+        fp8 ? append<64, true>(a, s) : append<64, false>(a, s);
     return cudaGetLastError();
 }
 
