@@ -9,8 +9,8 @@
 //    values' columns) and whose 8-column side is the query heads, so up to 8
 //    heads waste nothing and the cache is read from shared memory once;
 //  * work is cut into units of 64 keys of one (sequence, key/value head);
-//    the units of the whole batch, in order, are shared out evenly over two
-//    blocks per SM whatever the lengths are.  A pair cut by a block's end is
+//    the units of the whole batch, in order, are shared out evenly over two or
+//    three blocks per SM whatever the lengths are.  A pair cut by a block's end is
 //    joined by a second kernel, in key order, so results do not depend on
 //    timing;
 //  * one warp of a block copies (TMA, a ring of stages), four warps take 16
@@ -58,10 +58,11 @@ __host__ __device__ inline DecodeLayout decode_layout(int rows, int D) {
 template <int D, bool FP8, int NT>
 struct Cfg {
     static constexpr int kRows = 8 * NT;                   // query heads of a tile
-    // two blocks on an SM (one's set-up and joins under the other's copies);
-    // 32 heads need the registers of one
-    static constexpr int kBlocks = NT == 4 ? 1 : 2;
-    static constexpr int kSmemLimit = (kBlocks == 1 ? 226 : 113) * 1024;
+    // Several blocks on an SM hide each other's set-up, joins and latencies:
+    // two, for fp8 three (half the bytes for the same steps: 256 sequences up
+    // to 8192 keys 282 -> 277 us); 32 heads need the registers of one.
+    static constexpr int kBlocks = NT == 4 ? 1 : (FP8 ? 3 : 2);
+    static constexpr int kSmemLimit = (kBlocks == 1 ? 226 : (kBlocks == 2 ? 113 : 75)) * 1024;
     static constexpr int kEs = FP8 ? 1 : 2;
     static constexpr int kRowB = D * kEs < 128 ? D * kEs : 128;
     static constexpr int kHalves = D * kEs / kRowB;
@@ -384,18 +385,21 @@ decode_kernel(const DecodeAttnArgs a, const int HV, const int RT, const __grid_c
                 const int left = w.n - ((w.j + c) * kChunk + 16 * warp);  // keys of this warp
                 if (left > 0 && ok) {
                     const uint32_t kr = st + my_rows, vr = kr + kv_b;
-                    float sT[NT][4];
+                    // (two sums in turns: a chain of products into one is
+                    // as long as the tensor pipe's latency times D / 16)
+                    float sT[NT][4], sU[NT][4];
 #pragma unroll
                     for (int i = 0; i < NT; ++i)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sT[i][e] = 0.f;
+                        for (int e = 0; e < 4; ++e) sT[i][e] = sU[i][e] = 0.f;
                     if (!FP8) {
 #pragma unroll
                         for (int d = 0; d < D / 16; ++d) {
                             uint32_t k4[4];
                             ldsm4(k4, frag(kr, 2 * d));
 #pragma unroll
-                            for (int i = 0; i < NT; ++i) mma16816<true>(sT[i], k4, qf[i][d][0], qf[i][d][1]);
+                            for (int i = 0; i < NT; ++i)
+                                mma16816<true>(d & 1 ? sU[i] : sT[i], k4, qf[i][d][0], qf[i][d][1]);
                         }
                     } else {
 #pragma unroll
@@ -409,10 +413,14 @@ decode_kernel(const DecodeAttnArgs a, const int HV, const int RT, const __grid_c
                                                         e4m3_pair(hi >> 16)};
 #pragma unroll
                                 for (int i = 0; i < NT; ++i)
-                                    mma16816<false>(sT[i], af, qf[i][d + e][0], qf[i][d + e][1]);
+                                    mma16816<false>(e & 1 ? sU[i] : sT[i], af, qf[i][d + e][0], qf[i][d + e][1]);
                             }
                         }
                     }
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sT[i][e] += sU[i][e];
                     // this lane's keys gq and gq + 8
                     float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
                     if (FP8) {
@@ -424,7 +432,7 @@ decode_kernel(const DecodeAttnArgs a, const int HV, const int RT, const __grid_c
                         vs[1] = sc[R + gq + 8];
                     }
                     const bool see0 = gq < left, see1 = gq + 8 < left;
-                    uint32_t pf[NT][2];
+                    uint32_t pf[NT][2], pl[NT][2];  // the weights' upper and lower parts
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
                         float x[4];
@@ -464,17 +472,27 @@ decode_kernel(const DecodeAttnArgs a, const int HV, const int RT, const __grid_c
                         x[3] = ex2(x[3] - z1);
                         l[i][0] += x[0] + x[2];
                         l[i][1] += x[1] + x[3];
-                        // weights for the product with v: rounded to bf16 (8
-                        // bits, the values' own precision), v's scale with
-                        // them; the sum l keeps the unrounded ones
+                        // Weights for the product with v, v's scale with
+                        // them: for a bf16 cache as the sum of two bf16 (one
+                        // alone would add as much error as the result's own
+                        // rounding, and the second product is free: 109 us
+                        // either way for 90 sequences up to 8192 keys), for
+                        // fp8 one, far finer than the codes (the second
+                        // costs 7% there).  The sum l keeps the unrounded.
                         if (FP8) {
                             x[0] = see0 ? x[0] * vs[0] : 0.f;
                             x[1] = see0 ? x[1] * vs[0] : 0.f;
                             x[2] = see1 ? x[2] * vs[1] : 0.f;
                             x[3] = see1 ? x[3] * vs[1] : 0.f;
                         }
-                        pf[i][0] = transpose8x8(pack_bf16(x[0], x[1]));
-                        pf[i][1] = transpose8x8(pack_bf16(x[2], x[3]));
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t hi = pack_bf16(x[2 * e], x[2 * e + 1]);
+                            const float r0 = x[2 * e] - __uint_as_float(hi << 16);
+                            const float r1 = x[2 * e + 1] - __uint_as_float(hi & 0xFFFF0000u);
+                            pf[i][e] = transpose8x8(hi);
+                            if (!FP8) pl[i][e] = transpose8x8(pack_bf16(r0, r1));
+                        }
                     }
                     // keys past the end hold anything: zero v there (0 x NaN)
                     uint32_t mask0 = 0xFFFFFFFFu, mask1 = 0xFFFFFFFFu;
@@ -498,7 +516,10 @@ decode_kernel(const DecodeAttnArgs a, const int HV, const int RT, const __grid_c
                                 af[3] &= mask1;
                             }
 #pragma unroll
-                            for (int i = 0; i < NT; ++i) mma16816<true>(o[i][d], af, pf[i][0], pf[i][1]);
+                            for (int i = 0; i < NT; ++i) {
+                                mma16816<true>(o[i][d], af, pf[i][0], pf[i][1]);
+                                mma16816<true>(o[i][d], af, pl[i][0], pl[i][1]);
+                            }
                         }
                     } else {
 #pragma unroll

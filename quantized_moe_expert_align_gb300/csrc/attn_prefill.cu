@@ -21,7 +21,9 @@
 // fp32, where p <= 2^8 costs nothing.
 //
 // A planning kernel lists the items by falling number of key tiles; the
-// blocks take them from a counter, longest first.
+// blocks take them from a counter, longest first.  Where a few items have
+// more key tiles than an SM's even share of the whole work, they are cut into
+// parts, whose unscaled sums a last kernel joins in order.
 #include <type_traits>
 
 #include "attn_common.cuh"
@@ -41,28 +43,47 @@ constexpr int kBuckets = 1024;
 constexpr int kApart = 4;        // items of at least this many key tiles run their row tiles offset
 constexpr float kSlack = 8.f;    // a row's maximum may exceed its reference by this
 
+constexpr int kMinPart = 8;      // key tiles below which a range is not cut
+constexpr int kMaxSms = 160;     // blocks of the main kernel at most
+constexpr int kMaxParts = 2 * kMaxSms;  // of one call, all heads together
+
 struct PlanHead {
-    int32_t items, next;   // (sequence, block) pairs; the next item to take
+    int32_t items, next;   // (block, part) pairs; the next item to take
+    int32_t joins, slots;  // blocks in parts; places for parts
 };
-// One sequence's block of 256 rows for every head: what does not depend on
-// the head.
+// One sequence's block of 256 rows for every head (what does not depend on
+// the head), or one part of its keys.
 struct __align__(16) Block {
     int32_t q0, nq, k0, nk;   // rows of the sequence
     int32_t tok0;             // the block's first token within the sequence
-    int32_t tiles0, tiles1;   // key tiles of each row tile
-    int32_t pad;
+    int32_t j0;               // the first key tile
+    int32_t tiles0, tiles1;   // key tiles of each row tile, from j0 on
+    int32_t slot, parts, part, pad;  // slot: of the block's first head and part; -1: whole
+};
+struct __align__(16) Split {  // a block in parts
+    int32_t q0, nq, tok0, slot, parts, pad[3];
 };
 struct PrefillLayout {
-    size_t ctrl, head, list, total;
+    size_t ctrl, head, list, splits, ml, sums, total;
 };
-// Items: every sequence has at most one partly filled block.
-__host__ __device__ inline PrefillLayout prefill_layout(int B, int Tq, int tokens) {
+// Every sequence has at most one partly filled block; parts beyond a block's
+// first add up to at most kMaxSms.  The joined parts' places only exist where
+// there are more than kMinPart key tiles (unknown here: always counted).
+__host__ __device__ inline PrefillLayout prefill_layout(int B, int Tq, int tokens, int D) {
     PrefillLayout l;
     l.ctrl = 0;
     l.head = 256;
     l.list = 512;
-    l.total = l.list + ((size_t)Tq / tokens + B) * sizeof(Block);
+    l.splits = l.list + ((size_t)Tq / tokens + B + kMaxSms) * sizeof(Block);
+    l.ml = l.splits + kMaxParts * sizeof(Split);
+    l.sums = (l.ml + (size_t)kMaxParts * 2 * kTile * 8 + 255) / 256 * 256;
+    l.total = l.sums + (size_t)kMaxParts * 2 * kTile * D * 4;
     return l;
+}
+// Place of a part's four columns c .. c + 3 of row r of row tile t: rows are
+// neighbours, so a warp's stores and loads are whole lines.
+__host__ __device__ inline size_t part_at(int slot, int t, int c, int r, int D) {
+    return ((((size_t)slot * 2 + t) * (D / 4) + c / 4) * kTile + r) * 4;
 }
 // Query heads of a row tile and tokens of a row tile, for groups of G heads.
 __host__ __device__ inline int tile_heads(int G) { return G < kTile ? G : kTile; }
@@ -76,6 +97,13 @@ struct Cfg {
     // 128 columns for the weights P_t, so that the next scores can be computed
     // as soon as S_t is in registers; heads of 128 put P_t over S_t.
     static constexpr bool kOwnP = D == 64;
+    // The launch's 168 registers a thread, shared out anew (128 kRoleRegs +
+    // 256 kSoftmaxRegs = 384 x 168).  Measured both ways: 8192 causal tokens,
+    // 64 heads of 128, 656 -> 637 us with 104 / 200; chunks with heads of 64
+    // 245 us with 88 / 208, 259 with 104 / 200.
+    static constexpr int kRoleRegs = D == 128 ? 104 : 88;
+    static constexpr int kSoftmaxRegs = D == 128 ? 200 : 208;
+    static_assert(128 * kRoleRegs + 256 * kSoftmaxRegs <= 384 * 168, "register split");
     static constexpr size_t kSmem = (size_t)(2 + kStages) * kTileB + 1024 + 1024;
     static_assert(kSmem > 114 * 1024, "one block per SM: all of tensor memory is its own");
 };
@@ -84,6 +112,7 @@ struct Cfg {
 struct Item {
     Block b;
     int hk, h0, heads;     // key/value head; first query head and their number
+    int slot;              // this head's and part's place, -1: the block is whole
     int done;
 };
 
@@ -108,24 +137,29 @@ __device__ __forceinline__ int keys_seen(int causal, int tok, int nq, int nk) {
 }
 
 // ------------------------------------------------------------------- planning
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PrefillArgs a, const int tpt) {
+__device__ __forceinline__ unsigned long long warp_total(unsigned long long v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__global__ void __launch_bounds__(kPlanThreads)
+plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks) {
+    __shared__ int count[kBuckets], warp_sum[kPlanThreads / 32], first_bad, joins, slots, longest;
+    __shared__ unsigned long long all_tiles;
     const int tokens = 2 * tpt;  // of a block
-    __shared__ int count[kBuckets], warp_sum[kPlanThreads / 32], first_bad;
-    const PrefillLayout L = prefill_layout(a.B, a.Tq, tokens);
+    const PrefillLayout L = prefill_layout(a.B, a.Tq, tokens, a.D);
     const int tid = threadIdx.x, lane = tid & 31;
     pdl_trigger();
     count[tid] = 0;
-    if (tid == 0) first_bad = 0x7fffffff;
+    if (tid == 0) {
+        first_bad = 0x7fffffff;
+        joins = slots = longest = 0;
+        all_tiles = 0;
+    }
     __syncthreads();
-    const int64_t room = (int64_t)a.Tq / tokens + a.B;
-    // a block's bucket: fewest key tiles last
-    auto bucket = [&](int blk, int nq, int nk) {
-        const int last = min(nq, (blk + 1) * tokens) - 1;
-        const int tiles = (keys_seen(a.causal, last, nq, nk) + kTile - 1) / kTile;
-        return kBuckets - 1 - min(kBuckets - 1, tiles);
-    };
-    // one warp per sequence, one lane per block
-    for (int pass = 0; pass < 2; ++pass) {
+    const int64_t room = (int64_t)a.Tq / tokens + a.B + kMaxSms;
+    // one warp per sequence, one lane per block: f(block's first token, key tiles)
+    auto blocks = [&](auto f) {
         for (int b = tid >> 5; b < a.B; b += kPlanThreads / 32) {
             if (!seq_ok(a, b)) {
                 if (lane == 0) atomicMin(&first_bad, b);
@@ -133,43 +167,107 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PrefillArgs a,
             }
             const int q0 = __ldg(a.cu_q + b), nq = __ldg(a.cu_q + b + 1) - q0;
             const int k0 = __ldg(a.cu_k + b), nk = __ldg(a.cu_k + b + 1) - k0;
-            for (int blk = lane; blk < (nq + tokens - 1) / tokens; blk += 32) {
-                const int at = atomicAdd(&count[bucket(blk, nq, nk)], 1);
-                // (overlapping sequences may ask for more items than rows)
-                if (!pass || at >= room) continue;
-                auto tiles_of = [&](int t0) {  // of the row tile from token t0 on
-                    const int last = min(nq, t0 + tpt) - 1;
-                    return last < t0 ? 0 : (keys_seen(a.causal, last, nq, nk) + kTile - 1) / kTile;
+            for (int t0 = lane * tokens; t0 < nq; t0 += 32 * tokens) {
+                auto tiles_of = [&](int t) {  // of the row tile from token t on
+                    const int last = min(nq, t + tpt) - 1;
+                    return last < t ? 0 : (keys_seen(a.causal, last, nq, nk) + kTile - 1) / kTile;
                 };
-                const int t0 = blk * tokens;
-                const Block e = {q0, nq, k0, nk, t0, tiles_of(t0), tiles_of(t0 + tpt), 0};
-                reinterpret_cast<Block *>(a.workspace + L.list)[at] = e;
+                f(Block{q0, nq, k0, nk, t0, 0, tiles_of(t0), tiles_of(t0 + tpt), -1, 1, 0, 0});
             }
         }
+    };
+    auto bucket = [&](const Block &e) {  // fewest key tiles last
+        return kBuckets - 1 - min(kBuckets - 1, max(e.tiles0, e.tiles1));
+    };
+    // Blocks by their key tiles, if none is cut; all key tiles; the most.
+    unsigned long long mine_tiles = 0;
+    int longest_mine = 0;
+    blocks([&](const Block &e) {
+        const int tiles = max(e.tiles0, e.tiles1);
+        mine_tiles += tiles;
+        longest_mine = max(longest_mine, tiles);
+        atomicAdd(&count[bucket(e)], 1);
+    });
+    int most = kMinPart;
+    if (a.Tk > kMinPart * kTile) {
+        // A key range longer than a block's even share of everything is cut.
+        mine_tiles = warp_total(mine_tiles);
+        longest_mine = __reduce_max_sync(0xffffffffu, longest_mine);
+        if (lane == 0 && mine_tiles) {
+            atomicAdd(&all_tiles, mine_tiles);
+            atomicMax(&longest, longest_mine);
+        }
         __syncthreads();
-        if (pass) break;
-        // counts -> first places
-        const int mine = count[tid];
-        int scan = mine;
+        const unsigned long long share = (all_tiles * HV + n_blocks - 1) / n_blocks;
+        most = (int)min((unsigned long long)0x7fffff, max(share, (unsigned long long)kMinPart));
+    }
+    __syncthreads();
+    const bool cut = longest > most;
+    auto parts_of = [&](const Block &e) {
+        return cut ? max(1, (max(e.tiles0, e.tiles1) + most - 1) / most) : 1;
+    };
+    auto part = [&](const Block &e, int n, int p) {
+        if (n == 1) return e;
+        const int tiles = max(e.tiles0, e.tiles1);
+        Block x = e;
+        x.j0 = (int)((int64_t)tiles * p / n);
+        const int j1 = (int)((int64_t)tiles * (p + 1) / n);
+        x.tiles0 = max(0, min(j1, e.tiles0) - x.j0);
+        x.tiles1 = max(0, min(j1, e.tiles1) - x.j0);
+        x.parts = n;
+        x.part = p;
+        return x;
+    };
+    if (cut) {  // count again, by parts
+        count[tid] = 0;
+        __syncthreads();
+        blocks([&](const Block &e) {
+            const int n = parts_of(e);
+            for (int p = 0; p < n; ++p) atomicAdd(&count[bucket(part(e, n, p))], 1);
+        });
+        __syncthreads();
+    }
+    // counts -> first places
+    const int mine = count[tid];
+    int scan = mine;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, scan, o);
-            if (lane >= o) scan += v;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += v;
+    }
+    if (lane == 31) warp_sum[tid >> 5] = scan;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < tid >> 5; ++w) before += warp_sum[w];
+    count[tid] = before + scan - mine;
+    const int total = before + scan;  // (of the last thread: of all)
+    __syncthreads();
+    blocks([&](const Block &e) {
+        const int n = parts_of(e);
+        int slot = -1;
+        if (n > 1) {
+            slot = atomicAdd(&slots, n * HV);
+            const int at = atomicAdd(&joins, 1);
+            // (a block of T > most key tiles has n < 2 T / most parts, and
+            // most is at least all tiles / n_blocks: at most 2 n_blocks parts
+            // in all)
+            reinterpret_cast<Split *>(a.workspace + L.splits)[at] = Split{e.q0, e.nq, e.tok0, slot, n, {0, 0, 0}};
         }
-        if (lane == 31) warp_sum[tid >> 5] = scan;
-        __syncthreads();
-        int before = 0;
-        for (int w = 0; w < tid >> 5; ++w) before += warp_sum[w];
-        count[tid] = before + scan - mine;
-        if (tid == kPlanThreads - 1) {
-            PlanHead *h = reinterpret_cast<PlanHead *>(a.workspace + L.head);
-            h->items = (int)min((int64_t)(before + scan), room);
-            h->next = 0;
-            Ctrl *ctrl = reinterpret_cast<Ctrl *>(a.workspace);
-            ctrl->status = first_bad == 0x7fffffff ? MOE_OK : MOE_ERR_DEVICE_BAD_INDEX;
-            ctrl->detail = first_bad == 0x7fffffff ? 0 : first_bad;
+        for (int p = 0; p < n; ++p) {
+            Block x = part(e, n, p);
+            x.slot = slot;
+            const int at = atomicAdd(&count[bucket(x)], 1);
+            // (overlapping sequences may ask for more items than rows)
+            if (at < room) reinterpret_cast<Block *>(a.workspace + L.list)[at] = x;
         }
-        __syncthreads();
+    });
+    __syncthreads();
+    if (tid == kPlanThreads - 1) {
+        *reinterpret_cast<PlanHead *>(a.workspace + L.head) =
+            PlanHead{(int)min((int64_t)total, room), 0, joins, slots};
+        Ctrl *ctrl = reinterpret_cast<Ctrl *>(a.workspace);
+        ctrl->status = first_bad == 0x7fffffff ? MOE_OK : MOE_ERR_DEVICE_BAD_INDEX;
+        ctrl->detail = first_bad == 0x7fffffff ? 0 : first_bad;
     }
 }
 
@@ -253,7 +351,7 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
     // the copy and product instructions want their operands in uniform registers)
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int G = a.Hq / a.Hkv, Gt = tile_heads(G), tpt = tile_tokens(G);
-    const PrefillLayout L = prefill_layout(a.B, a.Tq, 2 * tpt);
+    const PrefillLayout L = prefill_layout(a.B, a.Tq, 2 * tpt, D);
     Ctrl *ctrl = reinterpret_cast<Ctrl *>(a.workspace);
 
     if (warp == kMmaWarp) tmem_alloc(&sm->tmem, 512);
@@ -302,11 +400,11 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
     };
     // A value tile whose rows past the sequence's end belong to others.
     auto ragged = [&](const Item &it, int j) {
-        return (j + 1) * kTile > it.b.nk && it.b.k0 + it.b.nk < a.Tk;
+        return (it.b.j0 + j + 1) * kTile > it.b.nk && it.b.k0 + it.b.nk < a.Tk;
     };
 
     if (warp >= kMmaWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRoleRegs));
         if (warp == kLoadWarp) {
             // ---------------- copies, and the items for everyone
             pdl_wait();
@@ -330,6 +428,7 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
                 it.hk = hv / HT;
                 it.h0 = it.hk * G + g0;
                 it.heads = min(Gt, G - g0);
+                it.slot = blk.slot < 0 ? -1 : blk.slot + hv * blk.parts + blk.part;
                 if (!warp_wait_flag(&sm->item_empty[n & 1], ((n >> 1) & 1) ^ 1, &sm->abort, 2)) break;
                 if (lane == 0) {
                     sm->item[n & 1] = it;
@@ -349,7 +448,7 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
                     if (lane == 0) {
                         uint64_t *bar = tail ? &sm->tail[s] : &sm->kv_full[s];
                         mbar_arrive_expect_tx(bar, C::kTileB);
-                        tma_load_4d(base + (2 + s) * C::kTileB, map, 0, it.b.k0 + j * kTile, it.hk, 0, bar);
+                        tma_load_4d(base + (2 + s) * C::kTileB, map, 0, it.b.k0 + (it.b.j0 + j) * kTile, it.hk, 0, bar);
                     }
                     __syncwarp();
                     ++kv;
@@ -525,7 +624,7 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
                 if (!warp_wait_flag(&sm->tail[s], (ph >> s) & 1, &sm->abort, 8)) break;
                 ph ^= 1u << s;
                 uint8_t *v = base + (2 + s) * C::kTileB;
-                const int from = it.b.nk - (tiles - 1) * kTile;
+                const int from = it.b.nk - (it.b.j0 + tiles - 1) * kTile;
                 for (int h = 0; h < kHalves; ++h)
                     for (int i = from * 8 + lane; i < kTile * 8; i += 32)
                         *reinterpret_cast<uint4 *>(v + h * kHalfB + i * 16) = make_uint4(0, 0, 0, 0);
@@ -536,7 +635,7 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
         }
     } else {
         // ---------------- softmax: warpgroup t has row tile t, a thread a row
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
         const int t = warp >> 2;
         const int r = threadIdx.x & 127;
         const uint32_t lane_base = (uint32_t)(warp & 3) * 32 << 16;
@@ -569,11 +668,12 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm->s_free[t]);
                 }
-                if ((j + 1) * kTile > least) {
-                    const int lim = limit - j * kTile;
+                const int key0 = (it.b.j0 + j) * kTile;
+                if (key0 + kTile > least) {
+                    const int lim = limit - key0;
 #pragma unroll
                     for (int c = 0; c < kTile; c += 32)
-                        if (j * kTile + c + 32 > least) {
+                        if (key0 + c + 32 > least) {
 #pragma unroll
                             for (int e = c; e < c + 32; ++e) x[e] = e < lim ? x[e] : -INFINITY;
                         }
@@ -646,6 +746,35 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
             // ---- the rows' outputs
             const float inv = 1.f / l;
             const bool none = l == 0.f;  // no key: zeros
+            if (it.slot >= 0) {  // one part of several: its sums as they are
+                if (tiles > 0) {
+                    ok = warp_wait_flag(&sm->o_done[t], ph ^ 1, &sm->abort, 11);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                float *to = reinterpret_cast<float *>(a.workspace + L.sums);
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    if (tiles > 0) {
+                        tmem_ld32(o_t + c, o);
+                        tc_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                    }
+                    if (live)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(to + part_at(it.slot, t, c + e, r, D)) =
+                                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+                if (live)
+                    reinterpret_cast<float2 *>(a.workspace + L.ml)[((size_t)it.slot * 2 + t) * kTile + r] =
+                        make_float2(ref, l);
+                tc_fence_before();
+                continue;
+            }
             // Four neighbouring lanes hand each other 16-byte pieces, so that
             // a store covers 64 bytes of each of 8 rows: this lane's rows are
             // then those of its four, its piece lane % 4.
@@ -711,6 +840,58 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
     }
 }
 
+// Joins the parts of cut key ranges: a thread has one row and 8 columns, a
+// warp 32 neighbouring rows; parts are added in order.
+template <int D>
+__global__ void __launch_bounds__(kTile) join_kernel(const PrefillArgs a, const int HT) {
+    pdl_wait();
+    const int G = a.Hq / a.Hkv, Gt = tile_heads(G), tpt = tile_tokens(G), HV = a.Hkv * HT;
+    const PrefillLayout L = prefill_layout(a.B, a.Tq, 2 * tpt, D);
+    const PlanHead head = *reinterpret_cast<const PlanHead *>(a.workspace + L.head);
+    const float2 *ml = reinterpret_cast<const float2 *>(a.workspace + L.ml);
+    const float *sums = reinterpret_cast<const float *>(a.workspace + L.sums);
+    const int r = threadIdx.x;
+    constexpr int kCols = D / 8;
+    const int64_t work = (int64_t)head.joins * HV * 2 * kCols;
+    for (int64_t w = blockIdx.x; w < work; w += gridDim.x) {
+        const int c = (int)(w % kCols) * 8, t = (int)(w / kCols) & 1;
+        const int64_t bh = w / (2 * kCols);
+        const Split sp = reinterpret_cast<const Split *>(a.workspace + L.splits)[bh / HV];
+        const int hv = (int)(bh % HV);
+        const int g = r % Gt, g0 = (hv % HT) * Gt;
+        const int tok = sp.tok0 + t * tpt + r / Gt;
+        if (r / Gt >= tpt || tok >= sp.nq || g >= min(Gt, G - g0)) continue;
+        const int slot = sp.slot + hv * sp.parts;
+        float top = -INFINITY;
+#pragma unroll 4
+        for (int p = 0; p < sp.parts; ++p)
+            top = fmaxf(top, ml[((size_t)(slot + p) * 2 + t) * kTile + r].x);
+        const float z = top == -INFINITY ? 0.f : top;
+        float sum = 0.f, o[8] = {};
+#pragma unroll 4
+        for (int p = 0; p < sp.parts; ++p) {
+            const float2 v = ml[((size_t)(slot + p) * 2 + t) * kTile + r];
+            const float4 x = *reinterpret_cast<const float4 *>(sums + part_at(slot + p, t, c, r, D));
+            const float4 y = *reinterpret_cast<const float4 *>(sums + part_at(slot + p, t, c + 4, r, D));
+            const float f = ex2(v.x - z);
+            if (f == 0.f && v.y == 0.f) continue;  // no key of this part
+            sum += f * v.y;
+            const float e[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = fmaf(f, e[i], o[i]);
+        }
+        const bool none = sum == 0.f;
+        const float inv = 1.f / sum;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = none ? 0.f : o[i] * inv;
+        const int h = (hv / HT) * G + g0 + g;
+        *reinterpret_cast<uint4 *>(a.out + (sp.q0 + tok) * a.out_stride + h * D + c) =
+            make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
+        if (a.lse && c == 0)
+            a.lse[(size_t)(sp.q0 + tok) * a.Hq + h] = none ? -INFINITY : (top + __log2f(sum)) * kLn2;
+    }
+}
+
 template <int D>
 cudaError_t run(const PrefillArgs &a, int sms, cudaStream_t s) {
     using C = Cfg<D>;
@@ -734,16 +915,20 @@ cudaError_t run(const PrefillArgs &a, int sms, cudaStream_t s) {
                                box, CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
     }
-    plan_kernel<<<1, kPlanThreads, 0, s>>>(a, tpt);
+    // (no key range is cut below this many keys: then no joins either)
+    const bool cuts = a.Tk > kMinPart * kTile;
+    const int64_t most = ((int64_t)a.Tq / (2 * tpt) + a.B) * a.Hkv * HT;
+    if (sms > kMaxSms) sms = kMaxSms;
+    const int grid = (int)(cuts || most > sms ? sms : most);
+    plan_kernel<<<1, kPlanThreads, 0, s>>>(a, tpt, a.Hkv * HT, grid);
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     auto fn = prefill_kernel<D>;
     static SmemOnce once;
     err = once.set(reinterpret_cast<const void *>(fn), C::kSmem);
     if (err != cudaSuccess) return err;
-    const int64_t most = ((int64_t)a.Tq / (2 * tpt) + a.B) * a.Hkv * HT;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
+    cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = s;
@@ -752,13 +937,21 @@ cudaError_t run(const PrefillArgs &a, int sms, cudaStream_t s) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fn, a, HT, mq, mk, mv);
+    err = cudaLaunchKernelEx(&cfg, fn, a, HT, mq, mk, mv);
+    if (err != cudaSuccess || !cuts) return err;
+    cudaLaunchConfig_t cj = {};
+    cj.gridDim = dim3(4 * sms);
+    cj.blockDim = dim3(kTile);
+    cj.stream = s;
+    cj.attrs = at;
+    cj.numAttrs = 1;
+    return cudaLaunchKernelEx(&cj, join_kernel<D>, a, HT);
 }
 
 }  // namespace
 
-size_t prefill_workspace(int B, int Tq, int Hq, int Hkv, int) {
-    return align_up(prefill_layout(B, Tq, 2 * tile_tokens(Hq / Hkv)).total, 256);
+size_t prefill_workspace(int B, int Tq, int Hq, int Hkv, int D) {
+    return align_up(prefill_layout(B, Tq, 2 * tile_tokens(Hq / Hkv), D).total, 256);
 }
 
 cudaError_t launch_attn_prefill(const PrefillArgs &a, cudaStream_t s) {

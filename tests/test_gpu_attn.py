@@ -219,6 +219,15 @@ def test_prefill(gpu, nq, nk, Hq, Hkv, D, causal):
     _prefill(nq, nk, Hq, Hkv, D, causal)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("nq,nk,Hq,Hkv,D", [
+    ([16], [15016], 16, 2, 128), ([1, 40, 3], [9000, 1030, 20011], 8, 2, 64),
+    ([3000], [2500], 2, 1, 64), ([700, 5], [700, 7003], 5, 1, 128), ([1], [30000], 1, 1, 128)])
+def test_prefill_few_rows_over_many_keys(gpu, nq, nk, Hq, Hkv, D, causal):
+    """Key ranges that are cut into parts and joined."""
+    _prefill(nq, nk, Hq, Hkv, D, causal, seed=8)
+
+
 def test_prefill_contiguous_rows_and_scales(gpu):
     _prefill([300, 17], [300, 400], 4, 2, 128, True, seed=2, scale=2.0, fused=False)
     _prefill([300, 17], [300, 400], 4, 2, 64, False, seed=3, scale=1e-6, fused=False)
@@ -239,6 +248,8 @@ def test_prefill_other_sequences_do_not_matter(gpu, D):
     edit.poisoned = {1}
     _prefill([100, 50, 77], [100, 50, 77], 4, 2, D, True, seed=5, edit=edit)
     _prefill([100, 50, 77], [100, 50, 77], 4, 2, D, False, seed=5, edit=edit)
+    # (key ranges in parts)
+    _prefill([100, 50, 7], [100, 50, 5007], 4, 2, D, True, seed=5, edit=edit)
 
 
 def test_prefill_extreme_scores(gpu):
