@@ -176,8 +176,8 @@ plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks
             }
         }
     };
-    auto bucket = [&](const Block &e) {  // fewest key tiles last
-        return kBuckets - 1 - min(kBuckets - 1, max(e.tiles0, e.tiles1));
+    auto bucket_of = [&](int tiles) {  // fewest key tiles last
+        return kBuckets - 1 - min(kBuckets - 1, tiles);
     };
     // Blocks by their key tiles, if none is cut; all key tiles; the most.
     unsigned long long mine_tiles = 0;
@@ -186,7 +186,7 @@ plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks
         const int tiles = max(e.tiles0, e.tiles1);
         mine_tiles += tiles;
         longest_mine = max(longest_mine, tiles);
-        atomicAdd(&count[bucket(e)], 1);
+        atomicAdd(&count[bucket_of(tiles)], 1);
     });
     int most = kMinPart;
     if (a.Tk > kMinPart * kTile) {
@@ -206,24 +206,15 @@ plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks
     auto parts_of = [&](const Block &e) {
         return cut ? max(1, (max(e.tiles0, e.tiles1) + most - 1) / most) : 1;
     };
-    auto part = [&](const Block &e, int n, int p) {
-        if (n == 1) return e;
-        const int tiles = max(e.tiles0, e.tiles1);
-        Block x = e;
-        x.j0 = (int)((int64_t)tiles * p / n);
-        const int j1 = (int)((int64_t)tiles * (p + 1) / n);
-        x.tiles0 = max(0, min(j1, e.tiles0) - x.j0);
-        x.tiles1 = max(0, min(j1, e.tiles1) - x.j0);
-        x.parts = n;
-        x.part = p;
-        return x;
-    };
     if (cut) {  // count again, by parts
         count[tid] = 0;
         __syncthreads();
         blocks([&](const Block &e) {
-            const int n = parts_of(e);
-            for (int p = 0; p < n; ++p) atomicAdd(&count[bucket(part(e, n, p))], 1);
+            // n parts: the first `longer` of base + 1 key tiles, the others of base
+            const int tiles = max(e.tiles0, e.tiles1), n = parts_of(e);
+            const int base = tiles / n, longer = tiles % n;
+            if (longer) atomicAdd(&count[bucket_of(base + 1)], longer);
+            atomicAdd(&count[bucket_of(base)], n - longer);
         });
         __syncthreads();
     }
@@ -253,10 +244,19 @@ plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks
             // in all)
             reinterpret_cast<Split *>(a.workspace + L.splits)[at] = Split{e.q0, e.nq, e.tok0, slot, n, {0, 0, 0}};
         }
+        const int tiles = max(e.tiles0, e.tiles1), base = tiles / n, longer = tiles % n;
+        const int at0 = longer ? atomicAdd(&count[bucket_of(base + 1)], longer) : 0;
+        const int at1 = atomicAdd(&count[bucket_of(base)], n - longer);
         for (int p = 0; p < n; ++p) {
-            Block x = part(e, n, p);
+            Block x = e;
+            x.j0 = p * base + min(p, longer);
+            const int j1 = x.j0 + base + (p < longer ? 1 : 0);
+            x.tiles0 = max(0, min(j1, e.tiles0) - x.j0);
+            x.tiles1 = max(0, min(j1, e.tiles1) - x.j0);
             x.slot = slot;
-            const int at = atomicAdd(&count[bucket(x)], 1);
+            x.parts = n;
+            x.part = p;
+            const int at = p < longer ? at0 + p : at1 + p - longer;
             // (overlapping sequences may ask for more items than rows)
             if (at < room) reinterpret_cast<Block *>(a.workspace + L.list)[at] = x;
         }
@@ -840,55 +840,88 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
     }
 }
 
-// Joins the parts of cut key ranges: a thread has one row and 8 columns, a
-// warp 32 neighbouring rows; parts are added in order.
+// Joins the parts of cut key ranges: a block takes 32 neighbouring rows and 8
+// columns, its warps every fourth part each, a lane a row; the warps' sums are
+// then added in order.
+constexpr int kJoinWarps = 4;
 template <int D>
-__global__ void __launch_bounds__(kTile) join_kernel(const PrefillArgs a, const int HT) {
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const PrefillArgs a, const int HT) {
+    __shared__ float shared[kJoinWarps][10][32];  // per warp: maximum, sum, 8 columns
     pdl_wait();
     const int G = a.Hq / a.Hkv, Gt = tile_heads(G), tpt = tile_tokens(G), HV = a.Hkv * HT;
     const PrefillLayout L = prefill_layout(a.B, a.Tq, 2 * tpt, D);
     const PlanHead head = *reinterpret_cast<const PlanHead *>(a.workspace + L.head);
     const float2 *ml = reinterpret_cast<const float2 *>(a.workspace + L.ml);
     const float *sums = reinterpret_cast<const float *>(a.workspace + L.sums);
-    const int r = threadIdx.x;
-    constexpr int kCols = D / 8;
-    const int64_t work = (int64_t)head.joins * HV * 2 * kCols;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kCols = D / 8, kRowGroups = kTile / 32;
+    const int64_t work = (int64_t)head.joins * HV * 2 * kRowGroups * kCols;
     for (int64_t w = blockIdx.x; w < work; w += gridDim.x) {
-        const int c = (int)(w % kCols) * 8, t = (int)(w / kCols) & 1;
-        const int64_t bh = w / (2 * kCols);
+        const int c = (int)(w % kCols) * 8, rg = (int)(w / kCols) % kRowGroups;
+        const int t = (int)(w / (kCols * kRowGroups)) & 1;
+        const int64_t bh = w / (2 * kCols * kRowGroups);
         const Split sp = reinterpret_cast<const Split *>(a.workspace + L.splits)[bh / HV];
         const int hv = (int)(bh % HV);
+        const int r = rg * 32 + lane;
         const int g = r % Gt, g0 = (hv % HT) * Gt;
         const int tok = sp.tok0 + t * tpt + r / Gt;
-        if (r / Gt >= tpt || tok >= sp.nq || g >= min(Gt, G - g0)) continue;
+        const bool live = r / Gt < tpt && tok < sp.nq && g < min(Gt, G - g0);
+        if (!__any_sync(0xffffffffu, live)) continue;  // (the same in all warps)
         const int slot = sp.slot + hv * sp.parts;
-        float top = -INFINITY;
-#pragma unroll 4
-        for (int p = 0; p < sp.parts; ++p)
-            top = fmaxf(top, ml[((size_t)(slot + p) * 2 + t) * kTile + r].x);
-        const float z = top == -INFINITY ? 0.f : top;
-        float sum = 0.f, o[8] = {};
-#pragma unroll 4
-        for (int p = 0; p < sp.parts; ++p) {
-            const float2 v = ml[((size_t)(slot + p) * 2 + t) * kTile + r];
-            const float4 x = *reinterpret_cast<const float4 *>(sums + part_at(slot + p, t, c, r, D));
-            const float4 y = *reinterpret_cast<const float4 *>(sums + part_at(slot + p, t, c + 4, r, D));
-            const float f = ex2(v.x - z);
-            if (f == 0.f && v.y == 0.f) continue;  // no key of this part
-            sum += f * v.y;
-            const float e[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        float top = -INFINITY, sum = 0.f, o[8] = {};
+        if (live) {
+#pragma unroll 8
+            for (int p = warp; p < sp.parts; p += kJoinWarps)
+                top = fmaxf(top, ml[((size_t)(slot + p) * 2 + t) * kTile + r].x);
+            const float z = top == -INFINITY ? 0.f : top;
+#pragma unroll 8
+            for (int p = warp; p < sp.parts; p += kJoinWarps) {
+                const float2 v = ml[((size_t)(slot + p) * 2 + t) * kTile + r];
+                const float4 x = *reinterpret_cast<const float4 *>(sums + part_at(slot + p, t, c, r, D));
+                const float4 y = *reinterpret_cast<const float4 *>(sums + part_at(slot + p, t, c + 4, r, D));
+                const float f = ex2(v.x - z);
+                const bool empty = v.x == -INFINITY && v.y == 0.f;  // no key of this part
+                const float e[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                sum = empty ? sum : fmaf(f, v.y, sum);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = fmaf(f, e[i], o[i]);
+                for (int i = 0; i < 8; ++i) o[i] = empty ? o[i] : fmaf(f, e[i], o[i]);
+            }
         }
-        const bool none = sum == 0.f;
-        const float inv = 1.f / sum;
+        shared[warp][0][lane] = top;
+        shared[warp][1][lane] = sum;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = none ? 0.f : o[i] * inv;
-        const int h = (hv / HT) * G + g0 + g;
-        *reinterpret_cast<uint4 *>(a.out + (sp.q0 + tok) * a.out_stride + h * D + c) =
-            make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
-        if (a.lse && c == 0)
-            a.lse[(size_t)(sp.q0 + tok) * a.Hq + h] = none ? -INFINITY : (top + __log2f(sum)) * kLn2;
+        for (int i = 0; i < 8; ++i) shared[warp][2 + i][lane] = o[i];
+        __syncthreads();
+        if (warp == 0 && live) {
+#pragma unroll
+            for (int k = 1; k < kJoinWarps; ++k) top = fmaxf(top, shared[k][0][lane]);
+            const float z = top == -INFINITY ? 0.f : top;
+            sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < kJoinWarps; ++k) {
+                const float m = shared[k][0][lane], f = m == -INFINITY ? 0.f : ex2(m - z);
+                // (a warp without a key has sums of 0; NaN has no maximum)
+                const float s1 = shared[k][1][lane];
+                sum += m == -INFINITY ? s1 : f * s1;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float e = shared[k][2 + i][lane];
+                    o[i] += m == -INFINITY ? e : f * e;
+                }
+            }
+            const bool none = sum == 0.f;
+            const float inv = 1.f / sum;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = none ? 0.f : o[i] * inv;
+            const int h = (hv / HT) * G + g0 + g;
+            *reinterpret_cast<uint4 *>(a.out + (sp.q0 + tok) * a.out_stride + h * D + c) =
+                make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
+            if (a.lse && c == 0)
+                a.lse[(size_t)(sp.q0 + tok) * a.Hq + h] = none ? -INFINITY : (top + __log2f(sum)) * kLn2;
+        }
+        __syncthreads();
     }
 }
 
@@ -940,8 +973,8 @@ cudaError_t run(const PrefillArgs &a, int sms, cudaStream_t s) {
     err = cudaLaunchKernelEx(&cfg, fn, a, HT, mq, mk, mv);
     if (err != cudaSuccess || !cuts) return err;
     cudaLaunchConfig_t cj = {};
-    cj.gridDim = dim3(4 * sms);
-    cj.blockDim = dim3(kTile);
+    cj.gridDim = dim3(16 * sms);
+    cj.blockDim = dim3(32 * kJoinWarps);
     cj.stream = s;
     cj.attrs = at;
     cj.numAttrs = 1;
