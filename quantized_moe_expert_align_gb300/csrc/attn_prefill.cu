@@ -40,7 +40,10 @@ constexpr int kThreads = 384;    // two softmax warpgroups, one of single-warp r
 constexpr int kMmaWarp = 8, kLoadWarp = 10, kFixWarp = 11;  // (product warps: 8 and 9)
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 1024;
-constexpr int kApart = 4;        // items of at least this many key tiles run their row tiles offset
+// Items of at least this many key tiles run their row tiles offset.  Twice as
+// many stages as the ring has at most: the first tile's roles then cannot
+// signal twice before the second's have looked once.
+constexpr int kApart = 4;
 constexpr float kSlack = 8.f;    // a row's maximum may exceed its reference by this
 
 constexpr int kMinPart = 8;      // key tiles below which a range is not cut
@@ -93,16 +96,15 @@ template <int D>
 struct Cfg {
     static constexpr int kTileB = kTile * D * 2;           // a Q, K or V tile
     static constexpr int kStages = D == 128 ? 5 : 8;
+    static_assert(kStages <= 2 * kApart, "see kApart");
     // Tensor memory (512 columns): S_t 2 x 128, O_t 2 x D.  Heads of 64 leave
     // 128 columns for the weights P_t, so that the next scores can be computed
     // as soon as S_t is in registers; heads of 128 put P_t over S_t.
     static constexpr bool kOwnP = D == 64;
     // The launch's 168 registers a thread, shared out anew (128 kRoleRegs +
-    // 256 kSoftmaxRegs = 384 x 168).  Measured both ways: 8192 causal tokens,
-    // 64 heads of 128, 656 -> 637 us with 104 / 200; chunks with heads of 64
-    // 245 us with 88 / 208, 259 with 104 / 200.
-    static constexpr int kRoleRegs = D == 128 ? 104 : 88;
-    static constexpr int kSoftmaxRegs = D == 128 ? 200 : 208;
+    // 256 kSoftmaxRegs = 384 x 168).
+    static constexpr int kRoleRegs = 72;
+    static constexpr int kSoftmaxRegs = 216;
     static_assert(128 * kRoleRegs + 256 * kSoftmaxRegs <= 384 * 168, "register split");
     static constexpr size_t kSmem = (size_t)(2 + kStages) * kTileB + 1024 + 1024;
     static_assert(kSmem > 114 * 1024, "one block per SM: all of tensor memory is its own");
@@ -371,7 +373,7 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
             mbar_init(&sm->kv_empty[i], 2);
             mbar_init(&sm->tail[i], 1);
         }
-        mbar_init(&sm->offset, 1);
+        mbar_init(&sm->offset, C::kOwnP ? 1 : 4);
         mbar_init(&sm->finished, 2);
         fence_barrier_init();
         sm->abort = 0;
@@ -568,9 +570,13 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
                 ok = ok && warp_wait_flag(&sm->q_full[t], n & 1, &sm->abort, 6);
                 if (!ok) break;
                 tc_fence_after();
-                // The second tile starts half a softmax behind the first: two
-                // tiles in step would want the tensor pipe, and then the
-                // exponentials, at the same time.
+                // The second tile starts behind the first: two tiles in step
+                // would want the tensor pipe, and then the exponentials, at
+                // the same time.  Heads of 128: once the first tile's maxima
+                // are known, which puts the two half a round apart (8192
+                // causal tokens, 64 heads: 606 us, 640 us with the signal
+                // below, 656 in step); heads of 64: once the first half of
+                // its weights is (455, 483 us the other way, 484).
                 const bool apart = min(n0, n1) >= kApart;
                 if (apart && t == 1) {
                     ok = warp_wait_flag(&sm->offset, off_ph, &sm->abort, 13);
@@ -598,7 +604,7 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
                     const uint32_t v = next_stage();
                     if (!ok) break;
                     if (j < nt)
-                        pv(v, j == 0, j == 0 && apart && t == 0);
+                        pv(v, j == 0, C::kOwnP && j == 0 && apart && t == 0);
                     else
                         commit(&sm->kv_empty[v]);
                     if (!C::kOwnP && ok) next_scores(j);
@@ -644,6 +650,10 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
         const int tok_r = r / Gt, g = r % Gt;
         const float sl = a.scale * kLog2e;
         uint32_t ph = 0;  // parity of this warpgroup's count of key tiles
+        // A wait costs about 200 cycles even when its phase is over.  Where the
+        // phases usually are (heads of 64), they are tested ahead, and the
+        // answer used when it has come.
+        bool s_seen = false, o_seen = false;
         Item it;
         bool ok = true;
         for (uint32_t n = 0; ok && take(n, it); ++n) {
@@ -656,8 +666,10 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
             float l = 0.f;
             const int tiles = t ? it.b.tiles1 : it.b.tiles0;
             for (int j = 0; j < tiles; ++j) {
-                ok = warp_wait_flag(&sm->s_full[t], ph, &sm->abort, 9);
-                if (!ok) break;
+                if (!C::kOwnP || !__all_sync(0xffffffffu, s_seen)) {
+                    ok = warp_wait_flag(&sm->s_full[t], ph, &sm->abort, 9);
+                    if (!ok) break;
+                }
                 tc_fence_after();
                 float x[kTile];
 #pragma unroll
@@ -667,6 +679,7 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm->s_free[t]);
+                    o_seen = mbar_test_wait(&sm->o_done[t], ph ^ 1);
                 }
                 const int key0 = (it.b.j0 + j) * kTile;
                 if (key0 + kTile > least) {
@@ -711,11 +724,14 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
                         }
                     }
                 }
-                if (!over) {  // the last product with P_t has to be over
+                // the last product with P_t has to be over
+                if (!over && !__all_sync(0xffffffffu, o_seen)) {
                     ok = warp_wait_flag(&sm->o_done[t], ph ^ 1, &sm->abort, 10);
                     if (!ok) break;
-                    tc_fence_after();
                 }
+                if (C::kOwnP) tc_fence_after();
+                if (!C::kOwnP && t == 0 && j == 0 && min(it.b.tiles0, it.b.tiles1) >= kApart && lane == 0)
+                    mbar_arrive(&sm->offset);
                 const float z = ref == -INFINITY ? 0.f : ref;
                 const float2 sl2 = make_float2(sl, sl), nz2 = make_float2(-z, -z);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -730,6 +746,7 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
                         sum[e & 1] = add2(sum[e & 1], y);
                         p[e] = pack_bf16(y.x, y.y);
                     }
+                    if (C::kOwnP && c + 32 == kTile) s_seen = mbar_test_wait(&sm->s_full[t], ph ^ 1);
                     tmem_st16(p_t + c / 2, p);
                     if (c % kHalf) {  // half of the weights: their product may start
                         tc_wait_st();
