@@ -122,9 +122,13 @@ size_t moe_attn_decode_workspace_size(int B, int Hq, int Hkv, int D);
  * Results do not depend on timing: keys are split over the GPU by the
  * lengths alone and the parts are joined in a fixed order.
  * Limits: 0 <= B <= 65535, Hq <= 1024, scale > 0.
- * A page number out of range, a negative length or one beyond the table
- * reports MOE_ERR_DEVICE_BAD_INDEX (detail: such a sequence), and that
- * sequence's output is undefined.
+ * A page number out of range, a negative length or one beyond the table (or
+ * 2^30) reports MOE_ERR_DEVICE_BAD_INDEX (detail: the first such sequence),
+ * and that sequence's output is undefined.
+ * For testing the failure path only, MOE_ATTN_TEST_NO_COPIES=1 (read once per
+ * process) makes this call and moe_attn_prefill issue no copies: their
+ * bounded waits give up after about a second, the call reports
+ * MOE_ERR_DEVICE_TIMEOUT (detail: the role) and its output is undefined.
  */
 moe_status_t moe_attn_decode(const uint16_t *q, int64_t q_stride, const moe_kv_cache_t *cache,
                              const int32_t *page_table, int table_stride, const int32_t *seq_lens,

@@ -77,6 +77,7 @@ struct DecodeAttnArgs {
     float *lse;
     int B, Hq;
     uint8_t *workspace;
+    int test_no_copies;  // failure-path test: the kernel issues no copies
 };
 size_t decode_attn_workspace(int B, int Hq, int Hkv, int D);
 cudaError_t launch_attn_decode(const DecodeAttnArgs &a, cudaStream_t s);
@@ -91,6 +92,7 @@ struct PrefillArgs {
     int64_t out_stride;
     float *lse;
     uint8_t *workspace;
+    int test_no_copies;  // failure-path test: the kernel issues no copies
 };
 size_t prefill_workspace(int B, int Tq, int Hq, int Hkv, int D);
 cudaError_t launch_attn_prefill(const PrefillArgs &a, cudaStream_t s);

@@ -2,6 +2,7 @@
 // launches.
 #include <climits>
 #include <cmath>
+#include <cstdlib>
 
 #include "attn.h"
 
@@ -52,6 +53,15 @@ moe_status_t launched(cudaError_t e) {
     if (e == cudaSuccess) return MOE_OK;
     cudaGetLastError();
     return MOE_ERR_CUDA;
+}
+
+// Failure-path test switch, read once per process.
+int test_no_copies() {
+    static const int v = [] {
+        const char *e = std::getenv("MOE_ATTN_TEST_NO_COPIES");
+        return e && std::atoi(e) != 0 ? 1 : 0;
+    }();
+    return v;
 }
 
 cudaStream_t stream_of(moe_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
@@ -186,7 +196,7 @@ moe_status_t moe_attn_decode(const uint16_t *q, int64_t q_stride, const moe_kv_c
     if (B == 0) return launched(cudaMemsetAsync(workspace, 0, sizeof(Ctrl), stream_of(stream)));
     const DecodeAttnArgs a = {q,        q_stride, view_of(cache), cache->type, cache->D, page_table,
                               table_stride, seq_lens, scale, out, out_stride, lse, B, Hq,
-                              static_cast<uint8_t *>(workspace)};
+                              static_cast<uint8_t *>(workspace), test_no_copies()};
     return launched(launch_attn_decode(a, stream_of(stream)));
 }
 
@@ -220,7 +230,7 @@ moe_status_t moe_attn_prefill(const uint16_t *q, int64_t q_stride, const uint16_
         return launched(cudaMemsetAsync(workspace, 0, sizeof(Ctrl), stream_of(stream)));
     const PrefillArgs a = {q,  k,  v,  q_stride, k_stride, v_stride, cu_q,  cu_k, B,   Tq,
                            Tk, Hq, Hkv, D,       causal != 0, scale, out, out_stride, lse,
-                           static_cast<uint8_t *>(workspace)};
+                           static_cast<uint8_t *>(workspace), test_no_copies()};
     return launched(launch_attn_prefill(a, stream_of(stream)));
 }
 

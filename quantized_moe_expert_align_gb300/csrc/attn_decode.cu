@@ -94,7 +94,7 @@ struct Walk {
 };
 
 __device__ __forceinline__ int keys_of(const DecodeAttnArgs &a, int b) {
-    const int64_t most = (int64_t)a.table_stride << a.kv.page_shift;
+    const int64_t most = min((int64_t)a.table_stride << a.kv.page_shift, (int64_t)1 << 30);
     const int n = __ldg(a.seq_lens + b);
     return n < 0 ? 0 : (n > most ? (int)most : n);
 }
@@ -232,7 +232,7 @@ decode_kernel(const DecodeAttnArgs a, const int HV, const int RT, const __grid_c
             int64_t done = 0;
             int pg = page_of(w);
             bool fresh = true;  // the first unit of a pair (or of the block)
-            for (int64_t u = u0; u < u1; ++u) {
+            for (int64_t u = u0; u < u1 && !a.test_no_copies; ++u) {
                 const Walk x = w;
                 const int my = pg;
                 const bool with_q = fresh;

@@ -455,7 +455,7 @@ prefill_kernel(const PrefillArgs a, const int HT, const __grid_constant__ CUtens
                     __syncwarp();
                     ++kv;
                 };
-                for (int j = 0; j < tiles && ok; ++j) {
+                for (int j = 0; j < tiles && ok && !a.test_no_copies; ++j) {
                     if (!C::kOwnP || j == 0) copy_kv(&map_k, j, false);
                     if (j == 0) {
                         for (int t = 0; t < 2 && ok; ++t) {

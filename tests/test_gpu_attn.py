@@ -338,3 +338,54 @@ def test_python_refusals(gpu):
         moe.attn_prefill(q, q[:, :3], q[:, :3], lens, lens, workspace=small)
     with pytest.raises(ValueError):
         moe.KVCache(torch.zeros(2, 2, 2, 16, 64, device="cuda"))
+
+
+# ---------------------------------------------------------------- bounded waits
+_STALL_CHILD = r"""
+import json, sys, time
+sys.path.insert(0, sys.argv[1])
+import torch
+import quantized_moe_expert_align_gb300 as moe
+from tests import attn_util as au
+res = []
+for D in (64, 128):
+    for fp8 in (False, True):
+        cache = au.make_cache(1, 40, 2, 16, D, fp8)
+        ws = moe.AttnWorkspace("cuda", "decode", 2, 2, 8, 2, D)
+        table = au.make_table(2, [300, 40], 16, 40, 0)
+        t0 = time.time()
+        moe.attn_decode(au.randn(3, 2, 8, D), cache, table,
+                        torch.tensor([300, 40], dtype=torch.int32, device="cuda"), workspace=ws)
+        res.append([*au.status(ws), time.time() - t0])
+    ws = moe.AttnWorkspace("cuda", "prefill", 2, 700, 8, 2, D)
+    q, k = au.randn(4, 700, 8, D), au.randn(5, 700, 2, D)
+    cu = torch.tensor([0, 650, 700], dtype=torch.int32, device="cuda")
+    t0 = time.time()
+    moe.attn_prefill(q, k, k, cu, cu, workspace=ws)
+    res.append([*au.status(ws), time.time() - t0])
+# the context is still usable afterwards
+y = (torch.arange(1024, device="cuda", dtype=torch.float32) * 2).sum().item()
+print(json.dumps({"res": res, "y": y}))
+"""
+
+
+def test_bounded_waits_run_out(gpu):
+    """With the failure-path switch the kernels issue no copies: their waits
+    give up after about a second, the status word says so, the kernels wind
+    down and the context stays usable.  The switch is read once per process,
+    so in a child."""
+    import json
+    import os
+    import subprocess
+    import sys
+
+    import quantized_moe_expert_align_gb300 as moe
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _STALL_CHILD, root],
+                       env=dict(os.environ, MOE_ATTN_TEST_NO_COPIES="1"), capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    out = json.loads(r.stdout.strip().splitlines()[-1])
+    assert out["y"] == float(sum(2 * i for i in range(1024)))
+    for st, detail, secs in out["res"]:
+        assert st == moe.MOE_ERR_DEVICE_TIMEOUT and detail >= 1 and secs < 30
