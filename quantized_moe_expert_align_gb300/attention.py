@@ -17,13 +17,16 @@ import math
 
 import quantized_moe_expert_align_gb300 as _moe
 
-torch = None  # bound by the first call: importing this package does not import it
+# Bound by the first call: importing this package does not import torch.
+torch = _BF16 = _I32 = _F32 = _raw_stream = None
 
 
 def _need_torch():
-    global torch
+    global torch, _BF16, _I32, _F32, _raw_stream
     if torch is None:
         import torch as t
+        _BF16, _I32, _F32 = t.bfloat16, t.int32, t.float32
+        _raw_stream = t._C._cuda_getCurrentRawStream
         torch = t
 
 MOE_KV_BF16 = 0
@@ -144,14 +147,14 @@ class AttnWorkspace:
 
 
 def _bf16(t, name, n):
-    if t.dtype != torch.bfloat16 or t.shape != (n,) or not t.is_contiguous() or not t.is_cuda:
+    if t.dtype is not _BF16 or t.shape != (n,) or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name}: contiguous bfloat16 {(n,)} on a GPU expected, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
 
 
 def _rows(t, name, T, H, D):
     """Checks rows [T][H][D] with contiguous heads; the stride between tokens."""
-    if t.dtype != torch.bfloat16 or t.shape != (T, H, D) or not t.is_cuda:
+    if t.dtype is not _BF16 or t.shape != (T, H, D) or not t.is_cuda:
         raise ValueError(f"{name}: bfloat16 {(T, H, D)} on a GPU expected, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     st = t.stride()
@@ -161,7 +164,7 @@ def _rows(t, name, T, H, D):
 
 
 def _i32(t, name, shape):
-    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+    if t.dtype is not _I32 or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name}: contiguous int32 {shape} on a GPU expected, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
 
@@ -174,7 +177,7 @@ def _on(stream, t):
     """The stream handle of a call: the current stream of t's device unless
     ``stream`` (a torch stream or a handle) is given."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
+        return _raw_stream(t.get_device())
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -205,13 +208,14 @@ def qk_rope_append(q, k, v, cos_sin, positions, cache, slots, q_norm=None, k_nor
     [T][Hkv][D], cos_sin [max_pos][rot] (None: no rotation), positions and
     slots [T] int32, cache a KVCache or None.  Returns q_out; ``k_out`` True
     or a tensor also returns the rotated keys, as (q_out, k_out)."""
-    _need_torch()
+    if torch is None:
+        _need_torch()
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     sq, sk, sv = _rows(q, "q", T, Hq, D), _rows(k, "k", T, Hkv, D), _rows(v, "v", T, Hkv, D)
     max_pos, rot = cos_sin.shape if cos_sin is not None else (0, 0)
     if rot:
-        if cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous() or not cos_sin.is_cuda:
+        if cos_sin.dtype is not _F32 or not cos_sin.is_contiguous() or not cos_sin.is_cuda:
             raise ValueError("cos_sin: contiguous float32 [max_pos][rot] on a GPU expected")
         _i32(positions, "positions", (T,))
     for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
@@ -226,7 +230,7 @@ def qk_rope_append(q, k, v, cos_sin, positions, cache, slots, q_norm=None, k_nor
     sqo = _rows(q_out, "q_out", T, Hq, D)
     sko = _rows(k_out, "k_out", T, Hkv, D) if k_out is not None else 0
     ws = _workspace(workspace, stream, q.device)
-    _moe._check(_moe.load().moe_qk_rope_append(
+    _moe._check((_moe._lib or _moe.load()).moe_qk_rope_append(
         _p(q), sq, _p(k), sk, _p(v), sv, _p(q_norm), _p(k_norm), eps, _p(cos_sin), max_pos, rot,
         int(interleaved), _p(positions) if rot else None, _p(slots) if cache is not None else None,
         _p(q_out), sqo, _p(k_out), sko, cache._ref if cache is not None else None, T, Hq, Hkv, D,
@@ -237,7 +241,8 @@ def qk_rope_append(q, k, v, cos_sin, positions, cache, slots, q_norm=None, k_nor
 def kv_gather(cache, page_table, cu_k, total, k_out=None, v_out=None, workspace=None, stream=None):
     """The cached tokens of B sequences as packed bf16 (k, v)
     [total][Hkv][D]; page_table [B][n] and cu_k [B+1] int32."""
-    _need_torch()
+    if torch is None:
+        _need_torch()
     B, n = page_table.shape
     _i32(page_table, "page_table", (B, n))
     _i32(cu_k, "cu_k", (B + 1,))
@@ -247,7 +252,7 @@ def kv_gather(cache, page_table, cu_k, total, k_out=None, v_out=None, workspace=
     if v_out is None:
         v_out = _rows_out(*shape, page_table.device, stream)
     ws = _workspace(workspace, stream, page_table.device)
-    _moe._check(_moe.load().moe_kv_gather(
+    _moe._check((_moe._lib or _moe.load()).moe_kv_gather(
         cache._ref, _p(page_table), n, _p(cu_k), B, total, _p(k_out),
         _rows(k_out, "k_out", *shape), _p(v_out), _rows(v_out, "v_out", *shape), ws._ptr,
         ws.nbytes, _on(stream, page_table)), "moe_kv_gather")
@@ -260,7 +265,8 @@ def attn_decode(q, cache, page_table, seq_lens, scale=None, out=None, lse=None, 
     q [B][Hq][D], page_table [B][n] and seq_lens [B] int32; scale defaults to
     D^-1/2.  Returns out [B][Hq][D]; ``lse`` True or a float32 [B][Hq] tensor
     also returns the logsumexp, as (out, lse)."""
-    _need_torch()
+    if torch is None:
+        _need_torch()
     B, Hq, D = q.shape
     if D != cache.D:
         raise ValueError(f"q has heads of {D}, the cache of {cache.D}")
@@ -273,7 +279,7 @@ def attn_decode(q, cache, page_table, seq_lens, scale=None, out=None, lse=None, 
     so = _rows(out, "out", B, Hq, D)
     lse = _lse(lse, B, Hq, q.device, stream)
     ws = _workspace(workspace, stream, q.device, "decode", B, B, Hq, cache.Hkv, D)
-    _moe._check(_moe.load().moe_attn_decode(
+    _moe._check((_moe._lib or _moe.load()).moe_attn_decode(
         _p(q), sq, cache._ref, _p(page_table), n, _p(seq_lens), D ** -0.5 if scale is None else scale,
         _p(out), so, _p(lse), B, Hq, ws._ptr, ws.nbytes, _on(stream, q)), "moe_attn_decode")
     return out if lse is None else (out, lse)
@@ -285,7 +291,8 @@ def attn_prefill(q, k, v, cu_q, cu_k, causal=True, scale=None, out=None, lse=Non
     cu_q and cu_k [B+1] int32; the last query of a sequence stands at its last
     key.  Returns out [Tq][Hq][D]; ``lse`` True or a float32 [Tq][Hq] tensor
     also returns the logsumexp, as (out, lse)."""
-    _need_torch()
+    if torch is None:
+        _need_torch()
     Tq, Hq, D = q.shape
     Tk, Hkv, _ = k.shape
     B = cu_q.shape[0] - 1
@@ -297,7 +304,7 @@ def attn_prefill(q, k, v, cu_q, cu_k, causal=True, scale=None, out=None, lse=Non
     so = _rows(out, "out", Tq, Hq, D)
     lse = _lse(lse, Tq, Hq, q.device, stream)
     ws = _workspace(workspace, stream, q.device, "prefill", B, Tq, Hq, Hkv, D)
-    _moe._check(_moe.load().moe_attn_prefill(
+    _moe._check((_moe._lib or _moe.load()).moe_attn_prefill(
         _p(q), sq, _p(k), sk, _p(v), sv, _p(cu_q), _p(cu_k), B, Tq, Tk, Hq, Hkv, D, int(causal),
         D ** -0.5 if scale is None else scale, _p(out), so, _p(lse), ws._ptr, ws.nbytes,
         _on(stream, q)), "moe_attn_prefill")
