@@ -24,7 +24,7 @@
 // blocks take them from a counter, longest first.  Where a few items have
 // more key tiles than an SM's even share of the whole work, they are cut into
 // parts, whose unscaled sums a last kernel joins in order.  Small calls (at
-// most 32 sequences and kMinPart key tiles in all, where nothing is cut) do
+// most 32 sequences and kMinKeys keys in all, where nothing is cut) do
 // without the plan: every block finds its own items.
 #include <type_traits>
 
@@ -36,19 +36,14 @@ namespace {
 
 using namespace attn;
 
-constexpr int kTile = 128;       // rows of a tile, keys of a key tile
-constexpr int kHalf = kTile / 2;
-constexpr int kThreads = 384;    // two softmax warpgroups, one of single-warp roles
-constexpr int kMmaWarp = 8, kLoadWarp = 10, kFixWarp = 11;  // (product warps: 8 and 9)
+constexpr int kTile = 128;       // rows of a row tile
+constexpr int kM = 2;            // row tiles of an item
+constexpr int kKeys = 128;       // keys of a key tile
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 1024;
-// Items of at least this many key tiles run their row tiles offset.  Twice as
-// many stages as the ring has at most: the first tile's roles then cannot
-// signal twice before the second's have looked once.
-constexpr int kApart = 4;
 constexpr float kSlack = 8.f;    // a row's maximum may exceed its reference by this
 
-constexpr int kMinPart = 8;      // key tiles below which a range is not cut
+constexpr int kMinKeys = 1024;   // a key range is not cut below this
 constexpr int kMaxSms = 160;     // blocks of the main kernel at most
 constexpr int kMaxParts = 2 * kMaxSms;  // of one call, all heads together
 
@@ -56,8 +51,8 @@ struct PlanHead {
     int32_t items, next;   // (block, part) pairs; the next item to take
     int32_t joins, slots;  // blocks in parts; places for parts
 };
-// One sequence's block of 256 rows for every head (what does not depend on
-// the head), or one part of its keys.
+// One sequence's block of rows for every head (what does not depend on the
+// head), or one part of its keys.
 struct __align__(16) Block {
     int32_t q0, nq, k0, nk;   // rows of the sequence
     int32_t tok0;             // the block's first token within the sequence
@@ -72,8 +67,7 @@ struct PrefillLayout {
     size_t ctrl, head, list, splits, ml, sums, total;
 };
 // Every sequence has at most one partly filled block; parts beyond a block's
-// first add up to at most kMaxSms.  The joined parts' places only exist where
-// there are more than kMinPart key tiles (unknown here: always counted).
+// first add up to at most kMaxSms.
 __host__ __device__ inline PrefillLayout prefill_layout(int B, int Tq, int tokens, int D) {
     PrefillLayout l;
     l.ctrl = 0;
@@ -81,34 +75,45 @@ __host__ __device__ inline PrefillLayout prefill_layout(int B, int Tq, int token
     l.list = 512;
     l.splits = l.list + ((size_t)Tq / tokens + B + kMaxSms) * sizeof(Block);
     l.ml = l.splits + kMaxParts * sizeof(Split);
-    l.sums = (l.ml + (size_t)kMaxParts * 2 * kTile * 8 + 255) / 256 * 256;
-    l.total = l.sums + (size_t)kMaxParts * 2 * kTile * D * 4;
+    const size_t rows = (size_t)kMaxParts * kM * kTile;
+    l.sums = (l.ml + rows * 8 + 255) / 256 * 256;
+    l.total = l.sums + rows * D * 4;
     return l;
 }
 // Place of a part's four columns c .. c + 3 of row r of row tile t: rows are
 // neighbours, so a warp's stores and loads are whole lines.
 __host__ __device__ inline size_t part_at(int slot, int t, int c, int r, int D) {
-    return ((((size_t)slot * 2 + t) * (D / 4) + c / 4) * kTile + r) * 4;
+    return ((((size_t)slot * kM + t) * (D / 4) + c / 4) * kTile + r) * 4;
 }
 // Query heads of a row tile and tokens of a row tile, for groups of G heads.
 __host__ __device__ inline int tile_heads(int G) { return G < kTile ? G : kTile; }
 __host__ __device__ inline int tile_tokens(int G) { return kTile / tile_heads(G); }
 
+constexpr int kParts = 2;        // in which a key tile's weights come
+// Warps: two softmax warpgroups, one warp per row tile issuing products, one
+// copying, one clearing.
+constexpr int kMmaWarp = 4 * kM, kLoadWarp = 5 * kM, kFixWarp = 5 * kM + 1;
+constexpr int kThreads = 32 * (5 * kM + 2);
+// The launch's 168 registers a thread, shared out anew.
+constexpr int kRoleRegs = 72, kSoftmaxRegs = 216;
+static_assert(128 * kRoleRegs + 256 * kSoftmaxRegs <= 384 * 168, "register split");
+// Items of at least this many key tiles run their row tiles offset.  The first
+// tile's roles cannot signal twice before the second's have looked once: an
+// item of kApart key tiles fills the ring of stages.
+constexpr int kApart = 4;
+
 template <int D>
 struct Cfg {
-    static constexpr int kTileB = kTile * D * 2;           // a Q, K or V tile
+    static constexpr int kQB = kTile * D * 2, kKvB = kKeys * D * 2;  // a Q tile, a K or V tile
     static constexpr int kStages = D == 128 ? 5 : 8;
     static_assert(kStages <= 2 * kApart, "see kApart");
     // Tensor memory (512 columns): S_t 2 x 128, O_t 2 x D.  Heads of 64 leave
     // 128 columns for the weights P_t, so that the next scores can be computed
-    // as soon as S_t is in registers; heads of 128 put P_t over S_t.
+    // as soon as S_t is in registers; heads of 128 put P_t over S_t.  (Heads
+    // of 64 as three row tiles against key tiles of 64, for more warps to hide
+    // the softmax's latencies: 205 us instead of 148, 2432 rows over 4096 keys.)
     static constexpr bool kOwnP = D == 64;
-    // The launch's 168 registers a thread, shared out anew (128 kRoleRegs +
-    // 256 kSoftmaxRegs = 384 x 168).
-    static constexpr int kRoleRegs = 72;
-    static constexpr int kSoftmaxRegs = 216;
-    static_assert(128 * kRoleRegs + 256 * kSoftmaxRegs <= 384 * 168, "register split");
-    static constexpr size_t kSmem = (size_t)(2 + kStages) * kTileB + 1024 + 1024;
+    static constexpr size_t kSmem = (size_t)kM * kQB + kStages * kKvB + 1024 + 1024;
     static_assert(kSmem > 114 * 1024, "one block per SM: all of tensor memory is its own");
 };
 
@@ -121,9 +126,10 @@ struct Item {
 };
 
 struct Shared {
-    uint64_t q_full[2], q_empty[2], kv_full[8], kv_empty[8], s_full[2], s_free[2];
-    uint64_t p_ready[2][2], o_done[2];  // p_ready: [row tile][half of the key tile]
-    uint64_t item_full[2], item_empty[2], tail[8], offset, finished;
+    uint64_t q_full[kM], q_empty[kM], kv_full[8], kv_empty[8], tail[8], s_full[kM], s_free[kM];
+    uint64_t p_ready[kM][kParts], o_done[kM];
+    uint64_t offset;            // the second row tile may start
+    uint64_t item_full[2], item_empty[2], finished;
     uint32_t tmem;
     int abort;
     Item item[2];
@@ -144,10 +150,13 @@ __device__ __forceinline__ int keys_seen(int causal, int tok, int nq, int nk) {
 __device__ __forceinline__ Block block_at(int causal, int q0, int nq, int k0, int nk, int t0, int tpt) {
     auto tiles_of = [&](int t) {  // of the row tile from token t on
         const int last = min(nq, t + tpt) - 1;
-        return last < t ? 0 : (keys_seen(causal, last, nq, nk) + kTile - 1) / kTile;
+        return last < t ? 0 : (keys_seen(causal, last, nq, nk) + kKeys - 1) / kKeys;
     };
     return Block{q0, nq, k0, nk, t0, 0, tiles_of(t0), tiles_of(t0 + tpt), -1, 1, 0, 0};
 }
+__device__ __forceinline__ int most_tiles(const Block &b) { return max(b.tiles0, b.tiles1); }
+__device__ __forceinline__ int tiles_at(const Block &b, int t) { return t == 0 ? b.tiles0 : b.tiles1; }
+__device__ __forceinline__ bool run_apart(const Block &b) { return min(b.tiles0, b.tiles1) >= kApart; }
 
 // ------------------------------------------------------------------- planning
 __device__ __forceinline__ unsigned long long warp_total(unsigned long long v) {
@@ -159,7 +168,8 @@ __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks) {
     __shared__ int count[kBuckets], warp_sum[kPlanThreads / 32], first_bad, joins, slots, longest;
     __shared__ unsigned long long all_tiles;
-    const int tokens = 2 * tpt;  // of a block
+    const int tokens = kM * tpt;  // of a block
+    constexpr int kMinPart = kMinKeys / kKeys;
     const PrefillLayout L = prefill_layout(a.B, a.Tq, tokens, a.D);
     const int tid = threadIdx.x, lane = tid & 31;
     pdl_trigger();
@@ -191,13 +201,13 @@ plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks
     unsigned long long mine_tiles = 0;
     int longest_mine = 0;
     blocks([&](const Block &e) {
-        const int tiles = max(e.tiles0, e.tiles1);
+        const int tiles = most_tiles(e);
         mine_tiles += tiles;
         longest_mine = max(longest_mine, tiles);
         atomicAdd(&count[bucket_of(tiles)], 1);
     });
     int most = kMinPart;
-    if (a.Tk > kMinPart * kTile) {
+    if (a.Tk > kMinKeys) {
         // A key range longer than a block's even share of everything is cut.
         mine_tiles = warp_total(mine_tiles);
         longest_mine = __reduce_max_sync(0xffffffffu, longest_mine);
@@ -212,14 +222,14 @@ plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks
     __syncthreads();
     const bool cut = longest > most;
     auto parts_of = [&](const Block &e) {
-        return cut ? max(1, (max(e.tiles0, e.tiles1) + most - 1) / most) : 1;
+        return cut ? max(1, (most_tiles(e) + most - 1) / most) : 1;
     };
     if (cut) {  // count again, by parts
         count[tid] = 0;
         __syncthreads();
         blocks([&](const Block &e) {
             // n parts: the first `longer` of base + 1 key tiles, the others of base
-            const int tiles = max(e.tiles0, e.tiles1), n = parts_of(e);
+            const int tiles = most_tiles(e), n = parts_of(e);
             const int base = tiles / n, longer = tiles % n;
             if (longer) atomicAdd(&count[bucket_of(base + 1)], longer);
             atomicAdd(&count[bucket_of(base)], n - longer);
@@ -252,7 +262,7 @@ plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks
             // in all)
             reinterpret_cast<Split *>(a.workspace + L.splits)[at] = Split{e.q0, e.nq, e.tok0, slot, n, {0, 0, 0}};
         }
-        const int tiles = max(e.tiles0, e.tiles1), base = tiles / n, longer = tiles % n;
+        const int tiles = most_tiles(e), base = tiles / n, longer = tiles % n;
         const int at0 = longer ? atomicAdd(&count[bucket_of(base + 1)], longer) : 0;
         const int at1 = atomicAdd(&count[bucket_of(base)], n - longer);
         for (int p = 0; p < n; ++p) {
@@ -349,38 +359,41 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
     using C = Cfg<D>;
     constexpr int S = C::kStages;
     constexpr int kHalves = D / 64;
-    constexpr uint32_t kHalfB = kTile * 128;
+    constexpr uint32_t kQHalf = kTile * 128, kKvHalf = kKeys * 128;  // 64 columns of a tile
     extern __shared__ uint8_t raw[];
     const uint32_t raw_u = smem_u32(raw);
     uint8_t *base = raw + ((1024 - (raw_u & 1023)) & 1023);
-    const uint32_t q_smem = smem_u32(base), kv_smem = q_smem + 2 * C::kTileB;
-    Shared *sm = reinterpret_cast<Shared *>(base + (size_t)(2 + S) * C::kTileB);
+    uint8_t *kv_base = base + kM * C::kQB;
+    const uint32_t q_smem = smem_u32(base), kv_smem = smem_u32(kv_base);
+    Shared *sm = reinterpret_cast<Shared *>(kv_base + (size_t)S * C::kKvB);
     // (a broadcast tells the compiler that these are the same in all lanes:
     // the copy and product instructions want their operands in uniform registers)
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int G = a.Hq / a.Hkv, Gt = tile_heads(G), tpt = tile_tokens(G);
-    const PrefillLayout L = prefill_layout(a.B, a.Tq, 2 * tpt, D);
+    const PrefillLayout L = prefill_layout(a.B, a.Tq, kM * tpt, D);
     Ctrl *ctrl = reinterpret_cast<Ctrl *>(a.workspace);
 
     if (warp == kMmaWarp) tmem_alloc(&sm->tmem, 512);
     if (threadIdx.x == 0) {
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < kM; ++t) {
             mbar_init(&sm->q_full[t], 1);
             mbar_init(&sm->q_empty[t], 1);
             mbar_init(&sm->s_full[t], 1);
             mbar_init(&sm->s_free[t], 4);
-            for (int h = 0; h < 2; ++h) mbar_init(&sm->p_ready[t][h], 4);
+            for (int h = 0; h < kParts; ++h) mbar_init(&sm->p_ready[t][h], 4);
             mbar_init(&sm->o_done[t], 1);
-            mbar_init(&sm->item_full[t], 1);
-            mbar_init(&sm->item_empty[t], 8 + 3);  // softmax, product and clearing warps
+        }
+        for (int n = 0; n < 2; ++n) {
+            mbar_init(&sm->item_full[n], 1);
+            mbar_init(&sm->item_empty[n], 5 * kM + 1);  // all warps but the copying one
         }
         for (int i = 0; i < S; ++i) {
             mbar_init(&sm->kv_full[i], 1);
-            mbar_init(&sm->kv_empty[i], 2);
+            mbar_init(&sm->kv_empty[i], kM);
             mbar_init(&sm->tail[i], 1);
         }
         mbar_init(&sm->offset, C::kOwnP ? 1 : 4);
-        mbar_init(&sm->finished, 2);
+        mbar_init(&sm->finished, kM);
         fence_barrier_init();
         sm->abort = 0;
         prefetch_tensormap(&map_q);
@@ -393,9 +406,10 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
     // S_t, O_t and P_t in tensor memory, all of which is this block's: its
     // address is 0 (anything else is reported like a wait that gave up)
     if (sm->tmem != 0) sm->abort = 20;
-    constexpr uint32_t s_col = 0, o_col = 2 * kTile;
-    constexpr uint32_t p_col = C::kOwnP ? o_col + 2 * D : s_col;
-    constexpr uint32_t kPStep = C::kOwnP ? kTile / 2 : kTile;
+    constexpr uint32_t s_col = 0, o_col = kM * kKeys;
+    constexpr uint32_t p_col = C::kOwnP ? o_col + kM * D : s_col;
+    constexpr uint32_t kPStep = C::kOwnP ? kKeys / 2 : kKeys;
+    static_assert(kM * (kKeys + D + (C::kOwnP ? kKeys / 2 : 0)) <= 512, "tensor memory");
 
     // The next item; false when there is none or a wait gave up.  Every role
     // but the copying one walks the items with this.
@@ -408,11 +422,11 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
     };
     // A value tile whose rows past the sequence's end belong to others.
     auto ragged = [&](const Item &it, int j) {
-        return (it.b.j0 + j + 1) * kTile > it.b.nk && it.b.k0 + it.b.nk < a.Tk;
+        return (it.b.j0 + j + 1) * kKeys > it.b.nk && it.b.k0 + it.b.nk < a.Tk;
     };
 
     if (warp >= kMmaWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRoleRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
         if (warp == kLoadWarp) {
             // ---------------- copies, and the items for everyone
             const int HV = a.Hkv * HT;
@@ -434,7 +448,7 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                     k0 = __ldg(a.cu_k + lane);
                     nk = __ldg(a.cu_k + lane + 1) - k0;
                 }
-                up_to = (nq + 2 * tpt - 1) / (2 * tpt);
+                up_to = (nq + kM * tpt - 1) / (kM * tpt);
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int v = __shfl_up_sync(0xffffffffu, up_to, o);
@@ -454,7 +468,7 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                 const int sq0 = __shfl_sync(0xffffffffu, q0, b), snq = __shfl_sync(0xffffffffu, nq, b);
                 const int sk0 = __shfl_sync(0xffffffffu, k0, b), snk = __shfl_sync(0xffffffffu, nk, b);
                 const int left = __shfl_sync(0xffffffffu, up_to, b) - 1 - (int)i;
-                return block_at(a.causal, sq0, snq, sk0, snk, left * 2 * tpt, tpt);
+                return block_at(a.causal, sq0, snq, sk0, snk, left * kM * tpt, tpt);
             };
             // Item n + 1's entry and item n + 2's number are fetched while
             // item n's copies are issued.
@@ -488,7 +502,7 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                 idx = __shfl_sync(0xffffffffu, ahead, 0);
                 if (idx < total) blk = entry(idx / HV);
                 next_ahead();
-                const int tiles = max(it.b.tiles0, it.b.tiles1);
+                const int tiles = most_tiles(it.b);
                 bool ok = true;
                 auto copy_kv = [&](const CUtensorMap *map, int j, bool tail) {
                     const uint32_t s = kv % S, ph = (kv / S) & 1;
@@ -496,8 +510,8 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                     if (!ok) return;
                     if (lane == 0) {
                         uint64_t *bar = tail ? &sm->tail[s] : &sm->kv_full[s];
-                        mbar_arrive_expect_tx(bar, C::kTileB);
-                        tma_load_4d(base + (2 + s) * C::kTileB, map, 0, it.b.k0 + (it.b.j0 + j) * kTile, it.hk, 0, bar);
+                        mbar_arrive_expect_tx(bar, C::kKvB);
+                        tma_load_4d(kv_base + s * C::kKvB, map, 0, it.b.k0 + (it.b.j0 + j) * kKeys, it.hk, 0, bar);
                     }
                     __syncwarp();
                     ++kv;
@@ -505,13 +519,13 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                 for (int j = 0; j < tiles && ok && !a.test_no_copies; ++j) {
                     if (!C::kOwnP || j == 0) copy_kv(&map_k, j, false);
                     if (j == 0) {
-                        for (int t = 0; t < 2 && ok; ++t) {
+                        for (int t = 0; t < kM && ok; ++t) {
                             ok = warp_wait_flag(&sm->q_empty[t], (n & 1) ^ 1, &sm->abort, 4);
                             if (ok && lane == 0) {
                                 // (a tile without rows is loaded all the same: its phases go on)
                                 mbar_arrive_expect_tx(&sm->q_full[t], (uint32_t)(Gt * tpt) * D * 2);
                                 for (int h = 0; h < kHalves; ++h)
-                                    tma_load_4d(base + t * C::kTileB + h * kHalfB, &map_q, 0, it.h0,
+                                    tma_load_4d(base + t * C::kQB + h * kQHalf, &map_q, 0, it.h0,
                                                 it.b.q0 + it.b.tok0 + t * tpt, h, &sm->q_full[t]);
                             }
                             __syncwarp();
@@ -524,7 +538,7 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                 if (!ok) break;
                 if (tiles == 0) {
                     // no copies: the other roles' phases of q go on without them
-                    for (int t = 0; t < 2 && ok; ++t) {
+                    for (int t = 0; t < kM && ok; ++t) {
                         ok = warp_wait_flag(&sm->q_empty[t], (n & 1) ^ 1, &sm->abort, 4);
                         if (ok && lane == 0) mbar_arrive(&sm->q_full[t]);
                         __syncwarp();
@@ -542,14 +556,14 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
             auto products = [&](auto tile) {
             constexpr int t = decltype(tile)::value;
             const uint64_t q_desc = sdesc_k_sw128(q_smem), k_desc = sdesc_k_sw128(kv_smem);
-            const uint64_t v_desc = sdesc_mn_sw128(kv_smem, kHalfB);
-            constexpr uint32_t kIdS = idesc_bf16(kTile, false), kIdO = idesc_bf16(D, true);
+            const uint64_t v_desc = sdesc_mn_sw128(kv_smem, kKvHalf);
+            constexpr uint32_t kIdS = idesc_bf16(kKeys, false), kIdO = idesc_bf16(D, true);
             uint32_t stage = 0, stage_ph = 0;         // the next key or value tile
             uint32_t p_ph = 0, f_ph = 1, off_ph = 0;
             Item it;
             bool ok = true;
-            const uint64_t qd = q_desc + ((t * C::kTileB) >> 4);
-            const uint32_t s_t = s_col + t * kTile, o_t = o_col + t * D, p_t = p_col + t * kPStep;
+            const uint64_t qd = q_desc + ((t * C::kQB) >> 4);
+            constexpr uint32_t s_t = s_col + t * kKeys, o_t = o_col + t * D, p_t = p_col + t * kPStep;
             auto commit = [&](uint64_t *bar) {
                 if (elect_one()) tc_commit(bar);
                 __syncwarp();
@@ -573,11 +587,12 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                     tc_fence_after();
                 }
                 if (elect_one()) {
-                    const uint64_t kd = k_desc + ((s * C::kTileB) >> 4);
+                    const uint64_t kd = k_desc + ((s * C::kKvB) >> 4);
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j) {
-                        const uint32_t off = ((j >> 2) * kHalfB + (j & 3) * 32) >> 4;
-                        mma_bf16_ss(s_t, qd + off, kd + off, kIdS, j > 0);
+                        const uint32_t in = (j & 3) * 32;
+                        mma_bf16_ss(s_t, qd + (((j >> 2) * kQHalf + in) >> 4), kd + (((j >> 2) * kKvHalf + in) >> 4),
+                                    kIdS, j > 0);
                     }
                     tc_commit(&sm->s_full[t]);
                     tc_commit(&sm->kv_empty[s]);
@@ -585,20 +600,21 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                 }
                 __syncwarp();
             };
-            // O_t += P_t V, by halves of the keys
+            // O_t += P_t V, in the parts in which the weights come
             auto pv = [&](uint32_t s, bool first, bool tell) {
-                const uint64_t vd = v_desc + ((s * C::kTileB) >> 4);
+                const uint64_t vd = v_desc + ((s * C::kKvB) >> 4);
+                constexpr int kSteps = kKeys / 16 / kParts;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < kParts; ++h) {
                     ok = ok && warp_wait_flag(&sm->p_ready[t][h], p_ph, &sm->abort, 7);
                     if (!ok) return;
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
-                        for (int i = h * kTile / 32; i < (h + 1) * kTile / 32; ++i)
+                        for (int i = h * kSteps; i < (h + 1) * kSteps; ++i)
                             mma_f16_ts(o_t, p_t + i * 8, vd + ((i * 2048) >> 4), kIdO,
                                        i > 0 ? 1u : (first ? 0u : 1u));
-                        if (h == 1) {
+                        if (h == kParts - 1) {
                             tc_commit(&sm->o_done[t]);
                             tc_commit(&sm->kv_empty[s]);
                         }
@@ -609,9 +625,8 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                 p_ph ^= 1;
             };
             for (uint32_t n = 0; ok && take(n, it); ++n) {
-                const int n0 = __shfl_sync(0xffffffffu, it.b.tiles0, 0);
-                const int n1 = __shfl_sync(0xffffffffu, it.b.tiles1, 0);
-                const int nt = t ? n1 : n0, tiles = max(n0, n1);
+                const int nt = __shfl_sync(0xffffffffu, tiles_at(it.b, t), 0);
+                const int tiles = __shfl_sync(0xffffffffu, most_tiles(it.b), 0);
                 uint32_t s = 0;
                 if (tiles > 0) s = next_stage();
                 ok = ok && warp_wait_flag(&sm->q_full[t], n & 1, &sm->abort, 6);
@@ -624,7 +639,7 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                 // causal tokens, 64 heads: 606 us, 640 us with the signal
                 // below, 656 in step); heads of 64: once the first half of
                 // its weights is (455, 483 us the other way, 484).
-                const bool apart = min(n0, n1) >= kApart;
+                const bool apart = __shfl_sync(0xffffffffu, (int)run_apart(it.b), 0) != 0;
                 if (apart && t == 1) {
                     ok = warp_wait_flag(&sm->offset, off_ph, &sm->abort, 13);
                     if (!ok) break;
@@ -670,17 +685,17 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
             Item it;
             uint32_t kv = 0, ph = 0;  // ph: one phase bit per stage
             for (uint32_t n = 0; take(n, it); ++n) {
-                const int tiles = max(it.b.tiles0, it.b.tiles1);
+                const int tiles = most_tiles(it.b);
                 kv += 2 * tiles;
                 if (tiles == 0 || !ragged(it, tiles - 1)) continue;
                 const uint32_t s = (kv - 1) % S;
                 if (!warp_wait_flag(&sm->tail[s], (ph >> s) & 1, &sm->abort, 8)) break;
                 ph ^= 1u << s;
-                uint8_t *v = base + (2 + s) * C::kTileB;
-                const int from = it.b.nk - (it.b.j0 + tiles - 1) * kTile;
+                uint8_t *v = kv_base + s * C::kKvB;
+                const int from = it.b.nk - (it.b.j0 + tiles - 1) * kKeys;
                 for (int h = 0; h < kHalves; ++h)
-                    for (int i = from * 8 + lane; i < kTile * 8; i += 32)
-                        *reinterpret_cast<uint4 *>(v + h * kHalfB + i * 16) = make_uint4(0, 0, 0, 0);
+                    for (int i = from * 8 + lane; i < kKeys * 8; i += 32)
+                        *reinterpret_cast<uint4 *>(v + h * kKvHalf + i * 16) = make_uint4(0, 0, 0, 0);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm->kv_full[s]);
@@ -688,11 +703,11 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
         }
     } else {
         // ---------------- softmax: warpgroup t has row tile t, a thread a row
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int t = warp >> 2;
         const int r = threadIdx.x & 127;
         const uint32_t lane_base = (uint32_t)(warp & 3) * 32 << 16;
-        const uint32_t s_t = s_col + t * kTile + lane_base, o_t = o_col + t * D + lane_base;
+        const uint32_t s_t = s_col + t * kKeys + lane_base, o_t = o_col + t * D + lane_base;
         const uint32_t p_t = p_col + t * kPStep + lane_base;
         const int tok_r = r / Gt, g = r % Gt;
         const float sl = a.scale * kLog2e;
@@ -711,16 +726,17 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
             const int least = __reduce_min_sync(0xffffffffu, limit);
             float ref = -INFINITY;  // the row's reference, in log2 units
             float l = 0.f;
-            const int tiles = t ? it.b.tiles1 : it.b.tiles0;
+            const int tiles = tiles_at(it.b, t);
+            const bool apart = run_apart(it.b);
             for (int j = 0; j < tiles; ++j) {
                 if (!C::kOwnP || !__all_sync(0xffffffffu, s_seen)) {
                     ok = warp_wait_flag(&sm->s_full[t], ph, &sm->abort, 9);
                     if (!ok) break;
                 }
                 tc_fence_after();
-                float x[kTile];
+                float x[kKeys];
 #pragma unroll
-                for (int c = 0; c < kTile; c += 32) tmem_ld32(s_t + c, x + c);
+                for (int c = 0; c < kKeys; c += 32) tmem_ld32(s_t + c, x + c);
                 tc_wait_ld();
                 if (C::kOwnP) {
                     tc_fence_before();
@@ -728,11 +744,11 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                     if (lane == 0) mbar_arrive(&sm->s_free[t]);
                     o_seen = mbar_test_wait(&sm->o_done[t], ph ^ 1);
                 }
-                const int key0 = (it.b.j0 + j) * kTile;
-                if (key0 + kTile > least) {
+                const int key0 = (it.b.j0 + j) * kKeys;
+                if (key0 + kKeys > least) {
                     const int lim = limit - key0;
 #pragma unroll
-                    for (int c = 0; c < kTile; c += 32)
+                    for (int c = 0; c < kKeys; c += 32)
                         if (key0 + c + 32 > least) {
 #pragma unroll
                             for (int e = c; e < c + 32; ++e) x[e] = e < lim ? x[e] : -INFINITY;
@@ -740,11 +756,11 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                 }
                 float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                for (int c = 4; c + 8 <= kTile; c += 8)
+                for (int c = 4; c + 8 <= kKeys; c += 8)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], x[c + 2 * e], x[c + 2 * e + 1]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], x[kTile - 4 + e]);
+                for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], x[kKeys - 4 + e]);
                 const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl;
                 const bool raise = top > ref + kSlack;
                 bool over = !C::kOwnP || j == 0;  // P_t may be written
@@ -777,13 +793,12 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                     if (!ok) break;
                 }
                 if (C::kOwnP) tc_fence_after();
-                if (!C::kOwnP && t == 0 && j == 0 && min(it.b.tiles0, it.b.tiles1) >= kApart && lane == 0)
-                    mbar_arrive(&sm->offset);
+                if (!C::kOwnP && t == 0 && j == 0 && apart && lane == 0) mbar_arrive(&sm->offset);
                 const float z = ref == -INFINITY ? 0.f : ref;
                 const float2 sl2 = make_float2(sl, sl), nz2 = make_float2(-z, -z);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int c = 0; c < kTile; c += 32) {
+                for (int c = 0; c < kKeys; c += 32) {
                     uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
@@ -793,13 +808,13 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                         sum[e & 1] = add2(sum[e & 1], y);
                         p[e] = pack_bf16(y.x, y.y);
                     }
-                    if (C::kOwnP && c + 32 == kTile) s_seen = mbar_test_wait(&sm->s_full[t], ph ^ 1);
+                    if (C::kOwnP && c + 32 == kKeys) s_seen = mbar_test_wait(&sm->s_full[t], ph ^ 1);
                     tmem_st16(p_t + c / 2, p);
-                    if (c % kHalf) {  // half of the weights: their product may start
+                    if ((c + 32) % (kKeys / kParts) == 0) {  // their product may start
                         tc_wait_st();
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&sm->p_ready[t][c / kHalf]);
+                        if (lane == 0) mbar_arrive(&sm->p_ready[t][c / (kKeys / kParts)]);
                     }
                 }
                 const float2 both = add2(sum[0], sum[1]);
@@ -834,7 +849,7 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                                 make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 }
                 if (live)
-                    reinterpret_cast<float2 *>(a.workspace + L.ml)[((size_t)it.slot * 2 + t) * kTile + r] =
+                    reinterpret_cast<float2 *>(a.workspace + L.ml)[((size_t)it.slot * kM + t) * kTile + r] =
                         make_float2(ref, l);
                 tc_fence_before();
                 continue;
@@ -913,17 +928,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const PrefillArgs
     __shared__ float shared[kJoinWarps][10][32];  // per warp: maximum, sum, 8 columns
     pdl_wait();
     const int G = a.Hq / a.Hkv, Gt = tile_heads(G), tpt = tile_tokens(G), HV = a.Hkv * HT;
-    const PrefillLayout L = prefill_layout(a.B, a.Tq, 2 * tpt, D);
+    const PrefillLayout L = prefill_layout(a.B, a.Tq, kM * tpt, D);
     const PlanHead head = *reinterpret_cast<const PlanHead *>(a.workspace + L.head);
     const float2 *ml = reinterpret_cast<const float2 *>(a.workspace + L.ml);
     const float *sums = reinterpret_cast<const float *>(a.workspace + L.sums);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kCols = D / 8, kRowGroups = kTile / 32;
-    const int64_t work = (int64_t)head.joins * HV * 2 * kRowGroups * kCols;
+    const int64_t work = (int64_t)head.joins * HV * kM * kRowGroups * kCols;
     for (int64_t w = blockIdx.x; w < work; w += gridDim.x) {
         const int c = (int)(w % kCols) * 8, rg = (int)(w / kCols) % kRowGroups;
-        const int t = (int)(w / (kCols * kRowGroups)) & 1;
-        const int64_t bh = w / (2 * kCols * kRowGroups);
+        const int t = (int)(w / (kCols * kRowGroups)) % kM;
+        const int64_t bh = w / (kM * kCols * kRowGroups);
         const Split sp = reinterpret_cast<const Split *>(a.workspace + L.splits)[bh / HV];
         const int hv = (int)(bh % HV);
         const int r = rg * 32 + lane;
@@ -936,11 +951,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const PrefillArgs
         if (live) {
 #pragma unroll 8
             for (int p = warp; p < sp.parts; p += kJoinWarps)
-                top = fmaxf(top, ml[((size_t)(slot + p) * 2 + t) * kTile + r].x);
+                top = fmaxf(top, ml[((size_t)(slot + p) * kM + t) * kTile + r].x);
             const float z = top == -INFINITY ? 0.f : top;
 #pragma unroll 8
             for (int p = warp; p < sp.parts; p += kJoinWarps) {
-                const float2 v = ml[((size_t)(slot + p) * 2 + t) * kTile + r];
+                const float2 v = ml[((size_t)(slot + p) * kM + t) * kTile + r];
                 const float4 x = *reinterpret_cast<const float4 *>(sums + part_at(slot + p, t, c, r, D));
                 const float4 y = *reinterpret_cast<const float4 *>(sums + part_at(slot + p, t, c + 4, r, D));
                 const float f = ex2(v.x - z);
@@ -1007,14 +1022,14 @@ cudaError_t run(const PrefillArgs &a, int sms, cudaStream_t s) {
         const uint16_t *p = a.Tk > 0 ? (i ? a.v : a.k) : a.q;
         const uint64_t dims[4] = {64, (uint64_t)(a.Tk > 0 ? a.Tk : 1), (uint64_t)a.Hkv, D / 64};
         const uint64_t strides[3] = {(uint64_t)(i ? a.v_stride : a.k_stride) * 2, D * 2, 128};
-        const uint32_t box[4] = {64, kTile, 1, D / 64};
+        const uint32_t box[4] = {64, kKeys, 1, D / 64};
         if (!encode_tensor_map(i ? &mv : &mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p, dims, strides,
                                box, CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
     }
     // (no key range is cut below this many keys: then no joins either)
-    const bool cuts = a.Tk > kMinPart * kTile;
-    const int64_t most = ((int64_t)a.Tq / (2 * tpt) + a.B) * a.Hkv * HT;
+    const bool cuts = a.Tk > kMinKeys;
+    const int64_t most = ((int64_t)a.Tq / (kM * tpt) + a.B) * a.Hkv * HT;
     if (sms > kMaxSms) sms = kMaxSms;
     const int grid = (int)(cuts || most > sms ? sms : most);
     // (1024 tokens, 32 heads: 20.8 us with a plan, 18.7 without)
@@ -1053,7 +1068,7 @@ cudaError_t run(const PrefillArgs &a, int sms, cudaStream_t s) {
 }  // namespace
 
 size_t prefill_workspace(int B, int Tq, int Hq, int Hkv, int D) {
-    return align_up(prefill_layout(B, Tq, 2 * tile_tokens(Hq / Hkv), D).total, 256);
+    return align_up(prefill_layout(B, Tq, kM * tile_tokens(Hq / Hkv), D).total, 256);
 }
 
 cudaError_t launch_attn_prefill(const PrefillArgs &a, cudaStream_t s) {
