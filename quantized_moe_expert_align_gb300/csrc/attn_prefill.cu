@@ -26,6 +26,16 @@
 // parts, whose unscaled sums a last kernel joins in order.  Small calls (at
 // most 32 sequences and kMinKeys keys in all, where nothing is cut) do
 // without the plan: every block finds its own items.
+//
+// Measured on one GB300 (cuBLAS bf16 1876 TFLOP/s in a burst, 1697 sustained),
+// heads of 128: 8192 causal tokens, 64 heads over 8, 598 us (1840 TFLOP/s);
+// six prompts up to 4096 tokens 345 us in a burst, 380 back to back under the
+// power limit (1475 TFLOP/s).  A round of one row tile is softmax (1300 cycles)
+// then its 1024 cycles of products and two hand-overs; the two tiles, half a
+// round apart, keep the tensor pipe busy 75 to 85% of the time.  Heads of 64:
+// 8192 causal tokens 451 us (1220 TFLOP/s); there the two warps per scheduler
+// cannot hide the softmax's latencies (tensor pipe, exponentials and issue all
+// near 50%).  1024 tokens take 18.4 us: eight key tiles in turn at 1.4 us.
 #include <type_traits>
 
 #include "attn_common.cuh"

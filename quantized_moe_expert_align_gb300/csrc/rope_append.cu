@@ -2,6 +2,12 @@
 //   append: per-head RMS norm and rotation of q and k and the cache write of
 //           k and v, one pass over the projection's rows;
 //   gather: cached tokens of sequences back as packed bf16 rows.
+// Both move every byte once and do little else, so HBM bounds them; measured on
+// one GB300 (copy rate 6.79 TB/s): append of 16384 tokens, 64 + 8 + 8 heads of
+// 128, fp8 cache and k_out, 681 MB in 119 us (5.7 TB/s; 127 us when three such
+// batches take turns), gather of 8 contexts up to 32768 tokens, fp8, 605 MB in
+// 94.5 us (6.4 TB/s).  A call of a few tokens takes 4.7 us on the GPU, less
+// than the host needs to make it.
 #include "attn.h"
 #include "device_common.cuh"
 
@@ -302,7 +308,9 @@ __device__ __forceinline__ int find_seq(const int32_t *cu, int B, int t) {
 constexpr int kGatherTokens = 16;
 
 // Block 0 looks the tables over; every other block reads kGatherTokens
-// tokens, all heads, K and V.  A thread moves 8 values at a time.
+// tokens, all heads, K and V.  A thread moves 8 values at a time: half as many
+// bytes in (fp8) as out, whole 16-byte stores to neighbouring addresses.  Four
+// rows in flight per thread instead of one: 115 -> 94.5 us at 605 MB.
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads) gather_kernel(GatherKvArgs a) {
     constexpr int L = D / 8;
