@@ -4,6 +4,8 @@
 
 #include <atomic>
 
+#include <cuda.h>
+
 #include "moe_attn.h"
 #include "moe_internal.h"
 
@@ -24,6 +26,15 @@ struct SmemOnce {
         return err;
     }
 };
+
+// MOE_OK if the current device is an sm_103 GPU (api.cu).
+moe_status_t check_device();
+
+// Tiled tensor map of `rank` <= 5 dimensions (innermost first; strides in
+// bytes, of dimensions 1 and up; unit element strides, out-of-range reads 0).
+bool encode_tensor_map(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *ptr,
+                       const uint64_t *dims, const uint64_t *strides, const uint32_t *box,
+                       CUtensorMapSwizzle swizzle);
 
 // A paged cache as the kernels see it.
 struct KvView {

@@ -893,23 +893,6 @@ EncodeTiledFn encoder() {
 
 }  // namespace
 
-bool encode_tensor_map(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *ptr,
-                       const uint64_t *dims, const uint64_t *strides, const uint32_t *box,
-                       CUtensorMapSwizzle swizzle) {
-    EncodeTiledFn enc = encoder();
-    if (!enc) return false;
-    cuuint64_t d[5], st[4];
-    cuuint32_t bx[5], es[5] = {1, 1, 1, 1, 1};
-    for (int i = 0; i < rank; ++i) {
-        d[i] = dims[i];
-        bx[i] = box[i];
-        if (i + 1 < rank) st[i] = strides[i];
-    }
-    return enc(map, type, (cuuint32_t)rank, const_cast<void *>(ptr), d, st, bx, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 bool make_token_map(CUtensorMap *map, const void *ptr, int rows, int cols, int box_rows) {
     EncodeTiledFn enc = encoder();
     if (!enc) return false;

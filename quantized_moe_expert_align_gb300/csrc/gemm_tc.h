@@ -54,12 +54,6 @@ inline bool tc_pair_mode(int kind, int nt, int N) {
     return big && N % (2 * kTileRows) == 0;
 }
 
-// Tiled tensor map of `rank` <= 5 dimensions (innermost first; strides in
-// bytes, of dimensions 1 and up; unit element strides, out-of-range reads 0).
-bool encode_tensor_map(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *ptr,
-                       const uint64_t *dims, const uint64_t *strides, const uint32_t *box,
-                       CUtensorMapSwizzle swizzle);
-
 // Token operand of the gate+up GEMM: fp16 [rows][cols] (row-major) seen as
 // 3-D (64 columns, rows, cols/64) so that one copy brings a 128-column K
 // chunk of box_rows rows, stored as two 64-column slabs of box_rows x 128 B

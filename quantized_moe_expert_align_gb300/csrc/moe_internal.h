@@ -108,9 +108,6 @@ int down_token_tile(int nt, int H, int64_t n, int E);
 bool use_decode_kernel(int64_t n, int nt);
 FwdLayout fwd_layout(int M, int k, int E, int H, int I);
 
-// MOE_OK if the current device is an sm_103 GPU.
-moe_status_t check_device();
-
 // moe_w4a16_forward on a scratch buffer the caller of this function chose.
 moe_status_t forward_on_scratch(const uint16_t *hidden, const int32_t *ids, const float *topk_w,
                                 const void *w13, const void *w2,
