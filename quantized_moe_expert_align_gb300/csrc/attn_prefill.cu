@@ -10,15 +10,15 @@
 // group) pair, so grouped heads share every key tile and short prompts fill
 // the rows.  Key/value tiles have 128 keys.  Per tile t and key tile j:
 //   S_t = Q_t K_j^T      tcgen05.mma, operands in shared memory (TMA, 128 B swizzle)
-//   P_t = 2^(S_t - r)    one thread per row: registers, rounded to bf16 into
-//                        the tensor memory of S_t
+//   P_t = 2^(S_t - r)    one thread per row, in registers; rounded to bf16 (v's
+//                        type, which the product wants) into tensor memory
 //   O_t += P_t V_j       tcgen05.mma, P_t from tensor memory
-// One warp issues the products of both tiles alternately, so that one tile's
-// softmax runs under the other tile's products; one warp copies; one clears
-// the rows of a last value tile that belong to the next sequence (a weight
-// of 0 would not stop their NaN).  The reference r is raised, and O_t
-// rescaled, only when a row's maximum exceeds it by 2^8: the sums are in
-// fp32, where p <= 2^8 costs nothing.
+// One warp per row tile issues its products, so that one tile's softmax runs
+// under the other tile's products; one warp copies; one clears the rows of a
+// last value tile that belong to the next sequence (a weight of 0 would not
+// stop their NaN).  The reference r is raised, and O_t rescaled, only when a
+// row's maximum exceeds it by 2^8: the sums are in fp32, where p <= 2^8 costs
+// nothing (8192 causal tokens: 798 us when every rise rescales, 680 with this).
 //
 // A planning kernel lists the items by falling number of key tiles; the
 // blocks take them from a counter, longest first.  Where a few items have
@@ -104,7 +104,8 @@ constexpr int kParts = 2;        // in which a key tile's weights come
 // copying, one clearing.
 constexpr int kMmaWarp = 4 * kM, kLoadWarp = 5 * kM, kFixWarp = 5 * kM + 1;
 constexpr int kThreads = 32 * (5 * kM + 2);
-// The launch's 168 registers a thread, shared out anew.
+// The launch's 168 registers a thread, shared out anew (88 and 208: the same
+// for heads of 128, 237 us instead of 229 for prompt parts with heads of 64).
 constexpr int kRoleRegs = 72, kSoftmaxRegs = 216;
 static_assert(128 * kRoleRegs + 256 * kSoftmaxRegs <= 384 * 168, "register split");
 // Items of at least this many key tiles run their row tiles offset.  The first
@@ -564,127 +565,127 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
         } else if (warp < kLoadWarp) {
             // ---------------- products of row tile t
             auto products = [&](auto tile) {
-            constexpr int t = decltype(tile)::value;
-            const uint64_t q_desc = sdesc_k_sw128(q_smem), k_desc = sdesc_k_sw128(kv_smem);
-            const uint64_t v_desc = sdesc_mn_sw128(kv_smem, kKvHalf);
-            constexpr uint32_t kIdS = idesc_bf16(kKeys, false), kIdO = idesc_bf16(D, true);
-            uint32_t stage = 0, stage_ph = 0;         // the next key or value tile
-            uint32_t p_ph = 0, f_ph = 1, off_ph = 0;
-            Item it;
-            bool ok = true;
-            const uint64_t qd = q_desc + ((t * C::kQB) >> 4);
-            constexpr uint32_t s_t = s_col + t * kKeys, o_t = o_col + t * D, p_t = p_col + t * kPStep;
-            auto commit = [&](uint64_t *bar) {
-                if (elect_one()) tc_commit(bar);
-                __syncwarp();
-            };
-            auto next_stage = [&]() {  // waits for the next key or value tile
-                ok = ok && warp_wait_flag(&sm->kv_full[stage], stage_ph, &sm->abort, 5);
-                tc_fence_after();
-                const uint32_t s = stage;
-                if (++stage == S) {
-                    stage = 0;
-                    stage_ph ^= 1;
-                }
-                return s;
-            };
-            // S_t = Q_t K^T; `last`: of this item, so that Q_t is free after it
-            auto qk = [&](uint32_t s, bool last) {
-                if (C::kOwnP) {  // (else the last product with P_t came before)
-                    ok = ok && warp_wait_flag(&sm->s_free[t], f_ph, &sm->abort, 12);
-                    if (!ok) return;
-                    f_ph ^= 1;
+                constexpr int t = decltype(tile)::value;
+                const uint64_t q_desc = sdesc_k_sw128(q_smem), k_desc = sdesc_k_sw128(kv_smem);
+                const uint64_t v_desc = sdesc_mn_sw128(kv_smem, kKvHalf);
+                constexpr uint32_t kIdS = idesc_bf16(kKeys, false), kIdO = idesc_bf16(D, true);
+                uint32_t stage = 0, stage_ph = 0;         // the next key or value tile
+                uint32_t p_ph = 0, f_ph = 1, off_ph = 0;
+                Item it;
+                bool ok = true;
+                const uint64_t qd = q_desc + ((t * C::kQB) >> 4);
+                constexpr uint32_t s_t = s_col + t * kKeys, o_t = o_col + t * D, p_t = p_col + t * kPStep;
+                auto commit = [&](uint64_t *bar) {
+                    if (elect_one()) tc_commit(bar);
+                    __syncwarp();
+                };
+                auto next_stage = [&]() {  // waits for the next key or value tile
+                    ok = ok && warp_wait_flag(&sm->kv_full[stage], stage_ph, &sm->abort, 5);
                     tc_fence_after();
-                }
-                if (elect_one()) {
-                    const uint64_t kd = k_desc + ((s * C::kKvB) >> 4);
-#pragma unroll
-                    for (int j = 0; j < D / 16; ++j) {
-                        const uint32_t in = (j & 3) * 32;
-                        mma_bf16_ss(s_t, qd + (((j >> 2) * kQHalf + in) >> 4), kd + (((j >> 2) * kKvHalf + in) >> 4),
-                                    kIdS, j > 0);
+                    const uint32_t s = stage;
+                    if (++stage == S) {
+                        stage = 0;
+                        stage_ph ^= 1;
                     }
-                    tc_commit(&sm->s_full[t]);
-                    tc_commit(&sm->kv_empty[s]);
-                    if (last) tc_commit(&sm->q_empty[t]);
-                }
-                __syncwarp();
-            };
-            // O_t += P_t V, in the parts in which the weights come
-            auto pv = [&](uint32_t s, bool first, bool tell) {
-                const uint64_t vd = v_desc + ((s * C::kKvB) >> 4);
-                constexpr int kSteps = kKeys / 16 / kParts;
-#pragma unroll
-                for (int h = 0; h < kParts; ++h) {
-                    ok = ok && warp_wait_flag(&sm->p_ready[t][h], p_ph, &sm->abort, 7);
-                    if (!ok) return;
-                    tc_fence_after();
+                    return s;
+                };
+                // S_t = Q_t K^T; `last`: of this item, so that Q_t is free after it
+                auto qk = [&](uint32_t s, bool last) {
+                    if (C::kOwnP) {  // (else the last product with P_t came before)
+                        ok = ok && warp_wait_flag(&sm->s_free[t], f_ph, &sm->abort, 12);
+                        if (!ok) return;
+                        f_ph ^= 1;
+                        tc_fence_after();
+                    }
                     if (elect_one()) {
+                        const uint64_t kd = k_desc + ((s * C::kKvB) >> 4);
 #pragma unroll
-                        for (int i = h * kSteps; i < (h + 1) * kSteps; ++i)
-                            mma_f16_ts(o_t, p_t + i * 8, vd + ((i * 2048) >> 4), kIdO,
-                                       i > 0 ? 1u : (first ? 0u : 1u));
-                        if (h == kParts - 1) {
-                            tc_commit(&sm->o_done[t]);
-                            tc_commit(&sm->kv_empty[s]);
+                        for (int j = 0; j < D / 16; ++j) {
+                            const uint32_t in = (j & 3) * 32;
+                            mma_bf16_ss(s_t, qd + (((j >> 2) * kQHalf + in) >> 4), kd + (((j >> 2) * kKvHalf + in) >> 4),
+                                        kIdS, j > 0);
                         }
+                        tc_commit(&sm->s_full[t]);
+                        tc_commit(&sm->kv_empty[s]);
+                        if (last) tc_commit(&sm->q_empty[t]);
                     }
                     __syncwarp();
-                    if (tell && h == 0 && lane == 0) mbar_arrive(&sm->offset);
-                }
-                p_ph ^= 1;
-            };
-            for (uint32_t n = 0; ok && take(n, it); ++n) {
-                const int nt = __shfl_sync(0xffffffffu, tiles_at(it.b, t), 0);
-                const int tiles = __shfl_sync(0xffffffffu, most_tiles(it.b), 0);
-                uint32_t s = 0;
-                if (tiles > 0) s = next_stage();
-                ok = ok && warp_wait_flag(&sm->q_full[t], n & 1, &sm->abort, 6);
-                if (!ok) break;
-                tc_fence_after();
-                // The second tile starts behind the first: two tiles in step
-                // would want the tensor pipe, and then the exponentials, at
-                // the same time.  Heads of 128: once the first tile's maxima
-                // are known, which puts the two half a round apart (8192
-                // causal tokens, 64 heads: 606 us, 640 us with the signal
-                // below, 656 in step); heads of 64: once the first half of
-                // its weights is (455, 483 us the other way, 484).
-                const bool apart = __shfl_sync(0xffffffffu, (int)run_apart(it.b), 0) != 0;
-                if (apart && t == 1) {
-                    ok = warp_wait_flag(&sm->offset, off_ph, &sm->abort, 13);
-                    if (!ok) break;
-                    off_ph ^= 1;
-                }
-                if (nt > 0)
-                    qk(s, nt == 1);
-                else {  // (the other tile's stages, and a Q_t that is not used)
-                    commit(&sm->q_empty[t]);
-                    if (tiles > 0) commit(&sm->kv_empty[s]);
-                }
-                // the scores of key tile j + 1
-                auto next_scores = [&](int j) {
-                    if (j + 1 >= tiles) return;
-                    const uint32_t k = next_stage();
-                    if (!ok) return;
-                    if (j + 1 < nt)
-                        qk(k, j + 2 == nt);
-                    else
-                        commit(&sm->kv_empty[k]);
                 };
-                for (int j = 0; j < tiles && ok; ++j) {
-                    if (C::kOwnP) next_scores(j);
-                    const uint32_t v = next_stage();
+                // O_t += P_t V, in the parts in which the weights come
+                auto pv = [&](uint32_t s, bool first, bool tell) {
+                    const uint64_t vd = v_desc + ((s * C::kKvB) >> 4);
+                    constexpr int kSteps = kKeys / 16 / kParts;
+#pragma unroll
+                    for (int h = 0; h < kParts; ++h) {
+                        ok = ok && warp_wait_flag(&sm->p_ready[t][h], p_ph, &sm->abort, 7);
+                        if (!ok) return;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int i = h * kSteps; i < (h + 1) * kSteps; ++i)
+                                mma_f16_ts(o_t, p_t + i * 8, vd + ((i * 2048) >> 4), kIdO,
+                                           i > 0 ? 1u : (first ? 0u : 1u));
+                            if (h == kParts - 1) {
+                                tc_commit(&sm->o_done[t]);
+                                tc_commit(&sm->kv_empty[s]);
+                            }
+                        }
+                        __syncwarp();
+                        if (tell && h == 0 && lane == 0) mbar_arrive(&sm->offset);
+                    }
+                    p_ph ^= 1;
+                };
+                for (uint32_t n = 0; ok && take(n, it); ++n) {
+                    const int nt = __shfl_sync(0xffffffffu, tiles_at(it.b, t), 0);
+                    const int tiles = __shfl_sync(0xffffffffu, most_tiles(it.b), 0);
+                    uint32_t s = 0;
+                    if (tiles > 0) s = next_stage();
+                    ok = ok && warp_wait_flag(&sm->q_full[t], n & 1, &sm->abort, 6);
                     if (!ok) break;
-                    if (j < nt)
-                        pv(v, j == 0, C::kOwnP && j == 0 && apart && t == 0);
-                    else
-                        commit(&sm->kv_empty[v]);
-                    if (!C::kOwnP && ok) next_scores(j);
+                    tc_fence_after();
+                    // The second tile starts behind the first: two tiles in step
+                    // would want the tensor pipe, and then the exponentials, at
+                    // the same time.  Heads of 128: once the first tile's maxima
+                    // are known, which puts the two half a round apart (8192
+                    // causal tokens, 64 heads: 606 us, 640 us with the signal
+                    // below, 656 in step); heads of 64: once the first half of
+                    // its weights is (455, 483 us the other way, 484).
+                    const bool apart = __shfl_sync(0xffffffffu, (int)run_apart(it.b), 0) != 0;
+                    if (apart && t == 1) {
+                        ok = warp_wait_flag(&sm->offset, off_ph, &sm->abort, 13);
+                        if (!ok) break;
+                        off_ph ^= 1;
+                    }
+                    if (nt > 0)
+                        qk(s, nt == 1);
+                    else {  // (the other tile's stages, and a Q_t that is not used)
+                        commit(&sm->q_empty[t]);
+                        if (tiles > 0) commit(&sm->kv_empty[s]);
+                    }
+                    // the scores of key tile j + 1
+                    auto next_scores = [&](int j) {
+                        if (j + 1 >= tiles) return;
+                        const uint32_t k = next_stage();
+                        if (!ok) return;
+                        if (j + 1 < nt)
+                            qk(k, j + 2 == nt);
+                        else
+                            commit(&sm->kv_empty[k]);
+                    };
+                    for (int j = 0; j < tiles && ok; ++j) {
+                        if (C::kOwnP) next_scores(j);
+                        const uint32_t v = next_stage();
+                        if (!ok) break;
+                        if (j < nt)
+                            pv(v, j == 0, C::kOwnP && j == 0 && apart && t == 0);
+                        else
+                            commit(&sm->kv_empty[v]);
+                        if (!C::kOwnP && ok) next_scores(j);
+                    }
                 }
-            }
-            // everything issued has finished before the block ends
-            commit(&sm->finished);
-            wait_own(&sm->finished, 0);
+                // everything issued has finished before the block ends
+                commit(&sm->finished);
+                wait_own(&sm->finished, 0);
             };
             if (warp == kMmaWarp)
                 products(std::integral_constant<int, 0>{});

@@ -60,6 +60,15 @@ def test_decode(gpu, lens, Hq, Hkv, D, page, fp8):
     _decode(lens, Hq, Hkv, D, fp8, page)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_groups_of_more_heads_than_a_tile(gpu, D):
+    """150 query heads over one: several head tiles, the last one partly filled."""
+    _decode([700, 0, 33], 150, 1, D, False, 16, seed=11)
+    _decode([700, 0, 33], 150, 1, D, True, 64, seed=12)
+    _prefill([3, 40], [300, 40], 150, 1, D, True, seed=13)
+    _prefill([2], [3000], 150, 1, D, False, seed=14)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_decode_many_sequences(gpu, fp8):
     _decode([(37 * i * i) % 411 for i in range(200)], 8, 4, 128, fp8, 16, seed=3)
