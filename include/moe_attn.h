@@ -73,7 +73,8 @@ moe_status_t moe_kv_cache_size(int type, int num_pages, int page_size, int Hkv, 
  * slots[t] of the cache (-1: this token is not cached; cache NULL: none is):
  * rounded to bf16, or, MOE_KV_FP8, as scale = amax / 448 with amax the row's
  * largest magnitude, and code = e4m3(x * (448 / amax)), nearest-even (amax
- * 0: scale and codes 0; a row holding an infinity or a NaN: scale NaN).
+ * 0: scale and codes 0; an amax below 2^-119 counts as 2^-119; a row holding
+ * an infinity or a NaN: scale NaN).
  * Two tokens must not name the same slot.
  *  cos_sin [max_pos][rot] fp32, 16-byte aligned (NULL if rot == 0): scaling
  *          for long contexts is a matter of the table's angles.
@@ -146,6 +147,7 @@ size_t moe_attn_prefill_workspace_size(int B, int Tq, int Hq, int Hkv, int D);
  * none gets zeros and lse = -inf.
  *  q [Tq][Hq][D], k and v [Tk][Hkv][D], out [Tq][Hq][D] bf16;
  *  lse [Tq][Hq] fp32 or NULL.
+ * Rows of out and lse that belong to no sequence are not written.
  * Other sequences' rows never matter, whatever they hold.  Within a
  * sequence an infinity or NaN in v may also reach up to 255 rows before the
  * first that sees it (its weight there is 0, the product NaN).

@@ -219,7 +219,10 @@ __device__ __forceinline__ void walk(const AppendArgs &a, const Place &p, const 
                     }
 #pragma unroll
                     for (int o = L / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(p.group, top, o));
-                    const float amax = __uint_as_float(top >= 0x7F800000u ? 0x7FFFFFFFu : top);
+                    // (below 2^-119 the factor 448 / amax would overflow)
+                    constexpr uint32_t kLeast = (127 - 119) << 23;
+                    const float amax = __uint_as_float(
+                        top >= 0x7F800000u ? 0x7FFFFFFFu : (top == 0 ? 0 : max(top, kLeast)));
                     const float inv = top == 0 ? 0.f : 448.0f / amax;
                     *reinterpret_cast<uint32_t *>(a.data + row * D + p.dA) =
                         e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);

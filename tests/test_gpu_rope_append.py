@@ -136,6 +136,30 @@ def test_append_special_rows(gpu):
             2.0 ** -4 * x[fine][:, None].float().abs() + 2.0 ** -9 * sc[fine][..., None]).all()
 
 
+def test_append_tiny_rows(gpu):
+    """Rows whose largest magnitude is near or below 2^-128, with zeros among
+    them: codes stay numbers, values stay within half a step."""
+    import torch
+    import quantized_moe_expert_align_gb300 as moe
+    H, D = 2, 64
+    sizes = [2.0 ** -110, 2.0 ** -118, 2.0 ** -121, 2.0 ** -127, 2.0 ** -133]
+    x = torch.zeros(len(sizes), H, D, dtype=torch.float64, device="cuda")
+    for t, size in enumerate(sizes):
+        x[t, :, 3] = size
+        x[t, :, 40] = -size
+        x[t, 0, 8] = size / 4
+    x = x.bfloat16()
+    cache = au.make_cache(3, 1, H, 16, D, True)
+    slots = torch.arange(len(sizes), dtype=torch.int32, device="cuda")
+    moe.qk_rope_append(x, x, x, None, None, cache, slots)
+    sc = cache.scales[0, :, :, :len(sizes)].permute(2, 0, 1).double()
+    codes = cache.data[0, :, :, :len(sizes)].float().permute(2, 0, 1, 3).double()
+    want = x.double()[:, :, None].expand(-1, -1, 2, -1)
+    au.check(codes * sc[..., None], want,
+             (2.0 ** -4 + 2.0 ** -20) * want.abs() + 2.0 ** -10 * sc[..., None], "values")
+    assert (codes[want == 0] == 0).all()
+
+
 def test_append_without_a_cache_and_without_tokens(gpu):
     import torch
     import quantized_moe_expert_align_gb300 as moe
