@@ -66,9 +66,10 @@ struct Cfg {
     static constexpr int kRows = 8 * NT;                   // query heads of a tile
     // Several blocks on an SM hide each other's set-up, joins and latencies:
     // two, for fp8 three (half the bytes for the same steps: 256 sequences up
-    // to 8192 keys 282 -> 277 us); 32 heads need the registers of one.
-    static constexpr int kBlocks = NT == 4 ? 1 : (FP8 ? 3 : 2);
-    static constexpr int kSmemLimit = (kBlocks == 1 ? 226 : (kBlocks == 2 ? 113 : 75)) * 1024;
+    // to 8192 keys 282 -> 277 us), except where a tile of 16 heads needs the
+    // registers of two (64 sequences, 64 heads over 4: 122 us with three, 74).
+    static constexpr int kBlocks = FP8 && (NT == 1 || D == 64) ? 3 : 2;
+    static constexpr int kSmemLimit = (kBlocks == 2 ? 113 : 75) * 1024;
     static constexpr int kEs = FP8 ? 1 : 2;
     static constexpr int kRowB = D * kEs < 128 ? D * kEs : 128;
     static constexpr int kHalves = D * kEs / kRowB;
@@ -732,7 +733,11 @@ decode_join(const DecodeAttnArgs a, const int RT, const int tile_rows, const int
     if (a.lse && col == 0) a.lse[(size_t)jn.b * a.Hq + hq] = (top + __log2f(sum)) * kLn2;
 }
 
-int tiles_of(int G) { return G <= 8 ? 1 : (G <= 16 ? 2 : 4); }  // groups of 8 heads in a tile
+// Groups of 8 heads in a tile.  More than 16 heads are several tiles, which read
+// the cache again, mostly from L2: one tile of 32 needs the registers of a
+// whole SM (64 sequences up to 8192 keys, 64 heads over 2: 108 us for fp8 and
+// 110 for bf16 instead of 74 and 87).
+int tiles_of(int G) { return G <= 8 ? 1 : 2; }
 
 template <int D, bool FP8, int NT>
 cudaError_t run(const DecodeAttnArgs &a, int sms, cudaStream_t s) {
@@ -778,11 +783,7 @@ cudaError_t run(const DecodeAttnArgs &a, int sms, cudaStream_t s) {
 
 template <int D, bool FP8>
 cudaError_t pick(const DecodeAttnArgs &a, int sms, cudaStream_t s) {
-    switch (tiles_of(a.Hq / a.kv.Hkv)) {
-        case 1: return run<D, FP8, 1>(a, sms, s);
-        case 2: return run<D, FP8, 2>(a, sms, s);
-        default: return run<D, FP8, 4>(a, sms, s);
-    }
+    return tiles_of(a.Hq / a.kv.Hkv) == 1 ? run<D, FP8, 1>(a, sms, s) : run<D, FP8, 2>(a, sms, s);
 }
 
 }  // namespace

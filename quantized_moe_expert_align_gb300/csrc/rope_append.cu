@@ -247,7 +247,9 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     if (blockIdx.x == 0) {
         if (blockIdx.y) return;
         int bad = kNone, slot;
-#pragma unroll 4
+        // (the loads of 16 tokens a thread in flight at a time: 8689 tokens of 10
+        // rows would otherwise wait for this block)
+#pragma unroll 16
         for (int t = threadIdx.x; t < a.T; t += kAppendThreads)
             if (!token_ok(a, t, slot)) bad = min(bad, t);
         bad = block_min(bad);
