@@ -32,16 +32,18 @@ namespace {
 
 using namespace attn;
 
-constexpr int kChunk = 64;                 // keys per unit
-constexpr int kCWarps = 4;                 // consumer warps (16 keys of a unit each)
+constexpr int kCWarps = 4;                 // consumer warps
 constexpr int kThreads = (kCWarps + 1) * 32;
 constexpr int kMaxGrid = 512;
 
-// A pair that the end of block `c` cuts first: its other parts are those of
-// the blocks c + 1 .. c + parts - 1.
+// A (sequence, head tile) pair whose units the blocks first .. first + parts - 1
+// share; parts 0: none.
 struct Join {
-    int32_t b, hv, parts, pad;
+    int32_t b, hv, parts, first;
 };
+// Records by pair where the blocks are several times as many as the pairs, by
+// the block that a pair starts in otherwise.
+__host__ __device__ inline bool join_by_pair(int64_t B, int HV, int blocks) { return B * HV * 8 <= blocks; }
 struct Err {
     int32_t timeout, bad;  // role that gave up; first sequence with a bad page or length
 };
@@ -64,6 +66,8 @@ __host__ __device__ inline DecodeLayout decode_layout(int rows, int D) {
 template <int D, bool FP8, int NT>
 struct Cfg {
     static constexpr int kRows = 8 * NT;                   // query heads of a tile
+    // A consumer warp takes kGroups times 16 keys of a unit.
+    static constexpr int kGroups = D == 64 ? 2 : 1, kChunk = 16 * kCWarps * kGroups;
     // Several blocks on an SM hide each other's set-up, joins and latencies:
     // two, for fp8 three (half the bytes for the same steps: 256 sequences up
     // to 8192 keys 282 -> 277 us), except where a tile of 16 heads needs the
@@ -105,6 +109,7 @@ __device__ __forceinline__ int keys_of(const DecodeAttnArgs &a, int b) {
     const int n = __ldg(a.seq_lens + b);
     return n < 0 ? 0 : (n > most ? (int)most : n);
 }
+template <int kChunk>
 __device__ __forceinline__ void next_sequence(const DecodeAttnArgs &a, Walk &w) {
     do {
         ++w.b;
@@ -134,7 +139,7 @@ template <int D, bool FP8, int NT>
 __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, NT>::kBlocks))
 decode_kernel(const DecodeAttnArgs a, const int HV, const int RT, const __grid_constant__ CUtensorMap map) {
     using C = Cfg<D, FP8, NT>;
-    constexpr int S = C::kStages;
+    constexpr int S = C::kStages, kChunk = C::kChunk, KG = C::kGroups;
     extern __shared__ uint8_t raw[];
     const uint32_t raw_u = smem_u32(raw);
     uint8_t *base = raw + ((1024 - (raw_u & 1023)) & 1023);
@@ -198,6 +203,9 @@ decode_kernel(const DecodeAttnArgs a, const int HV, const int RT, const __grid_c
     }
     __syncthreads();
 
+    Join *const join = reinterpret_cast<Join *>(a.workspace + L.join);
+    const bool by_pair = join_by_pair(a.B, HV, gridDim.x);
+    if (!by_pair && tid == 0) join[g] = Join{0, 0, 0, 0};
     // sequences without keys: zeros
     for (int b = g; b < a.B; b += gridDim.x)
         if (keys_of(a, b) == 0) {
@@ -205,10 +213,10 @@ decode_kernel(const DecodeAttnArgs a, const int HV, const int RT, const __grid_c
                 reinterpret_cast<uint4 *>(a.out + b * a.out_stride)[i] = make_uint4(0, 0, 0, 0);
             if (a.lse)
                 for (int i = tid; i < a.Hq; i += kThreads) a.lse[(size_t)b * a.Hq + i] = -INFINITY;
+            if (by_pair)
+                for (int i = tid; i < HV; i += kThreads) join[b * HV + i] = Join{0, 0, 0, 0};
         }
 
-    Join *join = reinterpret_cast<Join *>(a.workspace + L.join) + g;
-    if (tid == 0) *join = Join{-1, 0, 0, 0};
     const int heads = a.Hq / a.kv.Hkv;  // query heads of one key/value head
     Walk w0;
     if (u0 < u1) {
@@ -249,7 +257,7 @@ decode_kernel(const DecodeAttnArgs a, const int HV, const int RT, const __grid_c
                     fresh = true;
                     if (++w.hv == HV) {
                         w.hv = 0;
-                        if (u + 1 < u1) next_sequence(a, w);
+                        if (u + 1 < u1) next_sequence<kChunk>(a, w);
                     }
                 }
                 if (u + 1 < u1) pg = page_of(w);
@@ -300,13 +308,18 @@ decode_kernel(const DecodeAttnArgs a, const int HV, const int RT, const __grid_c
                     wait_own(&sm->full[i % S], (i / S) & 1);
         }
     } else if (u0 < u1) {
-        // ---------------- consumers: keys [16 warp, 16 warp + 16) of each unit
+        // ---------------- consumers: keys [16 KG warp, 16 KG (warp + 1)) of each unit
         Walk w = w0;
         const int gq = lane >> 2, t = lane & 3;
         const uint32_t half_b = R * C::kRowB, kv_b = half_b * C::kHalves;
         // this warp's rows, then this lane's row and 16-byte column of the
         // fragment loads (K: row-major; V: transposed)
-        const uint32_t my_rows = ((16 * warp) >> box_shift) * box_bytes + ((16 * warp) & (R - 1)) * C::kRowB;
+        uint32_t my_rows[KG];
+#pragma unroll
+        for (int k = 0; k < KG; ++k) {
+            const int row = 16 * (warp * KG + k);
+            my_rows[k] = (row >> box_shift) * box_bytes + (row & (R - 1)) * C::kRowB;
+        }
         const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8;   // rows 0-7, 8-15, 0-7, 8-15
         const int lcol = lane >> 4;                            // columns 0, 0, 1, 1
         const int swz = C::kRowB == 128 ? (lrow & 7) : ((lrow >> 1) & 3);
@@ -389,66 +402,80 @@ decode_kernel(const DecodeAttnArgs a, const int HV, const int RT, const __grid_c
                         }
                     }
                 }
-                const int left = w.n - ((w.j + c) * kChunk + 16 * warp);  // keys of this warp
+                // keys of this warp's groups
+                const int left = w.n - ((w.j + c) * kChunk + 16 * KG * warp);
                 if (left > 0 && ok) {
-                    const uint32_t kr = st + my_rows, vr = kr + kv_b;
                     // (two sums in turns: a chain of products into one is
                     // as long as the tensor pipe's latency times D / 16)
-                    float sT[NT][4], sU[NT][4];
+                    float sT[KG][NT][4], sU[KG][NT][4];
 #pragma unroll
-                    for (int i = 0; i < NT; ++i)
+                    for (int k = 0; k < KG; ++k)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sT[i][e] = sU[i][e] = 0.f;
+                        for (int i = 0; i < NT; ++i)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) sT[k][i][e] = sU[k][i][e] = 0.f;
                     if (!FP8) {
 #pragma unroll
-                        for (int d = 0; d < D / 16; ++d) {
-                            uint32_t k4[4];
-                            ldsm4(k4, frag(kr, 2 * d));
+                        for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-                            for (int i = 0; i < NT; ++i)
-                                mma16816<true>(d & 1 ? sU[i] : sT[i], k4, qf[i][d][0], qf[i][d][1]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int d = 0; d < D / 16; d += 2) {
-                            uint32_t k4[4];
-                            ldsm4(k4, frag(kr, d));
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const uint32_t lo = k4[2 * e], hi = k4[2 * e + 1];
-                                const uint32_t af[4] = {e4m3_pair(lo), e4m3_pair(hi), e4m3_pair(lo >> 16),
-                                                        e4m3_pair(hi >> 16)};
+                            for (int k = 0; k < KG; ++k) {
+                                uint32_t k4[4];
+                                ldsm4(k4, frag(st + my_rows[k], 2 * d));
 #pragma unroll
                                 for (int i = 0; i < NT; ++i)
-                                    mma16816<false>(e & 1 ? sU[i] : sT[i], af, qf[i][d + e][0], qf[i][d + e][1]);
+                                    mma16816<true>(d & 1 ? sU[k][i] : sT[k][i], k4, qf[i][d][0], qf[i][d][1]);
                             }
+                    } else {
+#pragma unroll
+                        for (int d = 0; d < D / 16; d += 2)
+#pragma unroll
+                            for (int k = 0; k < KG; ++k) {
+                                uint32_t k4[4];
+                                ldsm4(k4, frag(st + my_rows[k], d));
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const uint32_t lo = k4[2 * e], hi = k4[2 * e + 1];
+                                    const uint32_t af[4] = {e4m3_pair(lo), e4m3_pair(hi), e4m3_pair(lo >> 16),
+                                                            e4m3_pair(hi >> 16)};
+#pragma unroll
+                                    for (int i = 0; i < NT; ++i)
+                                        mma16816<false>(e & 1 ? sU[k][i] : sT[k][i], af, qf[i][d + e][0],
+                                                        qf[i][d + e][1]);
+                                }
+                            }
+                    }
+                    // this lane's keys gq and gq + 8 of a group
+                    float ks[KG][2], vs[KG][2];
+                    bool see[KG][2];
+#pragma unroll
+                    for (int k = 0; k < KG; ++k) {
+                        if (FP8) {
+                            const int row = 16 * (warp * KG + k);
+                            const float *sc = reinterpret_cast<const float *>(base + s * C::kStage + C::kData + C::kQ) +
+                                              (row >> box_shift) * R * 2 + (row & (R - 1));
+                            ks[k][0] = sc[gq];
+                            ks[k][1] = sc[gq + 8];
+                            vs[k][0] = sc[R + gq];
+                            vs[k][1] = sc[R + gq + 8];
                         }
+                        see[k][0] = 16 * k + gq < left;
+                        see[k][1] = 16 * k + gq + 8 < left;
                     }
-#pragma unroll
-                    for (int i = 0; i < NT; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) sT[i][e] += sU[i][e];
-                    // this lane's keys gq and gq + 8
-                    float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
-                    if (FP8) {
-                        const float *sc = reinterpret_cast<const float *>(base + s * C::kStage + C::kData + C::kQ) +
-                                          ((16 * warp) >> box_shift) * R * 2 + ((16 * warp) & (R - 1));
-                        ks[0] = sc[gq];
-                        ks[1] = sc[gq + 8];
-                        vs[0] = sc[R + gq];
-                        vs[1] = sc[R + gq + 8];
-                    }
-                    const bool see0 = gq < left, see1 = gq + 8 < left;
-                    uint32_t pf[NT][2], pl[NT][2];  // the weights' upper and lower parts
+                    uint32_t pf[KG][NT][2], pl[KG][NT][2];  // the weights' upper and lower parts
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
-                        float x[4];
+                        float x[KG][4], t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float v = sT[i][e] * (FP8 ? sc2[i][e & 1] * ks[e >> 1] : sc2[i][e & 1]);
-                            x[e] = (e < 2 ? see0 : see1) ? v : -INFINITY;
+                        for (int k = 0; k < KG; ++k) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float v = (sT[k][i][e] + sU[k][i][e]) *
+                                                (FP8 ? sc2[i][e & 1] * ks[k][e >> 1] : sc2[i][e & 1]);
+                                x[k][e] = see[k][e >> 1] ? v : -INFINITY;
+                            }
+                            t0 = fmaxf(t0, fmaxf(x[k][0], x[k][2]));
+                            t1 = fmaxf(t1, fmaxf(x[k][1], x[k][3]));
                         }
-                        float t0 = fmaxf(x[0], x[2]), t1 = fmaxf(x[1], x[3]);
 #pragma unroll
                         for (int sh = 4; sh < 32; sh <<= 1) {
                             t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, sh));
@@ -473,74 +500,81 @@ decode_kernel(const DecodeAttnArgs a, const int HV, const int RT, const __grid_c
                         }
                         const float z0 = m[i][0] == -INFINITY ? 0.f : m[i][0];
                         const float z1 = m[i][1] == -INFINITY ? 0.f : m[i][1];
-                        x[0] = ex2(x[0] - z0);
-                        x[1] = ex2(x[1] - z1);
-                        x[2] = ex2(x[2] - z0);
-                        x[3] = ex2(x[3] - z1);
-                        l[i][0] += x[0] + x[2];
-                        l[i][1] += x[1] + x[3];
-                        // Weights for the product with v, v's scale with
-                        // them: for a bf16 cache as the sum of two bf16 (one
-                        // alone would add as much error as the result's own
-                        // rounding, and the second product is free: 109 us
-                        // either way for 90 sequences up to 8192 keys), for
-                        // fp8 one, far finer than the codes (the second
-                        // costs 7% there).  The sum l keeps the unrounded.
-                        if (FP8) {
-                            x[0] = see0 ? x[0] * vs[0] : 0.f;
-                            x[1] = see0 ? x[1] * vs[0] : 0.f;
-                            x[2] = see1 ? x[2] * vs[1] : 0.f;
-                            x[3] = see1 ? x[3] * vs[1] : 0.f;
-                        }
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t hi = pack_bf16(x[2 * e], x[2 * e + 1]);
-                            const float r0 = x[2 * e] - __uint_as_float(hi << 16);
-                            const float r1 = x[2 * e + 1] - __uint_as_float(hi & 0xFFFF0000u);
-                            pf[i][e] = transpose8x8(hi);
-                            if (!FP8) pl[i][e] = transpose8x8(pack_bf16(r0, r1));
-                        }
-                    }
-                    // keys past the end hold anything: zero v there (0 x NaN)
-                    uint32_t mask0 = 0xFFFFFFFFu, mask1 = 0xFFFFFFFFu;
-                    const bool cut = !FP8 && left < 16;
-                    if (cut) {
-                        mask0 = (2 * t < left ? 0xFFFFu : 0u) | (2 * t + 1 < left ? 0xFFFF0000u : 0u);
-                        mask1 = (2 * t + 8 < left ? 0xFFFFu : 0u) | (2 * t + 9 < left ? 0xFFFF0000u : 0u);
-                    }
-                    if (!FP8) {
-                        // a row-block pair (d, d + 8) per 16 columns: the
-                        // matrices arrive as (keys 0-7, 8-15) x (d 0-7, 8-15)
+                        for (int k = 0; k < KG; ++k) {
+                            x[k][0] = ex2(x[k][0] - z0);
+                            x[k][1] = ex2(x[k][1] - z1);
+                            x[k][2] = ex2(x[k][2] - z0);
+                            x[k][3] = ex2(x[k][3] - z1);
+                            l[i][0] += x[k][0] + x[k][2];
+                            l[i][1] += x[k][1] + x[k][3];
+                            // Weights for the product with v, v's scale with
+                            // them: for a bf16 cache as the sum of two bf16 (one
+                            // alone would add as much error as the result's own
+                            // rounding, and the second product is free: 109 us
+                            // either way for 90 sequences up to 8192 keys), for
+                            // fp8 one, far finer than the codes (the second
+                            // costs 7% there).  The sum l keeps the unrounded.
+                            if (FP8) {
 #pragma unroll
-                        for (int d = 0; d < D / 16; ++d) {
-                            uint32_t v4[4];
-                            ldsm4_t(v4, frag(vr, 2 * d));
-                            uint32_t af[4] = {v4[0], v4[2], v4[1], v4[3]};
-                            if (cut) {
-                                af[0] &= mask0;
-                                af[1] &= mask0;
-                                af[2] &= mask1;
-                                af[3] &= mask1;
+                                for (int e = 0; e < 4; ++e)
+                                    x[k][e] = see[k][e >> 1] ? x[k][e] * vs[k][e >> 1] : 0.f;
                             }
-#pragma unroll
-                            for (int i = 0; i < NT; ++i) {
-                                mma16816<true>(o[i][d], af, pf[i][0], pf[i][1]);
-                                mma16816<true>(o[i][d], af, pl[i][0], pl[i][1]);
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int d = 0; d < D / 16; d += 2) {
-                            uint32_t v4[4];
-                            ldsm4_t(v4, frag(vr, d));
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                uint32_t af[4];
-                                e4m3_columns(v4[2 * e], af[0], af[1]);
-                                e4m3_columns(v4[2 * e + 1], af[2], af[3]);
+                                const uint32_t hi = pack_bf16(x[k][2 * e], x[k][2 * e + 1]);
+                                const float r0 = x[k][2 * e] - __uint_as_float(hi << 16);
+                                const float r1 = x[k][2 * e + 1] - __uint_as_float(hi & 0xFFFF0000u);
+                                pf[k][i][e] = transpose8x8(hi);
+                                if (!FP8) pl[k][i][e] = transpose8x8(pack_bf16(r0, r1));
+                            }
+                        }
+                    }
 #pragma unroll
-                                for (int i = 0; i < NT; ++i)
-                                    mma16816<true>(o[i][d + e], af, pf[i][0], pf[i][1]);
+                    for (int k = 0; k < KG; ++k) {
+                        const uint32_t vr = st + my_rows[k] + kv_b;
+                        if (!FP8) {
+                            // keys past the end hold anything: zero v there (0 x NaN)
+                            const int rest = left - 16 * k;
+                            uint32_t mask0 = 0xFFFFFFFFu, mask1 = 0xFFFFFFFFu;
+                            const bool cut = rest < 16;
+                            if (cut) {
+                                mask0 = (2 * t < rest ? 0xFFFFu : 0u) | (2 * t + 1 < rest ? 0xFFFF0000u : 0u);
+                                mask1 = (2 * t + 8 < rest ? 0xFFFFu : 0u) | (2 * t + 9 < rest ? 0xFFFF0000u : 0u);
+                            }
+                            // a row-block pair (d, d + 8) per 16 columns: the
+                            // matrices arrive as (keys 0-7, 8-15) x (d 0-7, 8-15)
+#pragma unroll
+                            for (int d = 0; d < D / 16; ++d) {
+                                uint32_t v4[4];
+                                ldsm4_t(v4, frag(vr, 2 * d));
+                                uint32_t af[4] = {v4[0], v4[2], v4[1], v4[3]};
+                                if (cut) {
+                                    af[0] &= mask0;
+                                    af[1] &= mask0;
+                                    af[2] &= mask1;
+                                    af[3] &= mask1;
+                                }
+#pragma unroll
+                                for (int i = 0; i < NT; ++i) {
+                                    mma16816<true>(o[i][d], af, pf[k][i][0], pf[k][i][1]);
+                                    mma16816<true>(o[i][d], af, pl[k][i][0], pl[k][i][1]);
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int d = 0; d < D / 16; d += 2) {
+                                uint32_t v4[4];
+                                ldsm4_t(v4, frag(vr, d));
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    uint32_t af[4];
+                                    e4m3_columns(v4[2 * e], af[0], af[1]);
+                                    e4m3_columns(v4[2 * e + 1], af[2], af[3]);
+#pragma unroll
+                                    for (int i = 0; i < NT; ++i)
+                                        mma16816<true>(o[i][d + e], af, pf[k][i][0], pf[k][i][1]);
+                                }
                             }
                         }
                     }
@@ -627,11 +661,11 @@ decode_kernel(const DecodeAttnArgs a, const int HV, const int RT, const __grid_c
                 }
             }
             asm volatile("bar.sync 1, 128;" ::: "memory");  // ml is free again
-            if (starts && !ends && tid == 0) {
+            if (starts && tid == 0 && (by_pair || !ends)) {
                 // the block that holds the pair's last unit
                 const int64_t last = u + (w.units - 1);
                 const int owner = (int)(((last + 1) * G - 1) / W);
-                *join = Join{w.b, w.hv, owner - g + 1, 0};
+                join[by_pair ? w.b * HV + w.hv : g] = Join{w.b, w.hv, ends ? 0 : owner - g + 1, g};
             }
             u += todo;
             w.j += todo;
@@ -639,7 +673,7 @@ decode_kernel(const DecodeAttnArgs a, const int HV, const int RT, const __grid_c
                 w.j = 0;
                 if (++w.hv == HV) {
                     w.hv = 0;
-                    if (u < u1) next_sequence(a, w);
+                    if (u < u1) next_sequence<kChunk>(a, w);
                 }
             }
         }
@@ -649,21 +683,21 @@ decode_kernel(const DecodeAttnArgs a, const int HV, const int RT, const __grid_c
         reinterpret_cast<Err *>(a.workspace + L.err)[g] = Err{sm->abort, sm->bad};
 }
 
-// Joins the parts of a pair that the blocks' ends cut: block c looks at what
-// decode_kernel's block c left, blockIdx.y at 4 of its rows; 4 groups of
-// threads take every fourth part, then their sums are added in order.
-constexpr int kJoinRows = 4, kJoinGroups = 4;
-template <int D>
-__global__ void __launch_bounds__(kJoinRows *kJoinGroups *D / 4)
+// Joins the parts of a pair: blockIdx.x is its record, blockIdx.y has ROWS of
+// its rows; GROUPS groups of threads take every GROUPS-th part, then their sums
+// are added in order.  Few pairs in many parts (one sequence of 131072 keys: 57
+// parts) want many groups, many pairs in two or three parts few blocks.
+template <int D, int ROWS, int GROUPS>
+__global__ void __launch_bounds__(ROWS *GROUPS *D / 4)
 decode_join(const DecodeAttnArgs a, const int RT, const int tile_rows, const int n_blocks) {
-    constexpr int kCols = D / 4, kGroup = kJoinRows * kCols;
-    __shared__ float4 part[kJoinGroups][kGroup];
-    __shared__ float2 sums[kJoinGroups][kJoinRows];
+    constexpr int kCols = D / 4, kGroup = ROWS * kCols;
+    __shared__ float4 part[GROUPS][kGroup];
+    __shared__ float2 sums[GROUPS][ROWS];
     __shared__ int red[2];
     const DecodeLayout L = decode_layout(tile_rows, D);
-    const int c = blockIdx.x, tid = threadIdx.x;
+    const int tid = threadIdx.x;
     pdl_wait();
-    if (c == 0 && blockIdx.y == 0) {
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
         // the call's status word, from every block's record
         const Err *err = reinterpret_cast<const Err *>(a.workspace + L.err);
         if (tid == 0) red[0] = 0, red[1] = 0x7fffffff;
@@ -680,17 +714,17 @@ decode_join(const DecodeAttnArgs a, const int RT, const int tile_rows, const int
             ctrl->detail = red[0] ? red[0] : (red[1] != 0x7fffffff ? red[1] : 0);
         }
     }
-    const Join jn = reinterpret_cast<const Join *>(a.workspace + L.join)[c];
-    if (jn.b < 0) return;
+    const Join jn = reinterpret_cast<const Join *>(a.workspace + L.join)[blockIdx.x];
+    if (jn.parts == 0) return;
     const int heads = a.Hq / a.kv.Hkv;
     const int hk = jn.hv / RT, r0 = (jn.hv % RT) * tile_rows;
     const int grp = tid / kGroup, in = tid % kGroup, col = in % kCols;
-    const int r = blockIdx.y * kJoinRows + in / kCols;
+    const int r = blockIdx.y * ROWS + in / kCols;
     const bool live = r < min(tile_rows, heads - r0);
     const float2 *ml = reinterpret_cast<const float2 *>(a.workspace + L.ml);
     const float *pt = reinterpret_cast<const float *>(a.workspace + L.part);
-    // the first part is block c's last one, the others are first ones
-    auto row_of = [&](int i) { return ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * tile_rows + r; };
+    // the first part is its block's last one, the others are first ones
+    auto row_of = [&](int i) { return ((size_t)(jn.first + i) * 2 + (i == 0 ? 1 : 0)) * tile_rows + r; };
     float top = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (live)
@@ -700,7 +734,7 @@ decode_join(const DecodeAttnArgs a, const int RT, const int tile_rows, const int
     if (live) {
         const float z = top == -INFINITY ? 0.f : top;
 #pragma unroll 4
-        for (int i = grp; i < jn.parts; i += kJoinGroups) {
+        for (int i = grp; i < jn.parts; i += GROUPS) {
             const float2 v = ml[row_of(i)];
             const float4 y = *reinterpret_cast<const float4 *>(pt + row_of(i) * D + col * 4);
             const float f = ex2(v.x - z);
@@ -718,7 +752,7 @@ decode_join(const DecodeAttnArgs a, const int RT, const int tile_rows, const int
     sum = 0.f;
     acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < kJoinGroups; ++k) {
+    for (int k = 0; k < GROUPS; ++k) {
         const float4 y = part[k][in];
         sum += sums[k][in / kCols].x;
         acc.x += y.x;
@@ -743,7 +777,7 @@ template <int D, bool FP8, int NT>
 cudaError_t run(const DecodeAttnArgs &a, int sms, cudaStream_t s) {
     using C = Cfg<D, FP8, NT>;
     CUtensorMap map;
-    const int page = 1 << a.kv.page_shift, R = page < kChunk ? page : kChunk;
+    const int page = 1 << a.kv.page_shift, R = page < 64 ? page : 64;
     const size_t row_b = (size_t)D * C::kEs;
     const uint64_t dims[5] = {(uint64_t)C::kRowB / C::kEs, (uint64_t)page, (uint64_t)C::kHalves, 2,
                               (uint64_t)a.kv.num_pages * a.kv.Hkv};
@@ -755,7 +789,7 @@ cudaError_t run(const DecodeAttnArgs &a, int sms, cudaStream_t s) {
         return cudaErrorInvalidValue;
     const int G = a.Hq / a.kv.Hkv, RT = (G + C::kRows - 1) / C::kRows, HV = a.kv.Hkv * RT;
     // no more blocks than units could exist
-    const int64_t units = (int64_t)a.B * HV * (((int64_t)a.table_stride * page + kChunk - 1) / kChunk);
+    const int64_t units = (int64_t)a.B * HV * (((int64_t)a.table_stride * page + C::kChunk - 1) / C::kChunk);
     int grid = C::kBlocks * sms < kMaxGrid ? C::kBlocks * sms : kMaxGrid;
     if (units < grid) grid = (int)units;
     auto fn = decode_kernel<D, FP8, NT>;
@@ -770,15 +804,18 @@ cudaError_t run(const DecodeAttnArgs &a, int sms, cudaStream_t s) {
     err = cudaLaunchKernelEx(&cfg, fn, a, HV, RT, map);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cj = {};
-    cj.gridDim = dim3(grid, (C::kRows + kJoinRows - 1) / kJoinRows);
-    cj.blockDim = dim3(kJoinRows * kJoinGroups * D / 4);
+    const bool by_pair = join_by_pair(a.B, HV, grid);
+    const int rows = by_pair ? 1 : 4, groups = by_pair ? 16 : 4;
+    cj.gridDim = dim3(by_pair ? a.B * HV : grid, C::kRows / rows);
+    cj.blockDim = dim3(rows * groups * D / 4);
     cj.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cj.attrs = at;
     cj.numAttrs = 1;
-    return cudaLaunchKernelEx(&cj, decode_join<D>, a, RT, (int)C::kRows, grid);
+    return by_pair ? cudaLaunchKernelEx(&cj, decode_join<D, 1, 16>, a, RT, (int)C::kRows, grid)
+                   : cudaLaunchKernelEx(&cj, decode_join<D, 4, 4>, a, RT, (int)C::kRows, grid);
 }
 
 template <int D, bool FP8>
