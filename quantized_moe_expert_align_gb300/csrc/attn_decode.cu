@@ -8,13 +8,13 @@
 //    16 x 8 x 16 matrix instructions whose 16-row side is the keys (then the
 //    values' columns) and whose 8-column side is the query heads, so up to 8
 //    heads waste nothing and the cache is read from shared memory once;
-//  * work is cut into units of 64 keys of one (sequence, key/value head);
+//  * work is cut into units of 64 or 128 keys of one (sequence, key/value head);
 //    the units of the whole batch, in order, are shared out evenly over two or
 //    three blocks per SM whatever the lengths are.  A pair cut by a block's end is
 //    joined by a second kernel, in key order, so results do not depend on
 //    timing;
-//  * one warp of a block copies (TMA, a ring of stages), four warps take 16
-//    of a unit's 64 keys each, with a running maximum and sum of their own,
+//  * one warp of a block copies (TMA, a ring of stages), four warps take 16 or
+//    32 of a unit's keys each, with a running maximum and sum of their own,
 //    joined once per (sequence, head).
 // Rows of 128 bytes are swizzled by the copy (64-byte rows likewise), so the
 // fragment loads are free of bank conflicts.
@@ -22,8 +22,11 @@
 // Measured on one GB300 (copy rate 6.79 TB/s): 256 sequences up to 8192 keys,
 // 64 heads over 8, fp8, 1.79 GB in 276 us (6.5 TB/s); 90 up to 8192, 32 over 4,
 // bf16 pages of 16, 657 MB in 108 us (6.1 TB/s); one of 131072 keys, fp8, 277
-// MB in 54.7 us, of which 41 are the bytes and the rest the set-up (lengths,
-// page table, first copies) and the join (7 us); one of 517 keys 10.2 us.
+// MB in 53 us, of which 41 are the bytes and the rest the set-up (lengths, page
+// table, first copies) and the join; one of 517 keys 10.2 us.  More heads per
+// byte, or fewer bytes per key, are bound by the latency of a warp's chain of
+// steps instead: 64 sequences up to 8192 keys, 64 heads of 128 over 4, fp8, 66
+// us (39 for the bytes), bf16 94 (76); 64 of 64 over 8 54 (40) and 87 (75).
 #include "attn_common.cuh"
 #include "gemm_tc.h"
 
@@ -66,12 +69,17 @@ __host__ __device__ inline DecodeLayout decode_layout(int rows, int D) {
 template <int D, bool FP8, int NT>
 struct Cfg {
     static constexpr int kRows = 8 * NT;                   // query heads of a tile
-    // A consumer warp takes kGroups times 16 keys of a unit.
-    static constexpr int kGroups = D == 64 ? 2 : 1, kChunk = 16 * kCWarps * kGroups;
+    // A consumer warp takes kGroups times 16 keys of a unit: two where a unit's
+    // fixed steps (waits, maxima, votes) cost more than its bytes (64 sequences
+    // up to 8192 keys, fp8: 64 heads of 64 over 8 63.5 -> 54.4 us, 64 of 128
+    // over 4 72.9 -> 66.3).
+    static constexpr int kGroups = D == 64 || (FP8 && NT == 2) ? 2 : 1;
+    static constexpr int kChunk = 16 * kCWarps * kGroups;
     // Several blocks on an SM hide each other's set-up, joins and latencies:
     // two, for fp8 three (half the bytes for the same steps: 256 sequences up
     // to 8192 keys 282 -> 277 us), except where a tile of 16 heads needs the
-    // registers of two (64 sequences, 64 heads over 4: 122 us with three, 74).
+    // registers of two (64 sequences, 64 heads over 4, units of 64 keys:
+    // 122 us with three, 74).
     static constexpr int kBlocks = FP8 && (NT == 1 || D == 64) ? 3 : 2;
     static constexpr int kSmemLimit = (kBlocks == 2 ? 113 : 75) * 1024;
     static constexpr int kEs = FP8 ? 1 : 2;
