@@ -22,8 +22,8 @@
 //
 // A planning kernel lists the items by falling number of key tiles; the
 // blocks take them from a counter, longest first.  Where a few items have
-// more key tiles than an SM's even share of the whole work, they are cut into
-// parts, whose unscaled sums a last kernel joins in order.  Small calls (at
+// several times the key tiles of an SM's even share of the whole work, they are
+// cut into parts, whose unscaled sums a last kernel joins in order.  Small calls (at
 // most 32 sequences and kMinKeys keys in all, where nothing is cut) do
 // without the plan: every block finds its own items.
 //
@@ -53,7 +53,10 @@ constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 1024;
 constexpr float kSlack = 8.f;    // a row's maximum may exceed its reference by this
 
-constexpr int kMinKeys = 1024;   // a key range is not cut below this
+constexpr int kMinKeys = 1024;   // with no more keys in all, no key range is cut
+constexpr int kMinPart = 4;      // key tiles of a part at least
+// What the plan reckons with: a round of one key tile, a join, a part.
+constexpr int kRound = 32, kJoinCost = 128, kPartCost = 1;
 constexpr int kMaxSms = 160;     // blocks of the main kernel at most
 constexpr int kMaxParts = 2 * kMaxSms;  // of one call, all heads together
 
@@ -178,9 +181,8 @@ __device__ __forceinline__ unsigned long long warp_total(unsigned long long v) {
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks) {
     __shared__ int count[kBuckets], warp_sum[kPlanThreads / 32], first_bad, joins, slots, longest;
-    __shared__ unsigned long long all_tiles;
+    __shared__ unsigned long long all_tiles, best;  // best: cost, key tiles of an item
     const int tokens = kM * tpt;  // of a block
-    constexpr int kMinPart = kMinKeys / kKeys;
     const PrefillLayout L = prefill_layout(a.B, a.Tq, tokens, a.D);
     const int tid = threadIdx.x, lane = tid & 31;
     pdl_trigger();
@@ -189,6 +191,7 @@ plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks
         first_bad = 0x7fffffff;
         joins = slots = longest = 0;
         all_tiles = 0;
+        best = ~0ull;
     }
     __syncthreads();
     const int64_t room = (int64_t)a.Tq / tokens + a.B + kMaxSms;
@@ -217,9 +220,8 @@ plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks
         longest_mine = max(longest_mine, tiles);
         atomicAdd(&count[bucket_of(tiles)], 1);
     });
-    int most = kMinPart;
+    int most = 0x7fffff;  // key tiles of an item
     if (a.Tk > kMinKeys) {
-        // A key range longer than a block's even share of everything is cut.
         mine_tiles = warp_total(mine_tiles);
         longest_mine = __reduce_max_sync(0xffffffffu, longest_mine);
         if (lane == 0 && mine_tiles) {
@@ -227,8 +229,35 @@ plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks
             atomicMax(&longest, longest_mine);
         }
         __syncthreads();
-        const unsigned long long share = (all_tiles * HV + n_blocks - 1) / n_blocks;
-        most = (int)min((unsigned long long)0x7fffff, max(share, (unsigned long long)kMinPart));
+        // Warp n looks at the longest key range in n + 1 parts, the last one at
+        // parts of an even share of everything, and what that leaves the
+        // busiest block to do: its items one after another if they are few,
+        // little more than the share if they are many; and parts have to be
+        // written, read and joined.  (A cut of everything above the share: 76
+        // us instead of 54 for 1024 rows over 4096 keys, 32 heads over 4, 65
+        // instead of 37 for 16 sequences of 64 rows over 2048.)
+        const int64_t share = (int64_t)((all_tiles * HV + n_blocks - 1) / n_blocks);
+        const int64_t least = max(share, (int64_t)kMinPart);
+        if (longest > least) {
+            const int n = tid >> 5;
+            const uint32_t m = n == 31 ? (uint32_t)least : ((uint32_t)longest + n) / (n + 1);
+            uint32_t big = 0, parts = 0;  // items above half of m; parts of cut ranges
+            if (n == 0 || m >= least)
+                for (uint32_t tiles = lane; tiles <= (uint32_t)min(longest, kBuckets - 1); tiles += 32) {
+                    const uint32_t c = count[kBuckets - 1 - tiles];
+                    if (c == 0 || 2 * tiles <= m) continue;
+                    const uint32_t in = c * ((tiles + m - 1) / m);
+                    big += in;
+                    if (tiles > m) parts += in;
+                }
+            const int64_t all_big = (int64_t)__reduce_add_sync(0xffffffffu, big) * HV;
+            const int64_t all_parts = (int64_t)__reduce_add_sync(0xffffffffu, parts) * HV;
+            const int64_t rounds = max(share, min((all_big + n_blocks - 1) / n_blocks * m, share + m));
+            const int64_t cost = kRound * rounds + (all_parts ? kJoinCost + all_parts * kPartCost : 0);
+            if (lane == 0 && (n == 0 || m >= least)) atomicMin(&best, (unsigned long long)cost << 32 | m);
+            __syncthreads();
+            most = (int)(best & 0xffffffffu);
+        }
     }
     __syncthreads();
     const bool cut = longest > most;
@@ -930,10 +959,42 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
     }
 }
 
-// Joins the parts of cut key ranges: a block takes 32 neighbouring rows and 8
-// columns, its warps every fourth part each, a lane a row; the warps' sums are
-// then added in order.
-constexpr int kJoinWarps = 4;
+// Joins the parts of cut key ranges, 32 neighbouring rows (a lane each) and 8
+// columns at a time.  Up to kFewParts parts: by one warp, all of its loads in
+// flight (4 sequences of 100 rows over 3000 keys, 32 heads over 4: the call 45
+// -> 41 us).  More: by a block, whose warps take every fourth part; their sums
+// are then added in order.
+constexpr int kJoinWarps = 4, kFewParts = 8;
+
+// The sums of some parts of a row's 8 columns.
+struct PartSums {
+    float top = -INFINITY, sum = 0.f, o[8] = {};
+};
+// Parts first, first + step, ... of a block of `parts` whose first has place
+// `slot`: row r of row tile t, columns c to c + 7.
+template <int D>
+__device__ __forceinline__ PartSums take_parts(const float2 *ml, const float *sums, int slot, int parts, int first,
+                                               int step, int t, int c, int r) {
+    PartSums x;
+#pragma unroll 8
+    for (int p = first; p < parts; p += step)
+        x.top = fmaxf(x.top, ml[((size_t)(slot + p) * kM + t) * kTile + r].x);
+    const float z = x.top == -INFINITY ? 0.f : x.top;
+#pragma unroll 8
+    for (int p = first; p < parts; p += step) {
+        const float2 v = ml[((size_t)(slot + p) * kM + t) * kTile + r];
+        const float4 lo = *reinterpret_cast<const float4 *>(sums + part_at(slot + p, t, c, r, D));
+        const float4 hi = *reinterpret_cast<const float4 *>(sums + part_at(slot + p, t, c + 4, r, D));
+        const float f = ex2(v.x - z);
+        const bool empty = v.x == -INFINITY && v.y == 0.f;  // no key of this part
+        const float e[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        x.sum = empty ? x.sum : fmaf(f, v.y, x.sum);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x.o[i] = empty ? x.o[i] : fmaf(f, e[i], x.o[i]);
+    }
+    return x;
+}
+
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const PrefillArgs a, const int HT) {
     __shared__ float shared[kJoinWarps][10][32];  // per warp: maximum, sum, 8 columns
@@ -946,70 +1007,74 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const PrefillArgs
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kCols = D / 8, kRowGroups = kTile / 32;
     const int64_t work = (int64_t)head.joins * HV * kM * kRowGroups * kCols;
-    for (int64_t w = blockIdx.x; w < work; w += gridDim.x) {
-        const int c = (int)(w % kCols) * 8, rg = (int)(w / kCols) % kRowGroups;
-        const int t = (int)(w / (kCols * kRowGroups)) % kM;
+    // What number w is: a lane's row (if it has one), its part and its columns.
+    struct Work {
+        int t, c, r, h, slot, parts, tok;
+        int64_t row;  // of q, -1: none
+    };
+    auto work_of = [&](int64_t w) {
+        Work k;
+        k.c = (int)(w % kCols) * 8;
+        k.r = (int)(w / kCols) % kRowGroups * 32 + lane;
+        k.t = (int)(w / (kCols * kRowGroups)) % kM;
         const int64_t bh = w / (kM * kCols * kRowGroups);
         const Split sp = reinterpret_cast<const Split *>(a.workspace + L.splits)[bh / HV];
-        const int hv = (int)(bh % HV);
-        const int r = rg * 32 + lane;
-        const int g = r % Gt, g0 = (hv % HT) * Gt;
-        const int tok = sp.tok0 + t * tpt + r / Gt;
-        const bool live = r / Gt < tpt && tok < sp.nq && g < min(Gt, G - g0);
-        if (!__any_sync(0xffffffffu, live)) continue;  // (the same in all warps)
-        const int slot = sp.slot + hv * sp.parts;
-        float top = -INFINITY, sum = 0.f, o[8] = {};
-        if (live) {
-#pragma unroll 8
-            for (int p = warp; p < sp.parts; p += kJoinWarps)
-                top = fmaxf(top, ml[((size_t)(slot + p) * kM + t) * kTile + r].x);
-            const float z = top == -INFINITY ? 0.f : top;
-#pragma unroll 8
-            for (int p = warp; p < sp.parts; p += kJoinWarps) {
-                const float2 v = ml[((size_t)(slot + p) * kM + t) * kTile + r];
-                const float4 x = *reinterpret_cast<const float4 *>(sums + part_at(slot + p, t, c, r, D));
-                const float4 y = *reinterpret_cast<const float4 *>(sums + part_at(slot + p, t, c + 4, r, D));
-                const float f = ex2(v.x - z);
-                const bool empty = v.x == -INFINITY && v.y == 0.f;  // no key of this part
-                const float e[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-                sum = empty ? sum : fmaf(f, v.y, sum);
+        const int hv = (int)(bh % HV), g0 = (hv % HT) * Gt, g = k.r % Gt;
+        k.tok = sp.tok0 + k.t * tpt + k.r / Gt;
+        const bool live = k.r / Gt < tpt && k.tok < sp.nq && g < min(Gt, G - g0);
+        k.row = live ? (int64_t)sp.q0 + k.tok : -1;
+        k.h = (hv / HT) * G + g0 + g;
+        k.slot = sp.slot + hv * sp.parts;
+        k.parts = sp.parts;
+        return k;
+    };
+    auto put = [&](const Work &k, const PartSums &x) {
+        const bool none = x.sum == 0.f;
+        const float inv = 1.f / x.sum;
+        float o[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = empty ? o[i] : fmaf(f, e[i], o[i]);
-            }
-        }
-        shared[warp][0][lane] = top;
-        shared[warp][1][lane] = sum;
+        for (int i = 0; i < 8; ++i) o[i] = none ? 0.f : x.o[i] * inv;
+        *reinterpret_cast<uint4 *>(a.out + k.row * a.out_stride + k.h * D + k.c) =
+            make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
+        if (a.lse && k.c == 0)
+            a.lse[(size_t)k.row * a.Hq + k.h] = none ? -INFINITY : (x.top + __log2f(x.sum)) * kLn2;
+    };
+    for (int64_t w = (int64_t)blockIdx.x * kJoinWarps + warp; w < work; w += gridDim.x * kJoinWarps) {
+        const Work k = work_of(w);
+        if (k.parts <= kFewParts && k.row >= 0)
+            put(k, take_parts<D>(ml, sums, k.slot, k.parts, 0, 1, k.t, k.c, k.r));
+    }
+    for (int64_t w = blockIdx.x; w < work; w += gridDim.x) {
+        const Work k = work_of(w);
+        // (both the same in all warps)
+        if (k.parts <= kFewParts || !__any_sync(0xffffffffu, k.row >= 0)) continue;
+        PartSums x;
+        if (k.row >= 0) x = take_parts<D>(ml, sums, k.slot, k.parts, warp, kJoinWarps, k.t, k.c, k.r);
+        shared[warp][0][lane] = x.top;
+        shared[warp][1][lane] = x.sum;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) shared[warp][2 + i][lane] = o[i];
+        for (int i = 0; i < 8; ++i) shared[warp][2 + i][lane] = x.o[i];
         __syncthreads();
-        if (warp == 0 && live) {
+        if (warp == 0 && k.row >= 0) {
 #pragma unroll
-            for (int k = 1; k < kJoinWarps; ++k) top = fmaxf(top, shared[k][0][lane]);
-            const float z = top == -INFINITY ? 0.f : top;
-            sum = 0.f;
+            for (int p = 1; p < kJoinWarps; ++p) x.top = fmaxf(x.top, shared[p][0][lane]);
+            const float z = x.top == -INFINITY ? 0.f : x.top;
+            x.sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = 0.f;
+            for (int i = 0; i < 8; ++i) x.o[i] = 0.f;
 #pragma unroll
-            for (int k = 0; k < kJoinWarps; ++k) {
-                const float m = shared[k][0][lane], f = m == -INFINITY ? 0.f : ex2(m - z);
+            for (int p = 0; p < kJoinWarps; ++p) {
+                const float m = shared[p][0][lane], f = m == -INFINITY ? 0.f : ex2(m - z);
                 // (a warp without a key has sums of 0; NaN has no maximum)
-                const float s1 = shared[k][1][lane];
-                sum += m == -INFINITY ? s1 : f * s1;
+                const float s1 = shared[p][1][lane];
+                x.sum += m == -INFINITY ? s1 : f * s1;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float e = shared[k][2 + i][lane];
-                    o[i] += m == -INFINITY ? e : f * e;
+                    const float e = shared[p][2 + i][lane];
+                    x.o[i] += m == -INFINITY ? e : f * e;
                 }
             }
-            const bool none = sum == 0.f;
-            const float inv = 1.f / sum;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = none ? 0.f : o[i] * inv;
-            const int h = (hv / HT) * G + g0 + g;
-            *reinterpret_cast<uint4 *>(a.out + (sp.q0 + tok) * a.out_stride + h * D + c) =
-                make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
-            if (a.lse && c == 0)
-                a.lse[(size_t)(sp.q0 + tok) * a.Hq + h] = none ? -INFINITY : (top + __log2f(sum)) * kLn2;
+            put(k, x);
         }
         __syncthreads();
     }
@@ -1068,7 +1133,7 @@ cudaError_t run(const PrefillArgs &a, int sms, cudaStream_t s) {
     err = cudaLaunchKernelEx(&cfg, fn, a, HT, planned, mq, mk, mv);
     if (err != cudaSuccess || !cuts) return err;
     cudaLaunchConfig_t cj = {};
-    cj.gridDim = dim3(16 * sms);
+    cj.gridDim = dim3(8 * sms);  // (16: up to 2 us more where there is nothing to join)
     cj.blockDim = dim3(32 * kJoinWarps);
     cj.stream = s;
     cj.attrs = at;
