@@ -92,10 +92,10 @@ __device__ __forceinline__ void write_status(Ctrl *ctrl, int first_bad) {
     ctrl->detail = first_bad == kNone ? 0 : first_bad;
 }
 
-__device__ __forceinline__ bool token_ok(const AppendArgs &a, int t, int &slot) {
-    slot = (a.data && a.slots) ? __ldg(a.slots + t) : -1;
-    const bool pos_ok = a.rot == 0 || (unsigned)__ldg(a.positions + t) < (unsigned)a.max_pos;
-    return pos_ok && slot >= -1 && slot < (a.num_pages << a.page_shift);
+// (slot is -1 without a cache, the position 0 without a rotation)
+__device__ __forceinline__ bool token_ok(const AppendArgs &a, int pos, int slot) {
+    return (a.rot == 0 || (unsigned)pos < (unsigned)a.max_pos) && slot >= -1 &&
+           slot < (a.num_pages << a.page_shift);
 }
 
 // Block (0, 0) looks every token over and writes the status word; blocks
@@ -246,12 +246,22 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     constexpr int NG = kAppendThreads / L; // groups per block
     if (blockIdx.x == 0) {
         if (blockIdx.y) return;
-        int bad = kNone, slot;
-        // (the loads of 16 tokens a thread in flight at a time: 8689 tokens of 10
-        // rows would otherwise wait for this block)
-#pragma unroll 16
-        for (int t = threadIdx.x; t < a.T; t += kAppendThreads)
-            if (!token_ok(a, t, slot)) bad = min(bad, t);
+        // 16 tokens a thread at a time: what a block of its own can be late with
+        // is latency (15015 tokens of 7 rows: 47 us one after another)
+        constexpr int kAtOnce = 16;
+        int bad = kNone;
+        for (int64_t t0 = threadIdx.x; t0 < a.T; t0 += kAtOnce * kAppendThreads) {
+            int slot[kAtOnce], pos[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int64_t t = t0 + i * kAppendThreads;
+                slot[i] = t < a.T && a.data ? __ldg(a.slots + t) : -1;
+                pos[i] = t < a.T && a.rot ? __ldg(a.positions + t) : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+                if (!token_ok(a, pos[i], slot[i])) bad = min(bad, (int)t0 + i * kAppendThreads);
+        }
         bad = block_min(bad);
         if (threadIdx.x == 0) write_status(a.ctrl, bad);
         return;
@@ -277,12 +287,13 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
             ahead[u][0] = *reinterpret_cast<const uint2 *>(q + (r + u * step) * D + p.dA);
             ahead[u][1] = *reinterpret_cast<const uint2 *>(q + (r + u * step) * D + p.dB);
         }
-    int slot;
-    if (!token_ok(a, t, slot)) return;
+    const int slot = a.data ? __ldg(a.slots + t) : -1;
+    const int pos = a.rot ? __ldg(a.positions + t) : 0;
+    if (!token_ok(a, pos, slot)) return;
     // this lane's four pairs are the pairs 4 lane .. 4 lane + 3
     float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (turned) {
-        const float *row = a.cos_sin + (size_t)__ldg(a.positions + t) * a.rot + p.lane * 4;
+        const float *row = a.cos_sin + (size_t)pos * a.rot + p.lane * 4;
         c = __ldg(reinterpret_cast<const float4 *>(row));
         s = __ldg(reinterpret_cast<const float4 *>(row + half));
     }
