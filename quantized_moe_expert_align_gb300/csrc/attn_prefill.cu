@@ -236,7 +236,11 @@ plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks
         // written, read and joined.  (A cut of everything above the share: 76
         // us instead of 54 for 1024 rows over 4096 keys, 32 heads over 4, 65
         // instead of 37 for 16 sequences of 64 rows over 2048.)
-        const int64_t share = (int64_t)((all_tiles * HV + n_blocks - 1) / n_blocks);
+        // (64-bit divisions take long, and these operands are small as a rule)
+        auto by_blocks = [&](int64_t x) {
+            return x >> 32 ? (x + n_blocks - 1) / n_blocks : (int64_t)(((uint32_t)x - 1) / n_blocks + 1);
+        };
+        const int64_t share = all_tiles ? by_blocks(all_tiles * HV) : 0;
         const int64_t least = max(share, (int64_t)kMinPart);
         if (longest > least) {
             const int n = tid >> 5;
@@ -252,7 +256,7 @@ plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks
                 }
             const int64_t all_big = (int64_t)__reduce_add_sync(0xffffffffu, big) * HV;
             const int64_t all_parts = (int64_t)__reduce_add_sync(0xffffffffu, parts) * HV;
-            const int64_t rounds = max(share, min((all_big + n_blocks - 1) / n_blocks * m, share + m));
+            const int64_t rounds = max(share, min(all_big ? by_blocks(all_big) * m : 0, share + m));
             const int64_t cost = kRound * rounds + (all_parts ? kJoinCost + all_parts * kPartCost : 0);
             if (lane == 0 && (n == 0 || m >= least)) atomicMin(&best, (unsigned long long)cost << 32 | m);
             __syncthreads();
@@ -286,8 +290,7 @@ plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks
     }
     if (lane == 31) warp_sum[tid >> 5] = scan;
     __syncthreads();
-    int before = 0;
-    for (int w = 0; w < tid >> 5; ++w) before += warp_sum[w];
+    const int before = __reduce_add_sync(0xffffffffu, lane < tid >> 5 ? warp_sum[lane] : 0);
     count[tid] = before + scan - mine;
     const int total = before + scan;  // (of the last thread: of all)
     __syncthreads();
