@@ -4,10 +4,9 @@
 //   gather: cached tokens of sequences back as packed bf16 rows.
 // Both move every byte once and do little else, so HBM bounds them; measured on
 // one GB300 (copy rate 6.79 TB/s): append of 16384 tokens, 64 + 8 + 8 heads of
-// 128, fp8 cache and k_out, 681 MB in 119 us (5.7 TB/s; 127 us when three such
-// batches take turns), gather of 8 contexts up to 32768 tokens, fp8, 605 MB in
-// 94.5 us (6.4 TB/s).  A call of a few tokens takes 4.7 us on the GPU, less
-// than the host needs to make it.
+// 128, fp8 cache and k_out, 681 MB in 118 us (5.8 TB/s), gather of 8 contexts up
+// to 32768 tokens, fp8, 605 MB in 94.5 us (6.4 TB/s).  A call of a few tokens
+// takes 4.7 us on the GPU, less than the host needs to make it.
 #include "attn.h"
 #include "device_common.cuh"
 

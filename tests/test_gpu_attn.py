@@ -75,6 +75,14 @@ def test_decode_many_sequences(gpu, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_few_long_sequences(gpu, D, fp8):
+    """Few pairs over all of the GPU, empty sequences between them."""
+    _decode([0, 9001, 0, 20037, 1], 16, 1, D, fp8, 64, seed=21)
+    _decode([4111, 0], 5, 1, D, fp8, 32, seed=22)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_decode_score_ranges(gpu, fp8):
     """Scores from one dominating key to all but equal, wide and tiny q."""
     _decode([600, 77], 8, 2, 128, fp8, 16, seed=4, scale=3.0)
@@ -235,6 +243,13 @@ def test_prefill(gpu, nq, nk, Hq, Hkv, D, causal):
 def test_prefill_few_rows_over_many_keys(gpu, nq, nk, Hq, Hkv, D, causal):
     """Key ranges that are cut into parts and joined."""
     _prefill(nq, nk, Hq, Hkv, D, causal, seed=8)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_ranges_in_two_to_eight_parts(gpu, D):
+    _prefill([90, 0, 41], [3000, 100, 2500], 16, 2, D, True, seed=31)
+    _prefill([130], [4000], 9, 3, D, False, seed=32)
+    _prefill([33, 5], [8000, 6500], 16, 4, D, True, seed=33)
 
 
 def test_prefill_contiguous_rows_and_scales(gpu):
