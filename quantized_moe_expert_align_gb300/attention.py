@@ -8,7 +8,8 @@ word (``moe_w4a16_get_device_status(workspace.buf)``).
 Rows may be strided between tokens (the three parts of one fused projection);
 the heads of a token and the values of a head are contiguous.  Tensors have
 to live on the current device and be ready on the stream of the call (the
-current stream unless ``stream`` is given).
+current stream unless ``stream`` is given).  What a call allocates comes from
+the memory pool of that stream.
 """
 from __future__ import annotations
 
@@ -181,24 +182,36 @@ def _on(stream, t):
     return getattr(stream, "cuda_stream", stream)
 
 
-def _made(t, stream):
-    """A buffer allocated here for a call on ``stream``: when that is not the
-    current stream, torch must not reuse the memory before the call is done."""
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(stream)
-        t.record_stream(stream)
+def _pool_of(stream):
+    """A context in which torch takes memory from the pool of the call's
+    stream.  A block of the current stream's pool may still be read or written
+    by kernels queued there, which a call on another stream does not wait for."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream))
+    return torch.cuda.stream(stream)
+
+
+def _result(shape, dtype, device, stream):
+    """A new buffer for what a call returns.  On a stream of the call's own it
+    is marked as used by the current stream too, where the caller reads it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _pool_of(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
 def _rows_out(T, H, D, device, stream):
-    return _made(torch.empty((T, H, D), dtype=torch.bfloat16, device=device), stream)
+    return _result((T, H, D), torch.bfloat16, device, stream)
 
 
 def _workspace(ws, stream, device, *size):
     if ws is None:
-        ws = AttnWorkspace(device, *size)
-        _made(ws.buf, stream)
+        if stream is None:
+            return AttnWorkspace(device, *size)
+        with _pool_of(stream):
+            return AttnWorkspace(device, *size)
     return ws
 
 
@@ -313,7 +326,7 @@ def attn_prefill(q, k, v, cu_q, cu_k, causal=True, scale=None, out=None, lse=Non
 
 def _lse(lse, T, Hq, device, stream):
     if lse is True:
-        return _made(torch.empty((T, Hq), dtype=torch.float32, device=device), stream)
+        return _result((T, Hq), torch.float32, device, stream)
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, Hq) or
                             not lse.is_contiguous() or not lse.is_cuda):
         raise ValueError(f"lse: contiguous float32 {(T, Hq)} on a GPU expected")
