@@ -113,6 +113,7 @@ enum Kind { kQuery, kKey, kValue };
 // A lane's place in a row.
 struct Place {
     int lane, dA, dB;
+    bool turned;      // its values are rotated
     uint32_t group;   // the lanes of its group
 };
 
@@ -142,7 +143,9 @@ __device__ __forceinline__ Turn fold(const uint16_t *w, const Place &p, bool int
 }
 
 // Rows r, r + step, ... < n of one kind, the next two on the way at any time.
-template <int D, bool FP8, int KIND>
+// PART: some values of a row are not rotated (16384 tokens of 64 + 8 + 8 rows:
+// 118.7 us, 117.2 where all are).
+template <int D, bool FP8, bool PART, int KIND>
 __device__ __forceinline__ void walk(const AppendArgs &a, const Place &p, const Turn &f, bool norm,
                                      const uint16_t *src, uint16_t *dst, int &r, int n, int step, int slot,
                                      const uint2 (&ahead)[2][2]) {
@@ -190,8 +193,12 @@ __device__ __forceinline__ void walk(const AppendArgs &a, const Place &p, const 
                 for (int k = 0; k < 2; ++k) {
                     const float2 A = mul2(make_float2(x[2 * k], x[2 * k + 1]), rms);
                     const float2 B = mul2(make_float2(y[2 * k], y[2 * k + 1]), rms);
-                    const float2 A2 = fma2(A, f.ac[k], mul2(B, f.bs[k]));
-                    const float2 B2 = fma2(B, f.bc[k], mul2(A, f.as[k]));
+                    float2 A2 = mul2(B, f.bs[k]), B2 = mul2(A, f.as[k]);
+                    // (a value without a rotation must not meet its partner,
+                    // not even times 0: that may be an infinity or NaN)
+                    if (PART && !p.turned) A2 = B2 = make_float2(0.f, 0.f);
+                    A2 = fma2(A, f.ac[k], A2);
+                    B2 = fma2(B, f.bc[k], B2);
                     x[2 * k] = A2.x;
                     x[2 * k + 1] = A2.y;
                     y[2 * k] = B2.x;
@@ -239,7 +246,7 @@ __device__ __forceinline__ void walk(const AppendArgs &a, const Place &p, const 
     }
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool PART>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     constexpr int L = D / 8;               // lanes per head
     constexpr int NG = kAppendThreads / L; // groups per block
@@ -270,8 +277,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     p.lane = threadIdx.x % L;
     p.group = (L == 32 ? 0xffffffffu : (1u << (L & 31)) - 1) << ((threadIdx.x & 31) / L * L);
     const int half = a.rot / 2;
-    const bool turned = p.lane * 8 < a.rot;
-    const bool apart = turned && !a.interleaved;
+    p.turned = p.lane * 8 < a.rot;
+    const bool apart = p.turned && !a.interleaved;
     p.dA = apart ? p.lane * 4 : p.lane * 8;
     p.dB = apart ? half + p.lane * 4 : p.lane * 8 + 4;
     // The token's rows in order, q, k and v: this group takes r, r + step, ...
@@ -291,22 +298,23 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     if (!token_ok(a, pos, slot)) return;
     // this lane's four pairs are the pairs 4 lane .. 4 lane + 3
     float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (turned) {
+    if (p.turned) {
         const float *row = a.cos_sin + (size_t)pos * a.rot + p.lane * 4;
         c = __ldg(reinterpret_cast<const float4 *>(row));
         s = __ldg(reinterpret_cast<const float4 *>(row + half));
     }
     if (r < a.Hq)
-        walk<D, FP8, kQuery>(a, p, fold(a.q_norm, p, a.interleaved, c, s), a.q_norm != nullptr, q,
-                             a.q_out + t * a.q_out_stride, r, a.Hq, step, slot, ahead);
+        walk<D, FP8, PART, kQuery>(a, p, fold(a.q_norm, p, a.interleaved, c, s), a.q_norm != nullptr, q,
+                                   a.q_out + t * a.q_out_stride, r, a.Hq, step, slot, ahead);
     r -= a.Hq;
     if (r < a.Hkv)
-        walk<D, FP8, kKey>(a, p, fold(a.k_norm, p, a.interleaved, c, s), a.k_norm != nullptr,
-                           a.k + t * a.k_stride, a.k_out ? a.k_out + t * a.k_out_stride : nullptr, r,
-                           a.Hkv, step, slot, ahead);
+        walk<D, FP8, PART, kKey>(a, p, fold(a.k_norm, p, a.interleaved, c, s), a.k_norm != nullptr,
+                                 a.k + t * a.k_stride, a.k_out ? a.k_out + t * a.k_out_stride : nullptr, r,
+                                 a.Hkv, step, slot, ahead);
     r -= a.Hkv;
     if (r < a.Hkv && slot >= 0)
-        walk<D, FP8, kValue>(a, p, Turn{}, false, a.v + t * a.v_stride, nullptr, r, a.Hkv, step, slot, ahead);
+        walk<D, FP8, PART, kValue>(a, p, Turn{}, false, a.v + t * a.v_stride, nullptr, r, a.Hkv, step, slot,
+                                   ahead);
 }
 
 // Sequence of packed row t: the last b with cu[b] <= t (cu[0] <= t assumed;
@@ -427,7 +435,11 @@ static void append(const AppendArgs &a, cudaStream_t s) {
     constexpr int kGroups = kAppendThreads / (D / 8), kEnough = 16 * 152;
     const int passes = (a.Hq + 2 * a.Hkv + kGroups - 1) / kGroups;
     const int shares = kEnough / (a.T > 0 ? a.T : 1) + 1;
-    append_kernel<D, FP8><<<dim3(a.T + 1, passes < shares ? passes : shares), kAppendThreads, 0, s>>>(a);
+    const dim3 grid(a.T + 1, passes < shares ? passes : shares);
+    if (a.rot == D)
+        append_kernel<D, FP8, false><<<grid, kAppendThreads, 0, s>>>(a);
+    else
+        append_kernel<D, FP8, true><<<grid, kAppendThreads, 0, s>>>(a);
 }
 
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
