@@ -63,7 +63,9 @@ def rope_table(max_pos, rot, base=10000.0, factor=1.0, original_max=None, beta_f
     * ``original_max`` given: by parts.  A pair that makes at least
       ``beta_fast`` turns within ``original_max`` positions keeps f_i, one
       that makes at most ``beta_slow`` turns has it divided by ``factor``, and
-      in between the two are blended linearly in the pair's index.
+      in between the two are blended linearly in the pair's index, between
+      whole indexes in [0, rot - 1] (no pair is divided in full where the blend
+      ends past the last one, rot/2 - 1).
     ``magnitude`` multiplies cosines and sines (by parts, default
     0.1 ln(factor) + 1; else 1), which scales q and k and so the attention's
     scores by its square.
@@ -79,7 +81,7 @@ def rope_table(max_pos, rot, base=10000.0, factor=1.0, original_max=None, beta_f
         def index_of(turns):   # the (real) pair index that makes `turns` turns
             return rot / 2 * math.log(original_max / (2 * math.pi * turns)) / math.log(base)
         lo = max(math.floor(index_of(beta_fast)), 0)
-        hi = min(math.ceil(index_of(beta_slow)), rot // 2 - 1)
+        hi = min(math.ceil(index_of(beta_slow)), rot - 1)
         blend = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
         f = f * (1 - blend) + f / factor * blend
         if magnitude is None:
