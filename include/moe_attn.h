@@ -74,7 +74,8 @@ moe_status_t moe_kv_cache_size(int type, int num_pages, int page_size, int Hkv, 
  * rounded to bf16, or, MOE_KV_FP8, as scale = amax / 448 with amax the row's
  * largest magnitude, and code = e4m3(x * (448 / amax)), nearest-even (amax
  * 0: scale and codes 0; an amax below 2^-119 counts as 2^-119; a row holding
- * an infinity or a NaN: scale NaN).
+ * an infinity or a NaN: scale NaN).  (A cache that others filled may hold NaN
+ * codes with any scale: such a value is NaN to all that read it.)
  * Two tokens must not name the same slot.
  *  cos_sin [max_pos][rot] fp32, 16-byte aligned (NULL if rot == 0): scaling
  *          for long contexts is a matter of the table's angles.
@@ -122,6 +123,12 @@ size_t moe_attn_decode_workspace_size(int B, int Hq, int Hkv, int D);
  *  page_table, table_stride: as in moe_kv_gather.
  * Results do not depend on timing: keys are split over the GPU by the
  * lengths alone and the parts are joined in a fixed order.
+ * Rounding: sums are in fp32 and the result is rounded once to bf16.  Over a
+ * bf16 cache the weights exp(s - max) enter the product with v as sums of two
+ * bf16 (2^-16).  Over an fp8 cache each weight times its v's scale is rounded
+ * to one bf16, which moves a result by at most 2^-8 sum_j p_j |v_j| (p the
+ * normalised weights; with one key, all values of a head by one factor), and
+ * values of q below 2^-14 of their head's largest are off by up to 2^-25 of it.
  * Limits: 0 <= B <= 65535, Hq <= 1024, scale > 0.
  * A page number out of range, a negative length or one beyond the table (or
  * 2^30) reports MOE_ERR_DEVICE_BAD_INDEX (detail: the first such sequence),

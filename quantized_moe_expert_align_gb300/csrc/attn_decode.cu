@@ -527,12 +527,18 @@ decode_kernel(const DecodeAttnArgs a, const int HV, const int RT, const __grid_c
                             l[i][0] += x[k][0] + x[k][2];
                             l[i][1] += x[k][1] + x[k][3];
                             // Weights for the product with v, v's scale with
-                            // them: for a bf16 cache as the sum of two bf16 (one
-                            // alone would add as much error as the result's own
-                            // rounding, and the second product is free: 109 us
-                            // either way for 90 sequences up to 8192 keys), for
-                            // fp8 one, far finer than the codes (the second
-                            // costs 7% there).  The sum l keeps the unrounded.
+                            // them; the sum l keeps the unrounded.  For a bf16
+                            // cache the sum of two bf16: one alone would add as
+                            // much error as the result's own rounding, and the
+                            // second product is free (109 us either way for 90
+                            // sequences up to 8192 keys).  For fp8 one, which
+                            // adds up to 2^-8 of sum p |v| (2.3e-3 instead of
+                            // 1.7e-3 relative over random values): there the
+                            // work is bound by its instructions, and the second
+                            // costs 256 sequences up to 8192 keys 280 -> 287 us,
+                            // 64 with 64 heads over 4 69 -> 77.  (As fp16 times a
+                            // factor per head that follows the largest weight:
+                            // 2^-11, but 289 to 304 and 76 to 84 us.)
                             if (FP8) {
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
