@@ -178,6 +178,18 @@ __device__ __forceinline__ unsigned long long warp_total(unsigned long long v) {
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+// Items are sorted by their key tiles into classes: one a number up to kExact,
+// then 32 an octave (up to 2^24 tiles, all that 2^31 keys can make).
+constexpr int kExactLog = 9, kExact = 1 << kExactLog;
+static_assert(kExact + 32 * (25 - kExactLog) <= kBuckets, "classes");
+__device__ __forceinline__ int class_of(int tiles) {
+    if (tiles < kExact) return tiles;
+    const int e = 31 - __clz(tiles);
+    return kExact + (e - kExactLog) * 32 + (tiles >> (e - 5) & 31);
+}
+__device__ __forceinline__ int most_of_class(int c) {
+    return c < kExact ? c : ((33 + (c & 31)) << ((c - kExact) / 32 + kExactLog - 5)) - 1;
+}
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks) {
     __shared__ int count[kBuckets], warp_sum[kPlanThreads / 32], first_bad, joins, slots, longest;
@@ -209,7 +221,7 @@ plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks
         }
     };
     auto bucket_of = [&](int tiles) {  // fewest key tiles last
-        return kBuckets - 1 - min(kBuckets - 1, tiles);
+        return kBuckets - 1 - class_of(tiles);
     };
     // Blocks by their key tiles, if none is cut; all key tiles; the most.
     unsigned long long mine_tiles = 0;
@@ -247,8 +259,8 @@ plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks
             const uint32_t m = n == 31 ? (uint32_t)least : ((uint32_t)longest + n) / (n + 1);
             uint32_t big = 0, parts = 0;  // items above half of m; parts of cut ranges
             if (n == 0 || m >= least)
-                for (uint32_t tiles = lane; tiles <= (uint32_t)min(longest, kBuckets - 1); tiles += 32) {
-                    const uint32_t c = count[kBuckets - 1 - tiles];
+                for (int i = lane, last = class_of(longest); i <= last; i += 32) {
+                    const uint32_t tiles = min(longest, most_of_class(i)), c = count[kBuckets - 1 - i];
                     if (c == 0 || 2 * tiles <= m) continue;
                     const uint32_t in = c * ((tiles + m - 1) / m);
                     big += in;
