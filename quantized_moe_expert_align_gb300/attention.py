@@ -242,6 +242,8 @@ def qk_rope_append(q, k, v, cos_sin, positions, cache, slots, q_norm=None, k_nor
         q_out = _rows_out(T, Hq, D, q.device, stream)
     if k_out is True:
         k_out = _rows_out(T, Hkv, D, q.device, stream)
+    elif k_out is False:
+        k_out = None
     sqo = _rows(q_out, "q_out", T, Hq, D)
     sko = _rows(k_out, "k_out", T, Hkv, D) if k_out is not None else 0
     ws = _workspace(workspace, stream, q.device)
@@ -329,6 +331,8 @@ def attn_prefill(q, k, v, cu_q, cu_k, causal=True, scale=None, out=None, lse=Non
 def _lse(lse, T, Hq, device, stream):
     if lse is True:
         return _result((T, Hq), torch.float32, device, stream)
+    if lse is False:
+        return None
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, Hq) or
                             not lse.is_contiguous() or not lse.is_cuda):
         raise ValueError(f"lse: contiguous float32 {(T, Hq)} on a GPU expected")

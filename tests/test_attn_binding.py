@@ -139,3 +139,20 @@ def test_buffers_made_on_the_current_stream(fake, op):
     _calls()[op]()
     assert lib.calls[-1][1][-1] == 7
     assert len(t.made) == 3 and all(b.pool is t.home and not b.recorded for b in t.made)
+
+
+def test_no_logsumexp_and_no_keys(fake):
+    """False is the same as None: only the first result is returned."""
+    t, lib = fake
+    q, k = Tensor((5, 4, 64), BF16), Tensor((5, 2, 64), BF16)
+    cu, n, table = Tensor((4,), I32), Tensor((5,), I32), Tensor((5, 3), I32)
+    for no in (None, False):
+        t.made.clear()
+        outs = [moe.qk_rope_append(q, k, k, None, None, None, None, k_out=no),
+                moe.attn_decode(q, Cache(), table, n, lse=no), moe.attn_prefill(q, k, k, cu, cu, lse=no)]
+        assert all(isinstance(o, Tensor) and o.shape == (5, 4, 64) for o in outs)
+        assert len(t.made) == 6   # a result and a workspace each
+        names = [c[0] for c in lib.calls if not c[0].endswith("_size")]
+        assert names[-3:] == ["moe_qk_rope_append", "moe_attn_decode", "moe_attn_prefill"]
+        append, decode, prefill = [c[1] for c in lib.calls if not c[0].endswith("_size")][-3:]
+        assert append[17] is None and decode[9] is None and prefill[18] is None
