@@ -7,9 +7,9 @@ word (``moe_w4a16_get_device_status(workspace.buf)``).
 
 Rows may be strided between tokens (the three parts of one fused projection);
 the heads of a token and the values of a head are contiguous.  Tensors have
-to live on the current device and be ready on the stream of the call (the
-current stream unless ``stream`` is given).  What a call allocates comes from
-the memory pool of that stream.
+to live on the current device (others are refused: the library launches there)
+and be ready on the stream of the call (the current stream unless ``stream`` is
+given).  What a call allocates comes from the memory pool of that stream.
 """
 from __future__ import annotations
 
@@ -19,15 +19,15 @@ import math
 import quantized_moe_expert_align_gb300 as _moe
 
 # Bound by the first call: importing this package does not import torch.
-torch = _BF16 = _I32 = _F32 = _raw_stream = None
+torch = _BF16 = _I32 = _F32 = _raw_stream = _this_gpu = None
 
 
 def _need_torch():
-    global torch, _BF16, _I32, _F32, _raw_stream
+    global torch, _BF16, _I32, _F32, _raw_stream, _this_gpu
     if torch is None:
         import torch as t
         _BF16, _I32, _F32 = t.bfloat16, t.int32, t.float32
-        _raw_stream = t._C._cuda_getCurrentRawStream
+        _raw_stream, _this_gpu = t._C._cuda_getCurrentRawStream, t._C._cuda_getDevice
         torch = t
 
 MOE_KV_BF16 = 0
@@ -116,6 +116,7 @@ class KVCache:
         self._c = _moe.moe_kv_cache_t(data.data_ptr(), None if scales is None else scales.data_ptr(),
                                       kind, self.num_pages, self.page_size, self.Hkv, self.D)
         self._ref = ctypes.byref(self._c)
+        self._gpu = data.get_device()
 
     @classmethod
     def empty(cls, num_pages, Hkv, D, page_size=64, fp8=True, device="cuda"):
@@ -146,42 +147,50 @@ class AttnWorkspace:
             raise _moe.MoeError(_moe.MOE_ERR_INVALID_ARG, "AttnWorkspace")
         self.nbytes = n
         self.buf = _moe._empty_bytes(n, device)
-        self._ptr = self.buf.data_ptr()
+        self._ptr, self._gpu = self.buf.data_ptr(), self.buf.get_device()
 
 
-def _bf16(t, name, n):
-    if t.dtype is not _BF16 or t.shape != (n,) or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name}: contiguous bfloat16 {(n,)} on a GPU expected, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
+def _wrong(t, name, what, dev):
+    return ValueError(f"{name}: {what} on cuda:{dev} expected, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _rows(t, name, T, H, D):
+def _gpu(t, name):
+    """The GPU of a call's first tensor, which has to be the current one (the
+    library launches there) and to hold all the other tensors."""
+    dev = t.get_device()   # (-1: not on a GPU)
+    if dev != _this_gpu():
+        raise _wrong(t, name, "a tensor", _this_gpu())
+    return dev
+
+
+def _bf16(t, name, n, dev):
+    if t.dtype is not _BF16 or t.shape != (n,) or not t.is_contiguous() or t.get_device() != dev:
+        raise _wrong(t, name, f"contiguous bfloat16 {(n,)}", dev)
+
+
+def _rows(t, name, T, H, D, dev):
     """Checks rows [T][H][D] with contiguous heads; the stride between tokens."""
-    if t.dtype is not _BF16 or t.shape != (T, H, D) or not t.is_cuda:
-        raise ValueError(f"{name}: bfloat16 {(T, H, D)} on a GPU expected, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
+    if t.dtype is not _BF16 or t.shape != (T, H, D) or t.get_device() != dev:
+        raise _wrong(t, name, f"bfloat16 {(T, H, D)}", dev)
     st = t.stride()
     if T and (st[2] != 1 or (H > 1 and st[1] != D)):
         raise ValueError(f"{name}: the heads of a token have to be contiguous")
     return st[0] if T > 1 else H * D
 
 
-def _i32(t, name, shape):
-    if t.dtype is not _I32 or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name}: contiguous int32 {shape} on a GPU expected, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
+def _i32(t, name, shape, dev):
+    if t.dtype is not _I32 or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise _wrong(t, name, f"contiguous int32 {shape}", dev)
 
 
 def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _on(stream, t):
-    """The stream handle of a call: the current stream of t's device unless
+def _on(stream, dev):
+    """The stream handle of a call on GPU dev: its current stream unless
     ``stream`` (a torch stream or a handle) is given."""
-    if stream is None:
-        return _raw_stream(t.get_device())
-    return getattr(stream, "cuda_stream", stream)
+    return _raw_stream(dev) if stream is None else getattr(stream, "cuda_stream", stream)
 
 
 def _pool_of(stream):
@@ -208,13 +217,14 @@ def _rows_out(T, H, D, device, stream):
     return _result((T, H, D), torch.bfloat16, device, stream)
 
 
-def _workspace(ws, stream, device, *size):
-    if ws is None:
-        if stream is None:
-            return AttnWorkspace(device, *size)
-        with _pool_of(stream):
-            return AttnWorkspace(device, *size)
-    return ws
+def _workspace(ws, stream, dev, *size):
+    """A new workspace, if the caller has none."""
+    if ws is not None:
+        raise _wrong(ws.buf, "workspace", "a buffer", dev)
+    if stream is None:
+        return AttnWorkspace(f"cuda:{dev}", *size)
+    with _pool_of(stream):
+        return AttnWorkspace(f"cuda:{dev}", *size)
 
 
 def qk_rope_append(q, k, v, cos_sin, positions, cache, slots, q_norm=None, k_norm=None, eps=1e-6,
@@ -226,32 +236,39 @@ def qk_rope_append(q, k, v, cos_sin, positions, cache, slots, q_norm=None, k_nor
     if torch is None:
         _need_torch()
     T, Hq, D = q.shape
-    Hkv = k.shape[1]
-    sq, sk, sv = _rows(q, "q", T, Hq, D), _rows(k, "k", T, Hkv, D), _rows(v, "v", T, Hkv, D)
+    Hkv, dev = k.shape[1], _gpu(q, "q")
+    sq = _rows(q, "q", T, Hq, D, dev)
+    sk, sv = _rows(k, "k", T, Hkv, D, dev), _rows(v, "v", T, Hkv, D, dev)
     max_pos, rot = cos_sin.shape if cos_sin is not None else (0, 0)
     if rot:
-        if cos_sin.dtype is not _F32 or not cos_sin.is_contiguous() or not cos_sin.is_cuda:
-            raise ValueError("cos_sin: contiguous float32 [max_pos][rot] on a GPU expected")
-        _i32(positions, "positions", (T,))
-    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        if w is not None:
-            _bf16(w, name, D)
+        if cos_sin.dtype is not _F32 or not cos_sin.is_contiguous() or cos_sin.get_device() != dev:
+            raise _wrong(cos_sin, "cos_sin", "contiguous float32 [max_pos][rot]", dev)
+        _i32(positions, "positions", (T,), dev)
+    if q_norm is not None:
+        _bf16(q_norm, "q_norm", D, dev)
+    if k_norm is not None:
+        _bf16(k_norm, "k_norm", D, dev)
     if cache is not None:
-        _i32(slots, "slots", (T,))
+        _i32(slots, "slots", (T,), dev)
+        if cache._gpu != dev:
+            raise _wrong(cache.data, "cache", "data", dev)
     if q_out is None:
         q_out = _rows_out(T, Hq, D, q.device, stream)
     if k_out is True:
         k_out = _rows_out(T, Hkv, D, q.device, stream)
     elif k_out is False:
         k_out = None
-    sqo = _rows(q_out, "q_out", T, Hq, D)
-    sko = _rows(k_out, "k_out", T, Hkv, D) if k_out is not None else 0
-    ws = _workspace(workspace, stream, q.device)
+    sqo = _rows(q_out, "q_out", T, Hq, D, dev)
+    sko = _rows(k_out, "k_out", T, Hkv, D, dev) if k_out is not None else 0
+    ws = workspace
+    if ws is None or ws._gpu != dev:
+        ws = _workspace(ws, stream, dev)
     _moe._check((_moe._lib or _moe.load()).moe_qk_rope_append(
-        _p(q), sq, _p(k), sk, _p(v), sv, _p(q_norm), _p(k_norm), eps, _p(cos_sin), max_pos, rot,
-        int(interleaved), _p(positions) if rot else None, _p(slots) if cache is not None else None,
-        _p(q_out), sqo, _p(k_out), sko, cache._ref if cache is not None else None, T, Hq, Hkv, D,
-        ws._ptr, ws.nbytes, _on(stream, q)), "moe_qk_rope_append")
+        q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, _p(q_norm), _p(k_norm), eps, _p(cos_sin),
+        max_pos, rot, int(interleaved), positions.data_ptr() if rot else None,
+        slots.data_ptr() if cache is not None else None, q_out.data_ptr(), sqo, _p(k_out), sko,
+        cache._ref if cache is not None else None, T, Hq, Hkv, D, ws._ptr, ws.nbytes, _on(stream, dev)),
+        "moe_qk_rope_append")
     return q_out if k_out is None else (q_out, k_out)
 
 
@@ -260,19 +277,23 @@ def kv_gather(cache, page_table, cu_k, total, k_out=None, v_out=None, workspace=
     [total][Hkv][D]; page_table [B][n] and cu_k [B+1] int32."""
     if torch is None:
         _need_torch()
-    B, n = page_table.shape
-    _i32(page_table, "page_table", (B, n))
-    _i32(cu_k, "cu_k", (B + 1,))
+    (B, n), dev = page_table.shape, _gpu(page_table, "page_table")
+    _i32(page_table, "page_table", (B, n), dev)
+    _i32(cu_k, "cu_k", (B + 1,), dev)
+    if cache._gpu != dev:
+        raise _wrong(cache.data, "cache", "data", dev)
     shape = (total, cache.Hkv, cache.D)
     if k_out is None:
         k_out = _rows_out(*shape, page_table.device, stream)
     if v_out is None:
         v_out = _rows_out(*shape, page_table.device, stream)
-    ws = _workspace(workspace, stream, page_table.device)
+    ws = workspace
+    if ws is None or ws._gpu != dev:
+        ws = _workspace(ws, stream, dev)
     _moe._check((_moe._lib or _moe.load()).moe_kv_gather(
-        cache._ref, _p(page_table), n, _p(cu_k), B, total, _p(k_out),
-        _rows(k_out, "k_out", *shape), _p(v_out), _rows(v_out, "v_out", *shape), ws._ptr,
-        ws.nbytes, _on(stream, page_table)), "moe_kv_gather")
+        cache._ref, page_table.data_ptr(), n, cu_k.data_ptr(), B, total, k_out.data_ptr(),
+        _rows(k_out, "k_out", *shape, dev), v_out.data_ptr(), _rows(v_out, "v_out", *shape, dev), ws._ptr,
+        ws.nbytes, _on(stream, dev)), "moe_kv_gather")
     return k_out, v_out
 
 
@@ -287,18 +308,23 @@ def attn_decode(q, cache, page_table, seq_lens, scale=None, out=None, lse=None, 
     B, Hq, D = q.shape
     if D != cache.D:
         raise ValueError(f"q has heads of {D}, the cache of {cache.D}")
-    n = page_table.shape[1]
-    _i32(page_table, "page_table", (B, n))
-    _i32(seq_lens, "seq_lens", (B,))
-    sq = _rows(q, "q", B, Hq, D)
+    n, dev = page_table.shape[1], _gpu(q, "q")
+    if cache._gpu != dev:
+        raise _wrong(cache.data, "cache", "data", dev)
+    _i32(page_table, "page_table", (B, n), dev)
+    _i32(seq_lens, "seq_lens", (B,), dev)
+    sq = _rows(q, "q", B, Hq, D, dev)
     if out is None:
         out = _rows_out(B, Hq, D, q.device, stream)
-    so = _rows(out, "out", B, Hq, D)
-    lse = _lse(lse, B, Hq, q.device, stream)
-    ws = _workspace(workspace, stream, q.device, "decode", B, B, Hq, cache.Hkv, D)
+    so = _rows(out, "out", B, Hq, D, dev)
+    lse = _lse(lse, B, Hq, q.device, dev, stream)
+    ws = workspace
+    if ws is None or ws._gpu != dev:
+        ws = _workspace(ws, stream, dev, "decode", B, B, Hq, cache.Hkv, D)
     _moe._check((_moe._lib or _moe.load()).moe_attn_decode(
-        _p(q), sq, cache._ref, _p(page_table), n, _p(seq_lens), D ** -0.5 if scale is None else scale,
-        _p(out), so, _p(lse), B, Hq, ws._ptr, ws.nbytes, _on(stream, q)), "moe_attn_decode")
+        q.data_ptr(), sq, cache._ref, page_table.data_ptr(), n, seq_lens.data_ptr(),
+        D ** -0.5 if scale is None else scale, out.data_ptr(), so, _p(lse), B, Hq, ws._ptr, ws.nbytes,
+        _on(stream, dev)), "moe_attn_decode")
     return out if lse is None else (out, lse)
 
 
@@ -312,28 +338,31 @@ def attn_prefill(q, k, v, cu_q, cu_k, causal=True, scale=None, out=None, lse=Non
         _need_torch()
     Tq, Hq, D = q.shape
     Tk, Hkv, _ = k.shape
-    B = cu_q.shape[0] - 1
-    _i32(cu_q, "cu_q", (B + 1,))
-    _i32(cu_k, "cu_k", (B + 1,))
-    sq, sk, sv = _rows(q, "q", Tq, Hq, D), _rows(k, "k", Tk, Hkv, D), _rows(v, "v", Tk, Hkv, D)
+    B, dev = cu_q.shape[0] - 1, _gpu(q, "q")
+    _i32(cu_q, "cu_q", (B + 1,), dev)
+    _i32(cu_k, "cu_k", (B + 1,), dev)
+    sq = _rows(q, "q", Tq, Hq, D, dev)
+    sk, sv = _rows(k, "k", Tk, Hkv, D, dev), _rows(v, "v", Tk, Hkv, D, dev)
     if out is None:
         out = _rows_out(Tq, Hq, D, q.device, stream)
-    so = _rows(out, "out", Tq, Hq, D)
-    lse = _lse(lse, Tq, Hq, q.device, stream)
-    ws = _workspace(workspace, stream, q.device, "prefill", B, Tq, Hq, Hkv, D)
+    so = _rows(out, "out", Tq, Hq, D, dev)
+    lse = _lse(lse, Tq, Hq, q.device, dev, stream)
+    ws = workspace
+    if ws is None or ws._gpu != dev:
+        ws = _workspace(ws, stream, dev, "prefill", B, Tq, Hq, Hkv, D)
     _moe._check((_moe._lib or _moe.load()).moe_attn_prefill(
-        _p(q), sq, _p(k), sk, _p(v), sv, _p(cu_q), _p(cu_k), B, Tq, Tk, Hq, Hkv, D, int(causal),
-        D ** -0.5 if scale is None else scale, _p(out), so, _p(lse), ws._ptr, ws.nbytes,
-        _on(stream, q)), "moe_attn_prefill")
+        q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, cu_q.data_ptr(), cu_k.data_ptr(), B, Tq, Tk,
+        Hq, Hkv, D, int(causal), D ** -0.5 if scale is None else scale, out.data_ptr(), so, _p(lse),
+        ws._ptr, ws.nbytes, _on(stream, dev)), "moe_attn_prefill")
     return out if lse is None else (out, lse)
 
 
-def _lse(lse, T, Hq, device, stream):
+def _lse(lse, T, Hq, device, dev, stream):
     if lse is True:
         return _result((T, Hq), torch.float32, device, stream)
     if lse is False:
         return None
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, Hq) or
-                            not lse.is_contiguous() or not lse.is_cuda):
-        raise ValueError(f"lse: contiguous float32 {(T, Hq)} on a GPU expected")
+                            not lse.is_contiguous() or lse.get_device() != dev):
+        raise _wrong(lse, "lse", f"contiguous float32 {(T, Hq)}", dev)
     return lse

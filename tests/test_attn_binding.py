@@ -67,7 +67,7 @@ class Torch:
         c.stream, c.current_stream = staticmethod(stream), staticmethod(lambda device=None: self.now)
 
     def empty(self, shape, dtype=None, device=None):
-        t = Tensor(shape if isinstance(shape, tuple) else (shape,), dtype, 0, self.now)
+        t = Tensor(shape if isinstance(shape, tuple) else (shape,), dtype, int(device.split(":")[1]), self.now)
         self.made.append(t)
         return t
 
@@ -86,7 +86,7 @@ class Lib:
 
 
 class Cache:
-    D, Hkv, page_size, num_pages, _ref = 64, 2, 16, 8, None
+    D, Hkv, page_size, num_pages, _ref, _gpu = 64, 2, 16, 8, None, 0
     data = Tensor((8, 2, 2, 16, 64), BF16)
 
 
@@ -98,6 +98,7 @@ def fake(monkeypatch):
     monkeypatch.setattr(attention, "_I32", I32)
     monkeypatch.setattr(attention, "_F32", F32)
     monkeypatch.setattr(attention, "_raw_stream", lambda device: t.now.cuda_stream)
+    monkeypatch.setattr(attention, "_this_gpu", lambda: 0)
     monkeypatch.setattr(moe, "_lib", lib)
     monkeypatch.setattr(moe, "_empty_bytes", lambda n, device: t.empty(n, U8, device))
     return t, lib
@@ -156,3 +157,54 @@ def test_no_logsumexp_and_no_keys(fake):
         assert names[-3:] == ["moe_qk_rope_append", "moe_attn_decode", "moe_attn_prefill"]
         append, decode, prefill = [c[1] for c in lib.calls if not c[0].endswith("_size")][-3:]
         assert append[17] is None and decode[9] is None and prefill[18] is None
+
+
+def _another(t):
+    return Tensor(t.shape, t.dtype, 1)
+
+
+@pytest.mark.parametrize("op", ["append", "gather", "decode", "prefill"])
+def test_tensors_of_another_gpu_are_refused(fake, op):
+    """A kernel on one GPU must not be given another's memory: each tensor
+    argument in turn, outputs, caches and workspaces among them."""
+    t, lib = fake
+    q, k = Tensor((5, 4, 64), BF16), Tensor((5, 2, 64), BF16)
+    w, cs, i5, i6 = Tensor((64,), BF16), Tensor((9, 64), F32), Tensor((5,), I32), Tensor((6,), I32)
+    table, lse = Tensor((5, 3), I32), Tensor((5, 4), F32)
+    ws = attention.AttnWorkspace("cuda:0")
+    cache, far = Cache(), Cache()
+    far.data, far._gpu = _another(Cache.data), 1
+    f, args = {
+        "append": (moe.qk_rope_append, dict(q=q, k=k, v=k, cos_sin=cs, positions=i5, cache=cache, slots=i5,
+                                            q_norm=w, k_norm=w, q_out=q, k_out=k, workspace=ws)),
+        "gather": (moe.kv_gather, dict(cache=cache, page_table=table, cu_k=i6, total=5, k_out=k, v_out=k,
+                                       workspace=ws)),
+        "decode": (moe.attn_decode, dict(q=q, cache=cache, page_table=table, seq_lens=i5, out=q, lse=lse,
+                                         workspace=ws)),
+        "prefill": (moe.attn_prefill, dict(q=q, k=k, v=k, cu_q=i6, cu_k=i6, out=q, lse=lse, workspace=ws)),
+    }[op]
+    f(**args)
+    n = len(lib.calls)
+    for name, a in args.items():
+        if isinstance(a, Tensor):
+            bad = _another(a)
+        elif a is cache:
+            bad = far
+        elif a is ws:
+            bad = attention.AttnWorkspace("cuda:1")
+        else:
+            continue
+        with pytest.raises(ValueError):
+            f(**dict(args, **{name: bad}))
+    assert all(c[0].endswith("_size") for c in lib.calls[n:])   # nothing was launched
+
+
+@pytest.mark.parametrize("op", ["append", "gather", "decode", "prefill"])
+def test_tensors_off_the_current_gpu_are_refused(fake, monkeypatch, op):
+    """The library launches on the current device."""
+    t, lib = fake
+    monkeypatch.setattr(attention, "_this_gpu", lambda: 1)
+    for kw in (dict(), dict(stream=Stream(99))):
+        with pytest.raises(ValueError):
+            _calls()[op](**kw)
+    assert all(c[0].endswith("_size") for c in lib.calls)
