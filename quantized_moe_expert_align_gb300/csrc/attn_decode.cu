@@ -20,13 +20,17 @@
 // fragment loads are free of bank conflicts.
 //
 // Measured on one GB300 (copy rate 6.79 TB/s): 256 sequences up to 8192 keys,
-// 64 heads over 8, fp8, 1.79 GB in 276 us (6.5 TB/s); 90 up to 8192, 32 over 4,
+// 64 heads over 8, fp8, 1.79 GB in 280 us (6.4 TB/s); 90 up to 8192, 32 over 4,
 // bf16 pages of 16, 657 MB in 108 us (6.1 TB/s); one of 131072 keys, fp8, 277
 // MB in 53 us, of which 41 are the bytes and the rest the set-up (lengths, page
 // table, first copies) and the join; one of 517 keys 10.2 us.  More heads per
-// byte, or fewer bytes per key, are bound by the latency of a warp's chain of
-// steps instead: 64 sequences up to 8192 keys, 64 heads of 128 over 4, fp8, 66
-// us (39 for the bytes), bf16 94 (76); 64 of 64 over 8 54 (40) and 87 (75).
+// byte, or fewer bytes per key, are bound by what the warps of an SM get done
+// instead: 64 sequences up to 8192 keys, 64 heads of 128 over 4, fp8, 69 us (39
+// for the bytes), bf16 94 (76); 64 of 64 over 8 55 (40) and 87 (75).  With 16
+// heads of 128 over fp8 registers allow two blocks an SM (five warps each: 168
+// registers), too few to hide a warp's chain of steps, and spill: 1.3% of the
+// instructions are local loads and stores.  (The figures beside the choices
+// below were taken before NaN codes were looked for, which adds 1 to 4% to fp8.)
 #include "attn_common.cuh"
 #include "gemm_tc.h"
 

@@ -18,7 +18,8 @@
 // last value tile that belong to the next sequence (a weight of 0 would not
 // stop their NaN).  The reference r is raised, and O_t rescaled, only when a
 // row's maximum exceeds it by 2^8: the sums are in fp32, where p <= 2^8 costs
-// nothing (8192 causal tokens: 798 us when every rise rescales, 680 with this).
+// nothing (8192 causal tokens: 798 us when every rise rescales and 680 with this,
+// when it was added).
 //
 // A planning kernel lists the items by falling number of key tiles; the
 // blocks take them from a counter, longest first.  Where a few items have
@@ -28,14 +29,15 @@
 // without the plan: every block finds its own items.
 //
 // Measured on one GB300 (cuBLAS bf16 1876 TFLOP/s in a burst, 1697 sustained),
-// heads of 128: 8192 causal tokens, 64 heads over 8, 598 us (1840 TFLOP/s);
-// six prompts up to 4096 tokens 345 us in a burst, 380 back to back under the
-// power limit (1475 TFLOP/s).  A round of one row tile is softmax (1300 cycles)
-// then its 1024 cycles of products and two hand-overs; the two tiles, half a
-// round apart, keep the tensor pipe busy 75 to 85% of the time.  Heads of 64:
-// 8192 causal tokens 451 us (1220 TFLOP/s); there the two warps per scheduler
-// cannot hide the softmax's latencies (tensor pipe, exponentials and issue all
-// near 50%).  1024 tokens take 18.4 us: eight key tiles in turn at 1.4 us.
+// in bursts of 20 calls and back to back for two seconds under the power limit;
+// heads of 128: 8192 causal tokens, 64 heads over 8, 611 us (1801 TFLOP/s) and
+// 669 (1643); six prompts up to 4096 tokens 350 (1599) and 381 to 389 (1471 to
+// 1441).  A round of one row tile is softmax (1300 cycles) then its 1024 cycles
+// of products and two hand-overs; the two tiles, half a round apart, keep the
+// tensor pipe busy 75 to 85% of the time.  Heads of 64: 8192 causal tokens 455
+// us (1209 TFLOP/s) and 467; there the two warps per scheduler cannot hide the
+// softmax's latencies (tensor pipe, exponentials and issue all near 50%).  1024
+// tokens take 18.4 us: eight key tiles in turn at 1.4 us.
 #include <type_traits>
 
 #include "attn_common.cuh"
@@ -691,9 +693,10 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                     // would want the tensor pipe, and then the exponentials, at
                     // the same time.  Heads of 128: once the first tile's maxima
                     // are known, which puts the two half a round apart (8192
-                    // causal tokens, 64 heads: 606 us, 640 us with the signal
-                    // below, 656 in step); heads of 64: once the first half of
-                    // its weights is (455, 483 us the other way, 484).
+                    // causal tokens, 64 heads, when this was chosen: 606 us, 640
+                    // with the signal below, 656 in step); heads of 64: once the
+                    // first half of its weights is (455, 483 the other way, 484
+                    // in step).
                     const bool apart = __shfl_sync(0xffffffffu, (int)run_apart(it.b), 0) != 0;
                     if (apart && t == 1) {
                         ok = warp_wait_flag(&sm->offset, off_ph, &sm->abort, 13);
