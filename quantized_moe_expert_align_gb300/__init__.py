@@ -82,6 +82,23 @@ def _attn_signatures():
     }
 
 
+def _serve_signatures():
+    """The entry points of ``include/moe_attn_serve.h``."""
+    i, p, sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
+    n, f = ctypes.c_int64, ctypes.c_float
+    cache = ctypes.POINTER(moe_kv_cache_t)
+    return {
+        "moe_page_plan_workspace_size": (sz, [i]),
+        "moe_page_plan": (i, [p, i, p, p, p, i, i, p, p, p, p, i, i, i, i, p, p, p, p, p, p, p, sz, p]),
+        "moe_attn_decode_window": (i, [p, n, cache, p, i, p, i, i, f, p, n, p, i, i, p, sz, p]),
+        "moe_attn_prefill_window": (i, [p, n, p, n, p, n, p, p, i, i, i, i, i, i, i, i, f, p, n, p, p,
+                                        sz, p]),
+        "moe_attn_tree_workspace_size": (sz, [i, i, i, i, i]),
+        "moe_attn_tree": (i, [p, n, cache, p, i, p, p, p, f, p, n, p, i, i, i, p, sz, p]),
+        "moe_kv_accept": (i, [cache, p, i, p, p, i, i, p, sz, p]),
+    }
+
+
 def load(path: str = LIB_PATH):
     """Load the compiled library (raises OSError/RuntimeError if absent)."""
     global _lib
@@ -110,6 +127,7 @@ def load(path: str = LIB_PATH):
             "moe_w4a16_workspace_views": (i, [i, i, i, i, i, ctypes.POINTER(moe_ws_views_t)]),
         }
         sig.update(_attn_signatures())
+        sig.update(_serve_signatures())
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
             fn.restype = res
@@ -341,3 +359,7 @@ from .attention import (AttnWorkspace, KVCache, MOE_ATTN_STATUS_BYTES,  # noqa: 
                         MOE_KV_BF16, MOE_KV_FP8, attn_decode, attn_prefill, kv_gather,
                         moe_attn_decode_workspace_size, moe_attn_prefill_workspace_size,
                         moe_kv_cache_size, qk_rope_append, rope_table)
+
+# Serving over the paged cache (moe_attn_serve.h).
+from .serving import (MOE_TREE_TOKENS, PagePlan, PagePool, attn_tree, kv_accept,  # noqa: E402
+                      moe_attn_tree_workspace_size, moe_page_plan_workspace_size, page_plan)

@@ -130,9 +130,10 @@ class KVCache:
 
 
 class AttnWorkspace:
-    """A reusable workspace: ``op`` "decode" or "prefill" sized for up to B
-    sequences and ``rows`` query rows in all; without ``op``, for
-    qk_rope_append and kv_gather.  ``buf`` is what the status call takes."""
+    """A reusable workspace: ``op`` "decode", "prefill" or "tree" sized for up
+    to B sequences and ``rows`` query rows in all, "pages" (page_plan) for up to
+    B sequences; without ``op``, for qk_rope_append, kv_gather and kv_accept.
+    ``buf`` is what the status call takes."""
 
     def __init__(self, device, op=None, B=0, rows=0, Hq=1, Hkv=1, D=128):
         if op is None:
@@ -141,6 +142,10 @@ class AttnWorkspace:
             n = moe_attn_decode_workspace_size(B, Hq, Hkv, D)
         elif op == "prefill":
             n = moe_attn_prefill_workspace_size(B, rows, Hq, Hkv, D)
+        elif op == "tree":
+            n = _moe.moe_attn_tree_workspace_size(B, rows, Hq, Hkv, D)
+        elif op == "pages":
+            n = _moe.moe_page_plan_workspace_size(B)
         else:
             raise ValueError(f"AttnWorkspace: unknown op {op!r}")
         if n == 0:
@@ -298,11 +303,13 @@ def kv_gather(cache, page_table, cu_k, total, k_out=None, v_out=None, workspace=
 
 
 def attn_decode(q, cache, page_table, seq_lens, scale=None, out=None, lse=None, workspace=None,
-                stream=None):
+                stream=None, window=None, sinks=0):
     """Attention of one token of each of B sequences over its cached tokens:
     q [B][Hq][D], page_table [B][n] and seq_lens [B] int32; scale defaults to
-    D^-1/2.  Returns out [B][Hq][D]; ``lse`` True or a float32 [B][Hq] tensor
-    also returns the logsumexp, as (out, lse)."""
+    D^-1/2.  With a ``window`` the token sees the last ``window`` tokens (itself
+    among them) and the first ``sinks``; table entries of pages that hold none of
+    those are not read.  Returns out [B][Hq][D]; ``lse`` True or a float32
+    [B][Hq] tensor also returns the logsumexp, as (out, lse)."""
     if torch is None:
         _need_torch()
     B, Hq, D = q.shape
@@ -321,19 +328,38 @@ def attn_decode(q, cache, page_table, seq_lens, scale=None, out=None, lse=None, 
     ws = workspace
     if ws is None or ws._gpu != dev:
         ws = _workspace(ws, stream, dev, "decode", B, B, Hq, cache.Hkv, D)
-    _moe._check((_moe._lib or _moe.load()).moe_attn_decode(
-        q.data_ptr(), sq, cache._ref, page_table.data_ptr(), n, seq_lens.data_ptr(),
-        D ** -0.5 if scale is None else scale, out.data_ptr(), so, _p(lse), B, Hq, ws._ptr, ws.nbytes,
-        _on(stream, dev)), "moe_attn_decode")
+    lib = _moe._lib or _moe.load()
+    rest = (D ** -0.5 if scale is None else scale, out.data_ptr(), so, _p(lse), B, Hq, ws._ptr, ws.nbytes,
+            _on(stream, dev))
+    args = (q.data_ptr(), sq, cache._ref, page_table.data_ptr(), n, seq_lens.data_ptr())
+    if window is None:
+        _no_sinks(sinks)
+        _moe._check(lib.moe_attn_decode(*args, *rest), "moe_attn_decode")
+    else:
+        _moe._check(lib.moe_attn_decode_window(*args, *_window(window, sinks), *rest), "moe_attn_decode_window")
     return out if lse is None else (out, lse)
 
 
+def _no_sinks(sinks):
+    if sinks:
+        raise ValueError("sinks: only with a window")
+
+
+def _window(window, sinks):
+    """The two as the C calls take them (which refuse what is out of range):
+    more than 2^31 - 1 is all there is."""
+    most = 2 ** 31 - 1
+    return max(min(int(window), most), -1), max(min(int(sinks), most), -1)
+
+
 def attn_prefill(q, k, v, cu_q, cu_k, causal=True, scale=None, out=None, lse=None, workspace=None,
-                 stream=None):
+                 stream=None, window=None, sinks=0):
     """Attention over packed sequences: q [Tq][Hq][D], k and v [Tk][Hkv][D],
     cu_q and cu_k [B+1] int32; the last query of a sequence stands at its last
-    key.  Returns out [Tq][Hq][D]; ``lse`` True or a float32 [Tq][Hq] tensor
-    also returns the logsumexp, as (out, lse)."""
+    key.  With a ``window`` (causal only) a query sees the last ``window`` keys
+    up to its own and the first ``sinks`` of its sequence.  Returns out
+    [Tq][Hq][D]; ``lse`` True or a float32 [Tq][Hq] tensor also returns the
+    logsumexp, as (out, lse)."""
     if torch is None:
         _need_torch()
     Tq, Hq, D = q.shape
@@ -350,10 +376,19 @@ def attn_prefill(q, k, v, cu_q, cu_k, causal=True, scale=None, out=None, lse=Non
     ws = workspace
     if ws is None or ws._gpu != dev:
         ws = _workspace(ws, stream, dev, "prefill", B, Tq, Hq, Hkv, D)
-    _moe._check((_moe._lib or _moe.load()).moe_attn_prefill(
-        q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, cu_q.data_ptr(), cu_k.data_ptr(), B, Tq, Tk,
-        Hq, Hkv, D, int(causal), D ** -0.5 if scale is None else scale, out.data_ptr(), so, _p(lse),
-        ws._ptr, ws.nbytes, _on(stream, dev)), "moe_attn_prefill")
+    lib = _moe._lib or _moe.load()
+    args = (q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, cu_q.data_ptr(), cu_k.data_ptr(), B, Tq, Tk,
+            Hq, Hkv, D)
+    rest = (D ** -0.5 if scale is None else scale, out.data_ptr(), so, _p(lse), ws._ptr, ws.nbytes,
+            _on(stream, dev))
+    if window is None:
+        _no_sinks(sinks)
+        _moe._check(lib.moe_attn_prefill(*args, int(causal), *rest), "moe_attn_prefill")
+    else:
+        if not causal:
+            raise ValueError("window: only causal attention has one")
+        _moe._check(lib.moe_attn_prefill_window(*args, *_window(window, sinks), *rest),
+                    "moe_attn_prefill_window")
     return out if lse is None else (out, lse)
 
 

@@ -1,5 +1,5 @@
 // attn.h -- arguments and launchers of the attention half of a decoder layer
-// (rope_append.cu, attn_decode.cu, attn_prefill.cu).
+// (rope_append.cu, attn_decode*.cu, attn_prefill*.cu, attn_tree*.cu).
 #pragma once
 
 #include <atomic>
@@ -89,9 +89,22 @@ struct DecodeAttnArgs {
     int B, Hq;
     uint8_t *workspace;
     int test_no_copies;  // failure-path test: the kernel issues no copies
+    // a window: the keys it reaches over, the first keys that stay visible, the
+    // rows of a copy (1 << box_shift)
+    int window, sinks, box_shift;
+    // drafted tokens: their rows by sequence, which of them each sees, all rows
+    const int32_t *cu_q;
+    const uint64_t *tree;
+    int T;
 };
 size_t decode_attn_workspace(int B, int Hq, int Hkv, int D);
 cudaError_t launch_attn_decode(const DecodeAttnArgs &a, cudaStream_t s);
+cudaError_t launch_attn_decode_window(const DecodeAttnArgs &a, cudaStream_t s);
+constexpr int kTreeTokens = 64;  // drafted tokens of a sequence at most
+size_t tree_small_workspace(int T, int Hq, int Hkv, int D);
+cudaError_t launch_attn_tree_small(const DecodeAttnArgs &a, cudaStream_t s);
+size_t tree_workspace(int B, int T, int Hq, int Hkv, int D);
+cudaError_t launch_attn_tree(const DecodeAttnArgs &a, cudaStream_t s);
 
 struct PrefillArgs {
     const uint16_t *q, *k, *v;
@@ -104,8 +117,10 @@ struct PrefillArgs {
     float *lse;
     uint8_t *workspace;
     int test_no_copies;  // failure-path test: the kernel issues no copies
+    int window, sinks;   // through a window: keys it reaches over, first keys that stay visible
 };
 size_t prefill_workspace(int B, int Tq, int Hq, int Hkv, int D);
 cudaError_t launch_attn_prefill(const PrefillArgs &a, cudaStream_t s);
+cudaError_t launch_attn_prefill_window(const PrefillArgs &a, cudaStream_t s);
 
 }  // namespace moe

@@ -1,0 +1,19 @@
+// attn_tree_small.cu -- attention of drafted tokens over the paged cache, in
+// tiles of up to 16 rows.
+#include "attn_decode.cuh"
+
+namespace moe {
+
+size_t tree_small_workspace(int T, int Hq, int Hkv, int D) {
+    const int tokens = T < kTreeTokens ? T : kTreeTokens;
+    return align_up(decode_layout(8 * tiles_of(Hq / Hkv * tokens), D).total, 256);
+}
+
+cudaError_t launch_attn_tree_small(const DecodeAttnArgs &a, cudaStream_t s) {
+    return launch<kTree>(a, a.Hq / a.kv.Hkv * (a.T < kTreeTokens ? a.T : kTreeTokens), s);
+}
+
+size_t tree_workspace(int, int T, int Hq, int Hkv, int D) { return tree_small_workspace(T, Hq, Hkv, D); }
+cudaError_t launch_attn_tree(const DecodeAttnArgs &a, cudaStream_t s) { return launch_attn_tree_small(a, s); }
+
+}  // namespace moe

@@ -1,0 +1,321 @@
+// page_plan.cu -- page tables, slots and positions of one step from the
+// requests' lengths, and the pages that go back.
+//
+// A sequence of L0 cached tokens that gets n more needs pages p0 = ceil(L0 / P)
+// to p1 = ceil((L0 + n) / P) - 1; which free pages these are, and where its rows,
+// and the pages that it gives back, stand among everybody's, are prefix sums over
+// the sequences.  Free pages are a ring: taken from its head, given back behind
+// its tail, so that no place that is read is written by the same call.  All the
+// rest is a few integers a row: latency bounds small calls, bytes large ones.
+//
+// A plan kernel of one block makes the sums; if the step is valid and the pages
+// suffice, rows and pages follow from its records.  Small steps are finished by
+// the same block, large ones by a second kernel over the whole GPU.
+#include <climits>
+
+#include "device_common.cuh"
+#include "paging.h"
+
+namespace moe {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kFillThreads = 256;
+constexpr int kRowsPerWarp = 256;
+// Rows and sequences up to which the plan's own block finishes the step.
+constexpr int kSmallRows = 4096;
+
+// What the rest of the step needs to know of a sequence.
+struct __align__(16) Rec {
+    int32_t len, grow;    // cached tokens before, new tokens
+    int32_t row, take;    // first row; pages taken by the sequences before
+    int32_t give;         // pages given back by the sequences before
+    int32_t end0, lo, hi; // pages [0, end0) and [lo, hi) go back
+};
+struct PlanState {
+    int32_t ok, head, count, rows;
+};
+struct PlanLayout {
+    size_t state, rec, total;
+};
+__host__ __device__ inline PlanLayout plan_layout(int B) {
+    PlanLayout l;
+    l.state = 256;
+    l.rec = 512;
+    l.total = l.rec + (size_t)B * sizeof(Rec);
+    return l;
+}
+
+__device__ __forceinline__ int pages_for(int tokens, int shift) {
+    return (int)(((int64_t)tokens + (1 << shift) - 1) >> shift);
+}
+// The place of the ring that `at` < 3 cap means.
+__device__ __forceinline__ int ring_at(int64_t at, int cap) {
+    if (at >= 2 * (int64_t)cap) at -= 2 * (int64_t)cap;
+    return (int)(at >= cap ? at - cap : at);
+}
+
+// Four sums over a block's threads: the totals of the threads before this one,
+// and of all.
+struct Sums {
+    int64_t v[4];
+};
+__device__ __forceinline__ void block_scan(const Sums &mine, Sums &before, Sums &all, Sums *shared) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Sums x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x.v[i], o);
+            if (lane >= o) x.v[i] += y;
+        }
+    if (lane == 31) shared[warp] = x;
+    __syncthreads();
+    const Sums w = shared[lane];  // (32 warps)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        int64_t b = lane < warp ? w.v[i] : 0, t = w.v[i];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            b += __shfl_xor_sync(0xffffffffu, b, o);
+            t += __shfl_xor_sync(0xffffffffu, t, o);
+        }
+        before.v[i] = b + x.v[i] - mine.v[i];
+        all.v[i] = t;
+    }
+    __syncthreads();
+}
+
+// The pages of one sequence that a group of `step` threads takes and gives back.
+__device__ __forceinline__ void move_pages(const PagePlanArgs &a, int b, const Rec &r, const PlanState &st, int first,
+                                           int step) {
+    int32_t *row = a.table + (size_t)b * a.table_stride;
+    const int p0 = pages_for(r.len, a.page_shift);
+    const int need = r.grow ? pages_for(r.len + r.grow, a.page_shift) - p0 : 0;
+#pragma unroll 4
+    for (int i = first; i < need; i += step) row[p0 + i] = a.ring[ring_at((int64_t)st.head + r.take + i, a.cap)];
+    const int back = r.end0 + r.hi - r.lo;
+#pragma unroll 4
+    for (int i = first; i < back; i += step)
+        a.ring[ring_at((int64_t)st.head + st.count + r.give + i, a.cap)] =
+            row[i < r.end0 ? i : r.lo + i - r.end0];
+}
+
+// Position and slot of row t, row i of sequence b.
+__device__ __forceinline__ void put_row(const PagePlanArgs &a, const Rec *recs, const PlanState &st, int b, int t) {
+    int pos = 0, slot = -1;
+    if (t < st.rows) {
+        const Rec r = recs[b];
+        const int j = r.len + t - r.row, p = j >> a.page_shift, p0 = pages_for(r.len, a.page_shift);
+        const int pg = p < p0 ? a.table[(size_t)b * a.table_stride + p]
+                              : a.ring[ring_at((int64_t)st.head + r.take + p - p0, a.cap)];
+        slot = (int)(((uint32_t)pg << a.page_shift) + (j & ((1 << a.page_shift) - 1)));
+        if (pg < 0) slot = -1;
+        pos = a.offsets ? (int)((uint32_t)r.len + (uint32_t)a.offsets[t]) : j;
+    }
+    a.positions[t] = pos;
+    a.slots[t] = slot;
+}
+// The sequence of row t: the last one whose first row is at most t (one warp,
+// all lanes; 32 places are looked at together).
+__device__ __forceinline__ int find_sequence(const int32_t *cu, int B, int t) {
+    int lo = 0, n = B;  // it is in [lo, lo + n)
+    const int lane = threadIdx.x & 31;
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int at = lo + lane * step;
+        const bool le = lane * step < n && *(volatile const int32_t *)(cu + at) <= t;
+        const int k = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
+        n = min(step, n - k * step);
+        lo += k * step;
+    }
+    return lo;
+}
+// The same by one thread, among the sequences from b on.
+__device__ __forceinline__ int find_from(const int32_t *cu, int B, int b, int t) {
+    int n = B - b;
+    while (n > 1) {
+        const int half = n / 2;
+        if (*(volatile const int32_t *)(cu + b + half) <= t) {
+            b += half;
+            n -= half;
+        } else {
+            n = half;
+        }
+    }
+    return b;
+}
+// Rows [t0, t1) by one warp.
+__device__ __forceinline__ void put_rows(const PagePlanArgs &a, const Rec *recs, const PlanState &st, int t0, int t1) {
+    int b = t0 < st.rows ? find_sequence(a.cu_q, a.B, t0) : 0;
+    for (int t = t0 + (threadIdx.x & 31); t < t1; t += 32) {
+        if (t < st.rows && *(volatile const int32_t *)(a.cu_q + b + 1) <= t) b = find_from(a.cu_q, a.B, b, t);
+        put_row(a, recs, st, b, t);
+    }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_step(const PagePlanArgs a, const bool whole) {
+    __shared__ Sums shared[kPlanThreads / 32];
+    __shared__ int first_bad, head_count[2], cu_shared[kSmallRows];
+    pdl_trigger();
+    const int tid = threadIdx.x;
+    const PlanLayout L = plan_layout(a.B);
+    Rec *recs = reinterpret_cast<Rec *>(a.workspace + L.rec);
+    if (tid == 0) {
+        first_bad = INT_MAX;
+        head_count[0] = a.state[0];
+        head_count[1] = a.state[1];
+    }
+    __syncthreads();
+    const int head = head_count[0], count = head_count[1];
+    const int64_t room = min((int64_t)a.table_stride << a.page_shift, (int64_t)1 << 30);
+    const int first = a.window ? (int)(((int64_t)a.sinks + (1 << a.page_shift) - 1) >> a.page_shift) : 0;
+    const bool ring_ok = head >= 0 && head < a.cap && count >= 0 && count <= a.cap;
+    int len = 0, n = 0, kept = 0;  // (of the last pass's sequence)
+    Sums base = {{0, 0, 0, 0}};  // of the sequences before this pass: rows, pages taken, given back, lengths
+    for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        Rec r = {0, 0, 0, 0, 0, 0, 0, 0};
+        Sums mine = {{0, 0, 0, 0}};
+        bool bad = false;
+        if (b < a.B) {
+            len = a.seq_lens[b];
+            n = a.new_lens[b];
+            kept = a.window ? a.kept[b] : 0;
+            const int held = pages_for(max(len, 0), a.page_shift);
+            bad = len < 0 || len > room || n < -1 || (int64_t)len + max(n, 0) > room || kept < 0 || kept > held;
+            if (!bad) {
+                r.len = len;
+                r.grow = max(n, 0);
+                const int lo = max(kept, first);
+                int behind = kept;  // pages behind the window, none of which a later token sees
+                if (a.window) behind = max(kept, (int)(max((int64_t)len + 1 - a.window, (int64_t)0) >> a.page_shift));
+                if (n < 0) {
+                    r.end0 = a.window ? min(first, held) : held;
+                    r.lo = a.window ? lo : held;
+                    r.hi = max(r.lo, held);
+                } else if (a.window) {
+                    r.lo = lo;
+                    r.hi = max(lo, behind);
+                }
+                mine.v[0] = r.grow;
+                mine.v[1] = pages_for(len + r.grow, a.page_shift) - held;
+                if (n < 0) mine.v[1] = 0;
+                mine.v[2] = r.end0 + r.hi - r.lo;
+                mine.v[3] = n < 0 ? 0 : len + r.grow;
+            }
+        }
+        Sums before, all;
+        block_scan(mine, before, all, shared);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            before.v[i] += base.v[i];
+            base.v[i] += all.v[i];
+        }
+        if (b < a.B) {
+            bad = bad || before.v[0] + mine.v[0] > a.rows || before.v[1] + mine.v[1] > count ||
+                  before.v[3] + mine.v[3] > INT_MAX;
+            r.row = (int)before.v[0];
+            r.take = (int)before.v[1];
+            r.give = (int)before.v[2];
+            recs[b] = r;
+            a.cu_q[b] = r.row;
+            if (whole) cu_shared[b] = r.row;
+            if (a.cu_k) a.cu_k[b] = (int)before.v[3];
+            if (bad) atomicMin(&first_bad, b);
+        }
+    }
+    // (more pages given back than the ring has places for: one is given twice)
+    if (tid == 0 && (!ring_ok || base.v[2] > a.cap - count)) atomicMin(&first_bad, a.B);
+    __syncthreads();
+    const bool ok = first_bad == INT_MAX;
+    for (int b = tid; b < a.B; b += kPlanThreads) {
+        if (a.B > kPlanThreads) {
+            len = a.seq_lens[b];
+            n = a.new_lens[b];
+            kept = a.window ? a.kept[b] : 0;
+        }
+        const int behind = a.window ? (int)(max((int64_t)len + 1 - a.window, (int64_t)0) >> a.page_shift) : 0;
+        a.seq_lens_out[b] = !ok ? len : (n < 0 ? 0 : len + n);
+        if (a.window) a.kept_out[b] = !ok ? kept : (n < 0 ? 0 : max(kept, behind));
+        if (!ok) {
+            a.cu_q[b] = 0;
+            if (a.cu_k) a.cu_k[b] = 0;
+        }
+    }
+    const PlanState st = {ok, ok ? head : 0, ok ? count : 0, ok ? (int)base.v[0] : 0};
+    if (tid == 0) {
+        a.cu_q[a.B] = st.rows;
+        if (a.cu_k) a.cu_k[a.B] = ok ? (int)base.v[3] : 0;
+        a.state_out[0] = ok ? ring_at(head + base.v[1], a.cap) : head;
+        a.state_out[1] = ok ? (int)(count - base.v[1] + base.v[2]) : count;
+        Ctrl *ctrl = reinterpret_cast<Ctrl *>(a.workspace);
+        ctrl->status = ok ? MOE_OK : MOE_ERR_DEVICE_BAD_INDEX;
+        ctrl->detail = ok ? 0 : first_bad;
+        *reinterpret_cast<PlanState *>(a.workspace + L.state) = st;
+    }
+    if (!whole) return;
+    __syncthreads();
+    const int warp = tid >> 5, lane = tid & 31;
+    if (ok) {
+        // a thread its sequence; those with more pages than a few, a warp together
+        for (int b0 = warp * 32; b0 < a.B; b0 += kPlanThreads) {
+            Rec r = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (b0 + lane < a.B) r = recs[b0 + lane];
+            const int most = max(r.grow >> a.page_shift, r.end0 + r.hi - r.lo);
+            const uint32_t big = __ballot_sync(0xffffffffu, most > 2);
+            if (b0 + lane < a.B && most <= 2) move_pages(a, b0 + lane, r, st, 0, 1);
+            for (uint32_t m = big; m; m &= m - 1) {
+                const int b = b0 + __ffs(m) - 1;
+                move_pages(a, b, recs[b], st, lane, 32);
+            }
+        }
+    }
+    for (int t = tid; t < a.rows; t += kPlanThreads)
+        put_row(a, recs, st, t < st.rows ? find_from(cu_shared, a.B, 0, t) : 0, t);
+}
+
+__global__ void __launch_bounds__(kFillThreads) fill_step(const PagePlanArgs a) {
+    const PlanLayout L = plan_layout(a.B);
+    const Rec *recs = reinterpret_cast<const Rec *>(a.workspace + L.rec);
+    pdl_wait();
+    const PlanState st = *reinterpret_cast<const PlanState *>(a.workspace + L.state);
+    const int64_t warps = (int64_t)gridDim.x * (kFillThreads / 32);
+    const int64_t me = (int64_t)blockIdx.x * (kFillThreads / 32) + (threadIdx.x >> 5);
+    const int64_t row_items = ((int64_t)a.rows + kRowsPerWarp - 1) / kRowsPerWarp;
+    for (int64_t w = me; w < row_items + a.B; w += warps) {
+        if (w < row_items) {
+            const int t0 = (int)(w * kRowsPerWarp);
+            put_rows(a, recs, st, t0, min(a.rows, t0 + kRowsPerWarp));
+        } else if (st.ok) {
+            const int b = (int)(w - row_items);
+            move_pages(a, b, recs[b], st, threadIdx.x & 31, 32);
+        }
+    }
+}
+
+}  // namespace
+
+size_t page_plan_workspace(int B) { return align_up(plan_layout(B).total, 256); }
+
+cudaError_t launch_page_plan(const PagePlanArgs &a, cudaStream_t s) {
+    const bool whole = a.rows <= kSmallRows && a.B <= kSmallRows;
+    plan_step<<<1, kPlanThreads, 0, s>>>(a, whole);
+    cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess || whole) return err;
+    const int64_t warps = ((int64_t)a.rows + kRowsPerWarp - 1) / kRowsPerWarp + a.B;
+    const int64_t blocks = (warps * 32 + kFillThreads - 1) / kFillThreads;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks < 152 * 8 ? blocks : 152 * 8));
+    cfg.blockDim = dim3(kFillThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fill_step, a);
+}
+
+}  // namespace moe
