@@ -1,0 +1,1049 @@
+// attn_tree.cu -- attention of drafted tokens over the paged cache on the tensor
+// cores.
+//
+// A row is one (drafted token, query head of the group) pair; row tiles have 128
+// of them, key tiles 128 keys.  Every cached byte is used for up to 256 rows,
+// 2 multiply-adds each a value: HBM bounds the few-token trees, the tensor pipe
+// and the softmax (128 exponentials a key and row tile) the large ones.  The
+// products are those of the prompts (attn_prefill.cuh): S_t = Q_t K_j^T and
+// O_t += P_t V_j with P_t over S_t in tensor memory, two row tiles t in turns, one
+// warp issuing each one's products, one thread a softmax row with a reference
+// that is raised when the maximum exceeds it by 2^8.
+//  * 129 to 256 rows: the two row tiles share every key tile ("shared").
+//  * Up to 128 rows: both have the same rows, and take the key tiles in turns, so
+//    that one's softmax runs under the other's products all the same; their sums
+//    are joined in tensor memory, whose lanes are the rows of both.
+//  * More rows: blocks of 256, which read the keys again, mostly from L2.
+// The key tiles of the whole batch, in order, are shared out evenly over one block
+// per SM; a range cut by a block's end is joined by a second kernel, in key order.
+//
+// A bf16 cache is copied page by page into the swizzled operand tiles.  An fp8
+// cache is copied as it is; four warps turn its codes into operands: fp16 for the
+// scores (exact, as is Q times a power of two a row, but for values below 2^-14
+// of their row's largest, off by up to 2^-25 of it), bf16 for the product with
+// the weights (exact).  The scales of K multiply the scores, those of V the
+// weights, in fp32; a weight is rounded once, to bf16.
+#include <type_traits>
+
+#include "attn_tc.cuh"
+#include "gemm_tc.h"
+
+namespace moe {
+namespace {
+
+using namespace attn;
+
+constexpr int kTile = 128;       // rows of a row tile
+constexpr int kM = 2;            // row tiles in turns
+constexpr int kKeys = 128;       // keys of a key tile
+constexpr int kRawKeys = 64;     // keys of a copied tile of fp8 codes
+constexpr float kSlack = 8.f;    // a row's maximum may exceed its reference by this
+constexpr int kMaxGrid = 160;    // blocks at most
+constexpr int kParts = 2;        // in which a key tile's weights come
+constexpr int kScaleBufs = 4;    // key tiles whose scales are held
+
+// Warps: two softmax warpgroups; one warp per row tile issuing products, one
+// copying, one clearing; for fp8 a warpgroup that converts.
+constexpr int kMmaWarp = 8, kLoadWarp = 10, kFixWarp = 11, kConvWarp = 12;
+
+template <int D, bool FP8>
+struct Cfg {
+    static constexpr int kThreads = FP8 ? 512 : 384;
+    // The launch's registers a thread (128 or 168), shared out anew.
+    static constexpr int kRoleRegs = FP8 ? 64 : 72, kSoftmaxRegs = FP8 ? 192 : 216;
+    static_assert((kThreads - 256) * kRoleRegs + 256 * kSoftmaxRegs <= kThreads * (FP8 ? 128 : 168), "register split");
+    static constexpr int kQB = kTile * D * 2, kKvB = kKeys * D * 2;  // a Q tile, an operand tile of K or V
+    static constexpr int kOps = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
+    static constexpr int kRawB = kRawKeys * D;
+    static constexpr int kRaw = FP8 ? (D == 128 ? 7 : 12) : 1;
+    static constexpr int kRawStage = kRawB + 2 * kRawKeys * 4;  // codes; the scales of K and V with K's
+    static constexpr size_t kOpAt = (size_t)kM * kQB, kRawAt = kOpAt + (size_t)kOps * kKvB;
+    static constexpr size_t kSharedAt = kRawAt + (FP8 ? (size_t)kRaw * kRawStage : 0);
+    // fp8: the scales of kScaleBufs key tiles, [2][kKeys] floats each, those of K
+    // times the scores' factor
+    static constexpr size_t kScalesAt = kSharedAt + 2048;
+    static constexpr size_t kSmem = kScalesAt + (FP8 ? kScaleBufs * 2 * kKeys * 4 : 0) + 1024;
+    static_assert(kSmem > 114 * 1024 && kSmem <= 227 * 1024, "one block per SM: all of tensor memory is its own");
+};
+
+// Some key tiles of one block of rows.
+struct Item {
+    int32_t q0, nq, nk;       // the sequence's first row, drafted tokens, keys
+    int32_t tok0, hk, h0, heads;  // first token of the rows; key/value head; first query head and their number
+    int32_t shared;           // two row tiles share the key tiles
+    int32_t j0, tiles;        // key tiles
+    int32_t slot;             // place for its sums, -1: all of the keys
+    int32_t done;
+};
+struct Join {
+    int32_t b, hv, parts, first;
+};
+struct Err {
+    int32_t timeout, bad;
+};
+struct TreeLayout {
+    size_t err, join, ml, sums, total;
+};
+__host__ __device__ inline TreeLayout tree_layout(int D) {
+    TreeLayout l;
+    l.err = 256;
+    l.join = l.err + kMaxGrid * sizeof(Err);
+    l.ml = l.join + kMaxGrid * sizeof(Join);
+    const size_t rows = (size_t)2 * kMaxGrid * kM * kTile;
+    l.sums = (l.ml + rows * 8 + 255) / 256 * 256;
+    l.total = l.sums + rows * D * 4;
+    return l;
+}
+// Place of a part's four columns c .. c + 3 of row r of row tile t.
+__host__ __device__ inline size_t part_at(int slot, int t, int c, int r, int D) {
+    return ((((size_t)slot * kM + t) * (D / 4) + c / 4) * kTile + r) * 4;
+}
+// Query heads and tokens of a row tile, for groups of G heads.
+__host__ __device__ inline int tile_heads(int G) { return G < kTile ? G : kTile; }
+__host__ __device__ inline int tile_tokens(int G) { return kTile / tile_heads(G); }
+
+struct Shared {
+    uint64_t q_full[kM], q_ready[kM], q_empty[kM], op_full[8], op_empty[8], tail[8], raw_full[12], raw_empty[12];
+    uint64_t sc_full[kScaleBufs], s_full[kM], p_ready[kM][kParts], o_done[kM], merge[3];
+    uint64_t item_full[2], item_empty[2], finished;
+    uint32_t tmem;
+    int abort, bad;
+    int b0;                 // the sequence of this block's first key tile
+    int64_t first;          // and that tile's index among the sequence's
+    int64_t warp_sum[16];
+    Item item[2];
+    // rows whose two sums are joined: the second one's reference and sum, then the
+    // two factors
+    float2 pair[kTile];
+};
+static_assert(sizeof(Shared) <= 2048, "shared block");
+
+// What a sequence has to do.
+struct Seq {
+    int q0, nq, nk, tiles, RB, HV;  // blocks of rows per head tile, in all
+};
+__device__ __forceinline__ bool seq_of(const DecodeAttnArgs &a, int b, int tpt, int HT, Seq &s) {
+    const int64_t room = min((int64_t)a.table_stride << a.kv.page_shift, (int64_t)1 << 30);
+    s.q0 = __ldg(a.cu_q + b);
+    const int q1 = __ldg(a.cu_q + b + 1);
+    s.nk = __ldg(a.seq_lens + b);
+    s.nq = q1 - s.q0;
+    const bool ok = s.q0 >= 0 && q1 >= s.q0 && q1 <= a.T && s.nq <= kTreeTokens && s.nk >= 0 && s.nk <= room &&
+                    s.nq <= s.nk;
+    if (!ok) s.nq = 0;
+    s.tiles = s.nq ? (s.nk + kKeys - 1) / kKeys : 0;
+    s.RB = (s.nq + kM * tpt - 1) / (kM * tpt);
+    s.HV = a.kv.Hkv * HT * s.RB;
+    return ok;
+}
+
+// 4 e4m3 codes of neighbouring columns -> two pairs of bf16: a code's exponent and
+// mantissa bits moved to the bf16 places are its value times 2^-120.  Exact, but for
+// the NaN code, which comes out as 480.
+__device__ __forceinline__ uint2 e4m3_bf16(uint32_t w) {
+    const uint32_t up = 0x7B807B80u;  // bf16 2^120
+    w = __byte_perm(w, 0, 0x3120);    // codes 0, 2, 1, 3
+    const uint32_t l = ((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u);
+    const uint32_t h = ((w >> 4) & 0x07F007F0u) | (w & 0x80008000u);
+    uint2 r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(l), "r"(up));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(h), "r"(up));
+    return r;
+}
+// Whether one of 4 codes is NaN (0x7F or 0xFF).
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint2 with_nans(uint2 v, uint32_t w) {
+    const uint32_t n = nan_codes(w);
+    if (n & 0x80u) v.x = (v.x & 0xFFFF0000u) | 0x7FC0u;
+    if (n & 0x8000u) v.x = (v.x & 0xFFFFu) | 0x7FC00000u;
+    if (n & 0x800000u) v.y = (v.y & 0xFFFF0000u) | 0x7FC0u;
+    if (n & 0x80000000u) v.y = (v.y & 0xFFFFu) | 0x7FC00000u;
+    return v;
+}
+__device__ __forceinline__ uint2 e4m3_f16(uint32_t w) {
+    uint2 r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r.x) : "h"((uint16_t)w));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r.y) : "h"((uint16_t)(w >> 16)));
+    return r;
+}
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__((Cfg<D, FP8>::kThreads), 1)
+tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtensorMap map_q,
+            const __grid_constant__ CUtensorMap map_kv) {
+    using C = Cfg<D, FP8>;
+    constexpr int S = C::kOps, kHalves = D / 64, kThreads = C::kThreads;
+    constexpr uint32_t kQHalf = kTile * 128, kKvHalf = kKeys * 128;  // 64 columns of a tile
+    extern __shared__ uint8_t raw[];
+    const uint32_t raw_u = smem_u32(raw);
+    uint8_t *base = raw + ((1024 - (raw_u & 1023)) & 1023);
+    uint8_t *op_base = base + C::kOpAt, *raw_base = base + C::kRawAt;
+    Shared *sm = reinterpret_cast<Shared *>(base + C::kSharedAt);
+    float *scales = reinterpret_cast<float *>(base + C::kScalesAt);
+    const uint32_t q_smem = smem_u32(base), op_smem = smem_u32(op_base);
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int tid = threadIdx.x, g = blockIdx.x;
+    const int G = a.Hq / a.kv.Hkv, Gt = tile_heads(G), tpt = tile_tokens(G);
+    const TreeLayout L = tree_layout(D);
+
+    if (warp == kMmaWarp) tmem_alloc(&sm->tmem, 512);
+    if (tid == 0) {
+        for (int t = 0; t < kM; ++t) {
+            mbar_init(&sm->q_full[t], 1);
+            mbar_init(&sm->q_ready[t], 4);
+            mbar_init(&sm->q_empty[t], 1);
+            mbar_init(&sm->s_full[t], 1);
+            for (int h = 0; h < kParts; ++h) mbar_init(&sm->p_ready[t][h], 4);
+            mbar_init(&sm->o_done[t], 1);
+            mbar_init(&sm->merge[t], 4);
+            mbar_init(&sm->item_full[t], 1);
+            mbar_init(&sm->item_empty[t], FP8 ? 14 : 11);  // the warps that take items
+        }
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(&sm->op_full[i], FP8 ? 4 : 1);
+            mbar_init(&sm->op_empty[i], kM);
+            mbar_init(&sm->tail[i], 1);
+        }
+        for (int i = 0; i < 12; ++i) {
+            mbar_init(&sm->raw_full[i], 1);
+            mbar_init(&sm->raw_empty[i], 4);
+        }
+        for (int i = 0; i < kScaleBufs; ++i) mbar_init(&sm->sc_full[i], 4);
+        mbar_init(&sm->merge[2], 8);
+        mbar_init(&sm->finished, kM);
+        fence_barrier_init();
+        sm->abort = 0;
+        sm->bad = 0x7fffffff;
+        prefetch_tensormap(&map_q);
+        if (!FP8) prefetch_tensormap(&map_kv);
+    }
+    pdl_trigger();
+
+    // ---- this block's share: key tiles [u0, u1) of the batch's W
+    const int per = (a.B + kThreads - 1) / kThreads;
+    const int s0 = min(a.B, tid * per), s1 = min(a.B, s0 + per);
+    int64_t mine = 0;
+    int bad = 0x7fffffff;
+    for (int b = s0; b < s1; ++b) {
+        Seq s;
+        if (!seq_of(a, b, tpt, HT, s) && b < bad) bad = b;
+        mine += (int64_t)s.tiles * s.HV;
+    }
+    int64_t scan = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += v;
+    }
+    if (lane == 31) sm->warp_sum[warp] = scan;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int64_t before = scan - mine, W = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += sm->warp_sum[w];
+        W += sm->warp_sum[w];
+    }
+    if (bad != 0x7fffffff && g == 0) atomicMin(&sm->bad, bad);
+    const int NG = (int)min((int64_t)gridDim.x, W);  // blocks that have a share
+    const int64_t u0 = g < NG ? (int64_t)g * W / NG : 0, u1 = g < NG ? (int64_t)(g + 1) * W / NG : 0;
+    if (u0 < u1 && u0 >= before && u0 < before + mine) {
+        int64_t at = before;
+        int b = s0;
+        for (;; ++b) {
+            Seq s;
+            seq_of(a, b, tpt, HT, s);
+            const int64_t n = (int64_t)s.tiles * s.HV;
+            if (u0 < at + n) break;
+            at += n;
+        }
+        sm->b0 = b;
+        sm->first = u0 - at;
+    }
+    // (its address is 0; anything else is reported like a wait that gave up)
+    if (tid == 0 && sm->tmem != 0) sm->abort = 20;
+    __syncthreads();
+    constexpr uint32_t s_col = 0, o_col = kM * kKeys;
+    static_assert(kM * (kKeys + D) <= 512, "tensor memory");
+
+    auto take = [&](uint32_t n, Item &it) {
+        if (!warp_wait_flag(&sm->item_full[n & 1], (n >> 1) & 1, &sm->abort, 1)) return false;
+        it = sm->item[n & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->item_empty[n & 1]);
+        return it.done == 0;
+    };
+    // the item's key tiles that row tile t has
+    auto tiles_of = [&](const Item &it, int t) { return it.shared ? it.tiles : (it.tiles + 1 - t) / 2; };
+
+    if (warp >= kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRoleRegs));
+        if (warp == kLoadWarp) {
+            // ---------------- copies, and the items for everyone
+            Join *const join = reinterpret_cast<Join *>(a.workspace + L.join);
+            if (lane == 0) join[g] = Join{0, 0, 0, 0};
+            __syncwarp();
+            const int page_shift = a.kv.page_shift, page_mask = (1 << page_shift) - 1;
+            const int box_shift = min(page_shift, FP8 ? 6 : 7), R = 1 << box_shift;  // rows of one copy
+            const int chunks = kKeys >> box_shift;
+            Seq sq = {};
+            int b = 0, hv = 0, j = 0;
+            if (u0 < u1) {
+                b = sm->b0;
+                seq_of(a, b, tpt, HT, sq);
+                hv = (int)(sm->first / sq.tiles);
+                j = (int)(sm->first % sq.tiles);
+            }
+            // this lane's page of a key tile: chunk lane % chunks
+            auto page_of = [&](int bb, int jj, int nk) {
+                const int key = jj * kKeys + ((lane % chunks) << box_shift);
+                return key < nk ? __ldg(a.page_table + (size_t)bb * a.table_stride + (key >> page_shift)) : 0;
+            };
+            int pg = u0 < u1 ? page_of(b, j, sq.nk) : 0;
+            uint32_t n = 0, op = 0, rw = 0;
+            bool ok = true;
+            int64_t u = u0;
+            for (;; ++n) {
+                Item it;
+                it.done = u >= u1;
+                if (!it.done) {
+                    const int left = (int)min((int64_t)(sq.tiles - j), u1 - u);
+                    const bool starts = j == 0, ends = j + left == sq.tiles;
+                    const int rest = hv % (HT * sq.RB), ht = rest / sq.RB, rb = rest % sq.RB;
+                    it.q0 = sq.q0;
+                    it.nq = sq.nq;
+                    it.nk = sq.nk;
+                    it.tok0 = rb * kM * tpt;
+                    it.hk = hv / (HT * sq.RB);
+                    it.h0 = it.hk * G + ht * Gt;
+                    it.heads = min(Gt, G - ht * Gt);
+                    it.shared = sq.nq - it.tok0 > tpt;
+                    it.j0 = j;
+                    it.tiles = left;
+                    it.slot = starts && ends ? -1 : 2 * g + (starts ? 1 : 0);
+                    if (starts && !ends && lane == 0) {
+                        // up to the block that holds the range's last tile
+                        const int owner = (int)(((u + sq.tiles) * NG - 1) / W);
+                        join[g] = Join{b, hv, owner - g + 1, g};
+                    }
+                }
+                if (!warp_wait_flag(&sm->item_empty[n & 1], ((n >> 1) & 1) ^ 1, &sm->abort, 2)) break;
+                if (lane == 0) {
+                    sm->item[n & 1] = it;
+                    mbar_arrive(&sm->item_full[n & 1]);
+                }
+                __syncwarp();
+                if (it.done) break;
+                const int b_now = b;
+                const int64_t head = (int64_t)it.hk;
+                // where the next item starts
+                u += it.tiles;
+                j += it.tiles;
+                if (j == sq.tiles) {
+                    j = 0;
+                    if (++hv == sq.HV) {
+                        hv = 0;
+                        if (u < u1)
+                            do {
+                                ++b;
+                                seq_of(a, b, tpt, HT, sq);
+                            } while (sq.tiles == 0);
+                    }
+                }
+                for (int i = 0; i < it.tiles && ok && !a.test_no_copies; ++i) {
+                    const int key0 = (it.j0 + i) * kKeys;
+                    const int key = key0 + ((lane % chunks) << box_shift);
+                    const bool live = key < it.nk;
+                    int p = pg;
+                    if (live && (unsigned)p >= (unsigned)a.kv.num_pages) {
+                        atomicMin(&sm->bad, b_now);
+                        p = 0;
+                    }
+                    // (the next tile's page is fetched while this one's copies wait)
+                    if (i + 1 < it.tiles)
+                        pg = page_of(b_now, it.j0 + i + 1, it.nk);
+                    else if (u < u1)
+                        pg = page_of(b, j, sq.nk);
+                    const int64_t ph = (int64_t)p * a.kv.Hkv + head;
+                    const int n_live = min(kKeys, it.nk - key0);  // keys
+                    if (!FP8) {
+                        const int copied = min(kKeys, (n_live + R - 1) & -R);  // rows that are copied
+                        for (int kv = 0; kv < 2; ++kv) {
+                            const uint32_t s = op % S, par = (op / S) & 1;
+                            ok = ok && warp_wait_flag(&sm->op_empty[s], par ^ 1, &sm->abort, 3);
+                            if (!ok) break;
+                            // values past the sequence's end are cleared before they are used
+                            uint64_t *bar = kv && n_live < kKeys ? &sm->tail[s] : &sm->op_full[s];
+                            if (lane == 0) mbar_arrive_expect_tx(bar, copied * D * 2);
+                            __syncwarp();
+                            if (live && lane < chunks * kHalves) {
+                                const int h = lane / chunks;
+                                tma_load_4d(op_base + s * C::kKvB + h * kKvHalf + ((lane % chunks) << box_shift) * 128,
+                                            &map_kv, 0, key & page_mask, h, (int)(ph * 2 + kv), bar);
+                            }
+                            __syncwarp();
+                            ++op;
+                            if (kv == 0 && i == 0) {
+                                for (int t = 0; t < kM && ok; ++t) {
+                                    ok = warp_wait_flag(&sm->q_empty[t], (n & 1) ^ 1, &sm->abort, 4);
+                                    if (ok && lane == 0) {
+                                        mbar_arrive_expect_tx(&sm->q_full[t], (uint32_t)(Gt * tpt) * D * 2);
+                                        for (int h = 0; h < kHalves; ++h)
+                                            tma_load_4d(base + t * C::kQB + h * kQHalf, &map_q, 0, it.h0,
+                                                        it.q0 + it.tok0 + (it.shared ? t * tpt : 0), h, &sm->q_full[t]);
+                                    }
+                                    __syncwarp();
+                                }
+                            }
+                        }
+                    } else {
+                        if (i == 0)
+                            for (int t = 0; t < kM && ok; ++t) {
+                                ok = warp_wait_flag(&sm->q_empty[t], (n & 1) ^ 1, &sm->abort, 4);
+                                if (ok && lane == 0) {
+                                    mbar_arrive_expect_tx(&sm->q_full[t], (uint32_t)(Gt * tpt) * D * 2);
+                                    for (int h = 0; h < kHalves; ++h)
+                                        tma_load_4d(base + t * C::kQB + h * kQHalf, &map_q, 0, it.h0,
+                                                    it.q0 + it.tok0 + (it.shared ? t * tpt : 0), h, &sm->q_full[t]);
+                                }
+                                __syncwarp();
+                            }
+                        const int row = key & page_mask;
+                        for (int part = 0; part < 4 && ok; ++part) {  // K's two halves, V's
+                            const int half = part & 1, kv = part >> 1;
+                            const uint32_t s = rw % C::kRaw, par = (rw / C::kRaw) & 1;
+                            ok = warp_wait_flag(&sm->raw_empty[s], par ^ 1, &sm->abort, 3);
+                            if (!ok) break;
+                            const int keys = max(0, min(kRawKeys, ((n_live - half * kRawKeys) + R - 1) & -R));
+                            if (lane == 0) mbar_arrive_expect_tx(&sm->raw_full[s], keys * (D + (kv ? 0 : 8)));
+                            __syncwarp();
+                            const int c = lane - half * (kRawKeys >> box_shift);  // chunk of this half
+                            if (live && lane < chunks && c >= 0 && c < kRawKeys >> box_shift) {
+                                const uint32_t to = smem_u32(raw_base + s * C::kRawStage);
+                                bulk_g2s(to + c * R * D, a.kv.data + (((ph * 2 + kv) << page_shift) + row) * D, R * D,
+                                         &sm->raw_full[s]);
+                                if (!kv) {
+                                    const float *sc = a.kv.scales + ((ph * 2) << page_shift) + row;
+                                    bulk_g2s(to + C::kRawB + c * R * 4, sc, R * 4, &sm->raw_full[s]);
+                                    bulk_g2s(to + C::kRawB + kRawKeys * 4 + c * R * 4, sc + ((size_t)1 << page_shift),
+                                             R * 4, &sm->raw_full[s]);
+                                }
+                            }
+                            __syncwarp();
+                            ++rw;
+                        }
+                    }
+                }
+                if (!ok) break;
+            }
+            // (after a give-up) nothing of this warp's may still be in flight
+            if (*(volatile int *)&sm->abort) {
+                const long long t0 = clock64();
+                while (clock64() - t0 < (1ll << 24)) __nanosleep(1000);
+            }
+        } else if (warp < kLoadWarp) {
+            // ---------------- products of row tile t
+            auto products = [&](auto tile) {
+                constexpr int t = decltype(tile)::value;
+                const uint64_t qd = sdesc_k_sw128(q_smem) + ((t * C::kQB) >> 4), k_desc = sdesc_k_sw128(op_smem);
+                const uint64_t v_desc = sdesc_mn_sw128(op_smem, kKvHalf);
+                constexpr uint32_t kIdS = FP8 ? idesc_f16_m128(kKeys) : idesc_bf16(kKeys, false);
+                constexpr uint32_t kIdO = idesc_bf16(D, true);
+                constexpr uint32_t s_t = s_col + t * kKeys, o_t = o_col + t * D;
+                uint32_t stage = 0, stage_ph = 0, p_ph = 0;
+                Item it;
+                bool ok = true;
+                auto next_stage = [&]() {
+                    ok = ok && warp_wait_flag(&sm->op_full[stage], stage_ph, &sm->abort, 5);
+                    tc_fence_after();
+                    const uint32_t s = stage;
+                    if (++stage == S) {
+                        stage = 0;
+                        stage_ph ^= 1;
+                    }
+                    return s;
+                };
+                for (uint32_t n = 0; ok && take(n, it); ++n) {
+                    const int tiles = __shfl_sync(0xffffffffu, it.tiles, 0);
+                    const int mine = __shfl_sync(0xffffffffu, tiles_of(it, t), 0);
+                    const bool both = __shfl_sync(0xffffffffu, it.shared, 0) != 0;
+                    int done = 0;  // own tiles whose scores were issued
+                    for (int j = 0; j < tiles && ok; ++j) {
+                        const uint32_t k = next_stage();
+                        if (j == 0) {
+                            ok = ok && warp_wait_flag(FP8 ? &sm->q_ready[t] : &sm->q_full[t], n & 1, &sm->abort, 6);
+                            tc_fence_after();
+                        }
+                        if (!ok) break;
+                        const bool is_own = both || (j & 1) == t;
+                        if (is_own) {
+                            ++done;
+                            if (elect_one()) {
+                                const uint64_t kd = k_desc + ((k * C::kKvB) >> 4);
+#pragma unroll
+                                for (int i = 0; i < D / 16; ++i) {
+                                    const uint32_t in = (i & 3) * 32;
+                                    mma_bf16_ss(s_t, qd + (((i >> 2) * kQHalf + in) >> 4),
+                                                kd + (((i >> 2) * kKvHalf + in) >> 4), kIdS, i > 0);
+                                }
+                                tc_commit(&sm->s_full[t]);
+                                tc_commit(&sm->op_empty[k]);
+                                if (done == mine) tc_commit(&sm->q_empty[t]);
+                            }
+                        } else if (lane == 0) {
+                            mbar_arrive(&sm->op_empty[k]);
+                        }
+                        __syncwarp();
+                        const uint32_t v = next_stage();
+                        if (!ok) break;
+                        if (is_own) {
+                            const uint64_t vd = v_desc + ((v * C::kKvB) >> 4);
+                            constexpr int kSteps = kKeys / 16 / kParts;
+#pragma unroll
+                            for (int h = 0; h < kParts; ++h) {
+                                ok = ok && warp_wait_flag(&sm->p_ready[t][h], p_ph, &sm->abort, 7);
+                                if (!ok) break;
+                                tc_fence_after();
+                                if (elect_one()) {
+#pragma unroll
+                                    for (int i = h * kSteps; i < (h + 1) * kSteps; ++i)
+                                        mma_f16_ts(o_t, s_t + i * 8, vd + ((i * 2048) >> 4), kIdO,
+                                                   i > 0 ? 1u : (done == 1 ? 0u : 1u));
+                                    if (h == kParts - 1) {
+                                        tc_commit(&sm->o_done[t]);
+                                        tc_commit(&sm->op_empty[v]);
+                                    }
+                                }
+                                __syncwarp();
+                            }
+                            p_ph ^= 1;
+                        } else if (lane == 0) {
+                            mbar_arrive(&sm->op_empty[v]);
+                        }
+                        __syncwarp();
+                    }
+                    if (ok && mine == 0 && lane == 0) mbar_arrive(&sm->q_empty[t]);  // (not used)
+                    __syncwarp();
+                }
+                // everything issued has finished before the block ends
+                if (elect_one()) tc_commit(&sm->finished);
+                __syncwarp();
+                wait_own(&sm->finished, 0);
+            };
+            if (warp == kMmaWarp)
+                products(std::integral_constant<int, 0>{});
+            else
+                products(std::integral_constant<int, 1>{});
+        } else if (!FP8 && warp == kFixWarp) {
+            // ---------------- last value tiles: zeros past the sequence's end
+            Item it;
+            uint32_t op = 0, ph = 0;  // ph: one phase bit per stage
+            for (uint32_t n = 0; take(n, it); ++n) {
+                op += 2 * it.tiles;
+                const int from = it.nk - (it.j0 + it.tiles - 1) * kKeys;
+                if (from >= kKeys) continue;
+                const uint32_t s = (op - 1) % S;
+                if (!warp_wait_flag(&sm->tail[s], (ph >> s) & 1, &sm->abort, 8)) break;
+                ph ^= 1u << s;
+                uint8_t *v = op_base + s * C::kKvB;
+                for (int h = 0; h < kHalves; ++h)
+                    for (int i = from * 8 + lane; i < kKeys * 8; i += 32)
+                        *reinterpret_cast<uint4 *>(v + h * kKvHalf + i * 16) = make_uint4(0, 0, 0, 0);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm->op_full[s]);
+            }
+        } else if (FP8 && warp >= kConvWarp) {
+            // ---------------- codes into operands
+            const int ct = tid - 32 * kConvWarp;
+            const float factor = a.scale * kLog2e;
+            Item it;
+            uint32_t op = 0, rw = 0, tile = 0;
+            bool ok = true;
+            for (uint32_t n = 0; ok && take(n, it); ++n)
+                for (int j = 0; j < it.tiles && ok; ++j, ++tile) {
+                    const int n_live = it.nk - (it.j0 + j) * kKeys;
+                    float *sc = scales + (tile % kScaleBufs) * 2 * kKeys;
+#pragma unroll 1
+                    for (int kv = 0; kv < 2 && ok; ++kv, ++op) {
+                        const uint32_t s = op % S;
+                        ok = warp_wait_flag(&sm->op_empty[s], ((op / S) & 1) ^ 1, &sm->abort, 14);
+                        uint8_t *to = op_base + s * C::kKvB;
+#pragma unroll 1
+                        for (int half = 0; half < 2 && ok; ++half, ++rw) {
+                            const uint32_t r = rw % C::kRaw;
+                            ok = warp_wait_flag(&sm->raw_full[r], (rw / C::kRaw) & 1, &sm->abort, 15);
+                            if (!ok) break;
+                            const uint8_t *from = raw_base + r * C::kRawStage;
+                            constexpr int kRow = D / 16, kEach = kRawKeys * kRow / 128;  // 16-byte pieces
+                            uint4 c[kEach];
+#pragma unroll
+                            for (int k = 0; k < kEach; ++k)
+                                c[k] = *reinterpret_cast<const uint4 *>(from + (ct + k * 128) * 16);
+                            if (kv == 0) {
+                                const int key = half * kRawKeys + (ct & 63), v = ct >> 6;
+                                const float x = reinterpret_cast<const float *>(from + C::kRawB)[ct];
+                                sc[v * kKeys + key] = key < n_live ? (v ? x : x * factor) : 0.f;
+                            }
+#pragma unroll
+                            for (int k = 0; k < kEach; ++k) {
+                                const int i = ct + k * 128, key = half * kRawKeys + i / kRow, piece = i % kRow;
+                                if (key >= n_live) c[k] = make_uint4(0, 0, 0, 0);
+                                uint2 o[4];
+                                const uint32_t w[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
+                                if (kv == 0) {
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) o[e] = e4m3_f16(w[e]);
+                                } else {
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) o[e] = e4m3_bf16(w[e]);
+                                    if (nan_codes(w[0]) | nan_codes(w[1]) | nan_codes(w[2]) | nan_codes(w[3]))
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e) o[e] = with_nans(o[e], w[e]);
+                                }
+                                // two 16-byte units of a 128-byte row of 64 columns; the
+                                // second half's lanes write theirs in the other order
+                                // (else two lanes of a store meet in the same banks)
+                                uint8_t *row = to + (piece >> 2) * kKvHalf + key * 128;
+                                const int unit = (piece & 3) * 2, turn = piece >> 2;
+#pragma unroll
+                                for (int x = 0; x < 2; ++x) {
+                                    const bool second = (x ^ turn) != 0;
+                                    const uint4 v = second ? make_uint4(o[2].x, o[2].y, o[3].x, o[3].y)
+                                                           : make_uint4(o[0].x, o[0].y, o[1].x, o[1].y);
+                                    *reinterpret_cast<uint4 *>(row + (((unit + (second ? 1 : 0)) ^ (key & 7)) << 4)) = v;
+                                }
+                            }
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sm->raw_empty[r]);
+                        }
+                        if (!ok) break;
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&sm->op_full[s]);
+                            if (kv == 0) mbar_arrive(&sm->sc_full[tile % kScaleBufs]);
+                        }
+                        __syncwarp();
+                    }
+                }
+        }
+    } else {
+        // ---------------- softmax: warpgroup t has row tile t, a thread a row
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
+        const int t = warp >> 2;
+        const int r = tid & 127;
+        const uint32_t lane_base = (uint32_t)(warp & 3) * 32 << 16;
+        const uint32_t s_t = s_col + t * kKeys + lane_base, o_t = o_col + t * D + lane_base;
+        const int tok_r = r / Gt, gr = r % Gt;
+        uint32_t ph = 0;        // parity of this warpgroup's count of key tiles
+        uint32_t tile0 = 0;     // key tiles of the items before
+        uint32_t merges = 0;    // parity of the count of joined items
+        Item it;
+        bool ok = true;
+        for (uint32_t n = 0; ok && take(n, it); ++n) {
+            const int tok = it.tok0 + (it.shared ? t * tpt : 0) + tok_r;
+            const bool live = tok_r < tpt && tok < it.nq && gr < it.heads;
+            const bool any_live = __any_sync(0xffffffffu, live);
+            const int ctx = it.nk - it.nq;
+            const uint64_t mask = live ? __ldg(a.tree + it.q0 + tok) & (~0ull >> (64 - it.nq)) : 0;
+            float sl = a.scale * kLog2e;
+            if (FP8) {
+                // this row of Q to fp16, its largest value in [1, 2)
+                ok = warp_wait_flag(&sm->q_full[t], n & 1, &sm->abort, 16);
+                if (!ok) break;
+                uint8_t *q = base + t * C::kQB + r * 128;
+                float most = 0.f;
+                if (any_live) {
+#pragma unroll
+                    for (int u = 0; u < D / 8; ++u) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(q + (u >> 3) * kQHalf + (((u & 7) ^ (r & 7)) << 4));
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            most = max3(most, fabsf(__uint_as_float(w[e] << 16)),
+                                        fabsf(__uint_as_float(w[e] & 0xFFFF0000u)));
+                    }
+                    const int e2 = max((int)(__float_as_uint(most) >> 23) - 127, -126);
+                    const float down = e2 >= 127 ? 0x1p-127f : __uint_as_float((127 - e2) << 23);
+                    sl = e2 <= -126 ? 0x1p-126f : __uint_as_float((127 + e2) << 23);
+#pragma unroll
+                    for (int u = 0; u < D / 8; ++u) {
+                        uint4 *at = reinterpret_cast<uint4 *>(q + (u >> 3) * kQHalf + (((u & 7) ^ (r & 7)) << 4));
+                        const uint4 v = *at;
+                        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const __half2 h = __floats2half2_rn(__uint_as_float(w[e] << 16) * down,
+                                                                __uint_as_float(w[e] & 0xFFFF0000u) * down);
+                            w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                        }
+                        *at = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm->q_ready[t]);
+            }
+            float ref = -INFINITY;  // the row's reference, in log2 units
+            float l = 0.f;
+            int done = 0;
+            for (int j = it.shared ? 0 : t; j < it.tiles; j += it.shared ? 1 : 2, ++done) {
+                ok = warp_wait_flag(&sm->s_full[t], ph, &sm->abort, 9);
+                if (!ok) break;
+                if (FP8) {
+                    const uint32_t at = tile0 + j;
+                    ok = warp_wait_flag(&sm->sc_full[at % kScaleBufs], (at / kScaleBufs) & 1, &sm->abort, 17);
+                    if (!ok) break;
+                }
+                const float *sc = scales + ((tile0 + j) % kScaleBufs) * 2 * kKeys;
+                tc_fence_after();
+                if (!any_live) {  // (no row of this warp's is used)
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        for (int h = 0; h < kParts; ++h) mbar_arrive(&sm->p_ready[t][h]);
+                    ph ^= 1;
+                    continue;
+                }
+                float x[kKeys];
+#pragma unroll
+                for (int c = 0; c < kKeys; c += 32) tmem_ld32(s_t + c, x + c);
+                tc_wait_ld();
+                if (FP8) {
+#pragma unroll
+                    for (int c = 0; c < kKeys; c += 4) {
+                        const float4 k = *reinterpret_cast<const float4 *>(sc + c);
+                        x[c] *= k.x;
+                        x[c + 1] *= k.y;
+                        x[c + 2] *= k.z;
+                        x[c + 3] *= k.w;
+                    }
+                }
+                const int key0 = (it.j0 + j) * kKeys;
+                if (key0 + kKeys > ctx) {
+#pragma unroll
+                    for (int c = 0; c < kKeys; c += 32) {
+                        const int d = key0 + c - ctx;  // the drafted token of column c
+                        if (d > -32) {
+                            const uint32_t vis = d >= 64  ? 0u
+                                                 : d >= 0 ? (uint32_t)(mask >> d)
+                                                          : ((uint32_t)mask << -d) | ((1u << -d) - 1u);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[c + e] = vis >> e & 1 ? x[c + e] : -INFINITY;
+                        }
+                    }
+                }
+                float m4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                for (int c = 4; c + 8 <= kKeys; c += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], x[c + 2 * e], x[c + 2 * e + 1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], x[kKeys - 4 + e]);
+                const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl;
+                const bool raise = top > ref + kSlack;
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float to = raise ? top : ref;
+                    const float f = raise ? ex2(ref - to) : 1.f;
+                    l *= f;
+                    ref = to;
+                    if (done > 0) {
+                        // the last product into O_t has to be over
+                        ok = warp_wait_flag(&sm->o_done[t], ph ^ 1, &sm->abort, 10);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(o_t + c, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st16(o_t + c, o);
+                        }
+                    }
+                }
+                const float z = ref == -INFINITY ? 0.f : ref;
+                const float2 sl2 = make_float2(sl, sl), nz2 = make_float2(-z, -z);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int c = 0; c < kKeys; c += 32) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float2 y = fma2(make_float2(x[c + 2 * e], x[c + 2 * e + 1]), sl2, nz2);
+                        y.x = ex2(y.x);
+                        y.y = ex2(y.y);
+                        sum[e & 1] = add2(sum[e & 1], y);
+                        if (FP8) {
+                            const float2 v = *reinterpret_cast<const float2 *>(sc + kKeys + c + 2 * e);
+                            y.x *= v.x;
+                            y.y *= v.y;
+                        }
+                        p[e] = pack_bf16(y.x, y.y);
+                    }
+                    tmem_st16(s_t + c / 2, p);
+                    if ((c + 32) % (kKeys / kParts) == 0) {  // their product may start
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm->p_ready[t][c / (kKeys / kParts)]);
+                    }
+                }
+                const float2 both = add2(sum[0], sum[1]);
+                l += both.x + both.y;
+                ph ^= 1;
+            }
+            if (!ok) break;
+            tile0 += it.tiles;
+            // ---- the rows' outputs
+            if (done > 0) {
+                ok = warp_wait_flag(&sm->o_done[t], ph ^ 1, &sm->abort, 11);
+                if (!ok) break;
+            }
+            const bool joined = !it.shared, whole = it.slot < 0;
+            const bool second = joined && it.tiles > 1;  // O_1 has sums too
+            // What the row's sums are multiplied by: 1 over the sum if these are all
+            // keys.  Joined: warpgroup 1 hands over its reference and sum,
+            // warpgroup 0 the two factors.
+            auto arrive = [&](int i) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm->merge[i]);
+            };
+            float top = ref, sum = l, f0 = 1.f, f1 = 0.f;
+            if (joined && t == 1) {
+                sm->pair[r] = make_float2(ref, l);
+                arrive(0);
+                ok = warp_wait_flag(&sm->merge[1], merges, &sm->abort, 12);
+                if (!ok) break;
+                const float2 f = sm->pair[r];
+                f0 = f.x;
+                f1 = f.y;
+            } else {
+                if (joined) {
+                    ok = warp_wait_flag(&sm->merge[0], merges, &sm->abort, 12);
+                    if (!ok) break;
+                    const float2 m1 = sm->pair[r];
+                    top = fmaxf(ref, m1.x);
+                    const float z = top == -INFINITY ? 0.f : top;
+                    f0 = ex2(ref - z);
+                    f1 = ex2(m1.x - z);
+                    // (no tile: reference -inf and sum 0)
+                    sum = f0 * l + f1 * m1.y;
+                }
+                if (whole) {
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    f0 *= inv;
+                    f1 *= inv;
+                }
+                if (joined) {
+                    sm->pair[r] = make_float2(f0, f1);
+                    arrive(1);
+                }
+            }
+            tc_fence_after();
+            const bool none = f0 == 0.f && f1 == 0.f;  // (a row that sees nothing)
+            // joined: each warpgroup has half of the columns of both
+            const uint32_t o_0 = it.shared ? o_t : o_col + lane_base, o_1 = o_col + D + lane_base;
+            const int c0 = it.shared ? 0 : t * (D / 2), c1 = it.shared ? D : c0 + D / 2;
+            const int row_tile = it.shared ? t : 0;
+            uint16_t *to = a.out + (int64_t)(it.q0 + tok) * a.out_stride + (it.h0 + gr) * D;
+            if (any_live)
+#pragma unroll 1
+                for (int c = c0; c < c1; c += 32) {
+                    float o[32];
+                    tmem_ld32(o_0 + c, o);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] *= f0;
+                    if (second) {
+                        float y[32];
+                        tmem_ld32(o_1 + c, y);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = fmaf(y[e], f1, o[e]);
+                    }
+                    if (!live) continue;
+                    if (!whole) {
+                        float *part = reinterpret_cast<float *>(a.workspace + L.sums);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(part + part_at(it.slot, row_tile, c + e, r, D)) =
+                                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            *reinterpret_cast<uint4 *>(to + c + e) =
+                                none ? make_uint4(0, 0, 0, 0)
+                                     : make_uint4(pack_bf16(o[e], o[e + 1]), pack_bf16(o[e + 2], o[e + 3]),
+                                                  pack_bf16(o[e + 4], o[e + 5]), pack_bf16(o[e + 6], o[e + 7]));
+                    }
+                }
+            if (live && (it.shared || t == 0)) {
+                if (!whole)
+                    reinterpret_cast<float2 *>(a.workspace + L.ml)[((size_t)it.slot * kM + row_tile) * kTile + r] =
+                        make_float2(top, sum);
+                else if (a.lse)
+                    a.lse[(size_t)(it.q0 + tok) * a.Hq + it.h0 + gr] =
+                        sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+            }
+            // (O_t and pair are read: the next item's first p_ready comes after this)
+            tc_fence_before();
+            if (joined) {
+                arrive(2);
+                ok = warp_wait_flag(&sm->merge[2], merges, &sm->abort, 13);
+                merges ^= 1;
+                tc_fence_after();
+            }
+        }
+    }
+    __syncthreads();
+    if (tid == 0) reinterpret_cast<Err *>(a.workspace + L.err)[g] = Err{sm->abort, sm->bad};
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_relinquish();
+        tmem_dealloc(sm->tmem, 512);
+    }
+}
+
+// Joins the parts of a range: blockIdx.x is its record, blockIdx.y 8 columns of
+// one row tile; a warp has 32 neighbouring rows of it.
+template <int D>
+__global__ void __launch_bounds__(kTile) tree_join(const DecodeAttnArgs a, const int HT, const int n_blocks) {
+    __shared__ int red[2];
+    const TreeLayout L = tree_layout(D);
+    const int tid = threadIdx.x;
+    pdl_wait();
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        // the call's status word, from every block's record
+        const Err *err = reinterpret_cast<const Err *>(a.workspace + L.err);
+        if (tid == 0) red[0] = 0, red[1] = 0x7fffffff;
+        __syncthreads();
+        for (int i = tid; i < n_blocks; i += blockDim.x) {
+            if (err[i].timeout) atomicMax(&red[0], err[i].timeout);
+            if (err[i].bad != 0x7fffffff) atomicMin(&red[1], err[i].bad);
+        }
+        __syncthreads();
+        if (tid == 0) {
+            Ctrl *ctrl = reinterpret_cast<Ctrl *>(a.workspace);
+            ctrl->status = red[0] ? MOE_ERR_DEVICE_TIMEOUT
+                                  : (red[1] != 0x7fffffff ? MOE_ERR_DEVICE_BAD_INDEX : MOE_OK);
+            ctrl->detail = red[0] ? red[0] : (red[1] != 0x7fffffff ? red[1] : 0);
+        }
+    }
+    const Join jn = reinterpret_cast<const Join *>(a.workspace + L.join)[blockIdx.x];
+    if (jn.parts == 0) return;
+    const int G = a.Hq / a.kv.Hkv, Gt = tile_heads(G), tpt = tile_tokens(G);
+    Seq s;
+    seq_of(a, jn.b, tpt, HT, s);
+    const int rest = jn.hv % (HT * s.RB), ht = rest / s.RB, rb = rest % s.RB, hk = jn.hv / (HT * s.RB);
+    const int t = blockIdx.y / (D / 8), c = blockIdx.y % (D / 8) * 8;
+    const int tok = (rb * kM + t) * tpt + tid / Gt, gr = tid % Gt;
+    if (tid / Gt >= tpt || tok >= s.nq || gr >= G - ht * Gt) return;
+    const float2 *ml = reinterpret_cast<const float2 *>(a.workspace + L.ml);
+    const float *sums = reinterpret_cast<const float *>(a.workspace + L.sums);
+    // the first part is its block's last one, the others are first ones
+    auto slot_of = [&](int i) { return 2 * (jn.first + i) + (i == 0 ? 1 : 0); };
+    float top = -INFINITY, sum = 0.f, o[8] = {};
+#pragma unroll 4
+    for (int i = 0; i < jn.parts; ++i) top = fmaxf(top, ml[((size_t)slot_of(i) * kM + t) * kTile + tid].x);
+    const float z = top == -INFINITY ? 0.f : top;
+#pragma unroll 4
+    for (int i = 0; i < jn.parts; ++i) {
+        const float2 v = ml[((size_t)slot_of(i) * kM + t) * kTile + tid];
+        const float4 lo = *reinterpret_cast<const float4 *>(sums + part_at(slot_of(i), t, c, tid, D));
+        const float4 hi = *reinterpret_cast<const float4 *>(sums + part_at(slot_of(i), t, c + 4, tid, D));
+        const float f = ex2(v.x - z);
+        const float e[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        sum = fmaf(f, v.y, sum);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = fmaf(f, e[k], o[k]);
+    }
+    const bool none = sum == 0.f;
+    const float inv = none ? 0.f : 1.f / sum;
+    const int64_t row = (int64_t)s.q0 + tok;
+    const int h = hk * G + ht * Gt + gr;
+    *reinterpret_cast<uint4 *>(a.out + row * a.out_stride + h * D + c) =
+        none ? make_uint4(0, 0, 0, 0)
+             : make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv),
+                          pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv));
+    if (a.lse && c == 0) a.lse[row * a.Hq + h] = none ? -INFINITY : (top + __log2f(sum)) * kLn2;
+}
+
+template <int D, bool FP8>
+cudaError_t run(const DecodeAttnArgs &a, int sms, cudaStream_t s) {
+    using C = Cfg<D, FP8>;
+    const int G = a.Hq / a.kv.Hkv, Gt = tile_heads(G), tpt = tile_tokens(G), HT = (G + Gt - 1) / Gt;
+    CUtensorMap mq, mkv;
+    {
+        const uint64_t dims[4] = {64, (uint64_t)a.Hq, (uint64_t)a.T, D / 64};
+        const uint64_t strides[3] = {D * 2, (uint64_t)a.q_stride * 2, 128};
+        const uint32_t box[4] = {64, (uint32_t)Gt, (uint32_t)tpt, 1};
+        if (!encode_tensor_map(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, a.q, dims, strides, box,
+                               CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+    }
+    const int page = 1 << a.kv.page_shift;
+    if (!FP8) {
+        const uint64_t row_b = D * 2;
+        const uint64_t dims[4] = {64, (uint64_t)page, D / 64, (uint64_t)a.kv.num_pages * a.kv.Hkv * 2};
+        const uint64_t strides[3] = {row_b, 128, page * row_b};
+        const uint32_t box[4] = {64, (uint32_t)(page < kKeys ? page : kKeys), 1, 1};
+        if (!encode_tensor_map(&mkv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, a.kv.data, dims, strides, box,
+                               CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+    } else {
+        mkv = mq;
+    }
+    // no more blocks than key tiles could exist
+    const int64_t tiles = ((int64_t)a.table_stride * page + kKeys - 1) / kKeys;
+    const int64_t rb = ((a.T < kTreeTokens ? a.T : kTreeTokens) + kM * tpt - 1) / (kM * tpt);
+    const int64_t most = (a.B < a.T ? a.B : a.T) * tiles * a.kv.Hkv * HT * rb;
+    int grid = sms < kMaxGrid ? sms : kMaxGrid;
+    if (most < grid) grid = (int)most;
+    auto fn = tree_kernel<D, FP8>;
+    static SmemOnce once;
+    cudaError_t err = once.set(reinterpret_cast<const void *>(fn), C::kSmem);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = s;
+    err = cudaLaunchKernelEx(&cfg, fn, a, HT, mq, mkv);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cj = {};
+    cj.gridDim = dim3(grid, kM * D / 8);
+    cj.blockDim = dim3(kTile);
+    cj.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cj.attrs = at;
+    cj.numAttrs = 1;
+    return cudaLaunchKernelEx(&cj, tree_join<D>, a, HT, grid);
+}
+
+}  // namespace
+
+size_t tree_workspace(int, int T, int Hq, int Hkv, int D) {
+    const size_t small = tree_small_workspace(T, Hq, Hkv, D), large = align_up(tree_layout(D).total, 256);
+    return small > large ? small : large;
+}
+
+cudaError_t launch_attn_tree(const DecodeAttnArgs &a, cudaStream_t s) {
+    const int tokens = a.T < kTreeTokens ? a.T : kTreeTokens;
+    if (tokens * (a.Hq / a.kv.Hkv) <= 16) return launch_attn_tree_small(a, s);
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const int sms = tc_grid(dev);
+    if (sms < 1) return cudaErrorInvalidDevice;
+    const bool fp8 = a.cache_type == MOE_KV_FP8;
+    if (a.D == 128) return fp8 ? run<128, true>(a, sms, s) : run<128, false>(a, sms, s);
+    return fp8 ? run<64, true>(a, sms, s) : run<64, false>(a, sms, s);
+}
+
+}  // namespace moe

@@ -13,7 +13,4 @@ cudaError_t launch_attn_tree_small(const DecodeAttnArgs &a, cudaStream_t s) {
     return launch<kTree>(a, a.Hq / a.kv.Hkv * (a.T < kTreeTokens ? a.T : kTreeTokens), s);
 }
 
-size_t tree_workspace(int, int T, int Hq, int Hkv, int D) { return tree_small_workspace(T, Hq, Hkv, D); }
-cudaError_t launch_attn_tree(const DecodeAttnArgs &a, cudaStream_t s) { return launch_attn_tree_small(a, s); }
-
 }  // namespace moe
