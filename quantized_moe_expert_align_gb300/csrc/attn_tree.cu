@@ -18,11 +18,15 @@
 // per SM; a range cut by a block's end is joined by a second kernel, in key order.
 //
 // A bf16 cache is copied page by page into the swizzled operand tiles.  An fp8
-// cache is copied as it is; four warps turn its codes into operands: fp16 for the
-// scores (exact, as is Q times a power of two a row, but for values below 2^-14
-// of their row's largest, off by up to 2^-25 of it), bf16 for the product with
-// the weights (exact).  The scales of K multiply the scores, those of V the
-// weights, in fp32; a weight is rounded once, to bf16.
+// cache is used as it is for the scores: a row of Q, times a power of two, is the
+// sum of two rows of e4m3 numbers, both multiplied with the codes (exact, but that
+// a value below 2^-9 of its row's largest is off by up to 2^-17 of it), which takes
+// as long as one product of 16-bit numbers.  For the product with the weights four
+// warps turn the codes of V into fp16 (exact).  The scales of K multiply the
+// scores in fp32.  Those of V multiply the weights, which are rounded once, to fp16
+// (2^-11): times a power of two that follows the largest scale met so far, so
+// that none overflows and those below 2^-29 of the largest lose bits; where it
+// grows, the sums are scaled down like where a reference grows.
 #include <type_traits>
 
 #include "attn_tc.cuh"
@@ -53,16 +57,18 @@ struct Cfg {
     static constexpr int kRoleRegs = FP8 ? 64 : 72, kSoftmaxRegs = FP8 ? 192 : 216;
     static_assert((kThreads - 256) * kRoleRegs + 256 * kSoftmaxRegs <= kThreads * (FP8 ? 128 : 168), "register split");
     static constexpr int kQB = kTile * D * 2, kKvB = kKeys * D * 2;  // a Q tile, an operand tile of K or V
-    static constexpr int kOps = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
-    static constexpr int kRawB = kRawKeys * D;
-    static constexpr int kRaw = FP8 ? (D == 128 ? 7 : 12) : 1;
-    static constexpr int kRawStage = kRawB + 2 * kRawKeys * 4;  // codes; the scales of K and V with K's
-    static constexpr size_t kOpAt = (size_t)kM * kQB, kRawAt = kOpAt + (size_t)kOps * kKvB;
-    static constexpr size_t kSharedAt = kRawAt + (FP8 ? (size_t)kRaw * kRawStage : 0);
-    // fp8: the scales of kScaleBufs key tiles, [2][kKeys] floats each, those of K
-    // times the scores' factor
+    // Rings: operand tiles (bf16: K and V; fp8: V), tiles of K's codes, tiles of
+    // 64 rows of V's codes.
+    static constexpr int kOps = FP8 ? (D == 128 ? 2 : 4) : (D == 128 ? 5 : 8);
+    static constexpr int kKs = FP8 ? (D == 128 ? 3 : 6) : 1, kKB = kKeys * D;
+    static constexpr int kRaw = FP8 ? (D == 128 ? 5 : 10) : 1, kRawB = kRawKeys * D;
+    static constexpr size_t kOpAt = (size_t)kM * kQB, kKAt = kOpAt + (size_t)kOps * kKvB;
+    static constexpr size_t kRawAt = kKAt + (FP8 ? (size_t)kKs * kKB : 0);
+    static constexpr size_t kSharedAt = kRawAt + (FP8 ? (size_t)kRaw * kRawB : 0);
+    // fp8: of kScaleBufs key tiles the scales of K and of V, and those of V as the
+    // weights take them, [3][kKeys] floats each
     static constexpr size_t kScalesAt = kSharedAt + 2048;
-    static constexpr size_t kSmem = kScalesAt + (FP8 ? kScaleBufs * 2 * kKeys * 4 : 0) + 1024;
+    static constexpr size_t kSmem = kScalesAt + (FP8 ? kScaleBufs * 3 * kKeys * 4 : 0) + 1024;
     static_assert(kSmem > 114 * 1024 && kSmem <= 227 * 1024, "one block per SM: all of tensor memory is its own");
 };
 
@@ -103,11 +109,12 @@ __host__ __device__ inline int tile_heads(int G) { return G < kTile ? G : kTile;
 __host__ __device__ inline int tile_tokens(int G) { return kTile / tile_heads(G); }
 
 struct Shared {
-    uint64_t q_full[kM], q_ready[kM], q_empty[kM], op_full[8], op_empty[8], tail[8], raw_full[12], raw_empty[12];
-    uint64_t sc_full[kScaleBufs], s_full[kM], p_ready[kM][kParts], o_done[kM], merge[3];
+    uint64_t q_full[kM], q_ready[kM], q_empty[kM], op_full[8], op_empty[8], tail[8], raw_full[10], raw_empty[10];
+    uint64_t k_full[6], k_empty[6], sc_full[kScaleBufs], sc_ready[kScaleBufs], sc_empty[kScaleBufs], s_full[kM], p_ready[kM][kParts], o_done[kM], merge[3];
     uint64_t item_full[2], item_empty[2], finished;
     uint32_t tmem;
     int abort, bad;
+    int expo[kScaleBufs], expo1;  // exponents of the largest scale so far: per key tile, row tile 1's last
     int b0;                 // the sequence of this block's first key tile
     int64_t first;          // and that tile's index among the sequence's
     int64_t warp_sum[16];
@@ -137,34 +144,42 @@ __device__ __forceinline__ bool seq_of(const DecodeAttnArgs &a, int b, int tpt, 
     return ok;
 }
 
-// 4 e4m3 codes of neighbouring columns -> two pairs of bf16: a code's exponent and
-// mantissa bits moved to the bf16 places are its value times 2^-120.  Exact, but for
-// the NaN code, which comes out as 480.
-__device__ __forceinline__ uint2 e4m3_bf16(uint32_t w) {
-    const uint32_t up = 0x7B807B80u;  // bf16 2^120
-    w = __byte_perm(w, 0, 0x3120);    // codes 0, 2, 1, 3
-    const uint32_t l = ((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u);
-    const uint32_t h = ((w >> 4) & 0x07F007F0u) | (w & 0x80008000u);
-    uint2 r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(l), "r"(up));
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(h), "r"(up));
-    return r;
-}
-// Whether one of 4 codes is NaN (0x7F or 0xFF).
-__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
-__device__ __forceinline__ uint2 with_nans(uint2 v, uint32_t w) {
-    const uint32_t n = nan_codes(w);
-    if (n & 0x80u) v.x = (v.x & 0xFFFF0000u) | 0x7FC0u;
-    if (n & 0x8000u) v.x = (v.x & 0xFFFFu) | 0x7FC00000u;
-    if (n & 0x800000u) v.y = (v.y & 0xFFFF0000u) | 0x7FC0u;
-    if (n & 0x80000000u) v.y = (v.y & 0xFFFFu) | 0x7FC00000u;
-    return v;
-}
+// 4 e4m3 codes of neighbouring columns -> two pairs of fp16
 __device__ __forceinline__ uint2 e4m3_f16(uint32_t w) {
     uint2 r;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r.x) : "h"((uint16_t)w));
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r.y) : "h"((uint16_t)(w >> 16)));
     return r;
+}
+// Two numbers to e4m3 (the first in the low byte), and what that leaves of them.
+__device__ __forceinline__ uint32_t take_e4m3(float2 &x) {
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(x.y), "f"(x.x));
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    x.x -= v.x;
+    x.y -= v.y;
+    return c;
+}
+// 2^e, -127 <= e <= 127
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(e > -127 ? (uint32_t)(e + 127) << 23 : 0x00400000u); }
+// Weights are 2^kShift-fold beside the largest scale's power of two: at most 2^8
+// (the slack) times 2 times this.
+constexpr int kShift = 5;
+// Codes [key][d] as a K-major operand, rows of 64 bytes with 64-byte swizzling.
+__device__ __forceinline__ uint64_t sdesc_k_sw64(uint32_t addr) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)1 << 16 | (uint64_t)(512u >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)4 << 61;
+}
+__device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 template <int D, bool FP8>
@@ -177,7 +192,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
     extern __shared__ uint8_t raw[];
     const uint32_t raw_u = smem_u32(raw);
     uint8_t *base = raw + ((1024 - (raw_u & 1023)) & 1023);
-    uint8_t *op_base = base + C::kOpAt, *raw_base = base + C::kRawAt;
+    uint8_t *op_base = base + C::kOpAt, *k_base = base + C::kKAt, *raw_base = base + C::kRawAt;
     Shared *sm = reinterpret_cast<Shared *>(base + C::kSharedAt);
     float *scales = reinterpret_cast<float *>(base + C::kScalesAt);
     const uint32_t q_smem = smem_u32(base), op_smem = smem_u32(op_base);
@@ -204,18 +219,26 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
             mbar_init(&sm->op_empty[i], kM);
             mbar_init(&sm->tail[i], 1);
         }
-        for (int i = 0; i < 12; ++i) {
+        for (int i = 0; i < 10; ++i) {
             mbar_init(&sm->raw_full[i], 1);
             mbar_init(&sm->raw_empty[i], 4);
         }
-        for (int i = 0; i < kScaleBufs; ++i) mbar_init(&sm->sc_full[i], 4);
+        for (int i = 0; i < 6; ++i) {
+            mbar_init(&sm->k_full[i], 1);
+            mbar_init(&sm->k_empty[i], kM);
+        }
+        for (int i = 0; i < kScaleBufs; ++i) {
+            mbar_init(&sm->sc_full[i], 1);
+            mbar_init(&sm->sc_ready[i], 4);
+            mbar_init(&sm->sc_empty[i], 8);
+        }
         mbar_init(&sm->merge[2], 8);
         mbar_init(&sm->finished, kM);
         fence_barrier_init();
         sm->abort = 0;
         sm->bad = 0x7fffffff;
         prefetch_tensormap(&map_q);
-        if (!FP8) prefetch_tensormap(&map_kv);
+        prefetch_tensormap(&map_kv);
     }
     pdl_trigger();
 
@@ -300,7 +323,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 return key < nk ? __ldg(a.page_table + (size_t)bb * a.table_stride + (key >> page_shift)) : 0;
             };
             int pg = u0 < u1 ? page_of(b, j, sq.nk) : 0;
-            uint32_t n = 0, op = 0, rw = 0;
+            uint32_t n = 0, op = 0, rw = 0, kt = 0;
             bool ok = true;
             int64_t u = u0;
             for (;; ++n) {
@@ -397,6 +420,35 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                             }
                         }
                     } else {
+                        const int row = key & page_mask, c = lane;  // this lane's chunk of rows
+                        const bool copies = live && lane < chunks;
+                        const int copied = min(kKeys, (n_live + R - 1) & -R);
+                        {
+                            const uint32_t s = kt % kScaleBufs;
+                            ok = ok && warp_wait_flag(&sm->sc_empty[s], ((kt / kScaleBufs) & 1) ^ 1, &sm->abort, 18);
+                            if (!ok) break;
+                            if (lane == 0) mbar_arrive_expect_tx(&sm->sc_full[s], copied * 8);
+                            __syncwarp();
+                            if (copies) {
+                                const uint32_t to = smem_u32(scales + s * 3 * kKeys + c * R);
+                                const float *sc = a.kv.scales + ((ph * 2) << page_shift) + row;
+                                bulk_g2s(to, sc, R * 4, &sm->sc_full[s]);
+                                bulk_g2s(to + kKeys * 4, sc + ((size_t)1 << page_shift), R * 4, &sm->sc_full[s]);
+                            }
+                            __syncwarp();
+                        }
+                        {
+                            const uint32_t s = kt % C::kKs;
+                            ok = warp_wait_flag(&sm->k_empty[s], ((kt / C::kKs) & 1) ^ 1, &sm->abort, 3);
+                            if (!ok) break;
+                            if (lane == 0) mbar_arrive_expect_tx(&sm->k_full[s], copied * D);
+                            __syncwarp();
+                            if (copies)
+                                tma_load_3d(k_base + s * C::kKB + c * R * D, &map_kv, 0, row, (int)(ph * 2),
+                                            &sm->k_full[s]);
+                            __syncwarp();
+                        }
+                        ++kt;
                         if (i == 0)
                             for (int t = 0; t < kM && ok; ++t) {
                                 ok = warp_wait_flag(&sm->q_empty[t], (n & 1) ^ 1, &sm->abort, 4);
@@ -408,27 +460,18 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                                 }
                                 __syncwarp();
                             }
-                        const int row = key & page_mask;
-                        for (int part = 0; part < 4 && ok; ++part) {  // K's two halves, V's
-                            const int half = part & 1, kv = part >> 1;
-                            const uint32_t s = rw % C::kRaw, par = (rw / C::kRaw) & 1;
-                            ok = warp_wait_flag(&sm->raw_empty[s], par ^ 1, &sm->abort, 3);
+                        for (int half = 0; half < 2 && ok; ++half) {
+                            const uint32_t s = rw % C::kRaw;
+                            ok = warp_wait_flag(&sm->raw_empty[s], ((rw / C::kRaw) & 1) ^ 1, &sm->abort, 3);
                             if (!ok) break;
-                            const int keys = max(0, min(kRawKeys, ((n_live - half * kRawKeys) + R - 1) & -R));
-                            if (lane == 0) mbar_arrive_expect_tx(&sm->raw_full[s], keys * (D + (kv ? 0 : 8)));
+                            const int keys = max(0, min(kRawKeys, copied - half * kRawKeys));
+                            if (lane == 0) mbar_arrive_expect_tx(&sm->raw_full[s], keys * D);
                             __syncwarp();
-                            const int c = lane - half * (kRawKeys >> box_shift);  // chunk of this half
-                            if (live && lane < chunks && c >= 0 && c < kRawKeys >> box_shift) {
-                                const uint32_t to = smem_u32(raw_base + s * C::kRawStage);
-                                bulk_g2s(to + c * R * D, a.kv.data + (((ph * 2 + kv) << page_shift) + row) * D, R * D,
+                            const int c_half = c - half * (kRawKeys >> box_shift);  // chunk of this half
+                            if (copies && c_half >= 0 && c_half < kRawKeys >> box_shift)
+                                bulk_g2s(smem_u32(raw_base + s * C::kRawB) + c_half * R * D,
+                                         a.kv.data + (((ph * 2 + 1) << page_shift) + row) * D, R * D,
                                          &sm->raw_full[s]);
-                                if (!kv) {
-                                    const float *sc = a.kv.scales + ((ph * 2) << page_shift) + row;
-                                    bulk_g2s(to + C::kRawB + c * R * 4, sc, R * 4, &sm->raw_full[s]);
-                                    bulk_g2s(to + C::kRawB + kRawKeys * 4 + c * R * 4, sc + ((size_t)1 << page_shift),
-                                             R * 4, &sm->raw_full[s]);
-                                }
-                            }
                             __syncwarp();
                             ++rw;
                         }
@@ -447,8 +490,11 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 constexpr int t = decltype(tile)::value;
                 const uint64_t qd = sdesc_k_sw128(q_smem) + ((t * C::kQB) >> 4), k_desc = sdesc_k_sw128(op_smem);
                 const uint64_t v_desc = sdesc_mn_sw128(op_smem, kKvHalf);
+                // (e4m3 operands, kind::f8f6f4, have the format number of fp16 ones)
                 constexpr uint32_t kIdS = FP8 ? idesc_f16_m128(kKeys) : idesc_bf16(kKeys, false);
-                constexpr uint32_t kIdO = idesc_bf16(D, true);
+                constexpr uint32_t kIdO = FP8 ? idesc_f16_m128(D) | 1u << 16 : idesc_bf16(D, true);
+                const uint64_t c_desc = D == 128 ? sdesc_k_sw128(smem_u32(k_base)) : sdesc_k_sw64(smem_u32(k_base));
+                uint32_t k_stage = 0, k_ph = 0;
                 constexpr uint32_t s_t = s_col + t * kKeys, o_t = o_col + t * D;
                 uint32_t stage = 0, stage_ph = 0, p_ph = 0;
                 Item it;
@@ -463,13 +509,24 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                     }
                     return s;
                 };
+                auto next_codes = [&]() {  // fp8: the next tile of K's codes
+                    ok = ok && warp_wait_flag(&sm->k_full[k_stage], k_ph, &sm->abort, 5);
+                    tc_fence_after();
+                    const uint32_t s = k_stage;
+                    if (++k_stage == C::kKs) {
+                        k_stage = 0;
+                        k_ph ^= 1;
+                    }
+                    return s;
+                };
                 for (uint32_t n = 0; ok && take(n, it); ++n) {
                     const int tiles = __shfl_sync(0xffffffffu, it.tiles, 0);
                     const int mine = __shfl_sync(0xffffffffu, tiles_of(it, t), 0);
                     const bool both = __shfl_sync(0xffffffffu, it.shared, 0) != 0;
                     int done = 0;  // own tiles whose scores were issued
                     for (int j = 0; j < tiles && ok; ++j) {
-                        const uint32_t k = next_stage();
+                        const uint32_t k = FP8 ? next_codes() : next_stage();
+                        uint64_t *const k_free = FP8 ? &sm->k_empty[k] : &sm->op_empty[k];
                         if (j == 0) {
                             ok = ok && warp_wait_flag(FP8 ? &sm->q_ready[t] : &sm->q_full[t], n & 1, &sm->abort, 6);
                             tc_fence_after();
@@ -479,19 +536,31 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                         if (is_own) {
                             ++done;
                             if (elect_one()) {
-                                const uint64_t kd = k_desc + ((k * C::kKvB) >> 4);
+                                if (FP8) {
+                                    // both terms of Q: tiles of their own, or (heads of
+                                    // 64) the two halves of a row
+                                    const uint64_t kd = c_desc + ((k * C::kKB) >> 4);
 #pragma unroll
-                                for (int i = 0; i < D / 16; ++i) {
-                                    const uint32_t in = (i & 3) * 32;
-                                    mma_bf16_ss(s_t, qd + (((i >> 2) * kQHalf + in) >> 4),
-                                                kd + (((i >> 2) * kKvHalf + in) >> 4), kIdS, i > 0);
+                                    for (int i = 0; i < 2 * (D / 32); ++i) {
+                                        const uint32_t term = i / (D / 32), in = i % (D / 32) * 32;
+                                        mma_e4m3_ss(s_t, qd + ((term * (D == 128 ? kQHalf : 64u) + in) >> 4),
+                                                    kd + (in >> 4), kIdS, i > 0);
+                                    }
+                                } else {
+                                    const uint64_t kd = k_desc + ((k * C::kKvB) >> 4);
+#pragma unroll
+                                    for (int i = 0; i < D / 16; ++i) {
+                                        const uint32_t in = (i & 3) * 32;
+                                        mma_bf16_ss(s_t, qd + (((i >> 2) * kQHalf + in) >> 4),
+                                                    kd + (((i >> 2) * kKvHalf + in) >> 4), kIdS, i > 0);
+                                    }
                                 }
                                 tc_commit(&sm->s_full[t]);
-                                tc_commit(&sm->op_empty[k]);
+                                tc_commit(k_free);
                                 if (done == mine) tc_commit(&sm->q_empty[t]);
                             }
                         } else if (lane == 0) {
-                            mbar_arrive(&sm->op_empty[k]);
+                            mbar_arrive(k_free);
                         }
                         __syncwarp();
                         const uint32_t v = next_stage();
@@ -554,79 +623,73 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 if (lane == 0) mbar_arrive(&sm->op_full[s]);
             }
         } else if (FP8 && warp >= kConvWarp) {
-            // ---------------- codes into operands
+            // ---------------- the scales of V for the weights, its codes as operands
             const int ct = tid - 32 * kConvWarp;
-            const float factor = a.scale * kLog2e;
             Item it;
             uint32_t op = 0, rw = 0, tile = 0;
             bool ok = true;
-            for (uint32_t n = 0; ok && take(n, it); ++n)
-                for (int j = 0; j < it.tiles && ok; ++j, ++tile) {
+            for (uint32_t n = 0; ok && take(n, it); ++n) {
+                int expo = -122;  // of the largest scale so far
+                for (int j = 0; j < it.tiles && ok; ++j, ++tile, ++op) {
                     const int n_live = it.nk - (it.j0 + j) * kKeys;
-                    float *sc = scales + (tile % kScaleBufs) * 2 * kKeys;
-#pragma unroll 1
-                    for (int kv = 0; kv < 2 && ok; ++kv, ++op) {
-                        const uint32_t s = op % S;
-                        ok = warp_wait_flag(&sm->op_empty[s], ((op / S) & 1) ^ 1, &sm->abort, 14);
-                        uint8_t *to = op_base + s * C::kKvB;
-#pragma unroll 1
-                        for (int half = 0; half < 2 && ok; ++half, ++rw) {
-                            const uint32_t r = rw % C::kRaw;
-                            ok = warp_wait_flag(&sm->raw_full[r], (rw / C::kRaw) & 1, &sm->abort, 15);
-                            if (!ok) break;
-                            const uint8_t *from = raw_base + r * C::kRawStage;
-                            constexpr int kRow = D / 16, kEach = kRawKeys * kRow / 128;  // 16-byte pieces
-                            uint4 c[kEach];
+                    const uint32_t buf = tile % kScaleBufs;
+                    float *sc = scales + buf * 3 * kKeys;
+                    ok = warp_wait_flag(&sm->sc_full[buf], (tile / kScaleBufs) & 1, &sm->abort, 19);
+                    if (!ok) break;
+                    // (every warp looks at all of them, and writes its own)
+                    const float4 v4 = *reinterpret_cast<const float4 *>(sc + kKeys + 4 * lane);
+                    const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+                    uint32_t most = 0;
 #pragma unroll
-                            for (int k = 0; k < kEach; ++k)
-                                c[k] = *reinterpret_cast<const uint4 *>(from + (ct + k * 128) * 16);
-                            if (kv == 0) {
-                                const int key = half * kRawKeys + (ct & 63), v = ct >> 6;
-                                const float x = reinterpret_cast<const float *>(from + C::kRawB)[ct];
-                                sc[v * kKeys + key] = key < n_live ? (v ? x : x * factor) : 0.f;
-                            }
-#pragma unroll
-                            for (int k = 0; k < kEach; ++k) {
-                                const int i = ct + k * 128, key = half * kRawKeys + i / kRow, piece = i % kRow;
-                                if (key >= n_live) c[k] = make_uint4(0, 0, 0, 0);
-                                uint2 o[4];
-                                const uint32_t w[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
-                                if (kv == 0) {
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) o[e] = e4m3_f16(w[e]);
-                                } else {
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) o[e] = e4m3_bf16(w[e]);
-                                    if (nan_codes(w[0]) | nan_codes(w[1]) | nan_codes(w[2]) | nan_codes(w[3]))
-#pragma unroll
-                                        for (int e = 0; e < 4; ++e) o[e] = with_nans(o[e], w[e]);
-                                }
-                                // two 16-byte units of a 128-byte row of 64 columns; the
-                                // second half's lanes write theirs in the other order
-                                // (else two lanes of a store meet in the same banks)
-                                uint8_t *row = to + (piece >> 2) * kKvHalf + key * 128;
-                                const int unit = (piece & 3) * 2, turn = piece >> 2;
-#pragma unroll
-                                for (int x = 0; x < 2; ++x) {
-                                    const bool second = (x ^ turn) != 0;
-                                    const uint4 v = second ? make_uint4(o[2].x, o[2].y, o[3].x, o[3].y)
-                                                           : make_uint4(o[0].x, o[0].y, o[1].x, o[1].y);
-                                    *reinterpret_cast<uint4 *>(row + (((unit + (second ? 1 : 0)) ^ (key & 7)) << 4)) = v;
-                                }
-                            }
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&sm->raw_empty[r]);
-                        }
-                        if (!ok) break;
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(&sm->op_full[s]);
-                            if (kv == 0) mbar_arrive(&sm->sc_full[tile % kScaleBufs]);
-                        }
-                        __syncwarp();
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t bits = __float_as_uint(v[e]) & 0x7FFFFFFFu;
+                        if (4 * lane + e < n_live && bits < 0x7F800000u) most = max(most, bits);
                     }
+                    most = __reduce_max_sync(0xffffffffu, most);
+                    expo = max(expo, min((int)(most >> 23) - 127, 126));
+                    sc[2 * kKeys + ct] = ct < n_live ? sc[kKeys + ct] * pow2(kShift - expo) : 0.f;
+                    if (ct == 0) sm->expo[buf] = expo;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm->sc_ready[buf]);
+                    const uint32_t s = op % S;
+                    ok = warp_wait_flag(&sm->op_empty[s], ((op / S) & 1) ^ 1, &sm->abort, 14);
+                    uint8_t *to = op_base + s * C::kKvB;
+#pragma unroll 1
+                    for (int half = 0; half < 2 && ok; ++half, ++rw) {
+                        const uint32_t r = rw % C::kRaw;
+                        ok = warp_wait_flag(&sm->raw_full[r], (rw / C::kRaw) & 1, &sm->abort, 15);
+                        if (!ok) break;
+                        const uint8_t *from = raw_base + r * C::kRawB;
+                        constexpr int kRow = D / 16, kEach = kRawKeys * kRow / 128;  // 16-byte pieces
+                        uint4 c[kEach];
+#pragma unroll
+                        for (int k = 0; k < kEach; ++k)
+                            c[k] = *reinterpret_cast<const uint4 *>(from + (ct + k * 128) * 16);
+#pragma unroll
+                        for (int k = 0; k < kEach; ++k) {
+                            const int i = ct + k * 128, key = half * kRawKeys + i / kRow, piece = i % kRow;
+                            if (key >= n_live) c[k] = make_uint4(0, 0, 0, 0);
+                            const uint2 o0 = e4m3_f16(c[k].x), o1 = e4m3_f16(c[k].y);
+                            const uint2 o2 = e4m3_f16(c[k].z), o3 = e4m3_f16(c[k].w);
+                            const uint4 lo = make_uint4(o0.x, o0.y, o1.x, o1.y), hi = make_uint4(o2.x, o2.y, o3.x, o3.y);
+                            // two 16-byte units of a 128-byte row of 64 columns; the
+                            // second half's lanes write theirs in the other order
+                            // (else two lanes of a store meet in the same banks)
+                            uint8_t *row = to + (piece >> 2) * kKvHalf + key * 128;
+                            const int unit = (piece & 3) * 2, turn = piece >> 2, x = key & 7;
+                            *reinterpret_cast<uint4 *>(row + (((unit + turn) ^ x) << 4)) = turn ? hi : lo;
+                            *reinterpret_cast<uint4 *>(row + (((unit + 1 - turn) ^ x) << 4)) = turn ? lo : hi;
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm->raw_empty[r]);
+                    }
+                    if (!ok) break;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm->op_full[s]);
+                    __syncwarp();
                 }
+            }
         }
     } else {
         // ---------------- softmax: warpgroup t has row tile t, a thread a row
@@ -649,36 +712,50 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
             const uint64_t mask = live ? __ldg(a.tree + it.q0 + tok) & (~0ull >> (64 - it.nq)) : 0;
             float sl = a.scale * kLog2e;
             if (FP8) {
-                // this row of Q to fp16, its largest value in [1, 2)
+                // this row of Q, its largest value in [128, 256), as two rows of
+                // e4m3 numbers in its place
                 ok = warp_wait_flag(&sm->q_full[t], n & 1, &sm->abort, 16);
                 if (!ok) break;
                 uint8_t *q = base + t * C::kQB + r * 128;
-                float most = 0.f;
                 if (any_live) {
+                    uint4 v[D / 8];
+                    float most = 0.f;
 #pragma unroll
                     for (int u = 0; u < D / 8; ++u) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(q + (u >> 3) * kQHalf + (((u & 7) ^ (r & 7)) << 4));
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                        v[u] = *reinterpret_cast<const uint4 *>(q + (u >> 3) * kQHalf + (((u & 7) ^ (r & 7)) << 4));
+                        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             most = max3(most, fabsf(__uint_as_float(w[e] << 16)),
                                         fabsf(__uint_as_float(w[e] & 0xFFFF0000u)));
                     }
-                    const int e2 = max((int)(__float_as_uint(most) >> 23) - 127, -126);
-                    const float down = e2 >= 127 ? 0x1p-127f : __uint_as_float((127 - e2) << 23);
-                    sl = e2 <= -126 ? 0x1p-126f : __uint_as_float((127 + e2) << 23);
+                    // (an infinity makes the row NaN, as its scores would)
+                    const int e2 = max((int)(__float_as_uint(most) >> 23) - 127, -119);
+                    const float down = e2 > 127 ? __uint_as_float(0x7FFFFFFFu) : pow2(7 - e2);
+                    sl *= pow2(min(e2, 127) - 7);
 #pragma unroll
-                    for (int u = 0; u < D / 8; ++u) {
-                        uint4 *at = reinterpret_cast<uint4 *>(q + (u >> 3) * kQHalf + (((u & 7) ^ (r & 7)) << 4));
-                        const uint4 v = *at;
-                        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    for (int u = 0; u < D / 16; ++u) {  // 16 columns: 16 bytes of each term
+                        const uint32_t w[8] = {v[2 * u].x,     v[2 * u].y,     v[2 * u].z,     v[2 * u].w,
+                                               v[2 * u + 1].x, v[2 * u + 1].y, v[2 * u + 1].z, v[2 * u + 1].w};
+                        uint32_t h[2][4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const __half2 h = __floats2half2_rn(__uint_as_float(w[e] << 16) * down,
-                                                                __uint_as_float(w[e] & 0xFFFF0000u) * down);
-                            w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                            float2 a0 = make_float2(__uint_as_float(w[2 * e] << 16) * down,
+                                                    __uint_as_float(w[2 * e] & 0xFFFF0000u) * down);
+                            float2 a1 = make_float2(__uint_as_float(w[2 * e + 1] << 16) * down,
+                                                    __uint_as_float(w[2 * e + 1] & 0xFFFF0000u) * down);
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const uint32_t c0 = take_e4m3(a0), c1 = take_e4m3(a1);
+                                h[x][e] = c0 | c1 << 16;
+                            }
                         }
-                        *at = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const int unit = D == 128 ? u : 4 * x + u;
+                            *reinterpret_cast<uint4 *>(q + (D == 128 ? x * kQHalf : 0) + ((unit ^ (r & 7)) << 4)) =
+                                make_uint4(h[x][0], h[x][1], h[x][2], h[x][3]);
+                        }
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -687,22 +764,28 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
             }
             float ref = -INFINITY;  // the row's reference, in log2 units
             float l = 0.f;
-            int done = 0;
+            int done = 0, expo = 0;  // expo: of the scales that O_t's sums were made with
             for (int j = it.shared ? 0 : t; j < it.tiles; j += it.shared ? 1 : 2, ++done) {
                 ok = warp_wait_flag(&sm->s_full[t], ph, &sm->abort, 9);
                 if (!ok) break;
+                const uint32_t buf = (tile0 + j) % kScaleBufs;
                 if (FP8) {
-                    const uint32_t at = tile0 + j;
-                    ok = warp_wait_flag(&sm->sc_full[at % kScaleBufs], (at / kScaleBufs) & 1, &sm->abort, 17);
+                    ok = warp_wait_flag(&sm->sc_ready[buf], ((tile0 + j) / kScaleBufs) & 1, &sm->abort, 17);
                     if (!ok) break;
                 }
-                const float *sc = scales + ((tile0 + j) % kScaleBufs) * 2 * kKeys;
+                const float *sc = scales + buf * 3 * kKeys;
+                auto scales_read = [&]() {  // (twice, where the other warpgroup has no part in the tile)
+                    if (FP8 && lane < (it.shared ? 1 : 2)) mbar_arrive(&sm->sc_empty[buf]);
+                };
                 tc_fence_after();
                 if (!any_live) {  // (no row of this warp's is used)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
                         for (int h = 0; h < kParts; ++h) mbar_arrive(&sm->p_ready[t][h]);
+                    if (FP8) expo = sm->expo[buf];
+                    __syncwarp();
+                    scales_read();
                     ph ^= 1;
                     continue;
                 }
@@ -743,11 +826,16 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], x[kKeys - 4 + e]);
                 const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl;
                 const bool raise = top > ref + kSlack;
-                if (__any_sync(0xffffffffu, raise)) {
+                const int larger = FP8 ? sm->expo[buf] : 0;  // (the same for all rows)
+                if (__any_sync(0xffffffffu, raise) || (FP8 && larger != expo)) {
                     const float to = raise ? top : ref;
-                    const float f = raise ? ex2(ref - to) : 1.f;
+                    float f = raise ? ex2(ref - to) : 1.f;
                     l *= f;
                     ref = to;
+                    if (FP8) {
+                        f *= pow2(max(expo - larger, -127));
+                        expo = larger;
+                    }
                     if (done > 0) {
                         // the last product into O_t has to be over
                         ok = warp_wait_flag(&sm->o_done[t], ph ^ 1, &sm->abort, 10);
@@ -777,11 +865,12 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                         y.y = ex2(y.y);
                         sum[e & 1] = add2(sum[e & 1], y);
                         if (FP8) {
-                            const float2 v = *reinterpret_cast<const float2 *>(sc + kKeys + c + 2 * e);
-                            y.x *= v.x;
-                            y.y *= v.y;
+                            const float2 v = *reinterpret_cast<const float2 *>(sc + 2 * kKeys + c + 2 * e);
+                            const __half2 w = __floats2half2_rn(y.x * v.x, y.y * v.y);
+                            p[e] = *reinterpret_cast<const uint32_t *>(&w);
+                        } else {
+                            p[e] = pack_bf16(y.x, y.y);
                         }
-                        p[e] = pack_bf16(y.x, y.y);
                     }
                     tmem_st16(s_t + c / 2, p);
                     if ((c + 32) % (kKeys / kParts) == 0) {  // their product may start
@@ -791,6 +880,8 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                         if (lane == 0) mbar_arrive(&sm->p_ready[t][c / (kKeys / kParts)]);
                     }
                 }
+                __syncwarp();
+                scales_read();
                 const float2 both = add2(sum[0], sum[1]);
                 l += both.x + both.y;
                 ph ^= 1;
@@ -813,8 +904,11 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 if (lane == 0) mbar_arrive(&sm->merge[i]);
             };
             float top = ref, sum = l, f0 = 1.f, f1 = 0.f;
+            // (fp8: and the power of two that their weights lack)
+            const float own_power = FP8 ? pow2(expo - kShift) : 1.f;
             if (joined && t == 1) {
                 sm->pair[r] = make_float2(ref, l);
+                if (FP8 && r == 0) sm->expo1 = expo;
                 arrive(0);
                 ok = warp_wait_flag(&sm->merge[1], merges, &sm->abort, 12);
                 if (!ok) break;
@@ -837,6 +931,10 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                     const float inv = sum == 0.f ? 0.f : 1.f / sum;
                     f0 *= inv;
                     f1 *= inv;
+                }
+                if (FP8) {
+                    f0 *= own_power;
+                    if (second) f1 *= pow2(sm->expo1 - kShift);
                 }
                 if (joined) {
                     sm->pair[r] = make_float2(f0, f1);
@@ -986,7 +1084,14 @@ cudaError_t run(const DecodeAttnArgs &a, int sms, cudaStream_t s) {
             return cudaErrorInvalidValue;
     }
     const int page = 1 << a.kv.page_shift;
-    if (!FP8) {
+    if (FP8) {  // K's codes (the rows of V are copied as they are)
+        const uint64_t dims[3] = {D, (uint64_t)page, (uint64_t)a.kv.num_pages * a.kv.Hkv * 2};
+        const uint64_t strides[2] = {D, (uint64_t)page * D};
+        const uint32_t box[3] = {D, (uint32_t)(page < kRawKeys ? page : kRawKeys), 1};
+        if (!encode_tensor_map(&mkv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.kv.data, dims, strides, box,
+                               D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+            return cudaErrorInvalidValue;
+    } else {
         const uint64_t row_b = D * 2;
         const uint64_t dims[4] = {64, (uint64_t)page, D / 64, (uint64_t)a.kv.num_pages * a.kv.Hkv * 2};
         const uint64_t strides[3] = {row_b, 128, page * row_b};
@@ -994,8 +1099,6 @@ cudaError_t run(const DecodeAttnArgs &a, int sms, cudaStream_t s) {
         if (!encode_tensor_map(&mkv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, a.kv.data, dims, strides, box,
                                CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
-    } else {
-        mkv = mq;
     }
     // no more blocks than key tiles could exist
     const int64_t tiles = ((int64_t)a.table_stride * page + kKeys - 1) / kKeys;
