@@ -51,7 +51,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-// x * a + b and x + y on pairs of fp32
+// x * a + b, x + y and x * y on pairs of fp32
 __device__ __forceinline__ float2 fma2(float2 x, float2 a, float2 b) {
     float2 r;
     asm("{\n\t.reg .b64 x, a, b, r;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 a, {%4, %5};\n\t"
@@ -64,6 +64,15 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
     float2 r;
     asm("{\n\t.reg .b64 x, y, r;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
         "add.rn.f32x2 r, x, y;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return r;
+}
+
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, r;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 r, x, y;\n\tmov.b64 {%0, %1}, r;\n\t}"
         : "=f"(r.x), "=f"(r.y)
         : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
     return r;

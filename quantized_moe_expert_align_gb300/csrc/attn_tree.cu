@@ -46,8 +46,13 @@ constexpr int kMaxGrid = 160;    // blocks at most
 constexpr int kParts = 2;        // in which a key tile's weights come
 constexpr int kScaleBufs = 4;    // key tiles whose scales are held
 
+// Items of at least this many key tiles run shared row tiles half a round apart.
+constexpr int kApart = 4;
+
 // Warps: two softmax warpgroups; one warp per row tile issuing products, one
-// copying, one clearing; for fp8 a warpgroup that converts.
+// copying, one clearing (bf16) or copying V's codes (fp8: one warp alone takes
+// 3300 cycles a key tile to issue its copies, the bytes 1400); for fp8 a warpgroup
+// that converts.
 constexpr int kMmaWarp = 8, kLoadWarp = 10, kFixWarp = 11, kConvWarp = 12;
 
 template <int D, bool FP8>
@@ -60,7 +65,10 @@ struct Cfg {
     // Rings: operand tiles (bf16: K and V; fp8: V), tiles of K's codes, tiles of
     // 64 rows of V's codes.
     static constexpr int kOps = FP8 ? (D == 128 ? 2 : 4) : (D == 128 ? 5 : 8);
-    static constexpr int kKs = FP8 ? (D == 128 ? 3 : 6) : 1, kKB = kKeys * D;
+    static constexpr int kKs = FP8 ? (D == 128 ? 3 : 4) : 1, kKB = kKeys * D;
+    // (the first row tile's roles cannot signal the second's twice before it has looked
+    // once: that many key tiles fill the ring of K)
+    static_assert(FP8 ? kKs <= kApart : kOps <= 2 * kApart, "see kApart");
     static constexpr int kRaw = FP8 ? (D == 128 ? 5 : 10) : 1, kRawB = kRawKeys * D;
     static constexpr size_t kOpAt = (size_t)kM * kQB, kKAt = kOpAt + (size_t)kOps * kKvB;
     static constexpr size_t kRawAt = kKAt + (FP8 ? (size_t)kKs * kKB : 0);
@@ -79,7 +87,7 @@ struct Item {
     int32_t shared;           // two row tiles share the key tiles
     int32_t j0, tiles;        // key tiles
     int32_t slot;             // place for its sums, -1: all of the keys
-    int32_t done;
+    int32_t done, b;
 };
 struct Join {
     int32_t b, hv, parts, first;
@@ -110,7 +118,7 @@ __host__ __device__ inline int tile_tokens(int G) { return kTile / tile_heads(G)
 
 struct Shared {
     uint64_t q_full[kM], q_ready[kM], q_empty[kM], op_full[8], op_empty[8], tail[8], raw_full[10], raw_empty[10];
-    uint64_t k_full[6], k_empty[6], sc_full[kScaleBufs], sc_ready[kScaleBufs], sc_empty[kScaleBufs], s_full[kM], p_ready[kM][kParts], o_done[kM], merge[3];
+    uint64_t k_full[4], k_empty[4], sc_full[kScaleBufs], sc_ready[kScaleBufs], sc_empty[kScaleBufs], s_full[kM], p_ready[kM][kParts], o_done[kM], merge[3], offset;
     uint64_t item_full[2], item_empty[2], finished;
     uint32_t tmem;
     int abort, bad;
@@ -212,7 +220,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
             mbar_init(&sm->o_done[t], 1);
             mbar_init(&sm->merge[t], 4);
             mbar_init(&sm->item_full[t], 1);
-            mbar_init(&sm->item_empty[t], FP8 ? 14 : 11);  // the warps that take items
+            mbar_init(&sm->item_empty[t], FP8 ? 15 : 11);  // the warps that take items
         }
         for (int i = 0; i < 8; ++i) {
             mbar_init(&sm->op_full[i], FP8 ? 4 : 1);
@@ -223,7 +231,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
             mbar_init(&sm->raw_full[i], 1);
             mbar_init(&sm->raw_empty[i], 4);
         }
-        for (int i = 0; i < 6; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&sm->k_full[i], 1);
             mbar_init(&sm->k_empty[i], kM);
         }
@@ -233,6 +241,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
             mbar_init(&sm->sc_empty[i], 8);
         }
         mbar_init(&sm->merge[2], 8);
+        mbar_init(&sm->offset, 4);
         mbar_init(&sm->finished, kM);
         fence_barrier_init();
         sm->abort = 0;
@@ -296,8 +305,25 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
         if (lane == 0) mbar_arrive(&sm->item_empty[n & 1]);
         return it.done == 0;
     };
+    auto run_apart = [&](const Item &it) { return it.shared && it.tiles >= kApart; };
     // the item's key tiles that row tile t has
     auto tiles_of = [&](const Item &it, int t) { return it.shared ? it.tiles : (it.tiles + 1 - t) / 2; };
+
+    const int page_shift = a.kv.page_shift, page_mask = (1 << page_shift) - 1;
+    const int box_shift = min(page_shift, FP8 ? 6 : 7), R = 1 << box_shift;  // rows of one copy
+    const int chunks = kKeys >> box_shift;
+    // a copying lane's page of a key tile: that of its rows, chunk lane % chunks
+    auto page_of = [&](int b, int j, int nk) {
+        const int key = j * kKeys + ((lane % chunks) << box_shift);
+        return key < nk ? __ldg(a.page_table + (size_t)b * a.table_stride + (key >> page_shift)) : 0;
+    };
+    // (after a give-up) nothing of a copying warp's may still be in flight
+    auto land = [&]() {
+        if (*(volatile int *)&sm->abort) {
+            const long long t0 = clock64();
+            while (clock64() - t0 < (1ll << 24)) __nanosleep(1000);
+        }
+    };
 
     if (warp >= kMmaWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRoleRegs));
@@ -306,9 +332,6 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
             Join *const join = reinterpret_cast<Join *>(a.workspace + L.join);
             if (lane == 0) join[g] = Join{0, 0, 0, 0};
             __syncwarp();
-            const int page_shift = a.kv.page_shift, page_mask = (1 << page_shift) - 1;
-            const int box_shift = min(page_shift, FP8 ? 6 : 7), R = 1 << box_shift;  // rows of one copy
-            const int chunks = kKeys >> box_shift;
             Seq sq = {};
             int b = 0, hv = 0, j = 0;
             if (u0 < u1) {
@@ -317,13 +340,8 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 hv = (int)(sm->first / sq.tiles);
                 j = (int)(sm->first % sq.tiles);
             }
-            // this lane's page of a key tile: chunk lane % chunks
-            auto page_of = [&](int bb, int jj, int nk) {
-                const int key = jj * kKeys + ((lane % chunks) << box_shift);
-                return key < nk ? __ldg(a.page_table + (size_t)bb * a.table_stride + (key >> page_shift)) : 0;
-            };
             int pg = u0 < u1 ? page_of(b, j, sq.nk) : 0;
-            uint32_t n = 0, op = 0, rw = 0, kt = 0;
+            uint32_t n = 0, op = 0, kt = 0;
             bool ok = true;
             int64_t u = u0;
             for (;; ++n) {
@@ -343,6 +361,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                     it.shared = sq.nq - it.tok0 > tpt;
                     it.j0 = j;
                     it.tiles = left;
+                    it.b = b;
                     it.slot = starts && ends ? -1 : 2 * g + (starts ? 1 : 0);
                     if (starts && !ends && lane == 0) {
                         // up to the block that holds the range's last tile
@@ -420,34 +439,30 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                             }
                         }
                     } else {
-                        const int row = key & page_mask, c = lane;  // this lane's chunk of rows
-                        const bool copies = live && lane < chunks;
+                        // K's codes and both scales; V's codes are the other warp's
+                        const int row = key & page_mask;
                         const int copied = min(kKeys, (n_live + R - 1) & -R);
-                        {
-                            const uint32_t s = kt % kScaleBufs;
-                            ok = ok && warp_wait_flag(&sm->sc_empty[s], ((kt / kScaleBufs) & 1) ^ 1, &sm->abort, 18);
-                            if (!ok) break;
-                            if (lane == 0) mbar_arrive_expect_tx(&sm->sc_full[s], copied * 8);
-                            __syncwarp();
-                            if (copies) {
-                                const uint32_t to = smem_u32(scales + s * 3 * kKeys + c * R);
-                                const float *sc = a.kv.scales + ((ph * 2) << page_shift) + row;
-                                bulk_g2s(to, sc, R * 4, &sm->sc_full[s]);
-                                bulk_g2s(to + kKeys * 4, sc + ((size_t)1 << page_shift), R * 4, &sm->sc_full[s]);
-                            }
-                            __syncwarp();
+                        const uint32_t sb = kt % kScaleBufs, s = kt % C::kKs;
+                        const bool sc_lane = lane == 0;
+                        ok = lane > 1 ||
+                             wait_flag(sc_lane ? &sm->sc_empty[sb] : &sm->k_empty[s],
+                                       ((sc_lane ? kt / kScaleBufs : kt / C::kKs) & 1) ^ 1, &sm->abort, 3);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        if (lane < 2)
+                            mbar_arrive_expect_tx(sc_lane ? &sm->sc_full[sb] : &sm->k_full[s],
+                                                  sc_lane ? copied * 8 : copied * D);
+                        __syncwarp();
+                        const int c = lane % chunks;
+                        if (live && lane < chunks)
+                            tma_load_3d(k_base + s * C::kKB + c * R * D, &map_kv, 0, row, (int)(ph * 2),
+                                        &sm->k_full[s]);
+                        if (live && lane < 2 * chunks) {  // scales of K, then of V
+                            const int kv = lane >= chunks;
+                            bulk_g2s(smem_u32(scales + sb * 3 * kKeys + kv * kKeys + c * R),
+                                     a.kv.scales + (((ph * 2 + kv) << page_shift) + row), R * 4, &sm->sc_full[sb]);
                         }
-                        {
-                            const uint32_t s = kt % C::kKs;
-                            ok = warp_wait_flag(&sm->k_empty[s], ((kt / C::kKs) & 1) ^ 1, &sm->abort, 3);
-                            if (!ok) break;
-                            if (lane == 0) mbar_arrive_expect_tx(&sm->k_full[s], copied * D);
-                            __syncwarp();
-                            if (copies)
-                                tma_load_3d(k_base + s * C::kKB + c * R * D, &map_kv, 0, row, (int)(ph * 2),
-                                            &sm->k_full[s]);
-                            __syncwarp();
-                        }
+                        __syncwarp();
                         ++kt;
                         if (i == 0)
                             for (int t = 0; t < kM && ok; ++t) {
@@ -460,30 +475,11 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                                 }
                                 __syncwarp();
                             }
-                        for (int half = 0; half < 2 && ok; ++half) {
-                            const uint32_t s = rw % C::kRaw;
-                            ok = warp_wait_flag(&sm->raw_empty[s], ((rw / C::kRaw) & 1) ^ 1, &sm->abort, 3);
-                            if (!ok) break;
-                            const int keys = max(0, min(kRawKeys, copied - half * kRawKeys));
-                            if (lane == 0) mbar_arrive_expect_tx(&sm->raw_full[s], keys * D);
-                            __syncwarp();
-                            const int c_half = c - half * (kRawKeys >> box_shift);  // chunk of this half
-                            if (copies && c_half >= 0 && c_half < kRawKeys >> box_shift)
-                                bulk_g2s(smem_u32(raw_base + s * C::kRawB) + c_half * R * D,
-                                         a.kv.data + (((ph * 2 + 1) << page_shift) + row) * D, R * D,
-                                         &sm->raw_full[s]);
-                            __syncwarp();
-                            ++rw;
-                        }
                     }
                 }
                 if (!ok) break;
             }
-            // (after a give-up) nothing of this warp's may still be in flight
-            if (*(volatile int *)&sm->abort) {
-                const long long t0 = clock64();
-                while (clock64() - t0 < (1ll << 24)) __nanosleep(1000);
-            }
+            land();
         } else if (warp < kLoadWarp) {
             // ---------------- products of row tile t
             auto products = [&](auto tile) {
@@ -494,105 +490,114 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 constexpr uint32_t kIdS = FP8 ? idesc_f16_m128(kKeys) : idesc_bf16(kKeys, false);
                 constexpr uint32_t kIdO = FP8 ? idesc_f16_m128(D) | 1u << 16 : idesc_bf16(D, true);
                 const uint64_t c_desc = D == 128 ? sdesc_k_sw128(smem_u32(k_base)) : sdesc_k_sw64(smem_u32(k_base));
-                uint32_t k_stage = 0, k_ph = 0;
                 constexpr uint32_t s_t = s_col + t * kKeys, o_t = o_col + t * D;
-                uint32_t stage = 0, stage_ph = 0, p_ph = 0;
+                uint32_t off_ph = 0, p_ph = 0;
+                uint32_t tile0 = 0;  // key tiles of the items before
                 Item it;
                 bool ok = true;
-                auto next_stage = [&]() {
-                    ok = ok && warp_wait_flag(&sm->op_full[stage], stage_ph, &sm->abort, 5);
-                    tc_fence_after();
-                    const uint32_t s = stage;
-                    if (++stage == S) {
-                        stage = 0;
-                        stage_ph ^= 1;
+                // Waits for K (part 0) or V (1) of key tile number i: its stage, which
+                // comes back with the barrier that frees it.
+                auto wait_tile = [&](uint32_t i, int part, uint64_t *&free) {
+                    uint32_t s;
+                    if (FP8 && part == 0) {
+                        s = i % C::kKs;
+                        ok = ok && warp_wait_flag(&sm->k_full[s], (i / C::kKs) & 1, &sm->abort, 5);
+                        free = &sm->k_empty[s];
+                    } else {
+                        const uint32_t at = FP8 ? i : 2 * i + part;
+                        s = at % S;
+                        ok = ok && warp_wait_flag(&sm->op_full[s], (at / S) & 1, &sm->abort, 5);
+                        free = &sm->op_empty[s];
                     }
+                    tc_fence_after();
                     return s;
                 };
-                auto next_codes = [&]() {  // fp8: the next tile of K's codes
-                    ok = ok && warp_wait_flag(&sm->k_full[k_stage], k_ph, &sm->abort, 5);
-                    tc_fence_after();
-                    const uint32_t s = k_stage;
-                    if (++k_stage == C::kKs) {
-                        k_stage = 0;
-                        k_ph ^= 1;
+                // A key tile of the other row tile's: done with.
+                auto pass = [&](uint32_t i) {
+                    for (int part = 0; part < 2; ++part) {
+                        uint64_t *free;
+                        wait_tile(i, part, free);
+                        if (ok && lane == 0) mbar_arrive(free);
                     }
-                    return s;
+                    __syncwarp();
                 };
                 for (uint32_t n = 0; ok && take(n, it); ++n) {
                     const int tiles = __shfl_sync(0xffffffffu, it.tiles, 0);
                     const int mine = __shfl_sync(0xffffffffu, tiles_of(it, t), 0);
                     const bool both = __shfl_sync(0xffffffffu, it.shared, 0) != 0;
                     int done = 0;  // own tiles whose scores were issued
-                    for (int j = 0; j < tiles && ok; ++j) {
-                        const uint32_t k = FP8 ? next_codes() : next_stage();
-                        uint64_t *const k_free = FP8 ? &sm->k_empty[k] : &sm->op_empty[k];
-                        if (j == 0) {
-                            ok = ok && warp_wait_flag(FP8 ? &sm->q_ready[t] : &sm->q_full[t], n & 1, &sm->abort, 6);
-                            tc_fence_after();
-                        }
-                        if (!ok) break;
-                        const bool is_own = both || (j & 1) == t;
-                        if (is_own) {
-                            ++done;
-                            if (elect_one()) {
-                                if (FP8) {
-                                    // both terms of Q: tiles of their own, or (heads of
-                                    // 64) the two halves of a row
-                                    const uint64_t kd = c_desc + ((k * C::kKB) >> 4);
-#pragma unroll
-                                    for (int i = 0; i < 2 * (D / 32); ++i) {
-                                        const uint32_t term = i / (D / 32), in = i % (D / 32) * 32;
-                                        mma_e4m3_ss(s_t, qd + ((term * (D == 128 ? kQHalf : 64u) + in) >> 4),
-                                                    kd + (in >> 4), kIdS, i > 0);
-                                    }
-                                } else {
-                                    const uint64_t kd = k_desc + ((k * C::kKvB) >> 4);
-#pragma unroll
-                                    for (int i = 0; i < D / 16; ++i) {
-                                        const uint32_t in = (i & 3) * 32;
-                                        mma_bf16_ss(s_t, qd + (((i >> 2) * kQHalf + in) >> 4),
-                                                    kd + (((i >> 2) * kKvHalf + in) >> 4), kIdS, i > 0);
-                                    }
-                                }
-                                tc_commit(&sm->s_full[t]);
-                                tc_commit(k_free);
-                                if (done == mine) tc_commit(&sm->q_empty[t]);
-                            }
-                        } else if (lane == 0) {
-                            mbar_arrive(k_free);
-                        }
-                        __syncwarp();
-                        const uint32_t v = next_stage();
-                        if (!ok) break;
-                        if (is_own) {
-                            const uint64_t vd = v_desc + ((v * C::kKvB) >> 4);
-                            constexpr int kSteps = kKeys / 16 / kParts;
-#pragma unroll
-                            for (int h = 0; h < kParts; ++h) {
-                                ok = ok && warp_wait_flag(&sm->p_ready[t][h], p_ph, &sm->abort, 7);
-                                if (!ok) break;
-                                tc_fence_after();
-                                if (elect_one()) {
-#pragma unroll
-                                    for (int i = h * kSteps; i < (h + 1) * kSteps; ++i)
-                                        mma_f16_ts(o_t, s_t + i * 8, vd + ((i * 2048) >> 4), kIdO,
-                                                   i > 0 ? 1u : (done == 1 ? 0u : 1u));
-                                    if (h == kParts - 1) {
-                                        tc_commit(&sm->o_done[t]);
-                                        tc_commit(&sm->op_empty[v]);
-                                    }
-                                }
-                                __syncwarp();
-                            }
-                            p_ph ^= 1;
-                        } else if (lane == 0) {
-                            mbar_arrive(&sm->op_empty[v]);
-                        }
-                        __syncwarp();
+                    // Shared: the second row tile starts when the first one's maxima
+                    // are known, which puts the two half a round apart; in step both
+                    // would want the tensor pipe, then the exponentials, together.
+                    const bool apart = __shfl_sync(0xffffffffu, (int)run_apart(it), 0) != 0;
+                    ok = warp_wait_flag(FP8 ? &sm->q_ready[t] : &sm->q_full[t], n & 1, &sm->abort, 6);
+                    if (apart && t == 1) {
+                        ok = ok && warp_wait_flag(&sm->offset, off_ph, &sm->abort, 21);
+                        off_ph ^= 1;
                     }
+                    tc_fence_after();
+                    const int step = both ? 1 : 2;
+                    for (int j = both ? 0 : t; j < tiles && ok; j += step) {
+                        uint64_t *k_free, *v_free;
+                        const uint32_t k = wait_tile(tile0 + j, 0, k_free);
+                        if (!ok) break;
+                        ++done;
+                        if (elect_one()) {
+                            if (FP8) {
+                                // both terms of Q: tiles of their own, or (heads of 64)
+                                // the two halves of a row
+                                const uint64_t kd = c_desc + ((k * C::kKB) >> 4);
+#pragma unroll
+                                for (int i = 0; i < 2 * (D / 32); ++i) {
+                                    const uint32_t term = i / (D / 32), in = i % (D / 32) * 32;
+                                    mma_e4m3_ss(s_t, qd + ((term * (D == 128 ? kQHalf : 64u) + in) >> 4),
+                                                kd + (in >> 4), kIdS, i > 0);
+                                }
+                            } else {
+                                const uint64_t kd = k_desc + ((k * C::kKvB) >> 4);
+#pragma unroll
+                                for (int i = 0; i < D / 16; ++i) {
+                                    const uint32_t in = (i & 3) * 32;
+                                    mma_bf16_ss(s_t, qd + (((i >> 2) * kQHalf + in) >> 4),
+                                                kd + (((i >> 2) * kKvHalf + in) >> 4), kIdS, i > 0);
+                                }
+                            }
+                            tc_commit(&sm->s_full[t]);
+                            tc_commit(k_free);
+                            if (done == mine) tc_commit(&sm->q_empty[t]);
+                        }
+                        __syncwarp();
+                        // (the other row tile's key tile before this one: no sooner, the
+                        // softmax waits for these products)
+                        if (!both && j > 0) pass(tile0 + j - 1);
+                        const uint32_t v = wait_tile(tile0 + j, 1, v_free);
+                        if (!ok) break;
+                        const uint64_t vd = v_desc + ((v * C::kKvB) >> 4);
+                        constexpr int kSteps = kKeys / 16 / kParts;
+#pragma unroll
+                        for (int h = 0; h < kParts; ++h) {
+                            ok = ok && warp_wait_flag(&sm->p_ready[t][h], p_ph, &sm->abort, 7);
+                            if (!ok) break;
+                            tc_fence_after();
+                            if (elect_one()) {
+#pragma unroll
+                                for (int i = h * kSteps; i < (h + 1) * kSteps; ++i)
+                                    mma_f16_ts(o_t, s_t + i * 8, vd + ((i * 2048) >> 4), kIdO,
+                                               i > 0 ? 1u : (done == 1 ? 0u : 1u));
+                                if (h == kParts - 1) {
+                                    tc_commit(&sm->o_done[t]);
+                                    tc_commit(v_free);
+                                }
+                            }
+                            __syncwarp();
+                        }
+                        p_ph ^= 1;
+                    }
+                    // the last tile, if it is the other's
+                    if (ok && !both && (tiles - 1) % 2 != t) pass(tile0 + tiles - 1);
                     if (ok && mine == 0 && lane == 0) mbar_arrive(&sm->q_empty[t]);  // (not used)
                     __syncwarp();
+                    tile0 += tiles;
                 }
                 // everything issued has finished before the block ends
                 if (elect_one()) tc_commit(&sm->finished);
@@ -603,6 +608,38 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 products(std::integral_constant<int, 0>{});
             else
                 products(std::integral_constant<int, 1>{});
+        } else if (FP8 && warp == kFixWarp) {
+            // ---------------- copies of V's codes, in two stages a key tile
+            Item it;
+            uint32_t rw = 0;
+            bool ok = true;
+            for (uint32_t n = 0; ok && take(n, it); ++n) {
+                int pg = page_of(it.b, it.j0, it.nk);
+                for (int i = 0; i < it.tiles && ok && !a.test_no_copies; ++i, rw += 2) {
+                    const int key0 = (it.j0 + i) * kKeys, key = key0 + ((lane % chunks) << box_shift);
+                    const int copied = min(kKeys, (it.nk - key0 + R - 1) & -R);
+                    int p = pg;
+                    if ((unsigned)p >= (unsigned)a.kv.num_pages) p = 0;  // (the other copying warp reports it)
+                    if (i + 1 < it.tiles) pg = page_of(it.b, it.j0 + i + 1, it.nk);
+                    const uint32_t mine = rw + lane;  // the stage that lane 0 or 1 looks after
+                    ok = lane > 1 || wait_flag(&sm->raw_empty[mine % C::kRaw], ((mine / C::kRaw) & 1) ^ 1, &sm->abort, 3);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (lane < 2)
+                        mbar_arrive_expect_tx(&sm->raw_full[mine % C::kRaw],
+                                              max(0, min(kRawKeys, copied - lane * kRawKeys)) * D);
+                    __syncwarp();
+                    if (lane < chunks && key < it.nk) {
+                        const int half = lane / (kRawKeys >> box_shift), c = lane % (kRawKeys >> box_shift);
+                        const uint32_t s = (rw + half) % C::kRaw;
+                        const int64_t row = ((((int64_t)p * a.kv.Hkv + it.hk) * 2 + 1) << page_shift) + (key & page_mask);
+                        bulk_g2s(smem_u32(raw_base + s * C::kRawB) + c * R * D, a.kv.data + row * D, R * D,
+                                 &sm->raw_full[s]);
+                    }
+                    __syncwarp();
+                }
+            }
+            land();
         } else if (!FP8 && warp == kFixWarp) {
             // ---------------- last value tiles: zeros past the sequence's end
             Item it;
@@ -766,24 +803,26 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
             float l = 0.f;
             int done = 0, expo = 0;  // expo: of the scales that O_t's sums were made with
             for (int j = it.shared ? 0 : t; j < it.tiles; j += it.shared ? 1 : 2, ++done) {
-                ok = warp_wait_flag(&sm->s_full[t], ph, &sm->abort, 9);
-                if (!ok) break;
                 const uint32_t buf = (tile0 + j) % kScaleBufs;
-                if (FP8) {
+                if (FP8) {  // (before the scores are)
                     ok = warp_wait_flag(&sm->sc_ready[buf], ((tile0 + j) / kScaleBufs) & 1, &sm->abort, 17);
                     if (!ok) break;
                 }
+                const int larger = FP8 ? sm->expo[buf] : 0;  // (the same for all rows)
+                ok = warp_wait_flag(&sm->s_full[t], ph, &sm->abort, 9);
+                if (!ok) break;
                 const float *sc = scales + buf * 3 * kKeys;
                 auto scales_read = [&]() {  // (twice, where the other warpgroup has no part in the tile)
                     if (FP8 && lane < (it.shared ? 1 : 2)) mbar_arrive(&sm->sc_empty[buf]);
                 };
                 tc_fence_after();
+                if (t == 0 && done == 0 && run_apart(it) && lane == 0 && !any_live) mbar_arrive(&sm->offset);
                 if (!any_live) {  // (no row of this warp's is used)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
                         for (int h = 0; h < kParts; ++h) mbar_arrive(&sm->p_ready[t][h]);
-                    if (FP8) expo = sm->expo[buf];
+                    if (FP8) expo = larger;
                     __syncwarp();
                     scales_read();
                     ph ^= 1;
@@ -797,10 +836,12 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
 #pragma unroll
                     for (int c = 0; c < kKeys; c += 4) {
                         const float4 k = *reinterpret_cast<const float4 *>(sc + c);
-                        x[c] *= k.x;
-                        x[c + 1] *= k.y;
-                        x[c + 2] *= k.z;
-                        x[c + 3] *= k.w;
+                        const float2 lo = mul2(make_float2(x[c], x[c + 1]), make_float2(k.x, k.y));
+                        const float2 hi = mul2(make_float2(x[c + 2], x[c + 3]), make_float2(k.z, k.w));
+                        x[c] = lo.x;
+                        x[c + 1] = lo.y;
+                        x[c + 2] = hi.x;
+                        x[c + 3] = hi.y;
                     }
                 }
                 const int key0 = (it.j0 + j) * kKeys;
@@ -826,7 +867,6 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], x[kKeys - 4 + e]);
                 const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl;
                 const bool raise = top > ref + kSlack;
-                const int larger = FP8 ? sm->expo[buf] : 0;  // (the same for all rows)
                 if (__any_sync(0xffffffffu, raise) || (FP8 && larger != expo)) {
                     const float to = raise ? top : ref;
                     float f = raise ? ex2(ref - to) : 1.f;
@@ -852,12 +892,14 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                         }
                     }
                 }
+                if (t == 0 && done == 0 && run_apart(it) && lane == 0) mbar_arrive(&sm->offset);
                 const float z = ref == -INFINITY ? 0.f : ref;
                 const float2 sl2 = make_float2(sl, sl), nz2 = make_float2(-z, -z);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int c = 0; c < kKeys; c += 32) {
                     uint32_t p[16];
+                    float4 v4;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         float2 y = fma2(make_float2(x[c + 2 * e], x[c + 2 * e + 1]), sl2, nz2);
@@ -865,8 +907,9 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                         y.y = ex2(y.y);
                         sum[e & 1] = add2(sum[e & 1], y);
                         if (FP8) {
-                            const float2 v = *reinterpret_cast<const float2 *>(sc + 2 * kKeys + c + 2 * e);
-                            const __half2 w = __floats2half2_rn(y.x * v.x, y.y * v.y);
+                            if (e % 2 == 0) v4 = *reinterpret_cast<const float4 *>(sc + 2 * kKeys + c + 2 * e);
+                            y = mul2(y, e % 2 ? make_float2(v4.z, v4.w) : make_float2(v4.x, v4.y));
+                            const __half2 w = __floats2half2_rn(y.x, y.y);
                             p[e] = *reinterpret_cast<const uint32_t *>(&w);
                         } else {
                             p[e] = pack_bf16(y.x, y.y);
