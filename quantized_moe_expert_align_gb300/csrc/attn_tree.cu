@@ -21,12 +21,15 @@
 // cache is used as it is for the scores: a row of Q, times a power of two, is the
 // sum of two rows of e4m3 numbers, both multiplied with the codes (exact, but that
 // a value below 2^-9 of its row's largest is off by up to 2^-17 of it), which takes
-// as long as one product of 16-bit numbers.  For the product with the weights four
-// warps turn the codes of V into fp16 (exact).  The scales of K multiply the
-// scores in fp32.  Those of V multiply the weights, which are rounded once, to fp16
-// (2^-11): times a power of two that follows the largest scale met so far, so
-// that none overflows and those below 2^-29 of the largest lose bits; where it
-// grows, the sums are scaled down like where a reference grows.
+// as long as one product of 16-bit numbers.  Its scales multiply the scores in
+// fp32.  Four warps turn V into fp16, code times scale times a power of two that
+// follows the largest scale met so far (2^-11 for the scale, 2^-11 for the value,
+// and 2^-25 times that power of two where a value is smaller than 2^-14 of it; where
+// it grows, the sums are scaled down like where a reference grows).  The weights are
+// fp16 too (2^-11), 2^6-fold, so that those below 2^-20 of the reference's lose bits.
+// (The scales of V in the weights, as fp32 products in the softmax: 110 us instead
+// of XXX for 32 sequences of 8192 keys, 16 tokens, 32 heads of 128 over 4: one more
+// value a key that every softmax thread loads from shared memory.)
 #include <type_traits>
 
 #include "attn_tc.cuh"
@@ -40,7 +43,7 @@ using namespace attn;
 constexpr int kTile = 128;       // rows of a row tile
 constexpr int kM = 2;            // row tiles in turns
 constexpr int kKeys = 128;       // keys of a key tile
-constexpr int kRawKeys = 64;     // keys of a copied tile of fp8 codes
+constexpr int kConvKeys = 32;    // keys that a converting warp has of a key tile
 constexpr float kSlack = 8.f;    // a row's maximum may exceed its reference by this
 constexpr int kMaxGrid = 160;    // blocks at most
 constexpr int kParts = 2;        // in which a key tile's weights come
@@ -62,21 +65,19 @@ struct Cfg {
     static constexpr int kRoleRegs = FP8 ? 64 : 72, kSoftmaxRegs = FP8 ? 192 : 216;
     static_assert((kThreads - 256) * kRoleRegs + 256 * kSoftmaxRegs <= kThreads * (FP8 ? 128 : 168), "register split");
     static constexpr int kQB = kTile * D * 2, kKvB = kKeys * D * 2;  // a Q tile, an operand tile of K or V
-    // Rings: operand tiles (bf16: K and V; fp8: V), tiles of K's codes, tiles of
-    // 64 rows of V's codes.
+    // Rings: operand tiles (bf16: K and V; fp8: V), tiles of K's and of V's codes.
     static constexpr int kOps = FP8 ? (D == 128 ? 2 : 4) : (D == 128 ? 5 : 8);
     static constexpr int kKs = FP8 ? (D == 128 ? 3 : 4) : 1, kKB = kKeys * D;
     // (the first row tile's roles cannot signal the second's twice before it has looked
     // once: that many key tiles fill the ring of K)
     static_assert(FP8 ? kKs <= kApart : kOps <= 2 * kApart, "see kApart");
-    static constexpr int kRaw = FP8 ? (D == 128 ? 5 : 10) : 1, kRawB = kRawKeys * D;
+    static constexpr int kRaw = FP8 ? (D == 128 ? 2 : 4) : 1;
     static constexpr size_t kOpAt = (size_t)kM * kQB, kKAt = kOpAt + (size_t)kOps * kKvB;
     static constexpr size_t kRawAt = kKAt + (FP8 ? (size_t)kKs * kKB : 0);
-    static constexpr size_t kSharedAt = kRawAt + (FP8 ? (size_t)kRaw * kRawB : 0);
-    // fp8: of kScaleBufs key tiles the scales of K and of V, and those of V as the
-    // weights take them, [3][kKeys] floats each
+    static constexpr size_t kSharedAt = kRawAt + (FP8 ? (size_t)kRaw * kKB : 0);
+    // fp8: of kScaleBufs key tiles the scales of K and of V, [2][kKeys]
     static constexpr size_t kScalesAt = kSharedAt + 2048;
-    static constexpr size_t kSmem = kScalesAt + (FP8 ? kScaleBufs * 3 * kKeys * 4 : 0) + 1024;
+    static constexpr size_t kSmem = kScalesAt + (FP8 ? kScaleBufs * 2 * kKeys * 4 : 0) + 1024;
     static_assert(kSmem > 114 * 1024 && kSmem <= 227 * 1024, "one block per SM: all of tensor memory is its own");
 };
 
@@ -117,7 +118,7 @@ __host__ __device__ inline int tile_heads(int G) { return G < kTile ? G : kTile;
 __host__ __device__ inline int tile_tokens(int G) { return kTile / tile_heads(G); }
 
 struct Shared {
-    uint64_t q_full[kM], q_ready[kM], q_empty[kM], op_full[8], op_empty[8], tail[8], raw_full[10], raw_empty[10];
+    uint64_t q_full[kM], q_ready[kM], q_empty[kM], op_full[8], op_empty[8], tail[8], raw_full[4], raw_empty[4];
     uint64_t k_full[4], k_empty[4], sc_full[kScaleBufs], sc_ready[kScaleBufs], sc_empty[kScaleBufs], s_full[kM], p_ready[kM][kParts], o_done[kM], merge[3], offset;
     uint64_t item_full[2], item_empty[2], finished;
     uint32_t tmem;
@@ -172,9 +173,8 @@ __device__ __forceinline__ uint32_t take_e4m3(float2 &x) {
 }
 // 2^e, -127 <= e <= 127
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(e > -127 ? (uint32_t)(e + 127) << 23 : 0x00400000u); }
-// Weights are 2^kShift-fold beside the largest scale's power of two: at most 2^8
-// (the slack) times 2 times this.
-constexpr int kShift = 5;
+// fp16 weights are 2^kShift-fold, at most 2^8 (the slack) times this.
+constexpr int kShift = 6;
 // Codes [key][d] as a K-major operand, rows of 64 bytes with 64-byte swizzling.
 __device__ __forceinline__ uint64_t sdesc_k_sw64(uint32_t addr) {
     return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)1 << 16 | (uint64_t)(512u >> 4) << 32 | (uint64_t)1 << 46 |
@@ -227,7 +227,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
             mbar_init(&sm->op_empty[i], kM);
             mbar_init(&sm->tail[i], 1);
         }
-        for (int i = 0; i < 10; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&sm->raw_full[i], 1);
             mbar_init(&sm->raw_empty[i], 4);
         }
@@ -310,7 +310,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
     auto tiles_of = [&](const Item &it, int t) { return it.shared ? it.tiles : (it.tiles + 1 - t) / 2; };
 
     const int page_shift = a.kv.page_shift, page_mask = (1 << page_shift) - 1;
-    const int box_shift = min(page_shift, FP8 ? 6 : 7), R = 1 << box_shift;  // rows of one copy
+    const int box_shift = min(page_shift, 7), R = 1 << box_shift;  // rows of one copy
     const int chunks = kKeys >> box_shift;
     // a copying lane's page of a key tile: that of its rows, chunk lane % chunks
     auto page_of = [&](int b, int j, int nk) {
@@ -439,27 +439,22 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                             }
                         }
                     } else {
-                        // K's codes and both scales; V's codes are the other warp's
-                        const int row = key & page_mask;
+                        // K's codes and both scales
                         const int copied = min(kKeys, (n_live + R - 1) & -R);
                         const uint32_t sb = kt % kScaleBufs, s = kt % C::kKs;
-                        const bool sc_lane = lane == 0;
-                        ok = lane > 1 ||
-                             wait_flag(sc_lane ? &sm->sc_empty[sb] : &sm->k_empty[s],
-                                       ((sc_lane ? kt / kScaleBufs : kt / C::kKs) & 1) ^ 1, &sm->abort, 3);
-                        ok = __all_sync(0xffffffffu, ok);
+                        ok = warp_wait_flag(&sm->k_empty[s], ((kt / C::kKs) & 1) ^ 1, &sm->abort, 3);
+                        ok = ok && warp_wait_flag(&sm->sc_empty[sb], ((kt / kScaleBufs) & 1) ^ 1, &sm->abort, 18);
                         if (!ok) break;
                         if (lane < 2)
-                            mbar_arrive_expect_tx(sc_lane ? &sm->sc_full[sb] : &sm->k_full[s],
-                                                  sc_lane ? copied * 8 : copied * D);
+                            mbar_arrive_expect_tx(lane ? &sm->sc_full[sb] : &sm->k_full[s], lane ? copied * 8 : copied * D);
                         __syncwarp();
-                        const int c = lane % chunks;
+                        const int c = lane % chunks, row = key & page_mask;
                         if (live && lane < chunks)
                             tma_load_3d(k_base + s * C::kKB + c * R * D, &map_kv, 0, row, (int)(ph * 2),
                                         &sm->k_full[s]);
                         if (live && lane < 2 * chunks) {  // scales of K, then of V
                             const int kv = lane >= chunks;
-                            bulk_g2s(smem_u32(scales + sb * 3 * kKeys + kv * kKeys + c * R),
+                            bulk_g2s(smem_u32(scales + (sb * 2 + kv) * kKeys + c * R),
                                      a.kv.scales + (((ph * 2 + kv) << page_shift) + row), R * 4, &sm->sc_full[sb]);
                         }
                         __syncwarp();
@@ -609,31 +604,25 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
             else
                 products(std::integral_constant<int, 1>{});
         } else if (FP8 && warp == kFixWarp) {
-            // ---------------- copies of V's codes, in two stages a key tile
+            // ---------------- copies of V's codes
             Item it;
-            uint32_t rw = 0;
+            uint32_t tile = 0;
             bool ok = true;
             for (uint32_t n = 0; ok && take(n, it); ++n) {
                 int pg = page_of(it.b, it.j0, it.nk);
-                for (int i = 0; i < it.tiles && ok && !a.test_no_copies; ++i, rw += 2) {
+                for (int i = 0; i < it.tiles && ok && !a.test_no_copies; ++i, ++tile) {
                     const int key0 = (it.j0 + i) * kKeys, key = key0 + ((lane % chunks) << box_shift);
-                    const int copied = min(kKeys, (it.nk - key0 + R - 1) & -R);
                     int p = pg;
                     if ((unsigned)p >= (unsigned)a.kv.num_pages) p = 0;  // (the other copying warp reports it)
                     if (i + 1 < it.tiles) pg = page_of(it.b, it.j0 + i + 1, it.nk);
-                    const uint32_t mine = rw + lane;  // the stage that lane 0 or 1 looks after
-                    ok = lane > 1 || wait_flag(&sm->raw_empty[mine % C::kRaw], ((mine / C::kRaw) & 1) ^ 1, &sm->abort, 3);
-                    ok = __all_sync(0xffffffffu, ok);
+                    const uint32_t s = tile % C::kRaw;
+                    ok = warp_wait_flag(&sm->raw_empty[s], ((tile / C::kRaw) & 1) ^ 1, &sm->abort, 3);
                     if (!ok) break;
-                    if (lane < 2)
-                        mbar_arrive_expect_tx(&sm->raw_full[mine % C::kRaw],
-                                              max(0, min(kRawKeys, copied - lane * kRawKeys)) * D);
+                    if (lane == 0) mbar_arrive_expect_tx(&sm->raw_full[s], min(kKeys, (it.nk - key0 + R - 1) & -R) * D);
                     __syncwarp();
                     if (lane < chunks && key < it.nk) {
-                        const int half = lane / (kRawKeys >> box_shift), c = lane % (kRawKeys >> box_shift);
-                        const uint32_t s = (rw + half) % C::kRaw;
                         const int64_t row = ((((int64_t)p * a.kv.Hkv + it.hk) * 2 + 1) << page_shift) + (key & page_mask);
-                        bulk_g2s(smem_u32(raw_base + s * C::kRawB) + c * R * D, a.kv.data + row * D, R * D,
+                        bulk_g2s(smem_u32(raw_base + s * C::kKB) + lane * R * D, a.kv.data + row * D, R * D,
                                  &sm->raw_full[s]);
                     }
                     __syncwarp();
@@ -660,70 +649,80 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 if (lane == 0) mbar_arrive(&sm->op_full[s]);
             }
         } else if (FP8 && warp >= kConvWarp) {
-            // ---------------- the scales of V for the weights, its codes as operands
-            const int ct = tid - 32 * kConvWarp;
+            // ---------------- V's scales and codes into operands
+            const int cw = warp - kConvWarp;
             Item it;
-            uint32_t op = 0, rw = 0, tile = 0;
+            uint32_t tile = 0;
             bool ok = true;
             for (uint32_t n = 0; ok && take(n, it); ++n) {
-                int expo = -122;  // of the largest scale so far
-                for (int j = 0; j < it.tiles && ok; ++j, ++tile, ++op) {
-                    const int n_live = it.nk - (it.j0 + j) * kKeys;
-                    const uint32_t buf = tile % kScaleBufs;
-                    float *sc = scales + buf * 3 * kKeys;
+                int expo = -126;  // of the largest scale so far
+                for (int j = 0; j < it.tiles && ok; ++j, ++tile) {
+                    const int n_tile = it.nk - (it.j0 + j) * kKeys, n_live = n_tile - kConvKeys * cw;  // (this warp's)
+                    const uint32_t buf = tile % kScaleBufs, s = tile % S, r = tile % C::kRaw;
+                    const float *sc = scales + (buf * 2 + 1) * kKeys;
                     ok = warp_wait_flag(&sm->sc_full[buf], (tile / kScaleBufs) & 1, &sm->abort, 19);
                     if (!ok) break;
-                    // (every warp looks at all of them, and writes its own)
-                    const float4 v4 = *reinterpret_cast<const float4 *>(sc + kKeys + 4 * lane);
+                    // (every warp looks at all of them)
+                    const float4 v4 = *reinterpret_cast<const float4 *>(sc + 4 * lane);
                     const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+                    const float mine = sc[kConvKeys * cw + lane];
                     uint32_t most = 0;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const uint32_t bits = __float_as_uint(v[e]) & 0x7FFFFFFFu;
-                        if (4 * lane + e < n_live && bits < 0x7F800000u) most = max(most, bits);
+                        if (4 * lane + e < n_tile && bits < 0x7F800000u) most = max(most, bits);
                     }
                     most = __reduce_max_sync(0xffffffffu, most);
-                    expo = max(expo, min((int)(most >> 23) - 127, 126));
-                    sc[2 * kKeys + ct] = ct < n_live ? sc[kKeys + ct] * pow2(kShift - expo) : 0.f;
-                    if (ct == 0) sm->expo[buf] = expo;
+                    expo = max(expo, (int)(most >> 23) - 127);
+                    const __half2 own = __float2half2_rn(mine * pow2(-expo));
+                    if (tid == 32 * kConvWarp) sm->expo[buf] = expo;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm->sc_ready[buf]);
-                    const uint32_t s = op % S;
-                    ok = warp_wait_flag(&sm->op_empty[s], ((op / S) & 1) ^ 1, &sm->abort, 14);
-                    uint8_t *to = op_base + s * C::kKvB;
-#pragma unroll 1
-                    for (int half = 0; half < 2 && ok; ++half, ++rw) {
-                        const uint32_t r = rw % C::kRaw;
-                        ok = warp_wait_flag(&sm->raw_full[r], (rw / C::kRaw) & 1, &sm->abort, 15);
-                        if (!ok) break;
-                        const uint8_t *from = raw_base + r * C::kRawB;
-                        constexpr int kRow = D / 16, kEach = kRawKeys * kRow / 128;  // 16-byte pieces
-                        uint4 c[kEach];
+                    ok = warp_wait_flag(&sm->raw_full[r], (tile / C::kRaw) & 1, &sm->abort, 15);
+                    ok = ok && warp_wait_flag(&sm->op_empty[s], ((tile / S) & 1) ^ 1, &sm->abort, 14);
+                    if (!ok) break;
+                    uint8_t *to = op_base + s * C::kKvB + kConvKeys * cw * 128;
+                    const uint8_t *from = raw_base + r * C::kKB + kConvKeys * cw * D;
+                    // A lane has 16 codes of a row at a time, and rows r8, r8 + 8, ...;
+                    // of heads of 128, odd rows the other half of the columns, so that
+                    // eight neighbouring lanes' loads and stores are in different banks.
+                    constexpr int kEach = kConvKeys * D / 16 / 32;
+                    const int r8 = lane >> 2, piece = lane & 3;
+                    const uint32_t u0 = ((2 * piece) ^ r8) << 4, u1 = ((2 * piece + 1) ^ r8) << 4;
+                    auto row_of = [&](int k) { return (D == 128 ? k >> 1 : k) * 8 + r8; };
+                    auto half_of = [&](int k) { return D == 128 ? (k ^ r8) & 1 : 0; };
+                    uint4 c[kEach];
+#pragma unroll
+                    for (int k = 0; k < kEach; ++k)
+                        c[k] = *reinterpret_cast<const uint4 *>(from + row_of(k) * D + half_of(k) * 64 + piece * 16);
+                    if (n_live < kConvKeys)
 #pragma unroll
                         for (int k = 0; k < kEach; ++k)
-                            c[k] = *reinterpret_cast<const uint4 *>(from + (ct + k * 128) * 16);
+                            if (row_of(k) >= n_live) c[k] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-                        for (int k = 0; k < kEach; ++k) {
-                            const int i = ct + k * 128, key = half * kRawKeys + i / kRow, piece = i % kRow;
-                            if (key >= n_live) c[k] = make_uint4(0, 0, 0, 0);
-                            const uint2 o0 = e4m3_f16(c[k].x), o1 = e4m3_f16(c[k].y);
-                            const uint2 o2 = e4m3_f16(c[k].z), o3 = e4m3_f16(c[k].w);
-                            const uint4 lo = make_uint4(o0.x, o0.y, o1.x, o1.y), hi = make_uint4(o2.x, o2.y, o3.x, o3.y);
-                            // two 16-byte units of a 128-byte row of 64 columns; the
-                            // second half's lanes write theirs in the other order
-                            // (else two lanes of a store meet in the same banks)
-                            uint8_t *row = to + (piece >> 2) * kKvHalf + key * 128;
-                            const int unit = (piece & 3) * 2, turn = piece >> 2, x = key & 7;
-                            *reinterpret_cast<uint4 *>(row + (((unit + turn) ^ x) << 4)) = turn ? hi : lo;
-                            *reinterpret_cast<uint4 *>(row + (((unit + 1 - turn) ^ x) << 4)) = turn ? lo : hi;
-                        }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sm->raw_empty[r]);
+                    for (int k = 0; k < kEach; ++k) {
+                        const uint32_t fb = __shfl_sync(0xffffffffu, *reinterpret_cast<const uint32_t *>(&own), row_of(k));
+                        // (a row that does not exist has zeros whatever its scale)
+                        const uint32_t f = n_live < kConvKeys && row_of(k) >= n_live ? 0u : fb;
+                        auto scaled = [&](uint32_t w) {
+                            uint2 h = e4m3_f16(w);
+                            __half2 x = __hmul2(*reinterpret_cast<__half2 *>(&h.x), *reinterpret_cast<const __half2 *>(&f));
+                            __half2 y = __hmul2(*reinterpret_cast<__half2 *>(&h.y), *reinterpret_cast<const __half2 *>(&f));
+                            h.x = *reinterpret_cast<uint32_t *>(&x);
+                            h.y = *reinterpret_cast<uint32_t *>(&y);
+                            return h;
+                        };
+                        const uint2 o0 = scaled(c[k].x), o1 = scaled(c[k].y), o2 = scaled(c[k].z), o3 = scaled(c[k].w);
+                        uint8_t *at = to + half_of(k) * kKvHalf + row_of(k) * 128;
+                        *reinterpret_cast<uint4 *>(at + u0) = make_uint4(o0.x, o0.y, o1.x, o1.y);
+                        *reinterpret_cast<uint4 *>(at + u1) = make_uint4(o2.x, o2.y, o3.x, o3.y);
                     }
-                    if (!ok) break;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm->op_full[s]);
+                    if (lane == 0) {
+                        mbar_arrive(&sm->op_full[s]);
+                        mbar_arrive(&sm->raw_empty[r]);
+                    }
                     __syncwarp();
                 }
             }
@@ -811,7 +810,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 const int larger = FP8 ? sm->expo[buf] : 0;  // (the same for all rows)
                 ok = warp_wait_flag(&sm->s_full[t], ph, &sm->abort, 9);
                 if (!ok) break;
-                const float *sc = scales + buf * 3 * kKeys;
+                const float *sc = scales + buf * 2 * kKeys;
                 auto scales_read = [&]() {  // (twice, where the other warpgroup has no part in the tile)
                     if (FP8 && lane < (it.shared ? 1 : 2)) mbar_arrive(&sm->sc_empty[buf]);
                 };
@@ -844,6 +843,8 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                         x[c + 3] = hi.y;
                     }
                 }
+                __syncwarp();
+                scales_read();
                 const int key0 = (it.j0 + j) * kKeys;
                 if (key0 + kKeys > ctx) {
 #pragma unroll
@@ -893,13 +894,12 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                     }
                 }
                 if (t == 0 && done == 0 && run_apart(it) && lane == 0) mbar_arrive(&sm->offset);
-                const float z = ref == -INFINITY ? 0.f : ref;
+                const float z = (ref == -INFINITY ? 0.f : ref) - (FP8 ? kShift : 0);
                 const float2 sl2 = make_float2(sl, sl), nz2 = make_float2(-z, -z);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int c = 0; c < kKeys; c += 32) {
                     uint32_t p[16];
-                    float4 v4;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         float2 y = fma2(make_float2(x[c + 2 * e], x[c + 2 * e + 1]), sl2, nz2);
@@ -907,8 +907,6 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                         y.y = ex2(y.y);
                         sum[e & 1] = add2(sum[e & 1], y);
                         if (FP8) {
-                            if (e % 2 == 0) v4 = *reinterpret_cast<const float4 *>(sc + 2 * kKeys + c + 2 * e);
-                            y = mul2(y, e % 2 ? make_float2(v4.z, v4.w) : make_float2(v4.x, v4.y));
                             const __half2 w = __floats2half2_rn(y.x, y.y);
                             p[e] = *reinterpret_cast<const uint32_t *>(&w);
                         } else {
@@ -923,8 +921,6 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                         if (lane == 0) mbar_arrive(&sm->p_ready[t][c / (kKeys / kParts)]);
                     }
                 }
-                __syncwarp();
-                scales_read();
                 const float2 both = add2(sum[0], sum[1]);
                 l += both.x + both.y;
                 ph ^= 1;
@@ -946,9 +942,10 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm->merge[i]);
             };
+            // (fp8: and the powers of two of the weights, in l too, and of the scales)
+            if (FP8) l *= 1.f / (1 << kShift);
             float top = ref, sum = l, f0 = 1.f, f1 = 0.f;
-            // (fp8: and the power of two that their weights lack)
-            const float own_power = FP8 ? pow2(expo - kShift) : 1.f;
+            const float own_power = FP8 ? pow2(expo) * (1.f / (1 << kShift)) : 1.f;
             if (joined && t == 1) {
                 sm->pair[r] = make_float2(ref, l);
                 if (FP8 && r == 0) sm->expo1 = expo;
@@ -977,7 +974,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 }
                 if (FP8) {
                     f0 *= own_power;
-                    if (second) f1 *= pow2(sm->expo1 - kShift);
+                    if (second) f1 *= pow2(sm->expo1) * (1.f / (1 << kShift));
                 }
                 if (joined) {
                     sm->pair[r] = make_float2(f0, f1);
@@ -1130,7 +1127,7 @@ cudaError_t run(const DecodeAttnArgs &a, int sms, cudaStream_t s) {
     if (FP8) {  // K's codes (the rows of V are copied as they are)
         const uint64_t dims[3] = {D, (uint64_t)page, (uint64_t)a.kv.num_pages * a.kv.Hkv * 2};
         const uint64_t strides[2] = {D, (uint64_t)page * D};
-        const uint32_t box[3] = {D, (uint32_t)(page < kRawKeys ? page : kRawKeys), 1};
+        const uint32_t box[3] = {D, (uint32_t)(page < kKeys ? page : kKeys), 1};
         if (!encode_tensor_map(&mkv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.kv.data, dims, strides, box,
                                D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
             return cudaErrorInvalidValue;
