@@ -90,8 +90,11 @@ struct Item {
     int32_t slot;             // place for its sums, -1: all of the keys
     int32_t done, b;
 };
-struct Join {
-    int32_t b, hv, parts, first;
+// A range of keys in parts: its rows (as in Item), the blocks first .. first +
+// parts - 1 that have them.
+struct __align__(16) Join {
+    int32_t parts, first, q0, nq;
+    int32_t tok0, h0, heads, tiles;  // row tiles
 };
 struct Err {
     int32_t timeout, bad;
@@ -330,7 +333,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
         if (warp == kLoadWarp) {
             // ---------------- copies, and the items for everyone
             Join *const join = reinterpret_cast<Join *>(a.workspace + L.join);
-            if (lane == 0) join[g] = Join{0, 0, 0, 0};
+            if (lane == 0) join[g].parts = 0;
             __syncwarp();
             Seq sq = {};
             int b = 0, hv = 0, j = 0;
@@ -366,7 +369,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                     if (starts && !ends && lane == 0) {
                         // up to the block that holds the range's last tile
                         const int owner = (int)(((u + sq.tiles) * NG - 1) / W);
-                        join[g] = Join{b, hv, owner - g + 1, g};
+                        join[g] = Join{owner - g + 1, g, it.q0, it.nq, it.tok0, it.h0, it.heads, it.shared ? 2 : 1};
                     }
                 }
                 if (!warp_wait_flag(&sm->item_empty[n & 1], ((n >> 1) & 1) ^ 1, &sm->abort, 2)) break;
@@ -1046,14 +1049,20 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
     }
 }
 
-// Joins the parts of a range: blockIdx.x is its record, blockIdx.y 8 columns of
-// one row tile; a warp has 32 neighbouring rows of it.
+// Joins the parts of a range: blockIdx.x is its record, blockIdx.y a row tile and
+// 32 columns of it; a thread has a row and 8 columns.  Latency counts: what the
+// record does not say is not looked up, and the loads of up to kAhead parts are in
+// flight together.
 template <int D>
-__global__ void __launch_bounds__(kTile) tree_join(const DecodeAttnArgs a, const int HT, const int n_blocks) {
+__global__ void __launch_bounds__(4 * kTile) tree_join(const DecodeAttnArgs a, const int n_blocks) {
     __shared__ int red[2];
+    constexpr int kAhead = 4;
     const TreeLayout L = tree_layout(D);
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, r = tid & (kTile - 1);
+    const int Gt = tile_heads(a.Hq / a.kv.Hkv), tpt = kTile / Gt;
+    const int t = blockIdx.y / (D / 32), c = blockIdx.y % (D / 32) * 32 + tid / kTile * 8;
     pdl_wait();
+    const Join jn = reinterpret_cast<const Join *>(a.workspace + L.join)[blockIdx.x];
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         // the call's status word, from every block's record
         const Err *err = reinterpret_cast<const Err *>(a.workspace + L.err);
@@ -1071,38 +1080,46 @@ __global__ void __launch_bounds__(kTile) tree_join(const DecodeAttnArgs a, const
             ctrl->detail = red[0] ? red[0] : (red[1] != 0x7fffffff ? red[1] : 0);
         }
     }
-    const Join jn = reinterpret_cast<const Join *>(a.workspace + L.join)[blockIdx.x];
-    if (jn.parts == 0) return;
-    const int G = a.Hq / a.kv.Hkv, Gt = tile_heads(G), tpt = tile_tokens(G);
-    Seq s;
-    seq_of(a, jn.b, tpt, HT, s);
-    const int rest = jn.hv % (HT * s.RB), ht = rest / s.RB, rb = rest % s.RB, hk = jn.hv / (HT * s.RB);
-    const int t = blockIdx.y / (D / 8), c = blockIdx.y % (D / 8) * 8;
-    const int tok = (rb * kM + t) * tpt + tid / Gt, gr = tid % Gt;
-    if (tid / Gt >= tpt || tok >= s.nq || gr >= G - ht * Gt) return;
+    if (jn.parts == 0 || t >= jn.tiles) return;
+    const int tok = jn.tok0 + t * tpt + r / Gt, gr = r % Gt;
+    if (r / Gt >= tpt || tok >= jn.nq || gr >= jn.heads) return;
     const float2 *ml = reinterpret_cast<const float2 *>(a.workspace + L.ml);
     const float *sums = reinterpret_cast<const float *>(a.workspace + L.sums);
     // the first part is its block's last one, the others are first ones
     auto slot_of = [&](int i) { return 2 * (jn.first + i) + (i == 0 ? 1 : 0); };
     float top = -INFINITY, sum = 0.f, o[8] = {};
-#pragma unroll 4
-    for (int i = 0; i < jn.parts; ++i) top = fmaxf(top, ml[((size_t)slot_of(i) * kM + t) * kTile + tid].x);
-    const float z = top == -INFINITY ? 0.f : top;
-#pragma unroll 4
-    for (int i = 0; i < jn.parts; ++i) {
-        const float2 v = ml[((size_t)slot_of(i) * kM + t) * kTile + tid];
-        const float4 lo = *reinterpret_cast<const float4 *>(sums + part_at(slot_of(i), t, c, tid, D));
-        const float4 hi = *reinterpret_cast<const float4 *>(sums + part_at(slot_of(i), t, c + 4, tid, D));
-        const float f = ex2(v.x - z);
-        const float e[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        sum = fmaf(f, v.y, sum);
+    for (int i0 = 0; i0 < jn.parts; i0 += kAhead) {
+        float2 v[kAhead];
+        float4 x[kAhead][2];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = fmaf(f, e[k], o[k]);
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = min(i0 + k, jn.parts - 1);
+            v[k] = ml[((size_t)slot_of(i) * kM + t) * kTile + r];
+            x[k][0] = *reinterpret_cast<const float4 *>(sums + part_at(slot_of(i), t, c, r, D));
+            x[k][1] = *reinterpret_cast<const float4 *>(sums + part_at(slot_of(i), t, c + 4, r, D));
+        }
+        float to = top;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) to = fmaxf(to, v[k].x);
+        const float z = to == -INFINITY ? 0.f : to, f0 = ex2(top - z);
+        top = to;
+        sum *= f0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= f0;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (i0 + k >= jn.parts) break;
+            const float f = ex2(v[k].x - z);
+            const float e[8] = {x[k][0].x, x[k][0].y, x[k][0].z, x[k][0].w, x[k][1].x, x[k][1].y, x[k][1].z, x[k][1].w};
+            sum = fmaf(f, v[k].y, sum);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = fmaf(f, e[i], o[i]);
+        }
     }
     const bool none = sum == 0.f;
     const float inv = none ? 0.f : 1.f / sum;
-    const int64_t row = (int64_t)s.q0 + tok;
-    const int h = hk * G + ht * Gt + gr;
+    const int64_t row = (int64_t)jn.q0 + tok;
+    const int h = jn.h0 + gr;
     *reinterpret_cast<uint4 *>(a.out + row * a.out_stride + h * D + c) =
         none ? make_uint4(0, 0, 0, 0)
              : make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv),
@@ -1142,7 +1159,8 @@ cudaError_t run(const DecodeAttnArgs &a, int sms, cudaStream_t s) {
     }
     // no more blocks than key tiles could exist
     const int64_t tiles = ((int64_t)a.table_stride * page + kKeys - 1) / kKeys;
-    const int64_t rb = ((a.T < kTreeTokens ? a.T : kTreeTokens) + kM * tpt - 1) / (kM * tpt);
+    const int tokens = a.T < kTreeTokens ? a.T : kTreeTokens, rows = tokens * Gt;
+    const int64_t rb = (tokens + kM * tpt - 1) / (kM * tpt);
     const int64_t most = (a.B < a.T ? a.B : a.T) * tiles * a.kv.Hkv * HT * rb;
     int grid = sms < kMaxGrid ? sms : kMaxGrid;
     if (most < grid) grid = (int)most;
@@ -1158,15 +1176,20 @@ cudaError_t run(const DecodeAttnArgs &a, int sms, cudaStream_t s) {
     err = cudaLaunchKernelEx(&cfg, fn, a, HT, mq, mkv);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cj = {};
-    cj.gridDim = dim3(grid, kM * D / 8);
-    cj.blockDim = dim3(kTile);
+    // (the same division of an SM's memory as the main kernel's: changing it costs
+    // XXX us each way)
+    static SmemOnce carve;
+    err = carve.set_carveout(reinterpret_cast<const void *>(tree_join<D>));
+    if (err != cudaSuccess) return err;
+    cj.gridDim = dim3(grid, (rows > tpt * Gt ? kM : 1) * D / 32);
+    cj.blockDim = dim3(4 * kTile);
     cj.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cj.attrs = at;
     cj.numAttrs = 1;
-    return cudaLaunchKernelEx(&cj, tree_join<D>, a, HT, grid);
+    return cudaLaunchKernelEx(&cj, tree_join<D>, a, grid);
 }
 
 }  // namespace
