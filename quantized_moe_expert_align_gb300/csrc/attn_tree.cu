@@ -328,6 +328,23 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
         }
     };
 
+    // Both tiles of Q for item number n, by the second copying (or the clearing)
+    // warp: the first one goes on with the item's keys, whose stages are free
+    // sooner than the last item's Q.
+    auto load_q = [&](const Item &it, uint32_t n) {
+        for (int t = 0; t < kM; ++t) {
+            if (!warp_wait_flag(&sm->q_empty[t], (n & 1) ^ 1, &sm->abort, 4)) return false;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&sm->q_full[t], (uint32_t)(Gt * tpt) * D * 2);
+                for (int h = 0; h < kHalves; ++h)
+                    tma_load_4d(base + t * C::kQB + h * kQHalf, &map_q, 0, it.h0,
+                                it.q0 + it.tok0 + (it.shared ? t * tpt : 0), h, &sm->q_full[t]);
+            }
+            __syncwarp();
+        }
+        return true;
+    };
+
     if (warp >= kMmaWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRoleRegs));
         if (warp == kLoadWarp) {
@@ -428,18 +445,6 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                             }
                             __syncwarp();
                             ++op;
-                            if (kv == 0 && i == 0) {
-                                for (int t = 0; t < kM && ok; ++t) {
-                                    ok = warp_wait_flag(&sm->q_empty[t], (n & 1) ^ 1, &sm->abort, 4);
-                                    if (ok && lane == 0) {
-                                        mbar_arrive_expect_tx(&sm->q_full[t], (uint32_t)(Gt * tpt) * D * 2);
-                                        for (int h = 0; h < kHalves; ++h)
-                                            tma_load_4d(base + t * C::kQB + h * kQHalf, &map_q, 0, it.h0,
-                                                        it.q0 + it.tok0 + (it.shared ? t * tpt : 0), h, &sm->q_full[t]);
-                                    }
-                                    __syncwarp();
-                                }
-                            }
                         }
                     } else {
                         // K's codes and both scales
@@ -462,17 +467,6 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                         }
                         __syncwarp();
                         ++kt;
-                        if (i == 0)
-                            for (int t = 0; t < kM && ok; ++t) {
-                                ok = warp_wait_flag(&sm->q_empty[t], (n & 1) ^ 1, &sm->abort, 4);
-                                if (ok && lane == 0) {
-                                    mbar_arrive_expect_tx(&sm->q_full[t], (uint32_t)(Gt * tpt) * D * 2);
-                                    for (int h = 0; h < kHalves; ++h)
-                                        tma_load_4d(base + t * C::kQB + h * kQHalf, &map_q, 0, it.h0,
-                                                    it.q0 + it.tok0 + (it.shared ? t * tpt : 0), h, &sm->q_full[t]);
-                                }
-                                __syncwarp();
-                            }
                     }
                 }
                 if (!ok) break;
@@ -613,6 +607,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
             bool ok = true;
             for (uint32_t n = 0; ok && take(n, it); ++n) {
                 int pg = page_of(it.b, it.j0, it.nk);
+                ok = a.test_no_copies || load_q(it, n);
                 for (int i = 0; i < it.tiles && ok && !a.test_no_copies; ++i, ++tile) {
                     const int key0 = (it.j0 + i) * kKeys, key = key0 + ((lane % chunks) << box_shift);
                     int p = pg;
@@ -637,6 +632,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
             Item it;
             uint32_t op = 0, ph = 0;  // ph: one phase bit per stage
             for (uint32_t n = 0; take(n, it); ++n) {
+                if (!a.test_no_copies && !load_q(it, n)) break;
                 op += 2 * it.tiles;
                 const int from = it.nk - (it.j0 + it.tiles - 1) * kKeys;
                 if (from >= kKeys) continue;
@@ -651,6 +647,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm->op_full[s]);
             }
+            land();
         } else if (FP8 && warp >= kConvWarp) {
             // ---------------- V's scales and codes into operands
             const int cw = warp - kConvWarp;
@@ -994,18 +991,19 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
             if (any_live)
 #pragma unroll 1
                 for (int c = c0; c < c1; c += 32) {
-                    float o[32];
+                    float o[32], y[32];
                     tmem_ld32(o_0 + c, o);
+                    if (!FP8 && second) tmem_ld32(o_1 + c, y);
                     tc_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] *= f0;
-                    if (second) {
-                        float y[32];
+                    if (FP8 && second) {  // (both at once: spills)
                         tmem_ld32(o_1 + c, y);
                         tc_wait_ld();
+                    }
+                    if (second)
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = fmaf(y[e], f1, o[e]);
-                    }
                     if (!live) continue;
                     if (!whole) {
                         float *part = reinterpret_cast<float *>(a.workspace + L.sums);

@@ -5,7 +5,9 @@
 // is still to be read, and a thread that moves one 16-byte column of a sequence's
 // rows, a few at a time, needs no others.  What it moves is read and written
 // once; a batch moves a few megabytes, so latency bounds it: all table entries are
-// looked up together, and up to kWay rows of a column are in flight.
+// looked up together, and up to kWay rows of a column are in flight.  One block looks
+// all paths over for the status word, a thread an element (256 paths of 8 tokens, 64
+// heads' worth of bf16: 31 us with a warp a path).
 #include <type_traits>
 
 #include "device_common.cuh"
@@ -14,9 +16,10 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kMost = 64;  // accepted tokens of a sequence
-constexpr int kWay = 4;
+constexpr int kWay = 8;
+constexpr int kLook = 2048;  // paths that are looked over together
 
 // Whether the path of sequence b may be moved: by one warp, all lanes agree.
 // n: its tokens; lane's tokens i = lane and lane + 32: from and to (slots).
@@ -57,28 +60,57 @@ __device__ __forceinline__ bool look(const AcceptArgs &a, int b, int &n, int (&f
     return !__any_sync(0xffffffffu, bad);
 }
 
+// The first sequence whose path may not be moved, into the status word: by one
+// block, a thread an element.
+__device__ void look_over(const AcceptArgs &a) {
+    __shared__ int length[kLook], first_bad;
+    const int tid = threadIdx.x;
+    const int64_t room = min((int64_t)a.table_stride << a.kv.page_shift, (int64_t)1 << 30);
+    if (tid == 0) first_bad = 0x7fffffff;
+    for (int b0 = 0; b0 < a.B; b0 += kLook) {
+        const int nb = min(kLook, a.B - b0), n = nb * a.P;
+        const int32_t *path = a.accept + (size_t)b0 * a.P;
+        __syncthreads();
+        for (int b = tid; b < nb; b += kThreads) length[b] = a.P;
+        __syncthreads();
+#pragma unroll 8
+        for (int e = tid; e < n; e += kThreads)
+            if (__ldg(path + e) == -1) atomicMin(&length[e / a.P], e % a.P);
+        __syncthreads();
+#pragma unroll 4
+        for (int e = tid; e < n; e += kThreads) {
+            const int b = e / a.P, i = e % a.P;
+            if (i >= length[b]) continue;
+            const int acc = __ldg(path + e), prev = i ? __ldg(path + e - 1) : -1, base = __ldg(a.base + b0 + b);
+            bool bad = base < 0 || acc <= prev || (int64_t)base + acc >= room;
+            if (!bad && acc != i) {
+                const int32_t *row = a.page_table + (size_t)(b0 + b) * a.table_stride;
+                bad = (unsigned)__ldg(row + ((base + acc) >> a.kv.page_shift)) >= (unsigned)a.kv.num_pages ||
+                      (unsigned)__ldg(row + ((base + i) >> a.kv.page_shift)) >= (unsigned)a.kv.num_pages;
+            }
+            if (bad) atomicMin(&first_bad, b0 + b);
+        }
+        // (a path without tokens has a base all the same)
+        for (int b = tid; b < nb; b += kThreads)
+            if (__ldg(a.base + b0 + b) < 0) atomicMin(&first_bad, b0 + b);
+    }
+    __syncthreads();
+    if (tid == 0) {
+        a.ctrl->status = first_bad == 0x7fffffff ? MOE_OK : MOE_ERR_DEVICE_BAD_INDEX;
+        a.ctrl->detail = first_bad == 0x7fffffff ? 0 : first_bad;
+    }
+}
+
 // Block 0 looks every path over and writes the status word; block (1 + b, y)
 // moves kThreads columns of sequence b.
 __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptArgs a, const int pieces) {
-    __shared__ int from[kMost], to[kMost], n_shared, first_bad;
+    __shared__ int from[kMost], to[kMost], n_shared;
     const int tid = threadIdx.x, warp = tid >> 5;
-    int n, f[2], t[2];
     if (blockIdx.x == 0) {
-        if (blockIdx.y) return;
-        if (tid == 0) first_bad = 0x7fffffff;
-        __syncthreads();
-        for (int b = warp; b < a.B; b += kThreads / 32)
-            if (!look(a, b, n, f, t)) {
-                if ((tid & 31) == 0) atomicMin(&first_bad, b);
-                break;
-            }
-        __syncthreads();
-        if (tid == 0) {
-            a.ctrl->status = first_bad == 0x7fffffff ? MOE_OK : MOE_ERR_DEVICE_BAD_INDEX;
-            a.ctrl->detail = first_bad == 0x7fffffff ? 0 : first_bad;
-        }
+        if (blockIdx.y == 0) look_over(a);
         return;
     }
+    int n, f[2], t[2];
     if (warp == 0) {
         const bool ok = look(a, blockIdx.x - 1, n, f, t);
 #pragma unroll

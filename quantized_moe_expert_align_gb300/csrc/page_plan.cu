@@ -23,7 +23,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kFillThreads = 256;
 constexpr int kRowsPerWarp = 256;
 // Rows and sequences up to which the plan's own block finishes the step.
-constexpr int kSmallRows = 4096;
+constexpr int kSmallRows = 4096, kSmallSeqs = kPlanThreads;
 
 // What the rest of the step needs to know of a sequence.
 struct __align__(16) Rec {
@@ -42,7 +42,7 @@ __host__ __device__ inline PlanLayout plan_layout(int B) {
     PlanLayout l;
     l.state = 256;
     l.rec = 512;
-    l.total = l.rec + (size_t)B * sizeof(Rec);
+    l.total = l.rec + (size_t)(B > 0 ? B : 1) * sizeof(Rec);
     return l;
 }
 
@@ -102,11 +102,10 @@ __device__ __forceinline__ void move_pages(const PagePlanArgs &a, int b, const R
             row[i < r.end0 ? i : r.lo + i - r.end0];
 }
 
-// Position and slot of row t, row i of sequence b.
-__device__ __forceinline__ void put_row(const PagePlanArgs &a, const Rec *recs, const PlanState &st, int b, int t) {
+// Position and slot of row t, of sequence b.
+__device__ __forceinline__ int2 look_up(const PagePlanArgs &a, const Rec &r, const PlanState &st, int b, int t) {
     int pos = 0, slot = -1;
     if (t < st.rows) {
-        const Rec r = recs[b];
         const int j = r.len + t - r.row, p = j >> a.page_shift, p0 = pages_for(r.len, a.page_shift);
         const int pg = p < p0 ? a.table[(size_t)b * a.table_stride + p]
                               : a.ring[ring_at((int64_t)st.head + r.take + p - p0, a.cap)];
@@ -114,8 +113,7 @@ __device__ __forceinline__ void put_row(const PagePlanArgs &a, const Rec *recs, 
         if (pg < 0) slot = -1;
         pos = a.offsets ? (int)((uint32_t)r.len + (uint32_t)a.offsets[t]) : j;
     }
-    a.positions[t] = pos;
-    a.slots[t] = slot;
+    return make_int2(pos, slot);
 }
 // The sequence of row t: the last one whose first row is at most t (one warp,
 // all lanes; 32 places are looked at together).
@@ -137,7 +135,7 @@ __device__ __forceinline__ int find_from(const int32_t *cu, int B, int b, int t)
     int n = B - b;
     while (n > 1) {
         const int half = n / 2;
-        if (*(volatile const int32_t *)(cu + b + half) <= t) {
+        if (cu[b + half] <= t) {
             b += half;
             n -= half;
         } else {
@@ -146,29 +144,40 @@ __device__ __forceinline__ int find_from(const int32_t *cu, int B, int b, int t)
     }
     return b;
 }
-// Rows [t0, t1) by one warp.
-__device__ __forceinline__ void put_rows(const PagePlanArgs &a, const Rec *recs, const PlanState &st, int t0, int t1) {
-    int b = t0 < st.rows ? find_sequence(a.cu_q, a.B, t0) : 0;
-    for (int t = t0 + (threadIdx.x & 31); t < t1; t += 32) {
-        if (t < st.rows && *(volatile const int32_t *)(a.cu_q + b + 1) <= t) b = find_from(a.cu_q, a.B, b, t);
-        put_row(a, recs, st, b, t);
+// Rows [t0, t0 + kRowsPerWarp) by one warp; the loads of all of a lane's rows are
+// in flight together.
+__device__ __forceinline__ void put_rows(const PagePlanArgs &a, const Rec *recs, const PlanState &st, int t0) {
+    const int lane = threadIdx.x & 31, b0 = t0 < st.rows ? find_sequence(a.cu_q, a.B, t0) : 0;
+    const Rec r0 = recs[b0];
+    constexpr int kEach = kRowsPerWarp / 32;
+    int2 v[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int t = min(t0 + 32 * i + lane, a.rows - 1);
+        const bool later = t < st.rows && t >= r0.row + r0.grow;  // a later sequence's
+        const int b = later ? find_from(a.cu_q, a.B, b0, t) : b0;
+        v[i] = look_up(a, later ? recs[b] : r0, st, b, t);
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int t = t0 + 32 * i + lane;
+        if (t < a.rows) {
+            a.positions[t] = v[i].x;
+            a.slots[t] = v[i].y;
+        }
     }
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_step(const PagePlanArgs a, const bool whole) {
     __shared__ Sums shared[kPlanThreads / 32];
-    __shared__ int first_bad, head_count[2], cu_shared[kSmallRows];
+    __shared__ int first_bad, cu_shared[kSmallSeqs];
+    __shared__ Rec recs_shared[kSmallSeqs];
     pdl_trigger();
     const int tid = threadIdx.x;
     const PlanLayout L = plan_layout(a.B);
-    Rec *recs = reinterpret_cast<Rec *>(a.workspace + L.rec);
-    if (tid == 0) {
-        first_bad = INT_MAX;
-        head_count[0] = a.state[0];
-        head_count[1] = a.state[1];
-    }
-    __syncthreads();
-    const int head = head_count[0], count = head_count[1];
+    Rec *recs = whole ? recs_shared : reinterpret_cast<Rec *>(a.workspace + L.rec);
+    if (tid == 0) first_bad = INT_MAX;
+    const int head = a.state[0], count = a.state[1];
     const int64_t room = min((int64_t)a.table_stride << a.page_shift, (int64_t)1 << 30);
     const int first = a.window ? (int)(((int64_t)a.sinks + (1 << a.page_shift) - 1) >> a.page_shift) : 0;
     const bool ring_ok = head >= 0 && head < a.cap && count >= 0 && count <= a.cap;
@@ -273,7 +282,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step(const PagePlanArgs a, 
         }
     }
     for (int t = tid; t < a.rows; t += kPlanThreads)
-        put_row(a, recs, st, t < st.rows ? find_from(cu_shared, a.B, 0, t) : 0, t);
+    {
+        const int b = t < st.rows ? find_from(cu_shared, a.B, 0, t) : 0;
+        const int2 v = look_up(a, recs[b], st, b, t);
+        a.positions[t] = v.x;
+        a.slots[t] = v.y;
+    }
 }
 
 __global__ void __launch_bounds__(kFillThreads) fill_step(const PagePlanArgs a) {
@@ -287,7 +301,7 @@ __global__ void __launch_bounds__(kFillThreads) fill_step(const PagePlanArgs a) 
     for (int64_t w = me; w < row_items + a.B; w += warps) {
         if (w < row_items) {
             const int t0 = (int)(w * kRowsPerWarp);
-            put_rows(a, recs, st, t0, min(a.rows, t0 + kRowsPerWarp));
+            put_rows(a, recs, st, t0);
         } else if (st.ok) {
             const int b = (int)(w - row_items);
             move_pages(a, b, recs[b], st, threadIdx.x & 31, 32);
@@ -300,7 +314,7 @@ __global__ void __launch_bounds__(kFillThreads) fill_step(const PagePlanArgs a) 
 size_t page_plan_workspace(int B) { return align_up(plan_layout(B).total, 256); }
 
 cudaError_t launch_page_plan(const PagePlanArgs &a, cudaStream_t s) {
-    const bool whole = a.rows <= kSmallRows && a.B <= kSmallRows;
+    const bool whole = a.rows <= kSmallRows && a.B <= kSmallSeqs;
     plan_step<<<1, kPlanThreads, 0, s>>>(a, whole);
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess || whole) return err;

@@ -31,11 +31,14 @@ class PagePool:
 
     def __init__(self, ring, state):
         _need_torch()
-        _i32(ring, "ring", (ring.numel(),), ring.get_device())
-        _i32(state, "state", (2,), ring.get_device())
+        dev = ring.get_device()
+        _i32(ring, "ring", (ring.numel(),), dev)
+        _i32(state, "state", (2,), dev)
         if not ring.is_cuda or ring.numel() < 1:
             raise ValueError("PagePool: ring is a contiguous int32 [n] on a GPU, n at least 1")
         self.ring, self.state = ring, state
+        self._gpu, self._size = dev, ring.numel()
+        self._ptrs = ring.data_ptr(), state.data_ptr()
 
     @classmethod
     def full(cls, num_pages, device="cuda"):
@@ -47,19 +50,48 @@ class PagePool:
 
 
 class PagePlan:
-    """What page_plan writes: ``seq_lens`` [B], ``cu_q`` and ``cu_k`` [B+1],
-    ``positions`` and ``slots`` [rows], ``kept`` [B] (None without windows),
-    ``state`` [2] (the pool's, unless set to a tensor of its own); all int32."""
+    """What page_plan writes: ``seq_lens`` [B], ``cu_q`` and ``cu_k`` [B+1]
+    (cu_k None: not written), ``positions`` and ``slots`` [rows], ``kept`` [B]
+    (None without windows), ``state`` [2] (None: the pool's own; it may be set);
+    all contiguous int32 on one GPU.  Its tensors are looked at when it is made:
+    another set of tensors is another plan."""
 
     def __init__(self, seq_lens, cu_q, cu_k, positions, slots, kept=None, state=None):
-        self.seq_lens, self.cu_q, self.cu_k = seq_lens, cu_q, cu_k
-        self.positions, self.slots, self.kept, self.state = positions, slots, kept, state
+        _need_torch()
+        B, rows, dev = seq_lens.numel(), positions.numel(), seq_lens.get_device()
+        for name, t, n in (("seq_lens", seq_lens, B), ("cu_q", cu_q, B + 1), ("cu_k", cu_k, B + 1),
+                           ("positions", positions, rows), ("slots", slots, rows), ("kept", kept, B),
+                           ("state", state, 2)):
+            if t is not None or name in ("seq_lens", "cu_q", "positions", "slots"):
+                _i32(t, name, (n,), dev)
+        self._all = seq_lens, cu_q, cu_k, positions, slots, kept, state
+        self._B, self._rows, self._gpu = B, rows, dev
+        self._ptrs = tuple(_p(t) for t in self._all)
+
+    seq_lens = property(lambda self: self._all[0])
+    cu_q = property(lambda self: self._all[1])
+    cu_k = property(lambda self: self._all[2])
+    positions = property(lambda self: self._all[3])
+    slots = property(lambda self: self._all[4])
+    kept = property(lambda self: self._all[5])
+    @property
+    def state(self):
+        return self._all[6]
+
+    @state.setter
+    def state(self, t):
+        if t is not None:
+            _i32(t, "state", (2,), self._gpu)
+        self._all = self._all[:6] + (t,)
+        self._ptrs = self._ptrs[:6] + (_p(t),)
 
     @classmethod
-    def empty(cls, B, rows, windows=False, device="cuda", stream=None):
+    def empty(cls, B, rows, windows=False, device="cuda", stream=None, seq_lens=None, kept=None, state=None):
+        """New tensors for those that are not given."""
         _need_torch()
         new = lambda n: _result((n,), _attn.torch.int32, device, stream)  # noqa: E731
-        return cls(new(B), new(B + 1), new(B + 1), new(rows), new(rows), new(B) if windows else None)
+        return cls(new(B) if seq_lens is None else seq_lens, new(B + 1), new(B + 1), new(rows), new(rows),
+                   new(B) if windows and kept is None else kept, state)
 
 
 def page_plan(pool, page_table, seq_lens, new_lens, page_size, rows, window=0, sinks=0, kept=None,
@@ -81,8 +113,8 @@ def page_plan(pool, page_table, seq_lens, new_lens, page_size, rows, window=0, s
         _need_torch()
     (B, n), dev = page_table.shape, _gpu(page_table, "page_table")
     _i32(page_table, "page_table", (B, n), dev)
-    _i32(pool.ring, "ring", (pool.ring.numel(),), dev)
-    _i32(pool.state, "state", (2,), dev)
+    if pool._gpu != dev:
+        raise _wrong(pool.ring, "pool", "a ring", dev)
     _i32(seq_lens, "seq_lens", (B,), dev)
     _i32(new_lens, "new_lens", (B,), dev)
     if offsets is not None:
@@ -95,29 +127,21 @@ def page_plan(pool, page_table, seq_lens, new_lens, page_size, rows, window=0, s
         raise ValueError("sinks: only with a window")
     if out is None:
         out = PagePlan.empty(B, rows, bool(window), page_table.device, stream)
-    if out.state is None:
-        out.state = pool.state
-    _i32(out.state, "out.state", (2,), dev)
-    _i32(out.seq_lens, "out.seq_lens", (B,), dev)
-    _i32(out.cu_q, "out.cu_q", (B + 1,), dev)
-    if out.cu_k is not None:
-        _i32(out.cu_k, "out.cu_k", (B + 1,), dev)
-    _i32(out.positions, "out.positions", (rows,), dev)
-    _i32(out.slots, "out.slots", (rows,), dev)
-    if window:
-        if out.kept is None:
-            raise ValueError("window: out.kept [B] is needed")
-        _i32(out.kept, "out.kept", (B,), dev)
+    if out._B != B or out._rows != rows or out._gpu != dev:
+        raise ValueError(f"out: a plan for {B} sequences and {rows} rows on cuda:{dev} expected, got "
+                         f"{out._B} and {out._rows} on cuda:{out._gpu}")
+    if window and out.kept is None:
+        raise ValueError("window: out.kept [B] is needed")
     ws = workspace
     if ws is None or ws._gpu != dev:
         ws = _workspace(ws, stream, dev, "pages", B)
-    w, s = _window(window, sinks)
+    w, s = _window(window, sinks) if window else (0, 0)
+    ring, state = pool._ptrs
+    lens_out, cu_q, cu_k, positions, slots, kept_out, state_out = out._ptrs
     _moe._check((_moe._lib or _moe.load()).moe_page_plan(
-        pool.ring.data_ptr(), pool.ring.numel(), pool.state.data_ptr(), out.state.data_ptr(),
-        page_table.data_ptr(), n, page_size, seq_lens.data_ptr(), new_lens.data_ptr(),
-        kept.data_ptr() if w else None, _p(offsets), w, s, B, rows, out.seq_lens.data_ptr(),
-        out.kept.data_ptr() if w else None, out.cu_q.data_ptr(), _p(out.cu_k), out.positions.data_ptr(),
-        out.slots.data_ptr(), ws._ptr, ws.nbytes, _on(stream, dev)), "moe_page_plan")
+        ring, pool._size, state, state_out or state, page_table.data_ptr(), n, page_size, seq_lens.data_ptr(),
+        new_lens.data_ptr(), kept.data_ptr() if w else None, _p(offsets), w, s, B, rows, lens_out, kept_out, cu_q,
+        cu_k, positions, slots, ws._ptr, ws.nbytes, _on(stream, dev)), "moe_page_plan")
     return out
 
 
