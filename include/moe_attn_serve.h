@@ -85,7 +85,7 @@ moe_status_t moe_attn_decode_window(const uint16_t *q, int64_t q_stride,
  * moe_attn_prefill, causal and through a window: a row at place p of its
  * sequence's keys (row i of nq stands at p = i + nk - nq) sees the keys j <= p
  * with j > p - window or j < sinks.  An infinity or NaN in v may reach the up to
- * 255 rows before the first that sees it, and those up to 382 rows after the
+ * 255 rows before the first that sees it, and those up to 270 rows after the
  * last one.  All else, and the workspace, as in moe_attn_prefill; window >= 1,
  * sinks >= 0.
  */

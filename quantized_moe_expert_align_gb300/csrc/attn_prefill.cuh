@@ -60,6 +60,11 @@ constexpr float kSlack = 8.f;    // a row's maximum may exceed its reference by 
 
 constexpr int kMinKeys = 1024;   // with no more keys in all, no key range is cut
 constexpr int kMinPart = 4;      // key tiles of a part at least
+// Keys that a block's rows see at most.
+__host__ __device__ inline int64_t reach_of(const PrefillArgs &a, int tokens, bool win) {
+    const int64_t seen = (int64_t)a.window + a.sinks + tokens;
+    return win && seen < a.Tk ? seen : a.Tk;
+}
 // What the plan reckons with: a round of one key tile, a join, a part.
 constexpr int kRound = 32, kJoinCost = 128, kPartCost = 1;
 constexpr int kMaxSms = 160;     // blocks of the main kernel at most
@@ -166,16 +171,26 @@ __device__ __forceinline__ int keys_seen(int causal, int tok, int nq, int nk) {
     return causal ? max(0, min(nk, tok + nk - nq + 1)) : nk;
 }
 
-// Through a window (WIN), a block's key tiles are those of the first keys, which
-// stay visible, then those from the first key on that its first token sees:
-// `base`, which is 0 where the two would meet (then all tiles are from key 0 on).
-__device__ __forceinline__ int lead_tiles(const PrefillArgs &a) { return (int)(((int64_t)a.sinks + kKeys - 1) / kKeys); }
-// The first key of key tile j.
+// Through a window (WIN), the keys between the first ones, which stay visible, and
+// `base`, the first one that a block's first token sees, are left out of the
+// block's numbering: it has the first ones, rounded up to kLead, then those from
+// base on.  The tile where the two meet (the seam) is copied in pieces.  Where they
+// would overlap, base is 0 and nothing is left out.
+constexpr int kLead = 16;
+__device__ __forceinline__ int lead_keys(const PrefillArgs &a) {
+    return (int)min((int64_t)(a.sinks + (int64_t)kLead - 1) & -(int64_t)kLead, (int64_t)1 << 30);
+}
+// What a key from the seam's tile on, by its number, has to be increased by.
+template <bool WIN>
+__device__ __forceinline__ int left_out(const PrefillArgs &a, int base) {
+    return WIN && base > 0 ? base - lead_keys(a) : 0;
+}
+// The place of key tile j's first key, as if nothing before it were left out (the
+// seam's tile: of the one that its last keys start from).
 template <bool WIN>
 __device__ __forceinline__ int tile_key(const PrefillArgs &a, int base, int j) {
-    if (!WIN || base == 0) return j * kKeys;
-    const int lead = lead_tiles(a);
-    return j < lead ? j * kKeys : base + (j - lead) * kKeys;
+    if (!WIN || base == 0 || (j + 1) * kKeys <= lead_keys(a)) return j * kKeys;
+    return j * kKeys + left_out<WIN>(a, base);
 }
 // The first key of its window that token `tok` of a sequence sees.
 __device__ __forceinline__ int window_from(const PrefillArgs &a, int tok, int nq, int nk) {
@@ -184,15 +199,15 @@ __device__ __forceinline__ int window_from(const PrefillArgs &a, int tok, int nq
 // The block of a sequence that starts at its token t0, whole.
 template <bool WIN>
 __device__ __forceinline__ Block block_at(const PrefillArgs &a, int q0, int nq, int k0, int nk, int t0, int tpt) {
-    int base = 0, lead = 0;
+    int base = 0;
     if (WIN) {
-        lead = lead_tiles(a);
         base = window_from(a, t0, nq, nk);
-        if (base <= (int64_t)lead * kKeys) base = lead = 0;
+        if (base <= lead_keys(a)) base = 0;
     }
+    const int less = left_out<WIN>(a, base);
     auto tiles_of = [&](int t) {  // of the row tile from token t on
         const int last = min(nq, t + tpt) - 1;
-        return last < t ? 0 : lead + (keys_seen(a.causal, last, nq, nk) - base + kKeys - 1) / kKeys;
+        return last < t ? 0 : (keys_seen(a.causal, last, nq, nk) - less + kKeys - 1) / kKeys;
     };
     return Block{q0, nq, k0, nk, t0, 0, tiles_of(t0), tiles_of(t0 + tpt), -1, 1, 0, base};
 }
@@ -262,7 +277,7 @@ plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks
         atomicAdd(&count[bucket_of(tiles)], 1);
     });
     int most = 0x7fffff;  // key tiles of an item
-    if (a.Tk > kMinKeys) {
+    if (reach_of(a, tokens, WIN) > kMinKeys) {
         mine_tiles = warp_total(mine_tiles);
         longest_mine = __reduce_max_sync(0xffffffffu, longest_mine);
         if (lane == 0 && mine_tiles) {
@@ -377,7 +392,8 @@ plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks
 template <int D, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __grid_constant__ CUtensorMap map_q,
-               const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+               const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+               const __grid_constant__ CUtensorMap map_k_piece, const __grid_constant__ CUtensorMap map_v_piece) {
     using C = Cfg<D>;
     constexpr int S = C::kStages;
     constexpr int kHalves = D / 64;
@@ -447,10 +463,14 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
     auto ragged = [&](const Item &it, int j) {
         return key_of(it, j) + kKeys > it.b.nk && it.b.k0 + it.b.nk < a.Tk;
     };
-    // The tile (of the item) that holds the last of the first keys, if there is
-    // a gap behind it; the keys past a.sinks in it are behind every window.
+    // Through a window, with keys left out: the item's tile with the seam, and the
+    // one whose first keys past a.sinks, which no row sees any more, are cleared of
+    // values; -1: none.
+    auto seam = [&](const Item &it) {
+        return WIN && it.b.base > 0 && lead_keys(a) % kKeys ? lead_keys(a) / kKeys - it.b.j0 : -1;
+    };
     auto last_lead = [&](const Item &it) {
-        return WIN && it.b.base > 0 && a.sinks % kKeys ? lead_tiles(a) - 1 - it.b.j0 : -1;
+        return WIN && it.b.base > 0 && a.sinks % kLead ? a.sinks / kKeys - it.b.j0 : -1;
     };
 
     if (warp >= kMmaWarp) {
@@ -532,20 +552,29 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                 next_ahead();
                 const int tiles = most_tiles(it.b);
                 bool ok = true;
-                auto copy_kv = [&](const CUtensorMap *map, int j, bool tail) {
+                auto copy_kv = [&](const CUtensorMap *map, const CUtensorMap *piece, int j, bool tail) {
                     const uint32_t s = kv % S, ph = (kv / S) & 1;
                     ok = ok && warp_wait_flag(&sm->kv_empty[s], ph ^ 1, &sm->abort, 3);
                     if (!ok) return;
                     if (lane == 0) {
                         uint64_t *bar = tail ? &sm->tail[s] : &sm->kv_full[s];
                         mbar_arrive_expect_tx(bar, C::kKvB);
-                        tma_load_4d(kv_base + s * C::kKvB, map, 0, it.b.k0 + key_of(it, j), it.hk, 0, bar);
+                        if (!WIN || j != seam(it))
+                            tma_load_4d(kv_base + s * C::kKvB, map, 0, it.b.k0 + key_of(it, j), it.hk, 0, bar);
+                    }
+                    __syncwarp();
+                    if (WIN && j == seam(it) && lane < kKeys / kLead * kHalves) {  // kLead keys a lane
+                        const int c = lane % (kKeys / kLead), h = lane / (kKeys / kLead);
+                        const int v = (it.b.j0 + j) * kKeys + c * kLead;
+                        const int key = v < lead_keys(a) ? v : v + left_out<WIN>(a, it.b.base);
+                        tma_load_4d(kv_base + s * C::kKvB + h * kKvHalf + c * kLead * 128, piece, 0, it.b.k0 + key, it.hk,
+                                    h, tail ? &sm->tail[s] : &sm->kv_full[s]);
                     }
                     __syncwarp();
                     ++kv;
                 };
                 for (int j = 0; j < tiles && ok && !a.test_no_copies; ++j) {
-                    if (!C::kOwnP || j == 0) copy_kv(&map_k, j, false);
+                    if (!C::kOwnP || j == 0) copy_kv(&map_k, &map_k_piece, j, false);
                     if (j == 0) {
                         for (int t = 0; t < kM && ok; ++t) {
                             ok = warp_wait_flag(&sm->q_empty[t], (n & 1) ^ 1, &sm->abort, 4);
@@ -560,8 +589,8 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                         }
                     }
                     // (in the order in which the products want them)
-                    if (C::kOwnP && ok && j + 1 < tiles) copy_kv(&map_k, j + 1, false);
-                    if (ok) copy_kv(&map_v, j, ragged(it, j) || j == last_lead(it));
+                    if (C::kOwnP && ok && j + 1 < tiles) copy_kv(&map_k, &map_k_piece, j + 1, false);
+                    if (ok) copy_kv(&map_v, &map_v_piece, j, ragged(it, j) || j == last_lead(it));
                 }
                 if (!ok) break;
                 if (tiles == 0) {
@@ -715,29 +744,36 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
             uint32_t kv = 0, ph = 0;  // ph: one phase bit per stage
             for (uint32_t n = 0; take(n, it); ++n) {
                 const int tiles = most_tiles(it.b);
-                // rows from `from` on of the value tile that is copy number c
-                auto clear = [&](uint32_t c, int from) {
+                // Of the value tile that is copy number c the rows [r0, r1) and those
+                // from `from` on.
+                auto clear = [&](uint32_t c, int r0, int r1, int from) {
                     const uint32_t s = c % S;
                     if (!warp_wait_flag(&sm->tail[s], (ph >> s) & 1, &sm->abort, 8)) return false;
                     ph ^= 1u << s;
                     uint8_t *v = kv_base + s * C::kKvB;
-                    for (int h = 0; h < kHalves; ++h)
+                    for (int h = 0; h < kHalves; ++h) {
+                        if (WIN)
+                            for (int i = r0 * 8 + lane; i < r1 * 8; i += 32)
+                                *reinterpret_cast<uint4 *>(v + h * kKvHalf + i * 16) = make_uint4(0, 0, 0, 0);
                         for (int i = from * 8 + lane; i < kKeys * 8; i += 32)
                             *reinterpret_cast<uint4 *>(v + h * kKvHalf + i * 16) = make_uint4(0, 0, 0, 0);
+                    }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm->kv_full[s]);
                     return true;
                 };
                 const int lead = last_lead(it);
+                auto past_end = [&](int j) { return ragged(it, j) ? it.b.nk - key_of(it, j) : kKeys; };
                 if (lead >= 0 && lead < tiles) {
                     // (heads of 64: the next key tile is copied first, if there is one)
                     const uint32_t at = kv + 2 * (uint32_t)lead + (C::kOwnP && lead + 1 < tiles ? 2 : 1);
-                    if (!clear(at, a.sinks % kKeys)) break;
+                    const int first = (it.b.j0 + lead) * kKeys;
+                    if (!clear(at, a.sinks - first, min(lead_keys(a) - first, kKeys), past_end(lead))) break;
                 }
                 kv += 2 * tiles;
                 if (tiles == 0 || lead == tiles - 1 || !ragged(it, tiles - 1)) continue;
-                if (!clear(kv - 1, it.b.nk - key_of(it, tiles - 1))) break;
+                if (!clear(kv - 1, 0, 0, past_end(tiles - 1))) break;
             }
         }
     } else {
@@ -788,7 +824,7 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                 }
                 const int key0 = key_of(it, j);
                 if (WIN && key0 < most_from && key0 + kKeys > a.sinks) {
-                    const int lo = from - key0, first = a.sinks - key0;
+                    const int lo = from - key0, first = a.sinks - (j == seam(it) ? (it.b.j0 + j) * kKeys : key0);
 #pragma unroll
                     for (int c = 0; c < kKeys; c += 32)
                         if (key0 + c < most_from) {
@@ -1114,8 +1150,18 @@ cudaError_t run(const PrefillArgs &a, int sms, cudaStream_t s) {
                                box, CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
     }
+    CUtensorMap mp[2] = {mk, mv};  // pieces of a seam
+    for (int i = 0; i < 2 && WIN; ++i) {
+        const uint16_t *p = a.Tk > 0 ? (i ? a.v : a.k) : a.q;
+        const uint64_t dims[4] = {64, (uint64_t)(a.Tk > 0 ? a.Tk : 1), (uint64_t)a.Hkv, D / 64};
+        const uint64_t strides[3] = {(uint64_t)(i ? a.v_stride : a.k_stride) * 2, D * 2, 128};
+        const uint32_t box[4] = {64, kLead, 1, 1};
+        if (!encode_tensor_map(&mp[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p, dims, strides, box,
+                               CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+    }
     // (no key range is cut below this many keys: then no joins either)
-    const bool cuts = a.Tk > kMinKeys;
+    const bool cuts = reach_of(a, kM * tpt, WIN) > kMinKeys;
     const int64_t most = ((int64_t)a.Tq / (kM * tpt) + a.B) * a.Hkv * HT;
     if (sms > kMaxSms) sms = kMaxSms;
     const int grid = (int)(cuts || most > sms ? sms : most);
@@ -1141,7 +1187,7 @@ cudaError_t run(const PrefillArgs &a, int sms, cudaStream_t s) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = planned ? 1 : 0;
-    err = cudaLaunchKernelEx(&cfg, fn, a, HT, planned, mq, mk, mv);
+    err = cudaLaunchKernelEx(&cfg, fn, a, HT, planned, mq, mk, mv, mp[0], mp[1]);
     if (err != cudaSuccess || !cuts) return err;
     cudaLaunchConfig_t cj = {};
     cj.gridDim = dim3(8 * sms);  // (16: up to 2 us more where there is nothing to join)
