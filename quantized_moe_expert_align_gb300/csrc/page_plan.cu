@@ -8,9 +8,16 @@
 // its tail, so that no place that is read is written by the same call.  All the
 // rest is a few integers a row: latency bounds small calls, bytes large ones.
 //
-// A plan kernel of one block makes the sums; if the step is valid and the pages
-// suffice, rows and pages follow from its records.  Small steps are finished by
-// the same block, large ones by a second kernel over the whole GPU.
+// One block makes the sums; if the step is valid and the pages suffice, rows and
+// pages follow from its records.
+//  kOwnBlock: small steps are finished by the same block.
+//  kEveryBlock: larger ones by a whole grid, every block of which makes the sums for
+//    itself: a sequence's numbers are read by all, so none of them may be written
+//    in place.
+//  kTwoKernels: in place, or too many sequences for that, by a second kernel.
+// Measured (in a captured graph): 90 sequences of a token each with windows 8 us;
+// 256 prompts of 898 thousand rows, 7.3 MB, XXX us by every block and 15.7 by two
+// kernels.
 #include <climits>
 
 #include "device_common.cuh"
@@ -24,6 +31,7 @@ constexpr int kFillThreads = 256;
 constexpr int kRowsPerWarp = 256;
 // Rows and sequences up to which the plan's own block finishes the step.
 constexpr int kSmallRows = 4096, kSmallSeqs = kPlanThreads;
+enum Mode { kOwnBlock, kEveryBlock, kTwoKernels };
 
 // What the rest of the step needs to know of a sequence.
 struct __align__(16) Rec {
@@ -60,9 +68,9 @@ __device__ __forceinline__ int ring_at(int64_t at, int cap) {
 struct Sums {
     int64_t v[4];
 };
-__device__ __forceinline__ void block_scan(const Sums &mine, Sums &before, Sums &all, Sums *shared) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Sums x = mine;
+// Only the first `used` threads have any; one warp adds up the warps' sums.
+__device__ __forceinline__ void warp_scan(Sums &x) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
@@ -70,20 +78,24 @@ __device__ __forceinline__ void block_scan(const Sums &mine, Sums &before, Sums 
             const int64_t y = __shfl_up_sync(0xffffffffu, x.v[i], o);
             if (lane >= o) x.v[i] += y;
         }
-    if (lane == 31) shared[warp] = x;
-    __syncthreads();
-    const Sums w = shared[lane];  // (32 warps)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        int64_t b = lane < warp ? w.v[i] : 0, t = w.v[i];
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            b += __shfl_xor_sync(0xffffffffu, b, o);
-            t += __shfl_xor_sync(0xffffffffu, t, o);
-        }
-        before.v[i] = b + x.v[i] - mine.v[i];
-        all.v[i] = t;
+}
+__device__ __forceinline__ void block_scan(const Sums &mine, int used, Sums &before, Sums &all, Sums *shared) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Sums x = mine;
+    if (warp * 32 < used) {
+        warp_scan(x);
+        if (lane == 31) shared[warp] = x;
     }
+    __syncthreads();
+    if (warp == 0) {  // (32 warps)
+        Sums w = lane * 32 < used ? shared[lane] : Sums{{0, 0, 0, 0}};
+        warp_scan(w);
+        shared[lane] = w;
+    }
+    __syncthreads();
+    all = shared[31];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) before.v[i] = (warp ? shared[warp - 1].v[i] : 0) + x.v[i] - mine.v[i];
     __syncthreads();
 }
 
@@ -146,8 +158,9 @@ __device__ __forceinline__ int find_from(const int32_t *cu, int B, int b, int t)
 }
 // Rows [t0, t0 + kRowsPerWarp) by one warp; the loads of all of a lane's rows are
 // in flight together.
-__device__ __forceinline__ void put_rows(const PagePlanArgs &a, const Rec *recs, const PlanState &st, int t0) {
-    const int lane = threadIdx.x & 31, b0 = t0 < st.rows ? find_sequence(a.cu_q, a.B, t0) : 0;
+__device__ __forceinline__ void put_rows(const PagePlanArgs &a, const Rec *recs, const int32_t *cu, const PlanState &st,
+                                         int t0) {
+    const int lane = threadIdx.x & 31, b0 = t0 < st.rows ? find_sequence(cu, a.B, t0) : 0;
     const Rec r0 = recs[b0];
     constexpr int kEach = kRowsPerWarp / 32;
     int2 v[kEach];
@@ -155,7 +168,7 @@ __device__ __forceinline__ void put_rows(const PagePlanArgs &a, const Rec *recs,
     for (int i = 0; i < kEach; ++i) {
         const int t = min(t0 + 32 * i + lane, a.rows - 1);
         const bool later = t < st.rows && t >= r0.row + r0.grow;  // a later sequence's
-        const int b = later ? find_from(a.cu_q, a.B, b0, t) : b0;
+        const int b = later ? find_from(cu, a.B, b0, t) : b0;
         v[i] = look_up(a, later ? recs[b] : r0, st, b, t);
     }
 #pragma unroll
@@ -168,14 +181,30 @@ __device__ __forceinline__ void put_rows(const PagePlanArgs &a, const Rec *recs,
     }
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_step(const PagePlanArgs a, const bool whole) {
+// All rows and all pages, by the warps of a grid.
+__device__ __forceinline__ void fill(const PagePlanArgs &a, const Rec *recs, const int32_t *cu, const PlanState &st) {
+    const int64_t warps = (int64_t)gridDim.x * (blockDim.x / 32);
+    const int64_t me = (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
+    const int64_t row_items = ((int64_t)a.rows + kRowsPerWarp - 1) / kRowsPerWarp;
+    for (int64_t w = me; w < row_items + a.B; w += warps) {
+        if (w < row_items) {
+            put_rows(a, recs, cu, st, (int)(w * kRowsPerWarp));
+        } else if (st.ok) {
+            const int b = (int)(w - row_items);
+            move_pages(a, b, recs[b], st, threadIdx.x & 31, 32);
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_step(const PagePlanArgs a, const Mode mode) {
     __shared__ Sums shared[kPlanThreads / 32];
     __shared__ int first_bad, cu_shared[kSmallSeqs];
     __shared__ Rec recs_shared[kSmallSeqs];
     pdl_trigger();
     const int tid = threadIdx.x;
     const PlanLayout L = plan_layout(a.B);
-    Rec *recs = whole ? recs_shared : reinterpret_cast<Rec *>(a.workspace + L.rec);
+    Rec *recs = mode == kTwoKernels ? reinterpret_cast<Rec *>(a.workspace + L.rec) : recs_shared;
+    const bool tells = blockIdx.x == 0;  // writes what is not a row's or a page's
     if (tid == 0) first_bad = INT_MAX;
     const int head = a.state[0], count = a.state[1];
     const int64_t room = min((int64_t)a.table_stride << a.page_shift, (int64_t)1 << 30);
@@ -216,7 +245,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step(const PagePlanArgs a, 
             }
         }
         Sums before, all;
-        block_scan(mine, before, all, shared);
+        block_scan(mine, a.B - b0, before, all, shared);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             before.v[i] += base.v[i];
@@ -229,9 +258,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step(const PagePlanArgs a, 
             r.take = (int)before.v[1];
             r.give = (int)before.v[2];
             recs[b] = r;
-            a.cu_q[b] = r.row;
-            if (whole) cu_shared[b] = r.row;
-            if (a.cu_k) a.cu_k[b] = (int)before.v[3];
+            if (tells) a.cu_q[b] = r.row;
+            if (mode != kTwoKernels) cu_shared[b] = r.row;
+            if (tells && a.cu_k) a.cu_k[b] = (int)before.v[3];
             if (bad) atomicMin(&first_bad, b);
         }
     }
@@ -239,7 +268,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step(const PagePlanArgs a, 
     if (tid == 0 && (!ring_ok || base.v[2] > a.cap - count)) atomicMin(&first_bad, a.B);
     __syncthreads();
     const bool ok = first_bad == INT_MAX;
-    for (int b = tid; b < a.B; b += kPlanThreads) {
+    for (int b = tid; b < a.B && tells; b += kPlanThreads) {
         if (a.B > kPlanThreads) {
             len = a.seq_lens[b];
             n = a.new_lens[b];
@@ -254,7 +283,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step(const PagePlanArgs a, 
         }
     }
     const PlanState st = {ok, ok ? head : 0, ok ? count : 0, ok ? (int)base.v[0] : 0};
-    if (tid == 0) {
+    if (tid == 0 && tells) {
         a.cu_q[a.B] = st.rows;
         if (a.cu_k) a.cu_k[a.B] = ok ? (int)base.v[3] : 0;
         a.state_out[0] = ok ? ring_at(head + base.v[1], a.cap) : head;
@@ -264,8 +293,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step(const PagePlanArgs a, 
         ctrl->detail = ok ? 0 : first_bad;
         *reinterpret_cast<PlanState *>(a.workspace + L.state) = st;
     }
-    if (!whole) return;
+    if (mode == kTwoKernels) return;
     __syncthreads();
+    if (mode == kEveryBlock) {
+        fill(a, recs, cu_shared, st);
+        return;
+    }
     const int warp = tid >> 5, lane = tid & 31;
     if (ok) {
         // a thread its sequence; those with more pages than a few, a warp together
@@ -295,18 +328,7 @@ __global__ void __launch_bounds__(kFillThreads) fill_step(const PagePlanArgs a) 
     const Rec *recs = reinterpret_cast<const Rec *>(a.workspace + L.rec);
     pdl_wait();
     const PlanState st = *reinterpret_cast<const PlanState *>(a.workspace + L.state);
-    const int64_t warps = (int64_t)gridDim.x * (kFillThreads / 32);
-    const int64_t me = (int64_t)blockIdx.x * (kFillThreads / 32) + (threadIdx.x >> 5);
-    const int64_t row_items = ((int64_t)a.rows + kRowsPerWarp - 1) / kRowsPerWarp;
-    for (int64_t w = me; w < row_items + a.B; w += warps) {
-        if (w < row_items) {
-            const int t0 = (int)(w * kRowsPerWarp);
-            put_rows(a, recs, st, t0);
-        } else if (st.ok) {
-            const int b = (int)(w - row_items);
-            move_pages(a, b, recs[b], st, threadIdx.x & 31, 32);
-        }
-    }
+    fill(a, recs, a.cu_q, st);
 }
 
 }  // namespace
@@ -314,11 +336,17 @@ __global__ void __launch_bounds__(kFillThreads) fill_step(const PagePlanArgs a) 
 size_t page_plan_workspace(int B) { return align_up(plan_layout(B).total, 256); }
 
 cudaError_t launch_page_plan(const PagePlanArgs &a, cudaStream_t s) {
-    const bool whole = a.rows <= kSmallRows && a.B <= kSmallSeqs;
-    plan_step<<<1, kPlanThreads, 0, s>>>(a, whole);
-    cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess || whole) return err;
+    const bool in_place =
+        a.state == a.state_out || a.seq_lens == a.seq_lens_out || (a.window && a.kept == a.kept_out);
+    const Mode mode = a.B > kSmallSeqs         ? kTwoKernels
+                      : a.rows <= kSmallRows ? kOwnBlock
+                      : in_place             ? kTwoKernels
+                                             : kEveryBlock;
     const int64_t warps = ((int64_t)a.rows + kRowsPerWarp - 1) / kRowsPerWarp + a.B;
+    const int64_t full = (warps * 32 + kPlanThreads - 1) / kPlanThreads;
+    plan_step<<<mode == kEveryBlock ? (unsigned)(full < 152 ? full : 152) : 1, kPlanThreads, 0, s>>>(a, mode);
+    cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess || mode != kTwoKernels) return err;
     const int64_t blocks = (warps * 32 + kFillThreads - 1) / kFillThreads;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(blocks < 152 * 8 ? blocks : 152 * 8));

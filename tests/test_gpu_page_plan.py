@@ -23,11 +23,13 @@ class Both:
         self.d_table, self.d_lens, self.d_kept = su.i32(self.table), su.i32(self.lens), su.i32(self.kept)
         self.ws = moe.AttnWorkspace("cuda", "pages", B)
 
-    def step(self, new, rows, offsets=None, in_place=True, detail=None):
+    def step(self, new, rows, offsets=None, in_place=True, detail=None, own_state=False):
         import torch
         import quantized_moe_expert_align_gb300 as moe
         own = dict(seq_lens=self.d_lens, kept=self.d_kept if self.window else None) if in_place else {}
         out = moe.PagePlan.empty(len(new), rows, self.window > 0, **own)
+        if own_state:
+            out.state = torch.full_like(self.pool.state, -9)
         self.ws.buf.random_(0, 255)
         got = moe.page_plan(self.pool, self.d_table, self.d_lens, su.i32(new), self.page, rows,
                             window=self.window, sinks=self.sinks, kept=self.d_kept if self.window else None,
@@ -47,6 +49,9 @@ class Both:
         for name, w in zip(names, want):
             if name != "state" and (name != "kept" or self.window):
                 assert getattr(out, name).tolist() == list(w), name
+        if own_state:
+            assert out.state.tolist() == self.state
+            self.pool.state.copy_(out.state)
         assert self.pool.state.tolist() == self.state
         assert torch.equal(self.d_table, su.i32(self.table))
         assert torch.equal(self.pool.ring, su.i32(self.ring))
@@ -73,13 +78,28 @@ def test_steps(gpu, B, page, in_place, window, sinks):
         x.step(new, n, offsets=[rng.randrange(9) for _ in range(n)], in_place=in_place)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("rows", [4096, 4097, 20000])
-def test_one_prompt(gpu, rows):
-    """Both sides of the size from which a second kernel fills the rows."""
+def test_one_prompt(gpu, rows, in_place):
+    """Both sides of the size up to which one block fills the rows."""
     x = Both(1, 1000, 1100, 16)
-    x.step([4000], rows)
-    x.step([-1], rows)
-    x.step([96], rows)
+    x.step([4000], rows, in_place=in_place)
+    x.step([-1], rows, in_place=in_place)
+    x.step([96], rows, in_place=in_place)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 20)])
+@pytest.mark.parametrize("B", [3, 900, 1024, 1025])
+def test_many_rows_with_new_outputs(gpu, B, window, sinks):
+    """Every block makes the sums for itself, up to 1024 sequences; lengths, kept
+    pages and the pool's state go to tensors of their own."""
+    rng = random.Random(B)
+    n = 9000 // B + 30
+    width = -(-4 * n // 16) + 1
+    x = Both(B, width, B * width, 16, window, sinks)
+    for last in range(3):
+        new = [rng.choice([n, n // 2, 0, 3, -1 if last else 1]) for _ in range(B)]
+        x.step(new, max(5000, sum(max(v, 0) for v in new) + 7), in_place=False, own_state=True)
 
 
 def test_empty_sequences_about_few_rows(gpu):
