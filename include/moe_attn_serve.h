@@ -43,6 +43,10 @@ size_t moe_page_plan_workspace_size(int B);
  * such a window may use that row from then on.  window 0: kept and kept_out are
  * not used.
  *
+ * dropped (NULL: none) says how many tokens sequence b has lost since its last
+ * step, rejected drafts: its table holds pages for seq_lens[b] + dropped[b].  New
+ * tokens use those first; what the new length does not need goes back.
+ *
  * Outputs (each input array that has an output may be that output):
  *  state_out [2];  seq_lens_out [B] (0 for a finished one);  kept_out [B];
  *  cu_q [B+1]: first row of each sequence's new tokens;
@@ -62,8 +66,8 @@ size_t moe_page_plan_workspace_size(int B);
  */
 moe_status_t moe_page_plan(int32_t *ring, int ring_size, const int32_t *state, int32_t *state_out,
                            int32_t *page_table, int table_stride, int page_size,
-                           const int32_t *seq_lens, const int32_t *new_lens, const int32_t *kept,
-                           const int32_t *offsets, int window, int sinks, int B, int rows,
+                           const int32_t *seq_lens, const int32_t *new_lens,
+                           const int32_t *dropped, const int32_t *kept, const int32_t *offsets, int window, int sinks, int B, int rows,
                            int32_t *seq_lens_out, int32_t *kept_out, int32_t *cu_q, int32_t *cu_k,
                            int32_t *positions, int32_t *slots, void *workspace, size_t ws_bytes,
                            moe_stream_t stream);

@@ -89,7 +89,7 @@ def _serve_signatures():
     cache = ctypes.POINTER(moe_kv_cache_t)
     return {
         "moe_page_plan_workspace_size": (sz, [i]),
-        "moe_page_plan": (i, [p, i, p, p, p, i, i, p, p, p, p, i, i, i, i, p, p, p, p, p, p, p, sz, p]),
+        "moe_page_plan": (i, [p, i, p, p, p, i, i, p, p, p, p, p, i, i, i, i, p, p, p, p, p, p, p, sz, p]),
         "moe_attn_decode_window": (i, [p, n, cache, p, i, p, i, i, f, p, n, p, i, i, p, sz, p]),
         "moe_attn_prefill_window": (i, [p, n, p, n, p, n, p, p, i, i, i, i, i, i, i, i, f, p, n, p, p,
                                         sz, p]),

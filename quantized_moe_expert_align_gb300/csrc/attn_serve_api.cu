@@ -14,7 +14,7 @@ size_t moe_page_plan_workspace_size(int B) { return B < 0 || B > 65535 ? 0 : pag
 
 moe_status_t moe_page_plan(int32_t *ring, int ring_size, const int32_t *state, int32_t *state_out,
                            int32_t *page_table, int table_stride, int page_size,
-                           const int32_t *seq_lens, const int32_t *new_lens, const int32_t *kept,
+                           const int32_t *seq_lens, const int32_t *new_lens, const int32_t *dropped, const int32_t *kept,
                            const int32_t *offsets, int window, int sinks, int B, int rows,
                            int32_t *seq_lens_out, int32_t *kept_out, int32_t *cu_q, int32_t *cu_k,
                            int32_t *positions, int32_t *slots, void *workspace, size_t ws_bytes,
@@ -26,8 +26,8 @@ moe_status_t moe_page_plan(int32_t *ring, int ring_size, const int32_t *state, i
         (rows > 0 && (!positions || !slots)) || (B > 0 && (!page_table || !seq_lens || !new_lens || !seq_lens_out)) ||
         (B > 0 && window > 0 && (!kept || !kept_out)))
         return MOE_ERR_INVALID_ARG;
-    const void *words[] = {ring,    state,  state_out, page_table, seq_lens,  new_lens, kept,
-                           offsets, cu_q,   cu_k,      seq_lens_out, kept_out, positions, slots};
+    const void *words[] = {ring,    state,  state_out, page_table, seq_lens,  new_lens, dropped,
+                           kept,    offsets, cu_q,     cu_k,       seq_lens_out, kept_out, positions, slots};
     for (const void *p : words)
         if (!aligned(p, 4)) return MOE_ERR_MISALIGNED;
     if (!aligned(workspace, 256)) return MOE_ERR_MISALIGNED;
@@ -35,7 +35,7 @@ moe_status_t moe_page_plan(int32_t *ring, int ring_size, const int32_t *state, i
     const moe_status_t st = check_device();
     if (st != MOE_OK) return st;
     const PagePlanArgs a = {ring,     ring_size, state,  state_out, page_table, table_stride, log2_of(page_size),
-                            seq_lens, new_lens,  kept,   offsets,   window,     sinks,        B,
+                            seq_lens, new_lens,  dropped, kept,     offsets,    window,       sinks, B,
                             rows,     seq_lens_out, kept_out, cu_q, cu_k,       positions,    slots,
                             static_cast<uint8_t *>(workspace)};
     return launched(launch_page_plan(a, stream_of(stream)));

@@ -1,8 +1,9 @@
 // page_plan.cu -- page tables, slots and positions of one step from the
 // requests' lengths, and the pages that go back.
 //
-// A sequence of L0 cached tokens that gets n more needs pages p0 = ceil(L0 / P)
-// to p1 = ceil((L0 + n) / P) - 1; which free pages these are, and where its rows,
+// A sequence of L0 cached tokens whose pages are there for d more (dropped ones)
+// and that gets n new ones needs pages ceil((L0 + d) / P) to ceil((L0 + n) / P) - 1,
+// or has some to give back; which free pages these are, and where its rows,
 // and the pages that it gives back, stand among everybody's, are prefix sums over
 // the sequences.  Free pages are a ring: taken from its head, given back behind
 // its tail, so that no place that is read is written by the same call.  All the
@@ -35,10 +36,12 @@ enum Mode { kOwnBlock, kEveryBlock, kTwoKernels };
 
 // What the rest of the step needs to know of a sequence.
 struct __align__(16) Rec {
-    int32_t len, grow;    // cached tokens before, new tokens
+    int32_t len, grow;    // cached tokens before, new tokens (-1: it has finished)
     int32_t row, take;    // first row; pages taken by the sequences before
-    int32_t give;         // pages given back by the sequences before
-    int32_t end0, lo, hi; // pages [0, end0) and [lo, hi) go back
+    int32_t give, held;   // pages given back by the sequences before; pages in its table
+    // Pages that go back: finished, [0, end) and [from, held); else [from, end), which
+    // are behind the window, and those past the new length.
+    int32_t from, end;
 };
 struct PlanState {
     int32_t ok, head, count, rows;
@@ -103,24 +106,23 @@ __device__ __forceinline__ void block_scan(const Sums &mine, int used, Sums &bef
 __device__ __forceinline__ void move_pages(const PagePlanArgs &a, int b, const Rec &r, const PlanState &st, int first,
                                            int step) {
     int32_t *row = a.table + (size_t)b * a.table_stride;
-    const int p0 = pages_for(r.len, a.page_shift);
-    const int need = r.grow ? pages_for(r.len + r.grow, a.page_shift) - p0 : 0;
+    const int p1 = r.grow >= 0 ? pages_for(r.len + r.grow, a.page_shift) : 0;
 #pragma unroll 4
-    for (int i = first; i < need; i += step) row[p0 + i] = a.ring[ring_at((int64_t)st.head + r.take + i, a.cap)];
-    const int back = r.end0 + r.hi - r.lo;
+    for (int i = first; i < p1 - r.held; i += step)
+        row[r.held + i] = a.ring[ring_at((int64_t)st.head + r.take + i, a.cap)];
+    const int a0 = r.grow < 0 ? 0 : r.from, an = r.end - a0, b0 = r.grow < 0 ? r.from : min(p1, r.held);
 #pragma unroll 4
-    for (int i = first; i < back; i += step)
-        a.ring[ring_at((int64_t)st.head + st.count + r.give + i, a.cap)] =
-            row[i < r.end0 ? i : r.lo + i - r.end0];
+    for (int i = first; i < an + r.held - b0; i += step)
+        a.ring[ring_at((int64_t)st.head + st.count + r.give + i, a.cap)] = row[i < an ? a0 + i : b0 + i - an];
 }
 
 // Position and slot of row t, of sequence b.
 __device__ __forceinline__ int2 look_up(const PagePlanArgs &a, const Rec &r, const PlanState &st, int b, int t) {
     int pos = 0, slot = -1;
     if (t < st.rows) {
-        const int j = r.len + t - r.row, p = j >> a.page_shift, p0 = pages_for(r.len, a.page_shift);
-        const int pg = p < p0 ? a.table[(size_t)b * a.table_stride + p]
-                              : a.ring[ring_at((int64_t)st.head + r.take + p - p0, a.cap)];
+        const int j = r.len + t - r.row, p = j >> a.page_shift;
+        const int pg = p < r.held ? a.table[(size_t)b * a.table_stride + p]
+                              : a.ring[ring_at((int64_t)st.head + r.take + p - r.held, a.cap)];
         slot = (int)(((uint32_t)pg << a.page_shift) + (j & ((1 << a.page_shift) - 1)));
         if (pg < 0) slot = -1;
         pos = a.offsets ? (int)((uint32_t)r.len + (uint32_t)a.offsets[t]) : j;
@@ -167,7 +169,7 @@ __device__ __forceinline__ void put_rows(const PagePlanArgs &a, const Rec *recs,
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         const int t = min(t0 + 32 * i + lane, a.rows - 1);
-        const bool later = t < st.rows && t >= r0.row + r0.grow;  // a later sequence's
+        const bool later = t < st.rows && t >= r0.row + max(r0.grow, 0);  // a later sequence's
         const int b = later ? find_from(cu, a.B, b0, t) : b0;
         v[i] = look_up(a, later ? recs[b] : r0, st, b, t);
     }
@@ -221,27 +223,30 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step(const PagePlanArgs a, 
             len = a.seq_lens[b];
             n = a.new_lens[b];
             kept = a.window ? a.kept[b] : 0;
-            const int held = pages_for(max(len, 0), a.page_shift);
-            bad = len < 0 || len > room || n < -1 || (int64_t)len + max(n, 0) > room || kept < 0 || kept > held;
+            const int dropped = a.dropped ? a.dropped[b] : 0;
+            bad = len < 0 || len > room || dropped < 0 || (int64_t)len + dropped > room || n < -1 ||
+                  (int64_t)len + max(n, 0) > room;
+            const int held = bad ? 0 : pages_for(len + dropped, a.page_shift);
+            bad = bad || kept < 0 || kept > held;
             if (!bad) {
                 r.len = len;
-                r.grow = max(n, 0);
-                const int lo = max(kept, first);
-                int behind = kept;  // pages behind the window, none of which a later token sees
-                if (a.window) behind = max(kept, (int)(max((int64_t)len + 1 - a.window, (int64_t)0) >> a.page_shift));
+                r.grow = n;
+                r.held = held;
+                const int p1 = pages_for(len + max(n, 0), a.page_shift);
                 if (n < 0) {
-                    r.end0 = a.window ? min(first, held) : held;
-                    r.lo = a.window ? lo : held;
-                    r.hi = max(r.lo, held);
+                    r.end = a.window ? min(first, held) : held;
+                    r.from = a.window ? max(max(kept, first), r.end) : held;
+                    if (r.from > held) r.from = held;
                 } else if (a.window) {
-                    r.lo = lo;
-                    r.hi = max(lo, behind);
+                    // behind the window: none of these does a later token see
+                    const int behind = (int)(max((int64_t)len + 1 - a.window, (int64_t)0) >> a.page_shift);
+                    r.from = max(kept, first);
+                    r.end = max(r.from, behind);
                 }
-                mine.v[0] = r.grow;
-                mine.v[1] = pages_for(len + r.grow, a.page_shift) - held;
-                if (n < 0) mine.v[1] = 0;
-                mine.v[2] = r.end0 + r.hi - r.lo;
-                mine.v[3] = n < 0 ? 0 : len + r.grow;
+                mine.v[0] = max(n, 0);
+                mine.v[1] = n < 0 ? 0 : max(p1 - held, 0);
+                mine.v[2] = n < 0 ? r.end + held - r.from : r.end - r.from + max(held - p1, 0);
+                mine.v[3] = n < 0 ? 0 : len + n;
             }
         }
         Sums before, all;
@@ -305,7 +310,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step(const PagePlanArgs a, 
         for (int b0 = warp * 32; b0 < a.B; b0 += kPlanThreads) {
             Rec r = {0, 0, 0, 0, 0, 0, 0, 0};
             if (b0 + lane < a.B) r = recs[b0 + lane];
-            const int most = max(r.grow >> a.page_shift, r.end0 + r.hi - r.lo);
+            const int most = r.grow < 0 ? r.end + r.held - r.from
+                                        : max(r.grow >> a.page_shift, r.held - (r.len >> a.page_shift) + r.end - r.from);
             const uint32_t big = __ballot_sync(0xffffffffu, most > 2);
             if (b0 + lane < a.B && most <= 2) move_pages(a, b0 + lane, r, st, 0, 1);
             for (uint32_t m = big; m; m &= m - 1) {

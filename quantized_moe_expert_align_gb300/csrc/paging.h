@@ -13,7 +13,7 @@ struct PagePlanArgs {
     int32_t *state_out;
     int32_t *table;
     int table_stride, page_shift;
-    const int32_t *seq_lens, *new_lens, *kept, *offsets;
+    const int32_t *seq_lens, *new_lens, *dropped, *kept, *offsets;
     int window, sinks, B, rows;
     int32_t *seq_lens_out, *kept_out, *cu_q, *cu_k, *positions, *slots;
     uint8_t *workspace;

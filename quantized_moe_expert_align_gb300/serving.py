@@ -95,14 +95,16 @@ class PagePlan:
 
 
 def page_plan(pool, page_table, seq_lens, new_lens, page_size, rows, window=0, sinks=0, kept=None,
-              offsets=None, out=None, workspace=None, stream=None):
+              offsets=None, out=None, workspace=None, stream=None, dropped=None):
     """Pages, slots and positions of one step: sequence b has seq_lens[b]
     cached tokens and gets new_lens[b] more (-1: it has finished; its pages go
     back to the pool).  page_table [B][n] gets the new pages; ``rows`` is the
     number of rows of the step's buffers, at least the new tokens.  With a
     ``window``, pages behind it go back too, ``kept`` [B] saying how far that
     has come (zeros at first).  offsets [rows]: positions are seq_lens[b] +
-    offsets[row] instead of seq_lens[b] + i (depths of drafted tokens).
+    offsets[row] instead of seq_lens[b] + i (depths of drafted tokens).  dropped
+    [B]: tokens that sequence b has lost since its last step (rejected drafts),
+    whose pages are still in its table: they are used first, or go back.
 
     Returns ``out``, a PagePlan (a new one by default); any of its seq_lens and
     kept may be the tensor passed in.  The pool's state moves on in place unless
@@ -119,6 +121,8 @@ def page_plan(pool, page_table, seq_lens, new_lens, page_size, rows, window=0, s
     _i32(new_lens, "new_lens", (B,), dev)
     if offsets is not None:
         _i32(offsets, "offsets", (rows,), dev)
+    if dropped is not None:
+        _i32(dropped, "dropped", (B,), dev)
     if window:
         if kept is None:
             raise ValueError("window: kept [B] is needed")
@@ -140,7 +144,7 @@ def page_plan(pool, page_table, seq_lens, new_lens, page_size, rows, window=0, s
     lens_out, cu_q, cu_k, positions, slots, kept_out, state_out = out._ptrs
     _moe._check((_moe._lib or _moe.load()).moe_page_plan(
         ring, pool._size, state, state_out or state, page_table.data_ptr(), n, page_size, seq_lens.data_ptr(),
-        new_lens.data_ptr(), kept.data_ptr() if w else None, _p(offsets), w, s, B, rows, lens_out, kept_out, cu_q,
+        new_lens.data_ptr(), _p(dropped), kept.data_ptr() if w else None, _p(offsets), w, s, B, rows, lens_out, kept_out, cu_q,
         cu_k, positions, slots, ws._ptr, ws.nbytes, _on(stream, dev)), "moe_page_plan")
     return out
 

@@ -64,7 +64,7 @@ def poison(cache, keep):
         cache.data[free] = float("nan")
 
 
-def plan(ring, state, table, page, lens, new, kept, offsets, window, sinks, rows):
+def plan(ring, state, table, page, lens, new, kept, offsets, window, sinks, rows, dropped=None):
     """One step on the host (lists; ring and table change): state, lens, kept,
     cu_q, cu_k, positions, slots, or None if the step cannot be made."""
     cap, (head, count) = len(ring), state
@@ -72,7 +72,7 @@ def plan(ring, state, table, page, lens, new, kept, offsets, window, sinks, rows
     lens2, kept2, cu, pos, slots, taken, back = [], [], [0], [], [], 0, []
     entries = {}
     for b, (n0, n) in enumerate(zip(lens, new)):
-        held = -(-n0 // page)
+        held = -(-(n0 + (dropped[b] if dropped else 0)) // page)
         if n < 0:
             back += [table[b][p] for p in range(held) if not window or p < first or p >= kept[b]]
             lens2.append(0)
@@ -83,6 +83,7 @@ def plan(ring, state, table, page, lens, new, kept, offsets, window, sinks, rows
         if window:
             back += [table[b][p] for p in range(max(first, kept[b]), behind)]
         kept2.append(max(kept[b], behind) if window else 0)
+        back += [table[b][p] for p in range(-(-(n0 + n) // page), held)]
         for i in range(n):
             j = n0 + i
             p = j // page

@@ -23,7 +23,8 @@ class Both:
         self.d_table, self.d_lens, self.d_kept = su.i32(self.table), su.i32(self.lens), su.i32(self.kept)
         self.ws = moe.AttnWorkspace("cuda", "pages", B)
 
-    def step(self, new, rows, offsets=None, in_place=True, detail=None, own_state=False):
+    def step(self, new, rows, offsets=None, in_place=True, detail=None, own_state=False,
+             dropped=None):
         import torch
         import quantized_moe_expert_align_gb300 as moe
         own = dict(seq_lens=self.d_lens, kept=self.d_kept if self.window else None) if in_place else {}
@@ -33,10 +34,11 @@ class Both:
         self.ws.buf.random_(0, 255)
         got = moe.page_plan(self.pool, self.d_table, self.d_lens, su.i32(new), self.page, rows,
                             window=self.window, sinks=self.sinks, kept=self.d_kept if self.window else None,
-                            offsets=None if offsets is None else su.i32(offsets), out=out, workspace=self.ws)
+                            offsets=None if offsets is None else su.i32(offsets), out=out, workspace=self.ws,
+                            dropped=None if dropped is None else su.i32(dropped))
         assert got is out
         want = su.plan(self.ring, self.state, self.table, self.page, self.lens, new, self.kept, offsets,
-                       self.window, self.sinks, rows)
+                       self.window, self.sinks, rows, dropped)
         status = au.status(self.ws)
         if want is None:
             assert detail is not None and status == (moe.MOE_ERR_DEVICE_BAD_INDEX, detail)
@@ -172,3 +174,23 @@ def test_pages_given_back_twice(gpu):
     moe.page_plan(pool, su.i32([[0, 1]]), su.i32([20]), su.i32([-1]), 16, 0, workspace=ws)
     assert au.status(ws) == (moe.MOE_ERR_DEVICE_BAD_INDEX, 1)
     assert pool.ring.tolist() == list(range(8)) and pool.state.tolist() == [3, 8]
+
+
+@pytest.mark.parametrize("B,in_place", [(5, True), (40, False), (1100, True)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (60, 4)])
+def test_drafts_that_are_dropped(gpu, B, in_place, window, sinks):
+    """Pages of rejected tokens are used by the next ones, or go back; none is lost."""
+    rng = random.Random(B)
+    width = 30
+    x = Both(B, width, B * width, 16, window, sinks)
+    x.step([rng.choice([1, 15, 16, 100]) for _ in range(B)], 100 * B, in_place=in_place)
+    for _ in range(6):
+        drafts = [rng.choice([1, 16, 40, 64]) for _ in range(B)]
+        x.step(drafts, 64 * B, in_place=in_place)
+        gone = [rng.randrange(n) for n in drafts]
+        x.lens = [a - b for a, b in zip(x.lens, gone)]
+        x.d_lens = su.i32(x.lens)
+        new = [rng.choice([0, 1, 1, 30, -1]) for _ in range(B)]
+        x.step(new, 30 * B, in_place=in_place, dropped=gone)
+    x.step([-1] * B, 0, in_place=in_place)
+    assert x.state[1] == B * width and sorted(x.pool.ring.tolist()) == list(range(B * width))

@@ -52,9 +52,9 @@ def test_workspace_sizes(lib):
 
 
 def test_page_plan_refusals(lib):
-    names = ("ring cap state state_out table tstride page lens new kept offsets window sinks B rows lens_out "
+    names = ("ring cap state state_out table tstride page lens new dropped kept offsets window sinks B rows lens_out "
              "kept_out cu_q cu_k pos slots ws wsb stream")
-    good = [P, 100, P, P, P, 8, 16, P, P, P, P, 100, 4, 2, 10, P, P, P, P, P, P, P, 1 << 20, None]
+    good = [P, 100, P, P, P, 8, 16, P, P, None, P, P, 100, 4, 2, 10, P, P, P, P, P, P, P, 1 << 20, None]
     _refuses(lib.moe_page_plan, names, good, [
         (dict(ring=None), INV), (dict(cap=0), INV), (dict(cap=1 << 30), INV), (dict(state=None), INV),
         (dict(state_out=None), INV), (dict(table=None), INV), (dict(tstride=0), INV), (dict(page=24), INV),
@@ -62,7 +62,7 @@ def test_page_plan_refusals(lib):
         (dict(kept_out=None), INV), (dict(window=-1), INV), (dict(sinks=-1), INV), (dict(B=-1), INV),
         (dict(B=65536), INV), (dict(rows=-1), INV), (dict(rows=(1 << 31) - 1), INV), (dict(lens_out=None), INV),
         (dict(cu_q=None), INV), (dict(pos=None), INV), (dict(slots=None), INV), (dict(ws=None), INV),
-        (dict(ring=P + 2), MIS), (dict(offsets=P + 1), MIS), (dict(slots=P + 2), MIS), (dict(ws=P + 128), MIS),
+        (dict(ring=P + 2), MIS), (dict(offsets=P + 1), MIS), (dict(dropped=P + 3), MIS), (dict(slots=P + 2), MIS), (dict(ws=P + 128), MIS),
         (dict(wsb=256), SMALL)])
 
 
