@@ -118,9 +118,13 @@ size_t moe_attn_tree_workspace_size(int B, int T, int Hq, int Hkv, int D);
  * Rows of out and lse that belong to no sequence are not written.  What the
  * pages hold from seq_lens[b] on is never used.  An infinity or NaN in the v of
  * a drafted token may reach all rows of its tree.
- * Results do not depend on timing.  Rounding as in moe_attn_decode, but that
- * weights may be rounded to one bf16 over a bf16 cache too (2^-8 sum_j p_j
- * |v_j|).
+ * Results do not depend on timing.  Rounding: sums are in fp32 and the result is
+ * rounded once to bf16; beside that weights may be rounded to one bf16, which moves
+ * a result by at most 2^-8 sum_j p_j |v_j|, as in moe_attn_decode over fp8.  Over an
+ * fp8 cache values of q below 2^-9 of their head's largest may be off by up to 2^-17
+ * of it, and values of v by up to 2^-24 of the sequence's largest scale of v,
+ * rounded up to a power of two, and 2^-9 of themselves (the weights then are fp16:
+ * the bound above holds for both together).
  * Limits: 0 <= B <= 65535, Hq <= 1024, 0 <= T, T * Hq < 2^31, scale > 0.
  * A page number out of range, a length that is negative or beyond the table (or
  * 2^30), a cu_q that decreases or leaves [0, T], more than 64 rows, or more than
