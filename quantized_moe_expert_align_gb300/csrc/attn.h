@@ -25,18 +25,6 @@ struct SmemOnce {
         if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
         return err;
     }
-    // A kernel without shared memory to speak of that runs beside one that uses
-    // all of it: the SMs need not divide their memory anew in between.
-    cudaError_t set_carveout(const void *fn) {
-        int dev = 0;
-        cudaError_t err = cudaGetDevice(&dev);
-        if (err != cudaSuccess) return err;
-        const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-        if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-        err = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-        if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-        return err;
-    }
 };
 
 // MOE_OK if the current device is an sm_103 GPU (api.cu).

