@@ -10,9 +10,10 @@
 // warp issuing each one's products, one thread a softmax row with a reference
 // that is raised when the maximum exceeds it by 2^8.
 //  * 129 to 256 rows: the two row tiles share every key tile ("shared").
-//  * Up to 128 rows: both have the same rows, and take the key tiles in turns, so
-//    that one's softmax runs under the other's products all the same; their sums
-//    are joined in tensor memory, whose lanes are the rows of both.
+//  * Up to 128 rows: both warpgroups have the same rows, each half of a key tile's
+//    keys (a maximum of both is exchanged, the reference is one); the scores of the
+//    next key tile are made under the softmax of this one, in the tensor memory that
+//    the second row tile has no use for.
 //  * More rows: blocks of 256, which read the keys again, mostly from L2.
 // The key tiles of the whole batch, in order, are shared out evenly over one block
 // per SM; a range cut by a block's end is joined by a second kernel, in key order.
@@ -76,8 +77,8 @@ struct Cfg {
     static constexpr size_t kRawAt = kKAt + (FP8 ? (size_t)kKs * kKB : 0);
     static constexpr size_t kSharedAt = kRawAt + (FP8 ? (size_t)kRaw * kKB : 0);
     // fp8: of kScaleBufs key tiles the scales of K and of V, [2][kKeys]
-    static constexpr size_t kScalesAt = kSharedAt + 2048;
-    static constexpr size_t kSmem = kScalesAt + (FP8 ? kScaleBufs * 2 * kKeys * 4 : 0) + 1024;
+    static constexpr size_t kScalesAt = kSharedAt + 3072;
+    static constexpr size_t kSmem = kScalesAt + (FP8 ? kScaleBufs * 2 * kKeys * 4 : 0);
     static_assert(kSmem > 114 * 1024 && kSmem <= 227 * 1024, "one block per SM: all of tensor memory is its own");
 };
 
@@ -122,20 +123,21 @@ __host__ __device__ inline int tile_tokens(int G) { return kTile / tile_heads(G)
 
 struct Shared {
     uint64_t q_full[kM], q_ready[kM], q_empty[kM], op_full[8], op_empty[8], tail[8], raw_full[4], raw_empty[4];
-    uint64_t k_full[4], k_empty[4], sc_full[kScaleBufs], sc_ready[kScaleBufs], sc_empty[kScaleBufs], s_full[kM], p_ready[kM][kParts], o_done[kM], merge[3], offset;
+    uint64_t k_full[4], k_empty[4], sc_full[kScaleBufs], sc_ready[kScaleBufs], sc_empty[kScaleBufs], s_full[kM], p_ready[kM][kParts], o_done[kM], offset;
+    // (a key tile in turn; items by number)
+    uint64_t s_split[2], p_split[2], o_split[2], exchange, item_done[kM][4];
     uint64_t item_full[2], item_empty[2], finished;
     uint32_t tmem;
     int abort, bad;
-    int expo[kScaleBufs], expo1;  // exponents of the largest scale so far: per key tile, row tile 1's last
+    int expo[kScaleBufs];   // exponents of the largest scale so far, per key tile
     int b0;                 // the sequence of this block's first key tile
     int64_t first;          // and that tile's index among the sequence's
     int64_t warp_sum[16];
     Item item[2];
-    // rows whose two sums are joined: the second one's reference and sum, then the
-    // two factors
-    float2 pair[kTile];
+    // up to 128 rows: the maxima of a key tile's halves, then the sums of the weights
+    float halves[2][2][kTile];
 };
-static_assert(sizeof(Shared) <= 2048, "shared block");
+static_assert(sizeof(Shared) <= 3072, "shared block");
 
 // What a sequence has to do.
 struct Seq {
@@ -200,9 +202,9 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
     using C = Cfg<D, FP8>;
     constexpr int S = C::kOps, kHalves = D / 64, kThreads = C::kThreads;
     constexpr uint32_t kQHalf = kTile * 128, kKvHalf = kKeys * 128;  // 64 columns of a tile
-    extern __shared__ uint8_t raw[];
-    const uint32_t raw_u = smem_u32(raw);
-    uint8_t *base = raw + ((1024 - (raw_u & 1023)) & 1023);
+    // (aligned for the swizzle; there is no room to align it by hand)
+    extern __shared__ __align__(1024) uint8_t raw[];
+    uint8_t *const base = raw;
     uint8_t *op_base = base + C::kOpAt, *k_base = base + C::kKAt, *raw_base = base + C::kRawAt;
     Shared *sm = reinterpret_cast<Shared *>(base + C::kSharedAt);
     float *scales = reinterpret_cast<float *>(base + C::kScalesAt);
@@ -221,7 +223,10 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
             mbar_init(&sm->s_full[t], 1);
             for (int h = 0; h < kParts; ++h) mbar_init(&sm->p_ready[t][h], 4);
             mbar_init(&sm->o_done[t], 1);
-            mbar_init(&sm->merge[t], 4);
+            mbar_init(&sm->s_split[t], 1);
+            mbar_init(&sm->p_split[t], 8);
+            mbar_init(&sm->o_split[t], 1);
+            for (int i = 0; i < 4; ++i) mbar_init(&sm->item_done[t][i], 1);
             mbar_init(&sm->item_full[t], 1);
             mbar_init(&sm->item_empty[t], FP8 ? 15 : 11);  // the warps that take items
         }
@@ -243,7 +248,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
             mbar_init(&sm->sc_ready[i], 4);
             mbar_init(&sm->sc_empty[i], 8);
         }
-        mbar_init(&sm->merge[2], 8);
+        mbar_init(&sm->exchange, 8);
         mbar_init(&sm->offset, 4);
         mbar_init(&sm->finished, kM);
         fence_barrier_init();
@@ -295,8 +300,9 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
         sm->b0 = b;
         sm->first = u0 - at;
     }
-    // (its address is 0; anything else is reported like a wait that gave up)
-    if (tid == 0 && sm->tmem != 0) sm->abort = 20;
+    // (its address is 0; anything else is reported like a wait that gave up, and so
+    // is shared memory that does not start where it should)
+    if (tid == 0 && (sm->tmem != 0 || (q_smem & 1023))) sm->abort = 20;
     __syncthreads();
     constexpr uint32_t s_col = 0, o_col = kM * kKeys;
     static_assert(kM * (kKeys + D) <= 512, "tensor memory");
@@ -309,9 +315,6 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
         return it.done == 0;
     };
     auto run_apart = [&](const Item &it) { return it.shared && it.tiles >= kApart; };
-    // the item's key tiles that row tile t has
-    auto tiles_of = [&](const Item &it, int t) { return it.shared ? it.tiles : (it.tiles + 1 - t) / 2; };
-
     const int page_shift = a.kv.page_shift, page_mask = (1 << page_shift) - 1;
     const int box_shift = min(page_shift, 7), R = 1 << box_shift;  // rows of one copy
     const int chunks = kKeys >> box_shift;
@@ -483,8 +486,10 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 constexpr uint32_t kIdO = FP8 ? idesc_f16_m128(D) | 1u << 16 : idesc_bf16(D, true);
                 const uint64_t c_desc = D == 128 ? sdesc_k_sw128(smem_u32(k_base)) : sdesc_k_sw64(smem_u32(k_base));
                 constexpr uint32_t s_t = s_col + t * kKeys, o_t = o_col + t * D;
-                uint32_t off_ph = 0, p_ph = 0;
-                uint32_t tile0 = 0;  // key tiles of the items before
+                uint32_t off_ph = 0;
+                uint32_t tile0 = 0, shared0 = 0;  // key tiles of the items before, and of those shared
+                uint32_t split_ph = 0;            // parities of p_split
+                bool before_shared = false;       // the item before
                 Item it;
                 bool ok = true;
                 // Waits for K (part 0) or V (1) of key tile number i: its stage, which
@@ -504,90 +509,110 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                     tc_fence_after();
                     return s;
                 };
-                // A key tile of the other row tile's: done with.
-                auto pass = [&](uint32_t i) {
-                    for (int part = 0; part < 2; ++part) {
-                        uint64_t *free;
-                        wait_tile(i, part, free);
-                        if (ok && lane == 0) mbar_arrive(free);
+                // Scores of key tile i of all into tensor memory from `to` on.
+                auto scores = [&](uint32_t i, uint32_t to, uint64_t *full, bool last) {
+                    uint64_t *k_free;
+                    const uint32_t k = wait_tile(i, 0, k_free);
+                    if (!ok) return;
+                    if (elect_one()) {
+                        if (FP8) {
+                            // both terms of Q: tiles of their own, or (heads of 64) the
+                            // two halves of a row
+                            const uint64_t kd = c_desc + ((k * C::kKB) >> 4);
+#pragma unroll
+                            for (int x = 0; x < 2 * (D / 32); ++x) {
+                                const uint32_t term = x / (D / 32), in = x % (D / 32) * 32;
+                                mma_e4m3_ss(to, qd + ((term * (D == 128 ? kQHalf : 64u) + in) >> 4), kd + (in >> 4), kIdS,
+                                            x > 0);
+                            }
+                        } else {
+                            const uint64_t kd = k_desc + ((k * C::kKvB) >> 4);
+#pragma unroll
+                            for (int x = 0; x < D / 16; ++x) {
+                                const uint32_t in = (x & 3) * 32;
+                                mma_bf16_ss(to, qd + (((x >> 2) * kQHalf + in) >> 4),
+                                            kd + (((x >> 2) * kKvHalf + in) >> 4), kIdS, x > 0);
+                            }
+                        }
+                        tc_commit(full);
+                        tc_commit(k_free);
+                        if (last) tc_commit(&sm->q_empty[t]);
+                    }
+                    __syncwarp();
+                };
+                // Steps [i0, i1) of 16 keys of O_t += P V, P from `from` on; the last
+                // ones of a key tile: its values are done with.
+                constexpr int kSteps = kKeys / 16;
+                auto product = [&](uint32_t v, uint32_t from, int i0, int i1, bool first, uint64_t *done, uint64_t *v_free) {
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t vd = v_desc + ((v * C::kKvB) >> 4);
+#pragma unroll
+                        for (int i = 0; i < kSteps; ++i)
+                            if (i >= i0 && i < i1)
+                                mma_f16_ts(o_t, from + i * 8, vd + ((i * 2048) >> 4), kIdO, i > 0 ? 1u : (first ? 0u : 1u));
+                        if (i1 == kSteps) {
+                            tc_commit(done);
+                            tc_commit(v_free);
+                        }
                     }
                     __syncwarp();
                 };
                 for (uint32_t n = 0; ok && take(n, it); ++n) {
                     const int tiles = __shfl_sync(0xffffffffu, it.tiles, 0);
-                    const int mine = __shfl_sync(0xffffffffu, tiles_of(it, t), 0);
                     const bool both = __shfl_sync(0xffffffffu, it.shared, 0) != 0;
-                    int done = 0;  // own tiles whose scores were issued
+                    ok = warp_wait_flag(FP8 ? &sm->q_ready[t] : &sm->q_full[t], n & 1, &sm->abort, 6);
+                    // The second row tile's tensor memory changes hands: its last products
+                    // are over (items by number: one role may be two ahead of the other).
+                    if (n > 0 && both != before_shared)
+                        ok = ok && warp_wait_flag(&sm->item_done[1 - t][(n - 1) & 3], ((n - 1) >> 2) & 1, &sm->abort, 22);
+                    before_shared = both;
                     // Shared: the second row tile starts when the first one's maxima
                     // are known, which puts the two half a round apart; in step both
                     // would want the tensor pipe, then the exponentials, together.
-                    const bool apart = __shfl_sync(0xffffffffu, (int)run_apart(it), 0) != 0;
-                    ok = warp_wait_flag(FP8 ? &sm->q_ready[t] : &sm->q_full[t], n & 1, &sm->abort, 6);
-                    if (apart && t == 1) {
+                    if (t == 1 && __shfl_sync(0xffffffffu, (int)run_apart(it), 0)) {
                         ok = ok && warp_wait_flag(&sm->offset, off_ph, &sm->abort, 21);
                         off_ph ^= 1;
                     }
                     tc_fence_after();
-                    const int step = both ? 1 : 2;
-                    for (int j = both ? 0 : t; j < tiles && ok; j += step) {
-                        uint64_t *k_free, *v_free;
-                        const uint32_t k = wait_tile(tile0 + j, 0, k_free);
-                        if (!ok) break;
-                        ++done;
-                        if (elect_one()) {
-                            if (FP8) {
-                                // both terms of Q: tiles of their own, or (heads of 64)
-                                // the two halves of a row
-                                const uint64_t kd = c_desc + ((k * C::kKB) >> 4);
+                    if (both) {
+                        for (int j = 0; j < tiles && ok; ++j) {
+                            scores(tile0 + j, s_t, &sm->s_full[t], j + 1 == tiles);
+                            uint64_t *v_free;
+                            const uint32_t v = wait_tile(tile0 + j, 1, v_free);
 #pragma unroll
-                                for (int i = 0; i < 2 * (D / 32); ++i) {
-                                    const uint32_t term = i / (D / 32), in = i % (D / 32) * 32;
-                                    mma_e4m3_ss(s_t, qd + ((term * (D == 128 ? kQHalf : 64u) + in) >> 4),
-                                                kd + (in >> 4), kIdS, i > 0);
-                                }
-                            } else {
-                                const uint64_t kd = k_desc + ((k * C::kKvB) >> 4);
-#pragma unroll
-                                for (int i = 0; i < D / 16; ++i) {
-                                    const uint32_t in = (i & 3) * 32;
-                                    mma_bf16_ss(s_t, qd + (((i >> 2) * kQHalf + in) >> 4),
-                                                kd + (((i >> 2) * kKvHalf + in) >> 4), kIdS, i > 0);
-                                }
+                            for (int h = 0; h < kParts; ++h) {
+                                ok = ok && warp_wait_flag(&sm->p_ready[t][h], (shared0 + j) & 1, &sm->abort, 7);
+                                if (!ok) break;
+                                product(v, s_t, h * (kSteps / kParts), (h + 1) * (kSteps / kParts), j == 0,
+                                        &sm->o_done[t], v_free);
                             }
-                            tc_commit(&sm->s_full[t]);
-                            tc_commit(k_free);
-                            if (done == mine) tc_commit(&sm->q_empty[t]);
                         }
-                        __syncwarp();
-                        // (the other row tile's key tile before this one: no sooner, the
-                        // softmax waits for these products)
-                        if (!both && j > 0) pass(tile0 + j - 1);
-                        const uint32_t v = wait_tile(tile0 + j, 1, v_free);
-                        if (!ok) break;
-                        const uint64_t vd = v_desc + ((v * C::kKvB) >> 4);
-                        constexpr int kSteps = kKeys / 16 / kParts;
-#pragma unroll
-                        for (int h = 0; h < kParts; ++h) {
-                            ok = ok && warp_wait_flag(&sm->p_ready[t][h], p_ph, &sm->abort, 7);
+                        shared0 += tiles;
+                    } else if (t == 0) {
+                        scores(tile0, s_col, &sm->s_split[0], tiles == 1);
+                        for (int j = 0; j < tiles && ok; ++j) {
+                            // (the last product with this memory's weights came before)
+                            if (j + 1 < tiles)
+                                scores(tile0 + j + 1, s_col + ((j + 1) & 1) * kKeys, &sm->s_split[(j + 1) & 1], j + 2 == tiles);
+                            uint64_t *v_free;
+                            const uint32_t v = wait_tile(tile0 + j, 1, v_free);
+                            ok = ok && warp_wait_flag(&sm->p_split[j & 1], split_ph >> (j & 1) & 1, &sm->abort, 7);
                             if (!ok) break;
-                            tc_fence_after();
-                            if (elect_one()) {
-#pragma unroll
-                                for (int i = h * kSteps; i < (h + 1) * kSteps; ++i)
-                                    mma_f16_ts(o_t, s_t + i * 8, vd + ((i * 2048) >> 4), kIdO,
-                                               i > 0 ? 1u : (done == 1 ? 0u : 1u));
-                                if (h == kParts - 1) {
-                                    tc_commit(&sm->o_done[t]);
-                                    tc_commit(v_free);
-                                }
-                            }
-                            __syncwarp();
+                            split_ph ^= 1u << (j & 1);
+                            product(v, s_col + (j & 1) * kKeys, 0, kSteps, j == 0, &sm->o_split[j & 1], v_free);
                         }
-                        p_ph ^= 1;
+                    } else {
+                        for (int j = 0; j < tiles && ok; ++j)  // (the first row tile's: done with)
+                            for (int part = 0; part < 2; ++part) {
+                                uint64_t *free;
+                                wait_tile(tile0 + j, part, free);
+                                if (ok && lane == 0) mbar_arrive(free);
+                            }
+                        if (ok && lane == 0) mbar_arrive(&sm->q_empty[t]);  // (not used)
                     }
-                    // the last tile, if it is the other's
-                    if (ok && !both && (tiles - 1) % 2 != t) pass(tile0 + tiles - 1);
-                    if (ok && mine == 0 && lane == 0) mbar_arrive(&sm->q_empty[t]);  // (not used)
+                    __syncwarp();
+                    if (elect_one()) tc_commit(&sm->item_done[t][n & 3]);
                     __syncwarp();
                     tile0 += tiles;
                 }
@@ -735,9 +760,16 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
         const uint32_t lane_base = (uint32_t)(warp & 3) * 32 << 16;
         const uint32_t s_t = s_col + t * kKeys + lane_base, o_t = o_col + t * D + lane_base;
         const int tok_r = r / Gt, gr = r % Gt;
-        uint32_t ph = 0;        // parity of this warpgroup's count of key tiles
-        uint32_t tile0 = 0;     // key tiles of the items before
-        uint32_t merges = 0;    // parity of the count of joined items
+        uint32_t tile0 = 0, shared0 = 0;  // key tiles of the items before, and of those shared
+        uint32_t split_ph = 0, ex_ph = 0; // parities: a bit a half of S; the exchange
+        // All 8 warps have come here.
+        auto exchange = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm->exchange);
+            const bool done = warp_wait_flag(&sm->exchange, ex_ph, &sm->abort, 12);
+            ex_ph ^= 1;
+            return done;
+        };
         Item it;
         bool ok = true;
         for (uint32_t n = 0; ok && take(n, it); ++n) {
@@ -800,40 +832,53 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
             }
             float ref = -INFINITY;  // the row's reference, in log2 units
             float l = 0.f;
-            int done = 0, expo = 0;  // expo: of the scales that O_t's sums were made with
-            for (int j = it.shared ? 0 : t; j < it.tiles; j += it.shared ? 1 : 2, ++done) {
+            int expo = 0;  // of the scales that O's sums were made with
+            // Products with key tile j, whose scores have been here and no later ones'
+            // weights.  (Up to 128 rows weights can be there two products ahead, hence
+            // barriers for every other key tile; all three have the same counts.)
+            auto wait_products = [&](int j) {
+                if (it.shared) return warp_wait_flag(&sm->o_done[t], (shared0 + j) & 1, &sm->abort, 10);
+                return warp_wait_flag(&sm->o_split[j & 1], ~(split_ph >> (j & 1)) & 1, &sm->abort, 11);
+            };
+            // Key tile j: W of its scores a thread, all, or this warpgroup's half.
+            auto round = [&](auto width, int j) {
+                constexpr int W = decltype(width)::value;
+                constexpr bool kSplit = W < kKeys;
+                const int half = j & 1, col0 = kSplit ? t * W : 0;
+                const uint32_t s_at = kSplit ? s_col + half * kKeys + lane_base + col0 : s_t;
+                const uint32_t p_at = kSplit ? s_col + half * kKeys + lane_base + col0 / 2 : s_t;
                 const uint32_t buf = (tile0 + j) % kScaleBufs;
-                if (FP8) {  // (before the scores are)
-                    ok = warp_wait_flag(&sm->sc_ready[buf], ((tile0 + j) / kScaleBufs) & 1, &sm->abort, 17);
-                    if (!ok) break;
-                }
+                // (before the scores are)
+                if (FP8 && !warp_wait_flag(&sm->sc_ready[buf], ((tile0 + j) / kScaleBufs) & 1, &sm->abort, 17)) return false;
                 const int larger = FP8 ? sm->expo[buf] : 0;  // (the same for all rows)
-                ok = warp_wait_flag(&sm->s_full[t], ph, &sm->abort, 9);
-                if (!ok) break;
-                const float *sc = scales + buf * 2 * kKeys;
-                auto scales_read = [&]() {  // (twice, where the other warpgroup has no part in the tile)
-                    if (FP8 && lane < (it.shared ? 1 : 2)) mbar_arrive(&sm->sc_empty[buf]);
-                };
+                if (kSplit) {
+                    if (!warp_wait_flag(&sm->s_split[half], split_ph >> half & 1, &sm->abort, 9)) return false;
+                    split_ph ^= 1u << half;
+                } else if (!warp_wait_flag(&sm->s_full[t], (shared0 + j) & 1, &sm->abort, 9)) {
+                    return false;
+                }
+                const float *sc = scales + buf * 2 * kKeys + col0;
                 tc_fence_after();
-                if (t == 0 && done == 0 && run_apart(it) && lane == 0 && !any_live) mbar_arrive(&sm->offset);
+                const bool tells = !kSplit && t == 0 && j == 0 && run_apart(it) && lane == 0;
                 if (!any_live) {  // (no row of this warp's is used)
+                    if (tells) mbar_arrive(&sm->offset);
+                    expo = larger;
                     tc_fence_before();
                     __syncwarp();
+                    if (FP8 && lane == 0) mbar_arrive(&sm->sc_empty[buf]);
+                    if (kSplit && !exchange()) return false;
                     if (lane == 0)
-                        for (int h = 0; h < kParts; ++h) mbar_arrive(&sm->p_ready[t][h]);
-                    if (FP8) expo = larger;
-                    __syncwarp();
-                    scales_read();
-                    ph ^= 1;
-                    continue;
+                        for (int h = 0; h < W / (kKeys / kParts); ++h)
+                            mbar_arrive(kSplit ? &sm->p_split[half] : &sm->p_ready[t][h]);
+                    return true;
                 }
-                float x[kKeys];
+                float x[W];
 #pragma unroll
-                for (int c = 0; c < kKeys; c += 32) tmem_ld32(s_t + c, x + c);
+                for (int c = 0; c < W; c += 32) tmem_ld32(s_at + c, x + c);
                 tc_wait_ld();
                 if (FP8) {
 #pragma unroll
-                    for (int c = 0; c < kKeys; c += 4) {
+                    for (int c = 0; c < W; c += 4) {
                         const float4 k = *reinterpret_cast<const float4 *>(sc + c);
                         const float2 lo = mul2(make_float2(x[c], x[c + 1]), make_float2(k.x, k.y));
                         const float2 hi = mul2(make_float2(x[c + 2], x[c + 3]), make_float2(k.z, k.w));
@@ -842,13 +887,13 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                         x[c + 2] = hi.x;
                         x[c + 3] = hi.y;
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm->sc_empty[buf]);
                 }
-                __syncwarp();
-                scales_read();
-                const int key0 = (it.j0 + j) * kKeys;
-                if (key0 + kKeys > ctx) {
+                const int key0 = (it.j0 + j) * kKeys + col0;
+                if (key0 + W > ctx) {
 #pragma unroll
-                    for (int c = 0; c < kKeys; c += 32) {
+                    for (int c = 0; c < W; c += 32) {
                         const int d = key0 + c - ctx;  // the drafted token of column c
                         if (d > -32) {
                             const uint32_t vis = d >= 64  ? 0u
@@ -861,12 +906,22 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 }
                 float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                for (int c = 4; c + 8 <= kKeys; c += 8)
+                for (int c = 4; c + 8 <= W; c += 8)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], x[c + 2 * e], x[c + 2 * e + 1]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], x[kKeys - 4 + e]);
-                const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl;
+                for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], x[W - 4 + e]);
+                float most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                if (kSplit) {
+                    // (both warpgroups have their scores in registers after this, too: the
+                    // weights of one lie where scores of the other were)
+                    sm->halves[half][t][r] = most;
+                    tc_fence_before();
+                    if (!exchange()) return false;
+                    tc_fence_after();
+                    most = fmaxf(most, sm->halves[half][1 - t][r]);
+                }
+                const float top = most * sl;
                 const bool raise = top > ref + kSlack;
                 if (__any_sync(0xffffffffu, raise) || (FP8 && larger != expo)) {
                     const float to = raise ? top : ref;
@@ -877,28 +932,29 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                         f *= pow2(max(expo - larger, -127));
                         expo = larger;
                     }
-                    if (done > 0) {
-                        // the last product into O_t has to be over
-                        ok = warp_wait_flag(&sm->o_done[t], ph ^ 1, &sm->abort, 10);
-                        if (!ok) break;
+                    if (j > 0) {
+                        // the last product into O has to be over; of one O each
+                        // warpgroup has half of the columns
+                        if (!wait_products(j - 1)) return false;
                         tc_fence_after();
+                        const uint32_t o_at = kSplit ? o_col + lane_base + t * (D / 2) : o_t;
 #pragma unroll
-                        for (int c = 0; c < D; c += 16) {
+                        for (int c = 0; c < (kSplit ? D / 2 : D); c += 16) {
                             uint32_t o[16];
-                            tmem_ld16(o_t + c, o);
+                            tmem_ld16(o_at + c, o);
                             tc_wait_ld();
 #pragma unroll
                             for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st16(o_t + c, o);
+                            tmem_st16(o_at + c, o);
                         }
                     }
                 }
-                if (t == 0 && done == 0 && run_apart(it) && lane == 0) mbar_arrive(&sm->offset);
+                if (tells) mbar_arrive(&sm->offset);
                 const float z = (ref == -INFINITY ? 0.f : ref) - (FP8 ? kShift : 0);
                 const float2 sl2 = make_float2(sl, sl), nz2 = make_float2(-z, -z);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int c = 0; c < kKeys; c += 32) {
+                for (int c = 0; c < W; c += 32) {
                     uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
@@ -913,97 +969,55 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                             p[e] = pack_bf16(y.x, y.y);
                         }
                     }
-                    tmem_st16(s_t + c / 2, p);
+                    tmem_st16(p_at + c / 2, p);
                     if ((c + 32) % (kKeys / kParts) == 0) {  // their product may start
                         tc_wait_st();
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&sm->p_ready[t][c / (kKeys / kParts)]);
+                        if (lane == 0) mbar_arrive(kSplit ? &sm->p_split[half] : &sm->p_ready[t][c / (kKeys / kParts)]);
                     }
                 }
                 const float2 both = add2(sum[0], sum[1]);
                 l += both.x + both.y;
-                ph ^= 1;
-            }
-            if (!ok) break;
-            tile0 += it.tiles;
-            // ---- the rows' outputs
-            if (done > 0) {
-                ok = warp_wait_flag(&sm->o_done[t], ph ^ 1, &sm->abort, 11);
-                if (!ok) break;
-            }
-            const bool joined = !it.shared, whole = it.slot < 0;
-            const bool second = joined && it.tiles > 1;  // O_1 has sums too
-            // What the row's sums are multiplied by: 1 over the sum if these are all
-            // keys.  Joined: warpgroup 1 hands over its reference and sum,
-            // warpgroup 0 the two factors.
-            auto arrive = [&](int i) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm->merge[i]);
+                return true;
             };
-            // (fp8: and the powers of two of the weights, in l too, and of the scales)
-            if (FP8) l *= 1.f / (1 << kShift);
-            float top = ref, sum = l, f0 = 1.f, f1 = 0.f;
-            const float own_power = FP8 ? pow2(expo) * (1.f / (1 << kShift)) : 1.f;
-            if (joined && t == 1) {
-                sm->pair[r] = make_float2(ref, l);
-                if (FP8 && r == 0) sm->expo1 = expo;
-                arrive(0);
-                ok = warp_wait_flag(&sm->merge[1], merges, &sm->abort, 12);
+            if (it.shared)
+                for (int j = 0; j < it.tiles && ok; ++j) ok = round(std::integral_constant<int, kKeys>{}, j);
+            else
+                for (int j = 0; j < it.tiles && ok; ++j) ok = round(std::integral_constant<int, kKeys / 2>{}, j);
+            if (!ok) break;
+            // ---- the rows' outputs
+            float sum = l;
+            if (!it.shared) {  // (the half that no reader of the last maxima can be at)
+                sm->halves[it.tiles & 1][t][r] = l;
+                ok = exchange();
                 if (!ok) break;
-                const float2 f = sm->pair[r];
-                f0 = f.x;
-                f1 = f.y;
-            } else {
-                if (joined) {
-                    ok = warp_wait_flag(&sm->merge[0], merges, &sm->abort, 12);
-                    if (!ok) break;
-                    const float2 m1 = sm->pair[r];
-                    top = fmaxf(ref, m1.x);
-                    const float z = top == -INFINITY ? 0.f : top;
-                    f0 = ex2(ref - z);
-                    f1 = ex2(m1.x - z);
-                    // (no tile: reference -inf and sum 0)
-                    sum = f0 * l + f1 * m1.y;
-                }
-                if (whole) {
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                    f0 *= inv;
-                    f1 *= inv;
-                }
-                if (FP8) {
-                    f0 *= own_power;
-                    if (second) f1 *= pow2(sm->expo1) * (1.f / (1 << kShift));
-                }
-                if (joined) {
-                    sm->pair[r] = make_float2(f0, f1);
-                    arrive(1);
-                }
+                sum = sm->halves[it.tiles & 1][0][r] + sm->halves[it.tiles & 1][1][r];
             }
+            ok = wait_products(it.tiles - 1);
+            if (!ok) break;
             tc_fence_after();
-            const bool none = f0 == 0.f && f1 == 0.f;  // (a row that sees nothing)
-            // joined: each warpgroup has half of the columns of both
-            const uint32_t o_0 = it.shared ? o_t : o_col + lane_base, o_1 = o_col + D + lane_base;
+            tile0 += it.tiles;
+            if (it.shared) shared0 += it.tiles;
+            const bool whole = it.slot < 0, none = sum == 0.f;  // (none: a row that sees nothing)
+            // What the row's sums are multiplied by: 1 over the sum if these are all
+            // keys; fp8: and the powers of two of the weights and of the scales.
+            if (FP8) sum *= 1.f / (1 << kShift);
+            float f = whole ? (none ? 0.f : 1.f / sum) : 1.f;
+            if (FP8) f *= pow2(expo) * (1.f / (1 << kShift));
+            // one O: each warpgroup has half of the columns
+            const uint32_t o_at = it.shared ? o_t : o_col + lane_base;
             const int c0 = it.shared ? 0 : t * (D / 2), c1 = it.shared ? D : c0 + D / 2;
             const int row_tile = it.shared ? t : 0;
             uint16_t *to = a.out + (int64_t)(it.q0 + tok) * a.out_stride + (it.h0 + gr) * D;
             if (any_live)
 #pragma unroll 1
                 for (int c = c0; c < c1; c += 32) {
-                    float o[32], y[32];
-                    tmem_ld32(o_0 + c, o);
-                    if (!FP8 && second) tmem_ld32(o_1 + c, y);
+                    float o[32];
+                    tmem_ld32(o_at + c, o);
                     tc_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] *= f0;
-                    if (FP8 && second) {  // (both at once: spills)
-                        tmem_ld32(o_1 + c, y);
-                        tc_wait_ld();
-                    }
-                    if (second)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = fmaf(y[e], f1, o[e]);
+                    for (int e = 0; e < 32; ++e) o[e] *= f;
                     if (!live) continue;
                     if (!whole) {
                         float *part = reinterpret_cast<float *>(a.workspace + L.sums);
@@ -1023,19 +1037,15 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
             if (live && (it.shared || t == 0)) {
                 if (!whole)
                     reinterpret_cast<float2 *>(a.workspace + L.ml)[((size_t)it.slot * kM + row_tile) * kTile + r] =
-                        make_float2(top, sum);
+                        make_float2(ref, sum);
                 else if (a.lse)
                     a.lse[(size_t)(it.q0 + tok) * a.Hq + it.h0 + gr] =
-                        sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+                        none ? -INFINITY : (ref + __log2f(sum)) * kLn2;
             }
-            // (O_t and pair are read: the next item's first p_ready comes after this)
+            // (O and the sums are read: the next item's first p_ready comes after this)
             tc_fence_before();
-            if (joined) {
-                arrive(2);
-                ok = warp_wait_flag(&sm->merge[2], merges, &sm->abort, 13);
-                merges ^= 1;
-                tc_fence_after();
-            }
+            if (!it.shared) ok = exchange();
+            tc_fence_after();
         }
     }
     __syncthreads();
