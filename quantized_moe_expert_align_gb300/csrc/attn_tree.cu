@@ -18,6 +18,13 @@
 // The key tiles of the whole batch, in order, are shared out evenly over one block
 // per SM; a range cut by a block's end is joined by a second kernel, in key order.
 //
+// Measured, 32 sequences of 8192 keys, 32 heads of 128 over 4, 16 tokens: bf16 103 us
+// (5.2 TB/s; the rest is start, joins and ends of ranges), fp8 89; 64 tokens
+// (512 rows) over fp8 286 us (961 TFLOP/s).  64 sequences of 4096 keys, 64 heads over
+// 8, 16 tokens: bf16 183 us (5.9 TB/s), fp8 174 (3.2 TB/s: not the bytes but the way
+// from scores over weights to products, some 2400 cycles a key tile of which the
+// exponentials are 512).
+//
 // A bf16 cache is copied page by page into the swizzled operand tiles.  An fp8
 // cache is used as it is for the scores: a row of Q, times a power of two, is the
 // sum of two rows of e4m3 numbers, both multiplied with the codes (exact, but that
@@ -48,7 +55,7 @@ constexpr int kConvKeys = 32;    // keys that a converting warp has of a key til
 constexpr float kSlack = 8.f;    // a row's maximum may exceed its reference by this
 constexpr int kMaxGrid = 160;    // blocks at most
 constexpr int kParts = 2;        // in which a key tile's weights come
-constexpr int kScaleBufs = 4;    // key tiles whose scales are held
+constexpr int kScaleBufs = 8;    // key tiles whose scales are held
 
 // Items of at least this many key tiles run shared row tiles half a round apart.
 constexpr int kApart = 4;
@@ -62,6 +69,12 @@ constexpr int kMmaWarp = 8, kLoadWarp = 10, kFixWarp = 11, kConvWarp = 12;
 template <int D, bool FP8>
 struct Cfg {
     static constexpr int kThreads = FP8 ? 512 : 384;
+    // Up to 128 rows of heads of 128 over fp8 the softmax warps' chain of waits is what a
+    // key tile takes, so these look ahead at the barriers (a wait takes some 200 cycles
+    // though its phase be over), poll where the halves meet, and Q is in tensor memory:
+    // 64 sequences of 4096 keys, 64 heads over 8, 189 -> 174 us for 16 tokens, 177 -> 171
+    // for 8.  Elsewhere it costs: heads of 64 81 -> 84, bf16 8 x 1000 keys 19.8 -> 21.4.
+    static constexpr bool kQuick = FP8 && D == 128;
     // The launch's registers a thread (128 or 168), shared out anew.
     static constexpr int kRoleRegs = FP8 ? 64 : 72, kSoftmaxRegs = FP8 ? 192 : 216;
     static_assert((kThreads - 256) * kRoleRegs + 256 * kSoftmaxRegs <= kThreads * (FP8 ? 128 : 168), "register split");
@@ -122,10 +135,13 @@ __host__ __device__ inline int tile_heads(int G) { return G < kTile ? G : kTile;
 __host__ __device__ inline int tile_tokens(int G) { return kTile / tile_heads(G); }
 
 struct Shared {
-    uint64_t q_full[kM], q_ready[kM], q_empty[kM], op_full[8], op_empty[8], tail[8], raw_full[4], raw_empty[4];
-    uint64_t k_full[4], k_empty[4], sc_full[kScaleBufs], sc_ready[kScaleBufs], sc_empty[kScaleBufs], s_full[kM], p_ready[kM][kParts], o_done[kM], offset;
+    uint64_t q_full[kM], q_ready[kM], q_empty[kM], op_full[8], op_empty[8], raw_full[4], raw_empty[4];
+    uint64_t k_full[4], k_empty[4], sc_ready[kScaleBufs], sc_empty[kScaleBufs], s_full[kM], p_ready[kM][kParts], o_done[kM], offset;
     // (a key tile in turn; items by number)
     uint64_t s_split[2], p_split[2], o_split[2], exchange, item_done[kM][4];
+    union {  // bf16; fp8
+        uint64_t tail[8], sc_full[kScaleBufs];
+    };
     uint64_t item_full[2], item_empty[2], finished;
     uint32_t tmem;
     int abort, bad;
@@ -137,6 +153,7 @@ struct Shared {
     // up to 128 rows: the maxima of a key tile's halves, then the sums of the weights
     float halves[2][2][kTile];
 };
+static_assert(kScaleBufs == 8, "as many as of tail");
 static_assert(sizeof(Shared) <= 3072, "shared block");
 
 // What a sequence has to do.
@@ -195,6 +212,17 @@ __device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, ui
         : "memory");
 }
 
+// A in tensor memory, a row a lane and four codes a column.
+__device__ __forceinline__ void mma_e4m3_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 template <int D, bool FP8>
 __global__ void __launch_bounds__((Cfg<D, FP8>::kThreads), 1)
 tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtensorMap map_q,
@@ -233,7 +261,6 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
         for (int i = 0; i < 8; ++i) {
             mbar_init(&sm->op_full[i], FP8 ? 4 : 1);
             mbar_init(&sm->op_empty[i], kM);
-            mbar_init(&sm->tail[i], 1);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&sm->raw_full[i], 1);
@@ -306,6 +333,10 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
     __syncthreads();
     constexpr uint32_t s_col = 0, o_col = kM * kKeys;
     static_assert(kM * (kKeys + D) <= 512, "tensor memory");
+    // kQuick: both terms of Q, where the second row tile's sums would be (its
+    // codes are read once a product from there, not from shared memory, whose bandwidth
+    // the products, copies and conversions share).
+    constexpr uint32_t q_col = o_col + D;
 
     auto take = [&](uint32_t n, Item &it) {
         if (!warp_wait_flag(&sm->item_full[n & 1], (n >> 1) & 1, &sm->abort, 1)) return false;
@@ -510,7 +541,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                     return s;
                 };
                 // Scores of key tile i of all into tensor memory from `to` on.
-                auto scores = [&](uint32_t i, uint32_t to, uint64_t *full, bool last) {
+                auto scores = [&](uint32_t i, uint32_t to, uint64_t *full, bool last, auto q_in_tmem) {
                     uint64_t *k_free;
                     const uint32_t k = wait_tile(i, 0, k_free);
                     if (!ok) return;
@@ -522,8 +553,11 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
 #pragma unroll
                             for (int x = 0; x < 2 * (D / 32); ++x) {
                                 const uint32_t term = x / (D / 32), in = x % (D / 32) * 32;
-                                mma_e4m3_ss(to, qd + ((term * (D == 128 ? kQHalf : 64u) + in) >> 4), kd + (in >> 4), kIdS,
-                                            x > 0);
+                                if (C::kQuick && decltype(q_in_tmem)::value)
+                                    mma_e4m3_ts(to, q_col + (term * D + in) / 4, kd + (in >> 4), kIdS, x > 0);
+                                else
+                                    mma_e4m3_ss(to, qd + ((term * (D == 128 ? kQHalf : 64u) + in) >> 4), kd + (in >> 4),
+                                                kIdS, x > 0);
                             }
                         } else {
                             const uint64_t kd = k_desc + ((k * C::kKvB) >> 4);
@@ -577,7 +611,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                     tc_fence_after();
                     if (both) {
                         for (int j = 0; j < tiles && ok; ++j) {
-                            scores(tile0 + j, s_t, &sm->s_full[t], j + 1 == tiles);
+                            scores(tile0 + j, s_t, &sm->s_full[t], j + 1 == tiles, std::false_type{});
                             uint64_t *v_free;
                             const uint32_t v = wait_tile(tile0 + j, 1, v_free);
 #pragma unroll
@@ -590,11 +624,12 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                         }
                         shared0 += tiles;
                     } else if (t == 0) {
-                        scores(tile0, s_col, &sm->s_split[0], tiles == 1);
+                        scores(tile0, s_col, &sm->s_split[0], tiles == 1, std::true_type{});
                         for (int j = 0; j < tiles && ok; ++j) {
                             // (the last product with this memory's weights came before)
                             if (j + 1 < tiles)
-                                scores(tile0 + j + 1, s_col + ((j + 1) & 1) * kKeys, &sm->s_split[(j + 1) & 1], j + 2 == tiles);
+                                scores(tile0 + j + 1, s_col + ((j + 1) & 1) * kKeys, &sm->s_split[(j + 1) & 1], j + 2 == tiles,
+                                       std::true_type{});
                             uint64_t *v_free;
                             const uint32_t v = wait_tile(tile0 + j, 1, v_free);
                             ok = ok && warp_wait_flag(&sm->p_split[j & 1], split_ph >> (j & 1) & 1, &sm->abort, 7);
@@ -762,11 +797,15 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
         const int tok_r = r / Gt, gr = r % Gt;
         uint32_t tile0 = 0, shared0 = 0;  // key tiles of the items before, and of those shared
         uint32_t split_ph = 0, ex_ph = 0; // parities: a bit a half of S; the exchange
+        bool before_shared = false;       // the item before
         // All 8 warps have come here.
         auto exchange = [&]() {
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->exchange);
-            const bool done = warp_wait_flag(&sm->exchange, ex_ph, &sm->abort, 12);
+            bool done = C::kQuick && mbar_test_wait(&sm->exchange, ex_ph);
+            if (C::kQuick)
+                for (int i = 0; i < 32 && !done; ++i) done = mbar_test_wait(&sm->exchange, ex_ph);
+            done = (C::kQuick && __all_sync(0xffffffffu, done)) || warp_wait_flag(&sm->exchange, ex_ph, &sm->abort, 12);
             ex_ph ^= 1;
             return done;
         };
@@ -783,7 +822,11 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 // this row of Q, its largest value in [128, 256), as two rows of
                 // e4m3 numbers in its place
                 ok = warp_wait_flag(&sm->q_full[t], n & 1, &sm->abort, 16);
+                // (the second row tile's sums of the item before are read)
+                if (C::kQuick && !it.shared && before_shared) ok = ok && exchange();
+                before_shared = it.shared;
                 if (!ok) break;
+                tc_fence_after();
                 uint8_t *q = base + t * C::kQB + r * 128;
                 if (any_live) {
                     uint4 v[D / 8];
@@ -825,7 +868,25 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                                 make_uint4(h[x][0], h[x][1], h[x][2], h[x][3]);
                         }
                     }
+                    if (C::kQuick && !it.shared && t == 0)
+#pragma unroll 1
+                        for (int part = 0; part < 4; ++part) {  // 64 codes: half of a term
+                            uint32_t w[16];
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const int unit = (part & 1) * 4 + u;
+                                const uint4 c = *reinterpret_cast<const uint4 *>(q + (part >> 1) * kQHalf +
+                                                                                 ((unit ^ (r & 7)) << 4));
+                                w[4 * u] = c.x;
+                                w[4 * u + 1] = c.y;
+                                w[4 * u + 2] = c.z;
+                                w[4 * u + 3] = c.w;
+                            }
+                            tmem_st16(q_col + lane_base + part * 16, w);
+                        }
                 }
+                tc_wait_st();
+                tc_fence_before();
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm->q_ready[t]);
@@ -840,6 +901,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 if (it.shared) return warp_wait_flag(&sm->o_done[t], (shared0 + j) & 1, &sm->abort, 10);
                 return warp_wait_flag(&sm->o_split[j & 1], ~(split_ph >> (j & 1)) & 1, &sm->abort, 11);
             };
+            bool seen = false;  // the next key tile's scores and scales
             // Key tile j: W of its scores a thread, all, or this warpgroup's half.
             auto round = [&](auto width, int j) {
                 constexpr int W = decltype(width)::value;
@@ -848,11 +910,22 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 const uint32_t s_at = kSplit ? s_col + half * kKeys + lane_base + col0 : s_t;
                 const uint32_t p_at = kSplit ? s_col + half * kKeys + lane_base + col0 / 2 : s_t;
                 const uint32_t buf = (tile0 + j) % kScaleBufs;
+                if (kSplit && C::kQuick && !any_live) {
+                    // (no row of this warp's is used: it is there when the others are)
+                    split_ph ^= 1u << half;
+                    if (!exchange()) return false;
+                    if (lane == 0) {
+                        if (FP8) mbar_arrive(&sm->sc_empty[buf]);
+                        mbar_arrive(&sm->p_split[half]);
+                    }
+                    return true;
+                }
                 // (before the scores are)
-                if (FP8 && !warp_wait_flag(&sm->sc_ready[buf], ((tile0 + j) / kScaleBufs) & 1, &sm->abort, 17)) return false;
+                if (FP8 && !seen && !warp_wait_flag(&sm->sc_ready[buf], ((tile0 + j) / kScaleBufs) & 1, &sm->abort, 17)) return false;
                 const int larger = FP8 ? sm->expo[buf] : 0;  // (the same for all rows)
+                bool both_there = false;  // of the next key tile
                 if (kSplit) {
-                    if (!warp_wait_flag(&sm->s_split[half], split_ph >> half & 1, &sm->abort, 9)) return false;
+                    if (!seen && !warp_wait_flag(&sm->s_split[half], split_ph >> half & 1, &sm->abort, 9)) return false;
                     split_ph ^= 1u << half;
                 } else if (!warp_wait_flag(&sm->s_full[t], (shared0 + j) & 1, &sm->abort, 9)) {
                     return false;
@@ -860,7 +933,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 const float *sc = scales + buf * 2 * kKeys + col0;
                 tc_fence_after();
                 const bool tells = !kSplit && t == 0 && j == 0 && run_apart(it) && lane == 0;
-                if (!any_live) {  // (no row of this warp's is used)
+                if (!(kSplit && C::kQuick) && !any_live) {
                     if (tells) mbar_arrive(&sm->offset);
                     expo = larger;
                     tc_fence_before();
@@ -969,6 +1042,11 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                             p[e] = pack_bf16(y.x, y.y);
                         }
                     }
+                    if (kSplit && C::kQuick && c + 32 == W) {
+                        const uint32_t i = tile0 + j + 1;
+                        both_there = mbar_test_wait(&sm->s_split[1 - half], split_ph >> (1 - half) & 1);
+                        both_there = both_there && mbar_test_wait(&sm->sc_ready[i % kScaleBufs], (i / kScaleBufs) & 1);
+                    }
                     tmem_st16(p_at + c / 2, p);
                     if ((c + 32) % (kKeys / kParts) == 0) {  // their product may start
                         tc_wait_st();
@@ -979,6 +1057,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 }
                 const float2 both = add2(sum[0], sum[1]);
                 l += both.x + both.y;
+                if (kSplit && C::kQuick) seen = __all_sync(0xffffffffu, both_there);
                 return true;
             };
             if (it.shared)
