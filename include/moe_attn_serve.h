@@ -8,7 +8,8 @@
  * Conventions are those of moe_attn.h: caller-owned buffers, asynchronous
  * calls on `stream`, host-detectable errors before anything is launched,
  * device errors in the workspace's status word (moe_w4a16_get_device_status).
- * All index arrays are int32 on the device, 4-byte aligned.
+ * All index arrays are int32 on the device, 4-byte aligned.  With
+ * MOE_ATTN_TEST_NO_COPIES=1 the attentions here fail as moe_attn_decode does.
  */
 #ifndef MOE_ATTN_SERVE_H
 #define MOE_ATTN_SERVE_H
@@ -67,7 +68,8 @@ size_t moe_page_plan_workspace_size(int B);
 moe_status_t moe_page_plan(int32_t *ring, int ring_size, const int32_t *state, int32_t *state_out,
                            int32_t *page_table, int table_stride, int page_size,
                            const int32_t *seq_lens, const int32_t *new_lens,
-                           const int32_t *dropped, const int32_t *kept, const int32_t *offsets, int window, int sinks, int B, int rows,
+                           const int32_t *dropped, const int32_t *kept, const int32_t *offsets,
+                           int window, int sinks, int B, int rows,
                            int32_t *seq_lens_out, int32_t *kept_out, int32_t *cu_q, int32_t *cu_k,
                            int32_t *positions, int32_t *slots, void *workspace, size_t ws_bytes,
                            moe_stream_t stream);

@@ -74,6 +74,7 @@ class PagePlan:
     positions = property(lambda self: self._all[3])
     slots = property(lambda self: self._all[4])
     kept = property(lambda self: self._all[5])
+
     @property
     def state(self):
         return self._all[6]
