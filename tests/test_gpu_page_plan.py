@@ -194,3 +194,21 @@ def test_drafts_that_are_dropped(gpu, B, in_place, window, sinks):
         x.step(new, 30 * B, in_place=in_place, dropped=gone)
     x.step([-1] * B, 0, in_place=in_place)
     assert x.state[1] == B * width and sorted(x.pool.ring.tolist()) == list(range(B * width))
+
+
+@pytest.mark.parametrize("new", [0, 1, -1])
+def test_dropped_tokens_that_a_window_has_left(gpu, new):
+    """Pages 0 to 2 went back behind the window; the sequence cannot lose tokens of page 2."""
+    import quantized_moe_expert_align_gb300 as moe
+    pool = moe.PagePool(su.i32([7, 6, 5, 0, 1, 2, -1, -1]), su.i32([0, 6]))
+    table, ws = su.i32([[0, 1, 2, 3]]), moe.AttnWorkspace("cuda", "pages", 1)
+    for left, status in ((30, (moe.MOE_ERR_DEVICE_BAD_INDEX, 0)), (48, (moe.MOE_OK, 0))):
+        before = pool.ring.tolist(), pool.state.tolist()
+        out = moe.page_plan(pool, table, su.i32([left]), su.i32([new]), 16, 1, window=8, kept=su.i32([3]),
+                            dropped=su.i32([60 - left]), workspace=ws)
+        assert au.status(ws) == status
+        if status[0]:
+            assert (pool.ring.tolist(), pool.state.tolist(), out.kept.tolist()) == (*before, [3])
+    # (48 tokens left: page 3 goes back too, unless a new token needs it)
+    assert pool.ring.tolist() == [7, 6, 5, 0, 1, 2, -1 if new == 1 else 3, -1]
+    assert pool.state.tolist() == [0, 6 if new == 1 else 7]
