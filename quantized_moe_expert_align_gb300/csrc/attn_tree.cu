@@ -72,7 +72,7 @@ struct Cfg {
     // Up to 128 rows of heads of 128 over fp8 the softmax warps' chain of waits is what a
     // key tile takes, so these look ahead at the barriers (a wait takes some 200 cycles
     // though its phase be over), poll where the halves meet, and Q is in tensor memory:
-    // 64 sequences of 4096 keys, 64 heads over 8, 189 -> 174 us for 16 tokens, 177 -> 171
+    // 64 sequences of 4096 keys, 64 heads over 8, 189 -> 166 us for 16 tokens, 177 -> 159
     // for 8.  Elsewhere it costs: heads of 64 81 -> 84, bf16 8 x 1000 keys 19.8 -> 21.4.
     static constexpr bool kQuick = FP8 && D == 128;
     // The launch's registers a thread (128 or 168), shared out anew.
@@ -596,6 +596,8 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                     const int tiles = __shfl_sync(0xffffffffu, it.tiles, 0);
                     const bool both = __shfl_sync(0xffffffffu, it.shared, 0) != 0;
                     ok = warp_wait_flag(FP8 ? &sm->q_ready[t] : &sm->q_full[t], n & 1, &sm->abort, 6);
+                    if (C::kQuick && t == 0 && !both)  // (half of Q by each warpgroup)
+                        ok = ok && warp_wait_flag(&sm->q_ready[1], n & 1, &sm->abort, 6);
                     // The second row tile's tensor memory changes hands: its last products
                     // are over (items by number: one role may be two ahead of the other).
                     if (n > 0 && both != before_shared)
@@ -751,31 +753,39 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                     const uint32_t u0 = ((2 * piece) ^ r8) << 4, u1 = ((2 * piece + 1) ^ r8) << 4;
                     auto row_of = [&](int k) { return (D == 128 ? k >> 1 : k) * 8 + r8; };
                     auto half_of = [&](int k) { return D == 128 ? (k ^ r8) & 1 : 0; };
-                    uint4 c[kEach];
+                    // Four at a time: what all warps run in turn has to stay near the schedulers
+                    // (eight in one stretch: 166 us instead of 160 for 64 sequences of 4096 keys,
+                    // 16 tokens, 64 heads of 128 over 8, and 312 instead of 279 for 32 of 8192, 64
+                    // tokens, 32 heads over 4).
+                    constexpr int kGroup = 4;
+#pragma unroll 1
+                    for (int k0 = 0; k0 < kEach; k0 += kGroup) {
+                        uint4 c[kGroup];
 #pragma unroll
-                    for (int k = 0; k < kEach; ++k)
-                        c[k] = *reinterpret_cast<const uint4 *>(from + row_of(k) * D + half_of(k) * 64 + piece * 16);
-                    if (n_live < kConvKeys)
+                        for (int k = 0; k < kGroup; ++k)
+                            c[k] = *reinterpret_cast<const uint4 *>(from + row_of(k0 + k) * D + half_of(k0 + k) * 64 + piece * 16);
+                        if (n_live < kConvKeys)
 #pragma unroll
-                        for (int k = 0; k < kEach; ++k)
-                            if (row_of(k) >= n_live) c[k] = make_uint4(0, 0, 0, 0);
+                            for (int k = 0; k < kGroup; ++k)
+                                if (row_of(k0 + k) >= n_live) c[k] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-                    for (int k = 0; k < kEach; ++k) {
-                        const uint32_t fb = __shfl_sync(0xffffffffu, *reinterpret_cast<const uint32_t *>(&own), row_of(k));
-                        // (a row that does not exist has zeros whatever its scale)
-                        const uint32_t f = n_live < kConvKeys && row_of(k) >= n_live ? 0u : fb;
-                        auto scaled = [&](uint32_t w) {
-                            uint2 h = e4m3_f16(w);
-                            __half2 x = __hmul2(*reinterpret_cast<__half2 *>(&h.x), *reinterpret_cast<const __half2 *>(&f));
-                            __half2 y = __hmul2(*reinterpret_cast<__half2 *>(&h.y), *reinterpret_cast<const __half2 *>(&f));
-                            h.x = *reinterpret_cast<uint32_t *>(&x);
-                            h.y = *reinterpret_cast<uint32_t *>(&y);
-                            return h;
-                        };
-                        const uint2 o0 = scaled(c[k].x), o1 = scaled(c[k].y), o2 = scaled(c[k].z), o3 = scaled(c[k].w);
-                        uint8_t *at = to + half_of(k) * kKvHalf + row_of(k) * 128;
-                        *reinterpret_cast<uint4 *>(at + u0) = make_uint4(o0.x, o0.y, o1.x, o1.y);
-                        *reinterpret_cast<uint4 *>(at + u1) = make_uint4(o2.x, o2.y, o3.x, o3.y);
+                        for (int k = 0; k < kGroup; ++k) {
+                            const uint32_t fb = __shfl_sync(0xffffffffu, *reinterpret_cast<const uint32_t *>(&own), row_of(k0 + k));
+                            // (a row that does not exist has zeros whatever its scale)
+                            const uint32_t f = n_live < kConvKeys && row_of(k0 + k) >= n_live ? 0u : fb;
+                            auto scaled = [&](uint32_t w) {
+                                uint2 h = e4m3_f16(w);
+                                __half2 x = __hmul2(*reinterpret_cast<__half2 *>(&h.x), *reinterpret_cast<const __half2 *>(&f));
+                                __half2 y = __hmul2(*reinterpret_cast<__half2 *>(&h.y), *reinterpret_cast<const __half2 *>(&f));
+                                h.x = *reinterpret_cast<uint32_t *>(&x);
+                                h.y = *reinterpret_cast<uint32_t *>(&y);
+                                return h;
+                            };
+                            const uint2 o0 = scaled(c[k].x), o1 = scaled(c[k].y), o2 = scaled(c[k].z), o3 = scaled(c[k].w);
+                            uint8_t *at = to + half_of(k0 + k) * kKvHalf + row_of(k0 + k) * 128;
+                            *reinterpret_cast<uint4 *>(at + u0) = make_uint4(o0.x, o0.y, o1.x, o1.y);
+                            *reinterpret_cast<uint4 *>(at + u1) = make_uint4(o2.x, o2.y, o3.x, o3.y);
+                        }
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
@@ -820,7 +830,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
             float sl = a.scale * kLog2e;
             if (FP8) {
                 // this row of Q, its largest value in [128, 256), as two rows of
-                // e4m3 numbers in its place
+                // e4m3 numbers, in its place or to tensor memory
                 ok = warp_wait_flag(&sm->q_full[t], n & 1, &sm->abort, 16);
                 // (the second row tile's sums of the item before are read)
                 if (C::kQuick && !it.shared && before_shared) ok = ok && exchange();
@@ -828,62 +838,63 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                 if (!ok) break;
                 tc_fence_after();
                 uint8_t *q = base + t * C::kQB + r * 128;
-                if (any_live) {
-                    uint4 v[D / 8];
-                    float most = 0.f;
+                auto unit = [&](int u) {  // 8 columns, 16 bytes
+                    return reinterpret_cast<uint4 *>(q + (u >> 3) * kQHalf + (((u & 7) ^ (r & 7)) << 4));
+                };
+                float most = 0.f;
+                auto look = [&](const uint4 &x) {
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                    for (int u = 0; u < D / 8; ++u) {
-                        v[u] = *reinterpret_cast<const uint4 *>(q + (u >> 3) * kQHalf + (((u & 7) ^ (r & 7)) << 4));
-                        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            most = max3(most, fabsf(__uint_as_float(w[e] << 16)),
-                                        fabsf(__uint_as_float(w[e] & 0xFFFF0000u)));
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        most = max3(most, fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u)));
+                };
+                auto factors = [&](float &down) {
                     // (an infinity makes the row NaN, as its scores would)
                     const int e2 = max((int)(__float_as_uint(most) >> 23) - 127, -119);
-                    const float down = e2 > 127 ? __uint_as_float(0x7FFFFFFFu) : pow2(7 - e2);
+                    down = e2 > 127 ? __uint_as_float(0x7FFFFFFFu) : pow2(7 - e2);
                     sl *= pow2(min(e2, 127) - 7);
+                };
+                // 16 columns: 16 bytes of each term
+                auto terms = [&](const uint4 &x, const uint4 &y, float down, uint32_t *h0, uint32_t *h1) {
+                    const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-                    for (int u = 0; u < D / 16; ++u) {  // 16 columns: 16 bytes of each term
-                        const uint32_t w[8] = {v[2 * u].x,     v[2 * u].y,     v[2 * u].z,     v[2 * u].w,
-                                               v[2 * u + 1].x, v[2 * u + 1].y, v[2 * u + 1].z, v[2 * u + 1].w};
-                        uint32_t h[2][4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float2 a0 = make_float2(__uint_as_float(w[2 * e] << 16) * down,
-                                                    __uint_as_float(w[2 * e] & 0xFFFF0000u) * down);
-                            float2 a1 = make_float2(__uint_as_float(w[2 * e + 1] << 16) * down,
-                                                    __uint_as_float(w[2 * e + 1] & 0xFFFF0000u) * down);
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const uint32_t c0 = take_e4m3(a0), c1 = take_e4m3(a1);
-                                h[x][e] = c0 | c1 << 16;
-                            }
-                        }
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const int unit = D == 128 ? u : 4 * x + u;
-                            *reinterpret_cast<uint4 *>(q + (D == 128 ? x * kQHalf : 0) + ((unit ^ (r & 7)) << 4)) =
-                                make_uint4(h[x][0], h[x][1], h[x][2], h[x][3]);
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        float2 a0 = make_float2(__uint_as_float(w[2 * e] << 16) * down,
+                                                __uint_as_float(w[2 * e] & 0xFFFF0000u) * down);
+                        float2 a1 = make_float2(__uint_as_float(w[2 * e + 1] << 16) * down,
+                                                __uint_as_float(w[2 * e + 1] & 0xFFFF0000u) * down);
+                        const uint32_t c0 = take_e4m3(a0), c1 = take_e4m3(a1);
+                        h0[e] = c0 | c1 << 16;
+                        const uint32_t d0 = take_e4m3(a0), d1 = take_e4m3(a1);
+                        h1[e] = d0 | d1 << 16;
                     }
-                    if (C::kQuick && !it.shared && t == 0)
-#pragma unroll 1
-                        for (int part = 0; part < 4; ++part) {  // 64 codes: half of a term
-                            uint32_t w[16];
+                };
+                if (C::kQuick && !it.shared) {
+                    // each warpgroup, from its copy, half of the columns, to tensor memory
 #pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const int unit = (part & 1) * 4 + u;
-                                const uint4 c = *reinterpret_cast<const uint4 *>(q + (part >> 1) * kQHalf +
-                                                                                 ((unit ^ (r & 7)) << 4));
-                                w[4 * u] = c.x;
-                                w[4 * u + 1] = c.y;
-                                w[4 * u + 2] = c.z;
-                                w[4 * u + 3] = c.w;
-                            }
-                            tmem_st16(q_col + lane_base + part * 16, w);
-                        }
+                    for (int u = 0; u < D / 8; ++u) look(*unit(u));
+                    float down;
+                    factors(down);
+                    uint32_t h0[16], h1[16];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        terms(*unit(8 * t + 2 * u), *unit(8 * t + 2 * u + 1), down, h0 + 4 * u, h1 + 4 * u);
+                    tmem_st16(q_col + lane_base + t * 16, h0);
+                    tmem_st16(q_col + lane_base + D / 4 + t * 16, h1);
+                } else if (any_live) {
+                    uint4 v[D / 8];
+#pragma unroll
+                    for (int u = 0; u < D / 8; ++u) look(v[u] = *unit(u));
+                    float down;
+                    factors(down);
+#pragma unroll
+                    for (int u = 0; u < D / 16; ++u) {
+                        uint32_t h0[4], h1[4];
+                        terms(v[2 * u], v[2 * u + 1], down, h0, h1);
+                        // (heads of 64: both terms in one row)
+                        *unit(u) = make_uint4(h0[0], h0[1], h0[2], h0[3]);
+                        *unit((D == 128 ? 8 : 4) + u) = make_uint4(h1[0], h1[1], h1[2], h1[3]);
+                    }
                 }
                 tc_wait_st();
                 tc_fence_before();
