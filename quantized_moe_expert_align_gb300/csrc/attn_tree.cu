@@ -19,11 +19,12 @@
 // per SM; a range cut by a block's end is joined by a second kernel, in key order.
 //
 // Measured, 32 sequences of 8192 keys, 32 heads of 128 over 4, 16 tokens: bf16 103 us
-// (5.2 TB/s; the rest is start, joins and ends of ranges), fp8 89; 64 tokens
-// (512 rows) over fp8 286 us (961 TFLOP/s).  64 sequences of 4096 keys, 64 heads over
-// 8, 16 tokens: bf16 183 us (5.9 TB/s), fp8 174 (3.2 TB/s: not the bytes but the way
-// from scores over weights to products, some 2400 cycles a key tile of which the
-// exponentials are 512).
+// (5.2 TB/s; the rest is start, joins and ends of ranges), fp8 84; 64 tokens
+// (512 rows) over fp8 278 us (990 TFLOP/s).  64 sequences of 4096 keys, 64 heads over
+// 8, 16 tokens: bf16 183 us (5.9 TB/s), fp8 160 (3.5 TB/s: not the bytes but the way
+// from scores over weights to products, some 2200 cycles a key tile of which the
+// exponentials are 512).  What all warps run in turn counts too: this code is large, and
+// a register spilled in the softmax costs a fifth.
 //
 // A bf16 cache is copied page by page into the swizzled operand tiles.  An fp8
 // cache is used as it is for the scores: a row of Q, times a power of two, is the

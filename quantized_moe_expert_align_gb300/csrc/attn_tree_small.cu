@@ -1,5 +1,5 @@
 // attn_tree_small.cu -- attention of drafted tokens over the paged cache, in
-// tiles of up to 16 rows.
+// tiles of up to 16 rows: for sequences that have few (attn_tree.cu has the rule).
 #include "attn_decode.cuh"
 
 namespace moe {
