@@ -57,6 +57,7 @@ constexpr float kSlack = 8.f;    // a row's maximum may exceed its reference by 
 constexpr int kMaxGrid = 160;    // blocks at most
 constexpr int kParts = 2;        // in which a key tile's weights come
 constexpr int kScaleBufs = 8;    // key tiles whose scales are held
+constexpr int kSharedBytes = 3 << 10;  // barriers and what the warps tell each other
 
 // Items of at least this many key tiles run shared row tiles half a round apart.
 constexpr int kApart = 4;
@@ -91,7 +92,7 @@ struct Cfg {
     static constexpr size_t kRawAt = kKAt + (FP8 ? (size_t)kKs * kKB : 0);
     static constexpr size_t kSharedAt = kRawAt + (FP8 ? (size_t)kRaw * kKB : 0);
     // fp8: of kScaleBufs key tiles the scales of K and of V, [2][kKeys]
-    static constexpr size_t kScalesAt = kSharedAt + 3072;
+    static constexpr size_t kScalesAt = kSharedAt + kSharedBytes;
     static constexpr size_t kSmem = kScalesAt + (FP8 ? kScaleBufs * 2 * kKeys * 4 : 0);
     static_assert(kSmem > 114 * 1024 && kSmem <= 227 * 1024, "one block per SM: all of tensor memory is its own");
 };
@@ -155,7 +156,7 @@ struct Shared {
     float halves[2][2][kTile];
 };
 static_assert(kScaleBufs == 8, "as many as of tail");
-static_assert(sizeof(Shared) <= 3072, "shared block");
+static_assert(sizeof(Shared) <= kSharedBytes, "shared block");
 
 // What a sequence has to do.
 struct Seq {

@@ -171,3 +171,20 @@ def test_accept_refuses(gpu, bad):
     moe.kv_accept(cache, table, su.i32([10, bad.get("base", 10), 10]), accept, workspace=ws)
     assert au.status(ws) == (moe.MOE_ERR_DEVICE_BAD_INDEX, 1)
     assert torch.equal(bits, want) and torch.equal(cache.scales, scales)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_sequences_of_few_and_many_rows_in_turns(gpu, D, fp8):
+    """Blocks that go from one row tile to two and back, several times."""
+    lens = [200 + (53 * i * i) % 700 for i in range(120)]
+    nodes = [(33, 5, 16, 20, 64, 1)[i % 6] for i in range(120)]
+    _tree(lens, nodes, 16, 2, D, fp8, 64, seed=11)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_few_rows_but_for_one_sequence(gpu, D, fp8):
+    """Tiles of 16 rows, and a sequence that has many of them."""
+    lens = [50 + 3 * i for i in range(40)]
+    _tree(lens, [64 if i == 17 else 1 for i in range(40)], 8, 4, D, fp8, 16, seed=12)
