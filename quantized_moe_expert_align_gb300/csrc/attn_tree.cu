@@ -1295,15 +1295,15 @@ size_t tree_workspace(int, int T, int Hq, int Hkv, int D) {
 }
 
 cudaError_t launch_attn_tree(const DecodeAttnArgs &a, cudaStream_t s) {
-    // Tiles of 16 rows where none can have more, or where there are few on average (what
-    // a sequence has the host does not know; any number is right either way).  64
+    // Tiles of 8 or 16 rows where none can have more, or where there are few on average
+    // (what a sequence has the host does not know; any number is right either way).  64
     // sequences of 4096 keys, 4 key/value heads, here and in small tiles: 8 rows each,
-    // heads of 128, bf16 91 and 94 us, fp8 81 and 70, heads of 64 53 and 50, 83 and 49; 16
+    // heads of 128, bf16 91 and 90 us, fp8 81 and 55, heads of 64 53 and 49, 83 and 33; 16
     // rows 92 and 99, 81 and 76, 52 and 52, 83 and 51; 24 rows 93 and 175, 81 and 130, 52 and
-    // 90, 83 and 84.  6 sequences of 4000 keys, one head, 4 rows, bf16 21 and 13; 162 of
-    // 300, 2 heads, 6 rows, bf16 21 and 21, fp8 33 and 22.
+    // 90, 83 and 84.  6 sequences of 4000 keys, one head, 4 rows, bf16 21 and 11; 162 of
+    // 300, 2 heads, 6 rows, bf16 21 and 16, fp8 33 and 17.
     const int tokens = a.T < kTreeTokens ? a.T : kTreeTokens, G = a.Hq / a.kv.Hkv;
-    const int few = a.cache_type == MOE_KV_BF16 && a.D == 128 ? 6 : 12;
+    const int few = a.cache_type == MOE_KV_BF16 && a.D == 128 ? 8 : 12;
     if (tokens * G <= 16 || (int64_t)a.T * G <= (int64_t)a.B * few) return launch_attn_tree_small(a, s);
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
