@@ -46,8 +46,9 @@ size_t moe_page_plan_workspace_size(int B);
  *
  * dropped (NULL: none) says how many tokens sequence b has lost since its last
  * step, rejected drafts: its table holds pages for seq_lens[b] + dropped[b].  New
- * tokens use those first; what the new length does not need goes back.  kept[b]
- * is at most the pages of seq_lens[b]: no token is dropped that a window has left.
+ * tokens use those first; what the new length does not need goes back.  No token is
+ * dropped whose page has gone back behind a window: kept[b] is at most seq_lens[b] /
+ * page_size rounded down (or ceil(sinks / page_size): then no page has).
  *
  * Outputs (each input array that has an output may be that output):
  *  state_out [2];  seq_lens_out [B] (0 for a finished one);  kept_out [B];

@@ -227,9 +227,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step(const PagePlanArgs a, 
             bad = len < 0 || len > room || dropped < 0 || (int64_t)len + dropped > room || n < -1 ||
                   (int64_t)len + max(n, 0) > room;
             const int held = bad ? 0 : pages_for(len + dropped, a.page_shift);
-            // (pages that went back behind a window lie below the length: else it has lost
-            // tokens whose pages it no longer has)
-            bad = bad || kept < 0 || kept > pages_for(len, a.page_shift);
+            // (pages [first, kept) went back behind a window and lie wholly below the length:
+            // else it has lost tokens of one of them, whose places are somebody else's by now)
+            bad = bad || kept < 0 || kept > max(first, len >> a.page_shift);
             if (!bad) {
                 r.len = len;
                 r.grow = n;
