@@ -854,7 +854,8 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                     // (an infinity makes the row NaN, as its scores would)
                     const int e2 = max((int)(__float_as_uint(most) >> 23) - 127, -119);
                     down = e2 > 127 ? __uint_as_float(0x7FFFFFFFu) : pow2(7 - e2);
-                    sl *= pow2(min(e2, 127) - 7);
+                    // (never 0, which times a masked score's -inf would be NaN)
+                    sl = fmaxf(sl * pow2(min(e2, 127) - 7), __uint_as_float(1));
                 };
                 // 16 columns: 16 bytes of each term
                 auto terms = [&](const uint4 &x, const uint4 &y, float down, uint32_t *h0, uint32_t *h1) {
