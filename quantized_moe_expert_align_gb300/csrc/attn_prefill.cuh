@@ -389,11 +389,19 @@ plan_kernel(const PrefillArgs a, const int tpt, const int HV, const int n_blocks
 }
 
 // ------------------------------------------------------------------ the products
+// Tensor maps of the pieces of a seam.
+template <bool WIN>
+struct Pieces {
+    CUtensorMap k, v;
+};
+template <>
+struct Pieces<false> {};
+
 template <int D, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __grid_constant__ CUtensorMap map_q,
                const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-               const __grid_constant__ CUtensorMap map_k_piece, const __grid_constant__ CUtensorMap map_v_piece) {
+               const __grid_constant__ Pieces<WIN> pieces) {
     using C = Cfg<D>;
     constexpr int S = C::kStages;
     constexpr int kHalves = D / 64;
@@ -552,7 +560,7 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                 next_ahead();
                 const int tiles = most_tiles(it.b);
                 bool ok = true;
-                auto copy_kv = [&](const CUtensorMap *map, const CUtensorMap *piece, int j, bool tail) {
+                auto copy_kv = [&](const CUtensorMap *map, bool values, int j, bool tail) {
                     const uint32_t s = kv % S, ph = (kv / S) & 1;
                     ok = ok && warp_wait_flag(&sm->kv_empty[s], ph ^ 1, &sm->abort, 3);
                     if (!ok) return;
@@ -563,18 +571,21 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                             tma_load_4d(kv_base + s * C::kKvB, map, 0, it.b.k0 + key_of(it, j), it.hk, 0, bar);
                     }
                     __syncwarp();
-                    if (WIN && j == seam(it) && lane < kKeys / kLead * kHalves) {  // kLead keys a lane
-                        const int c = lane % (kKeys / kLead), h = lane / (kKeys / kLead);
-                        const int v = (it.b.j0 + j) * kKeys + c * kLead;
-                        const int key = v < lead_keys(a) ? v : v + left_out<WIN>(a, it.b.base);
-                        tma_load_4d(kv_base + s * C::kKvB + h * kKvHalf + c * kLead * 128, piece, 0, it.b.k0 + key, it.hk,
-                                    h, tail ? &sm->tail[s] : &sm->kv_full[s]);
+                    if constexpr (WIN) {
+                        if (j == seam(it) && lane < kKeys / kLead * kHalves) {  // kLead keys a lane
+                            const int c = lane % (kKeys / kLead), h = lane / (kKeys / kLead);
+                            const int v = (it.b.j0 + j) * kKeys + c * kLead;
+                            const int key = v < lead_keys(a) ? v : v + left_out<WIN>(a, it.b.base);
+                            tma_load_4d(kv_base + s * C::kKvB + h * kKvHalf + c * kLead * 128,
+                                        values ? &pieces.v : &pieces.k, 0, it.b.k0 + key, it.hk, h,
+                                        tail ? &sm->tail[s] : &sm->kv_full[s]);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                     ++kv;
                 };
                 for (int j = 0; j < tiles && ok && !a.test_no_copies; ++j) {
-                    if (!C::kOwnP || j == 0) copy_kv(&map_k, &map_k_piece, j, false);
+                    if (!C::kOwnP || j == 0) copy_kv(&map_k, false, j, false);
                     if (j == 0) {
                         for (int t = 0; t < kM && ok; ++t) {
                             ok = warp_wait_flag(&sm->q_empty[t], (n & 1) ^ 1, &sm->abort, 4);
@@ -589,8 +600,8 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                         }
                     }
                     // (in the order in which the products want them)
-                    if (C::kOwnP && ok && j + 1 < tiles) copy_kv(&map_k, &map_k_piece, j + 1, false);
-                    if (ok) copy_kv(&map_v, &map_v_piece, j, ragged(it, j) || j == last_lead(it));
+                    if (C::kOwnP && ok && j + 1 < tiles) copy_kv(&map_k, false, j + 1, false);
+                    if (ok) copy_kv(&map_v, true, j, ragged(it, j) || (WIN && j == last_lead(it)));
                 }
                 if (!ok) break;
                 if (tiles == 0) {
@@ -763,17 +774,23 @@ prefill_kernel(const PrefillArgs a, const int HT, const bool planned, const __gr
                     if (lane == 0) mbar_arrive(&sm->kv_full[s]);
                     return true;
                 };
-                const int lead = last_lead(it);
-                auto past_end = [&](int j) { return ragged(it, j) ? it.b.nk - key_of(it, j) : kKeys; };
-                if (lead >= 0 && lead < tiles) {
-                    // (heads of 64: the next key tile is copied first, if there is one)
-                    const uint32_t at = kv + 2 * (uint32_t)lead + (C::kOwnP && lead + 1 < tiles ? 2 : 1);
-                    const int first = (it.b.j0 + lead) * kKeys;
-                    if (!clear(at, a.sinks - first, min(lead_keys(a) - first, kKeys), past_end(lead))) break;
+                if constexpr (WIN) {
+                    const int lead = last_lead(it);
+                    auto past_end = [&](int j) { return ragged(it, j) ? it.b.nk - key_of(it, j) : kKeys; };
+                    if (lead >= 0 && lead < tiles) {
+                        // (heads of 64: the next key tile is copied first, if there is one)
+                        const uint32_t at = kv + 2 * (uint32_t)lead + (C::kOwnP && lead + 1 < tiles ? 2 : 1);
+                        const int first = (it.b.j0 + lead) * kKeys;
+                        if (!clear(at, a.sinks - first, min(lead_keys(a) - first, kKeys), past_end(lead))) break;
+                    }
+                    kv += 2 * tiles;
+                    if (tiles == 0 || lead == tiles - 1 || !ragged(it, tiles - 1)) continue;
+                    if (!clear(kv - 1, 0, 0, past_end(tiles - 1))) break;
+                } else {
+                    kv += 2 * tiles;
+                    if (tiles == 0 || !ragged(it, tiles - 1)) continue;
+                    if (!clear(kv - 1, 0, 0, it.b.nk - (it.b.j0 + tiles - 1) * kKeys)) break;
                 }
-                kv += 2 * tiles;
-                if (tiles == 0 || lead == tiles - 1 || !ragged(it, tiles - 1)) continue;
-                if (!clear(kv - 1, 0, 0, past_end(tiles - 1))) break;
             }
         }
     } else {
@@ -1150,16 +1167,17 @@ cudaError_t run(const PrefillArgs &a, int sms, cudaStream_t s) {
                                box, CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
     }
-    CUtensorMap mp[2] = {mk, mv};  // pieces of a seam
-    for (int i = 0; i < 2 && WIN; ++i) {
-        const uint16_t *p = a.Tk > 0 ? (i ? a.v : a.k) : a.q;
-        const uint64_t dims[4] = {64, (uint64_t)(a.Tk > 0 ? a.Tk : 1), (uint64_t)a.Hkv, D / 64};
-        const uint64_t strides[3] = {(uint64_t)(i ? a.v_stride : a.k_stride) * 2, D * 2, 128};
-        const uint32_t box[4] = {64, kLead, 1, 1};
-        if (!encode_tensor_map(&mp[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p, dims, strides, box,
-                               CU_TENSOR_MAP_SWIZZLE_128B))
-            return cudaErrorInvalidValue;
-    }
+    Pieces<WIN> pieces;
+    if constexpr (WIN)
+        for (int i = 0; i < 2; ++i) {
+            const uint16_t *p = a.Tk > 0 ? (i ? a.v : a.k) : a.q;
+            const uint64_t dims[4] = {64, (uint64_t)(a.Tk > 0 ? a.Tk : 1), (uint64_t)a.Hkv, D / 64};
+            const uint64_t strides[3] = {(uint64_t)(i ? a.v_stride : a.k_stride) * 2, D * 2, 128};
+            const uint32_t box[4] = {64, kLead, 1, 1};
+            if (!encode_tensor_map(i ? &pieces.v : &pieces.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p, dims, strides,
+                                   box, CU_TENSOR_MAP_SWIZZLE_128B))
+                return cudaErrorInvalidValue;
+        }
     // (no key range is cut below this many keys: then no joins either)
     const bool cuts = reach_of(a, kM * tpt, WIN) > kMinKeys;
     const int64_t most = ((int64_t)a.Tq / (kM * tpt) + a.B) * a.Hkv * HT;
@@ -1187,7 +1205,7 @@ cudaError_t run(const PrefillArgs &a, int sms, cudaStream_t s) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = planned ? 1 : 0;
-    err = cudaLaunchKernelEx(&cfg, fn, a, HT, planned, mq, mk, mv, mp[0], mp[1]);
+    err = cudaLaunchKernelEx(&cfg, fn, a, HT, planned, mq, mk, mv, pieces);
     if (err != cudaSuccess || !cuts) return err;
     cudaLaunchConfig_t cj = {};
     cj.gridDim = dim3(8 * sms);  // (16: up to 2 us more where there is nothing to join)
