@@ -128,7 +128,8 @@ size_t moe_attn_tree_workspace_size(int B, int T, int Hq, int Hkv, int D);
  * fp8 cache values of q below 2^-9 of their head's largest may be off by up to 2^-17
  * of it, and values of v by up to 2^-24 of the sequence's largest scale of v,
  * rounded up to a power of two, and 2^-9 of themselves (the weights then are fp16:
- * the bound above holds for both together).
+ * the bound above holds for both together).  Which of these a sequence's rows have may
+ * depend on the other sequences and on the table's width.
  * Limits: 0 <= B <= 65535, Hq <= 1024, 0 <= T, T * Hq < 2^31, scale > 0.
  * A page number out of range, a length that is negative or beyond the table (or
  * 2^30), a cu_q that decreases or leaves [0, T], more than 64 rows, or more than

@@ -96,6 +96,9 @@ struct DecodeAttnArgs {
     const int32_t *cu_q;
     const uint64_t *tree;
     int T;
+    // tokens up to which a sequence's are small tiles', the others' large ones', in two
+    // launches (0: one launch has all)
+    int few;
 };
 size_t decode_attn_workspace(int B, int Hq, int Hkv, int D);
 cudaError_t launch_attn_decode(const DecodeAttnArgs &a, cudaStream_t s);

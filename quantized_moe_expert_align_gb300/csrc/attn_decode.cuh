@@ -144,13 +144,14 @@ __device__ __forceinline__ int keys_of(const DecodeAttnArgs &a, int b) {
     const int n = __ldg(a.seq_lens + b);
     return n < 0 ? 0 : (n > most ? (int)most : n);
 }
-// kTree: whether the tokens of sequence b may be used; their first row and number.
+// kTree: whether the tokens of sequence b may be used; their first row and number
+// (0 too where the other launch has them).
 __device__ __forceinline__ bool tokens_of(const DecodeAttnArgs &a, int b, int &q0, int &nq) {
     q0 = __ldg(a.cu_q + b);
     const int q1 = __ldg(a.cu_q + b + 1);
     nq = q1 - q0;
     const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.T && nq <= kTreeTokens && nq <= __ldg(a.seq_lens + b);
-    if (!ok) nq = 0;
+    if (!ok || (a.few && nq > a.few)) nq = 0;
     return ok;
 }
 // Fills in what depends on the sequence w.b alone.
@@ -978,7 +979,8 @@ cudaError_t run(const DecodeAttnArgs &a, int sms, cudaStream_t s) {
                     C::kRowB == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
         return cudaErrorInvalidValue;
     // rows of a key/value head (kTree: at most), tiles of them
-    const int G = a.Hq / a.kv.Hkv * (MODE == kTree ? (a.T < kTreeTokens ? a.T : kTreeTokens) : 1);
+    const int tokens = MODE != kTree ? 1 : a.few ? a.few : a.T < kTreeTokens ? a.T : kTreeTokens;
+    const int G = a.Hq / a.kv.Hkv * tokens;
     const int RT = (G + C::kRows - 1) / C::kRows, HV = a.kv.Hkv * RT;
     // no more blocks than units could exist
     int64_t keys = (int64_t)a.table_stride * page;

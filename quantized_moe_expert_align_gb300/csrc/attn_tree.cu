@@ -59,6 +59,11 @@ constexpr int kParts = 2;        // in which a key tile's weights come
 constexpr int kScaleBufs = 8;    // key tiles whose scales are held
 constexpr int kSharedBytes = 3 << 10;  // barriers and what the warps tell each other
 
+// Rows of a sequence's key/value head up to which small tiles have them where a batch
+// is in two launches; bytes up to which small tiles may read all of a batch.
+constexpr int kFewRows = 16;
+constexpr int64_t kFewBytes = 256 << 20;
+
 // Items of at least this many key tiles run shared row tiles half a round apart.
 constexpr int kApart = 4;
 
@@ -162,6 +167,8 @@ static_assert(sizeof(Shared) <= kSharedBytes, "shared block");
 struct Seq {
     int q0, nq, nk, tiles, RB, HV;  // blocks of rows per head tile, in all
 };
+// (REST: of more than a.few tokens)
+template <bool REST>
 __device__ __forceinline__ bool seq_of(const DecodeAttnArgs &a, int b, int tpt, int HT, Seq &s) {
     const int64_t room = min((int64_t)a.table_stride << a.kv.page_shift, (int64_t)1 << 30);
     s.q0 = __ldg(a.cu_q + b);
@@ -170,7 +177,7 @@ __device__ __forceinline__ bool seq_of(const DecodeAttnArgs &a, int b, int tpt, 
     s.nq = q1 - s.q0;
     const bool ok = s.q0 >= 0 && q1 >= s.q0 && q1 <= a.T && s.nq <= kTreeTokens && s.nk >= 0 && s.nk <= room &&
                     s.nq <= s.nk;
-    if (!ok) s.nq = 0;
+    if (!ok || (REST && s.nq <= a.few)) s.nq = 0;
     s.tiles = s.nq ? (s.nk + kKeys - 1) / kKeys : 0;
     s.RB = (s.nq + kM * tpt - 1) / (kM * tpt);
     s.HV = a.kv.Hkv * HT * s.RB;
@@ -225,7 +232,7 @@ __device__ __forceinline__ void mma_e4m3_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool REST>
 __global__ void __launch_bounds__((Cfg<D, FP8>::kThreads), 1)
 tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtensorMap map_q,
             const __grid_constant__ CUtensorMap map_kv) {
@@ -295,7 +302,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
     int bad = 0x7fffffff;
     for (int b = s0; b < s1; ++b) {
         Seq s;
-        if (!seq_of(a, b, tpt, HT, s) && b < bad) bad = b;
+        if (!seq_of<REST>(a, b, tpt, HT, s) && b < bad) bad = b;
         mine += (int64_t)s.tiles * s.HV;
     }
     int64_t scan = mine;
@@ -321,7 +328,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
         int b = s0;
         for (;; ++b) {
             Seq s;
-            seq_of(a, b, tpt, HT, s);
+            seq_of<REST>(a, b, tpt, HT, s);
             const int64_t n = (int64_t)s.tiles * s.HV;
             if (u0 < at + n) break;
             at += n;
@@ -392,7 +399,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
             int b = 0, hv = 0, j = 0;
             if (u0 < u1) {
                 b = sm->b0;
-                seq_of(a, b, tpt, HT, sq);
+                seq_of<REST>(a, b, tpt, HT, sq);
                 hv = (int)(sm->first / sq.tiles);
                 j = (int)(sm->first % sq.tiles);
             }
@@ -444,7 +451,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
                         if (u < u1)
                             do {
                                 ++b;
-                                seq_of(a, b, tpt, HT, sq);
+                                seq_of<REST>(a, b, tpt, HT, sq);
                             } while (sq.tiles == 0);
                     }
                 }
@@ -1154,7 +1161,7 @@ tree_kernel(const DecodeAttnArgs a, const int HT, const __grid_constant__ CUtens
 // 32 columns of it; a thread has a row and 8 columns.  Latency counts: what the
 // record does not say is not looked up, and the loads of up to kAhead parts are in
 // flight together.
-template <int D>
+template <int D, bool REST>
 __global__ void __launch_bounds__(4 * kTile) tree_join(const DecodeAttnArgs a, const int n_blocks) {
     __shared__ int red[2];
     constexpr int kAhead = 4;
@@ -1176,6 +1183,10 @@ __global__ void __launch_bounds__(4 * kTile) tree_join(const DecodeAttnArgs a, c
         __syncthreads();
         if (tid == 0) {
             Ctrl *ctrl = reinterpret_cast<Ctrl *>(a.workspace);
+            if (REST) {  // what the launch before has found counts too
+                if (ctrl->status == MOE_ERR_DEVICE_TIMEOUT) red[0] = max(red[0], ctrl->detail);
+                if (ctrl->status == MOE_ERR_DEVICE_BAD_INDEX) red[1] = min(red[1], ctrl->detail);
+            }
             ctrl->status = red[0] ? MOE_ERR_DEVICE_TIMEOUT
                                   : (red[1] != 0x7fffffff ? MOE_ERR_DEVICE_BAD_INDEX : MOE_OK);
             ctrl->detail = red[0] ? red[0] : (red[1] != 0x7fffffff ? red[1] : 0);
@@ -1228,7 +1239,7 @@ __global__ void __launch_bounds__(4 * kTile) tree_join(const DecodeAttnArgs a, c
     if (a.lse && c == 0) a.lse[row * a.Hq + h] = none ? -INFINITY : (top + __log2f(sum)) * kLn2;
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool REST>
 cudaError_t run(const DecodeAttnArgs &a, int sms, cudaStream_t s) {
     using C = Cfg<D, FP8>;
     const int G = a.Hq / a.kv.Hkv, Gt = tile_heads(G), tpt = tile_tokens(G), HT = (G + Gt - 1) / Gt;
@@ -1265,7 +1276,7 @@ cudaError_t run(const DecodeAttnArgs &a, int sms, cudaStream_t s) {
     const int64_t most = (a.B < a.T ? a.B : a.T) * tiles * a.kv.Hkv * HT * rb;
     int grid = sms < kMaxGrid ? sms : kMaxGrid;
     if (most < grid) grid = (int)most;
-    auto fn = tree_kernel<D, FP8>;
+    auto fn = tree_kernel<D, FP8, REST>;
     static SmemOnce once;
     cudaError_t err = once.set(reinterpret_cast<const void *>(fn), C::kSmem);
     if (err != cudaSuccess) return err;
@@ -1285,7 +1296,7 @@ cudaError_t run(const DecodeAttnArgs &a, int sms, cudaStream_t s) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cj.attrs = at;
     cj.numAttrs = 1;
-    return cudaLaunchKernelEx(&cj, tree_join<D>, a, grid);
+    return cudaLaunchKernelEx(&cj, tree_join<D, REST>, a, grid);
 }
 
 }  // namespace
@@ -1295,7 +1306,21 @@ size_t tree_workspace(int, int T, int Hq, int Hkv, int D) {
     return small > large ? small : large;
 }
 
-cudaError_t launch_attn_tree(const DecodeAttnArgs &a, cudaStream_t s) {
+// REST: the sequences of more than a.few tokens alone, over fp8.
+template <bool REST>
+static cudaError_t launch_large(const DecodeAttnArgs &a, cudaStream_t s) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const int sms = tc_grid(dev);
+    if (sms < 1) return cudaErrorInvalidDevice;
+    if (REST || a.cache_type == MOE_KV_FP8)
+        return a.D == 128 ? run<128, true, REST>(a, sms, s) : run<64, true, REST>(a, sms, s);
+    return a.D == 128 ? run<128, false, false>(a, sms, s) : run<64, false, false>(a, sms, s);
+}
+
+cudaError_t launch_attn_tree(const DecodeAttnArgs &args, cudaStream_t s) {
+    DecodeAttnArgs a = args;
     // Tiles of 8 or 16 rows where none can have more, or where there are few on average
     // (what a sequence has the host does not know; any number is right either way).  64
     // sequences of 4096 keys, 4 key/value heads, here and in small tiles: 8 rows each,
@@ -1304,16 +1329,27 @@ cudaError_t launch_attn_tree(const DecodeAttnArgs &a, cudaStream_t s) {
     // 90, 83 and 84.  6 sequences of 4000 keys, one head, 4 rows, bf16 21 and 11; 162 of
     // 300, 2 heads, 6 rows, bf16 21 and 16, fp8 33 and 17.
     const int tokens = a.T < kTreeTokens ? a.T : kTreeTokens, G = a.Hq / a.kv.Hkv;
-    const int few = a.cache_type == MOE_KV_BF16 && a.D == 128 ? 8 : 12;
-    if (tokens * G <= 16 || (int64_t)a.T * G <= (int64_t)a.B * few) return launch_attn_tree_small(a, s);
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess) return err;
-    const int sms = tc_grid(dev);
-    if (sms < 1) return cudaErrorInvalidDevice;
-    const bool fp8 = a.cache_type == MOE_KV_FP8;
-    if (a.D == 128) return fp8 ? run<128, true>(a, sms, s) : run<128, false>(a, sms, s);
-    return fp8 ? run<64, true>(a, sms, s) : run<64, false>(a, sms, s);
+    const bool bf16 = a.cache_type == MOE_KV_BF16;
+    const int few = bf16 && a.D == 128 ? 8 : 12;
+    if (tokens * G <= kFewRows) return launch_attn_tree_small(a, s);
+    if ((int64_t)a.T * G > (int64_t)a.B * few || G > kFewRows) return launch_large<false>(a, s);
+    // A few sequences may have most of the rows, and small tiles read such a one's keys
+    // for every 8 or 16 of them.  Where that could be many bytes (by the table's width),
+    // it is large tiles over bf16, where the small ones gain nothing from there on, and
+    // over fp8 small tiles for sequences of up to 16 rows, then large ones for the
+    // others.  One sequence of 64 tokens and 63 without, 32 heads of 128 over 4, in small
+    // tiles and so: bf16, 1024 keys (128 MB) 22 and 17 us, 2048 31 and 21, 8192 87 and 27;
+    // fp8, 2048 (132 MB) 31 and 30, 4096 50 and 33, 8192 87 and 37.  64 sequences of 6
+    // tokens, 4 heads over 4, 4096 keys: bf16 (384 MB) 90 and 90, heads of 64 49 and 52;
+    // 64 of 2 tokens, 16 heads, fp8 (264 MB), where the second launch finds nothing, 55 and
+    // 61.
+    const int64_t reads = ((int64_t)a.T * G + 7) / 8 * a.kv.Hkv * ((int64_t)a.table_stride << a.kv.page_shift) *
+                          (bf16 ? 4 * a.D : 2 * a.D + 8);
+    if (reads <= kFewBytes) return launch_attn_tree_small(a, s);
+    if (bf16) return launch_large<false>(a, s);
+    a.few = kFewRows / G;
+    const cudaError_t err = launch_attn_tree_small(a, s);
+    return err != cudaSuccess ? err : launch_large<true>(a, s);
 }
 
 }  // namespace moe
