@@ -1,9 +1,10 @@
-"""Windowed prompts: batches of more sequences than a warp has lanes, planned and
-not cut, planned and cut; how far a NaN in v can reach."""
+"""Windowed decode in copies of either size; windowed prompts: batches of more
+sequences than a warp has lanes, planned and not cut, planned and cut; how far a
+NaN in v can reach."""
 import pytest
 
 from tests import attn_util as au, serve_util as su
-from tests.test_gpu_window import _prefill
+from tests.test_gpu_window import _decode, _prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +48,11 @@ def test_a_nan_in_v_reaches_no_further_than_stated(gpu, sinks, at, H, D):
     assert not bad[rest].any() and torch.equal(out[rest], ref[rest])
     # beside the NaN nothing else changes
     assert torch.equal(out[~bad], ref[~bad])
+
+
+@pytest.mark.parametrize("D,page", [(64, 64), (64, 128), (64, 256), (128, 64), (128, 256)])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (32, 2)])
+@pytest.mark.parametrize("window,sinks", [(499, 4), (500, 4), (501, 70), (2299, 0), (2300, 5), (2301, 64)])
+def test_decode_with_copies_of_32_and_64_rows(gpu, window, sinks, Hq, Hkv, D, page):
+    """Both sides of the windows from which on copies over fp8 have 64 rows."""
+    _decode([0, 1, 63, 64, 65, 570, 2400, 3000, 2305], window, sinks, Hq, Hkv, D, True, page, seed=window)
