@@ -41,8 +41,10 @@ size_t moe_page_plan_workspace_size(int B);
  * seq_lens[b] + 1 - window.  kept[b] says up to which page (its number in the
  * sequence; 0 for a new one) earlier calls have done so, kept_out[b] the same
  * after this one.  Their entries keep their old numbers: only attention through
- * such a window may use that row from then on.  window 0: kept and kept_out are
- * not used.
+ * such a window may use that row from then on, not moe_attn_tree.  moe_kv_gather
+ * brings what those pages hold by now, and moe_attn_prefill_window of the tokens from
+ * seq_lens[b] on over what it brought takes nothing from there.  window 0: kept and
+ * kept_out are not used.
  *
  * dropped (NULL: none) says how many tokens sequence b has lost since its last
  * step, rejected drafts: its table holds pages for seq_lens[b] + dropped[b].  New
@@ -116,7 +118,8 @@ size_t moe_attn_tree_workspace_size(int B, int T, int Hq, int Hkv, int D);
  * cached tokens (appended before).  Its row i sees every token before the
  * drafted ones, and drafted token j where bit j of tree[row] is set (a tree: the
  * row's ancestors and itself; (2 << i) - 1: plain causal order).  A row that
- * sees nothing gets zeros and lse = -inf.
+ * sees nothing gets zeros and lse = -inf.  (There is no window: all of a sequence's
+ * pages are read, so none may have gone back.)
  *  q [T][Hq][D], out [T][Hq][D] bf16; tree [T] uint64, 8-byte aligned;
  *  lse [T][Hq] fp32 or NULL; page_table as in moe_kv_gather.
  * Rows of out and lse that belong to no sequence are not written.  What the

@@ -102,10 +102,12 @@ def page_plan(pool, page_table, seq_lens, new_lens, page_size, rows, window=0, s
     back to the pool).  page_table [B][n] gets the new pages; ``rows`` is the
     number of rows of the step's buffers, at least the new tokens.  With a
     ``window``, pages behind it go back too, ``kept`` [B] saying how far that
-    has come (zeros at first).  offsets [rows]: positions are seq_lens[b] +
+    has come (zeros at first); from then on the row is for attention through that
+    window alone (of the new tokens over what kv_gather brings, too).  offsets [rows]: positions are seq_lens[b] +
     offsets[row] instead of seq_lens[b] + i (depths of drafted tokens).  dropped
     [B]: tokens that sequence b has lost since its last step (rejected drafts),
-    whose pages are still in its table: they are used first, or go back.
+    whose pages are still in its table: they are used first, or go back (a step
+    that drops tokens of a page that has gone back is refused).
 
     Returns ``out``, a PagePlan (a new one by default); any of its seq_lens and
     kept may be the tensor passed in.  The pool's state moves on in place unless
@@ -156,7 +158,8 @@ def attn_tree(q, cache, page_table, seq_lens, cu_q, tree, scale=None, out=None, 
     which sequence b has the rows [cu_q[b], cu_q[b+1]) (64 at most), its last
     cached tokens.  tree [T] int64: bit j of a row's is set where it sees drafted
     token j of its sequence ((2 << i) - 1 for row i: plain causal order); it sees
-    all tokens before the drafted ones.  page_table [B][n], seq_lens [B] and cu_q
+    all tokens before the drafted ones (none of whose pages may have gone back behind
+    a window).  page_table [B][n], seq_lens [B] and cu_q
     [B+1] int32; scale defaults to D^-1/2.  Returns out [T][Hq][D]; ``lse`` True
     or a float32 [T][Hq] tensor also returns the logsumexp, as (out, lse)."""
     if _attn.torch is None:
