@@ -62,7 +62,7 @@ constexpr int kSharedBytes = 3 << 10;  // barriers and what the warps tell each 
 // Rows of a sequence's key/value head up to which small tiles have them where a batch
 // is in two launches; bytes up to which small tiles may read all of a batch.
 constexpr int kFewRows = 16;
-constexpr int64_t kFewBytes = 256 << 20;
+constexpr double kFewBytes = 256 << 20;
 
 // Items of at least this many key tiles run shared row tiles half a round apart.
 constexpr int kApart = 4;
@@ -1343,8 +1343,9 @@ cudaError_t launch_attn_tree(const DecodeAttnArgs &args, cudaStream_t s) {
     // tokens, 4 heads over 4, 4096 keys: bf16 (384 MB) 90 and 90, heads of 64 49 and 52;
     // 64 of 2 tokens, 16 heads, fp8 (264 MB), where the second launch finds nothing, 55 and
     // 61.
-    const int64_t reads = ((int64_t)a.T * G + 7) / 8 * a.kv.Hkv * ((int64_t)a.table_stride << a.kv.page_shift) *
-                          (bf16 ? 4 * a.D : 2 * a.D + 8);
+    // (a double: with the widest tables this is past 64 bits)
+    const double reads = (double)a.T * G / 8 * a.kv.Hkv * ((int64_t)a.table_stride << a.kv.page_shift) *
+                         (bf16 ? 4 * a.D : 2 * a.D + 8);
     if (reads <= kFewBytes) return launch_attn_tree_small(a, s);
     if (bf16) return launch_large<false>(a, s);
     a.few = kFewRows / G;
