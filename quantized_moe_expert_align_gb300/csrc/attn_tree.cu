@@ -18,8 +18,8 @@
 // The key tiles of the whole batch, in order, are shared out evenly over one block
 // per SM; a range cut by a block's end is joined by a second kernel, in key order.
 //
-// Measured, 32 sequences of 8192 keys, 32 heads of 128 over 4, 16 tokens: bf16 103 us
-// (5.2 TB/s; the rest is start, joins and ends of ranges), fp8 84; 64 tokens
+// Measured, 32 sequences of 8192 keys, 32 heads of 128 over 4, 16 tokens: bf16 102 us
+// (5.3 TB/s; the rest is start, joins and ends of ranges), fp8 85; 64 tokens
 // (512 rows) over fp8 278 us (990 TFLOP/s).  64 sequences of 4096 keys, 64 heads over
 // 8, 16 tokens: bf16 183 us (5.9 TB/s), fp8 160 (3.5 TB/s: not the bytes but the way
 // from scores over weights to products, some 2200 cycles a key tile of which the
@@ -36,9 +36,8 @@
 // and 2^-25 times that power of two where a value is smaller than 2^-14 of it; where
 // it grows, the sums are scaled down like where a reference grows).  The weights are
 // fp16 too (2^-11), 2^6-fold, so that those below 2^-20 of the reference's lose bits.
-// (The scales of V in the weights, as fp32 products in the softmax: 110 us instead
-// of 105 for 32 sequences of 8192 keys, 16 tokens, 32 heads of 128 over 4: one more
-// value a key that every softmax thread loads from shared memory.)
+// (The scales of V in the weights, as fp32 products in the softmax, cost 5% when that
+// was tried: one more value a key that every softmax thread loads from shared memory.)
 #include <type_traits>
 
 #include "attn_tc.cuh"

@@ -6,8 +6,10 @@
 // rows, a few at a time, needs no others.  What it moves is read and written
 // once; a batch moves a few megabytes, so latency bounds it: all table entries are
 // looked up together, and up to kWay rows of a column are in flight.  One block looks
-// all paths over for the status word, a thread an element (256 paths of 8 tokens, 64
-// heads' worth of bf16: 31 us with a warp a path).
+// all paths over for the status word, a thread an element.
+// Measured: 256 paths of up to 8 tokens, 8 heads of 128, bf16, 7.6 us on the GPU (31 with
+// a warp a path in the look over).  That look bounds very large calls: 2048 paths of 64
+// take 0.33 ms, 65535 of them 13.6.
 #include <type_traits>
 
 #include "device_common.cuh"

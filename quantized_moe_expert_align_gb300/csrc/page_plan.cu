@@ -16,9 +16,10 @@
 //    itself: a sequence's numbers are read by all, so none of them may be written
 //    in place.
 //  kTwoKernels: in place, or too many sequences for that, by a second kernel.
-// Measured (in a captured graph): 90 sequences of a token each with windows 7.4 us;
-// 256 prompts of 898 thousand rows, 7.3 MB, 9.3 us by every block and 15.7 by two
-// kernels.
+// Measured (in a captured graph): 90 sequences of a token each with windows 7.5 us, in
+// place 7.0; 256 prompts of 902 thousand rows, 7.3 MB, 9.4 us by every block, and 12.5 to
+// 15 by two kernels, as where the pool's state moves on in place (the Python layer's
+// default).
 #include <climits>
 
 #include "device_common.cuh"
