@@ -1334,12 +1334,12 @@ cudaError_t launch_attn_tree(const DecodeAttnArgs &args, cudaStream_t s) {
     if ((int64_t)a.T * G > (int64_t)a.B * few || G > kFewRows) return launch_large<false>(a, s);
     // A few sequences may have most of the rows, and small tiles read such a one's keys
     // for every 8 or 16 of them.  Where that could be many bytes (by the table's width),
-    // it is large tiles over bf16, where the small ones gain nothing from there on, and
+    // it is large tiles over bf16, where the small ones gain little from there on, and
     // over fp8 small tiles for sequences of up to 16 rows, then large ones for the
     // others.  One sequence of 64 tokens and 63 without, 32 heads of 128 over 4, in small
-    // tiles and so: bf16, 1024 keys (128 MB) 22 and 17 us, 2048 31 and 21, 8192 87 and 27;
+    // tiles and so: bf16, 1024 keys (128 MB) 22 and 16 us, 4096 50 and 23, 8192 87 and 26;
     // fp8, 2048 (132 MB) 31 and 30, 4096 50 and 33, 8192 87 and 37.  64 sequences of 6
-    // tokens, 4 heads over 4, 4096 keys: bf16 (384 MB) 90 and 90, heads of 64 49 and 52;
+    // tokens, 4 heads over 4, 4096 keys: bf16 (384 MB) 90 and 91, heads of 64 49 and 52;
     // 64 of 2 tokens, 16 heads, fp8 (264 MB), where the second launch finds nothing, 55 and
     // 61.
     // (a double: with the widest tables this is past 64 bits)
